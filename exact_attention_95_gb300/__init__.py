@@ -20,6 +20,12 @@ Functions carry the C names:
   ``attn_fwd_fp8(Qc, q_scale, Kc, k_scale, Vtc, v_scale, scale, causal)``: e4m3
   codes with one fp32 scale per 128-row block (V transposed) and the FP8
   forward on them (d = 128); ``attn_fp8_vt_stride(N)``
+* ``attn_kv_tables(cached, added, free_pages, block_table, page_size, T)``,
+  ``attn_kv_append_fp8(K, V, slots, k_pages, k_scale, v_pages, v_scale)`` and
+  ``attn_fwd_paged_fp8(Q, k_pages, k_scale, v_pages, v_scale, block_table, cu_q, kv_lens, ...)``:
+  a paged e4m3 key/value cache -- its block table and slot map from the requests'
+  lengths, the quantizing append, and ragged attention over it;
+  ``attn_fwd_paged_workspace_size(T, Hq, Hkv, d)``
 * ``attn_bwd(Q, K, V, O, dO, LSE, scale, causal) -> (dQ, dK, dV)``
 * ``attn_bwd_workspace_size(B, Hq, Hkv, N, d)``
 * ``attn_last_device_status(stream=None)``, ``attn_status_string(code)``
@@ -53,6 +59,7 @@ ATTN_BF16, ATTN_F32 = 0, 1
 EXPORTED = ("attn_fwd", "attn_fwd_split", "attn_fwd_split_workspace_size", "attn_fwd_masked",
             "attn_bwd_masked", "attn_quantize_fp8", "attn_fp8_vt_stride", "attn_fwd_fp8", "attn_bwd",
             "attn_bwd_preprocess", "attn_bwd_main", "attn_bwd_convert", "attn_bwd_workspace_size",
+            "attn_kv_tables", "attn_kv_append_fp8", "attn_fwd_paged_fp8", "attn_fwd_paged_workspace_size",
             "attn_status_string", "attn_last_device_status", "attn_selftest_wait_timeout")
 _BWD_STAGES = {"all": "attn_bwd", "preprocess": "attn_bwd_preprocess", "main": "attn_bwd_main",
                "convert": "attn_bwd_convert"}
@@ -102,6 +109,16 @@ def load_library(path: str = LIB_PATH):
         lib.attn_quantize_fp8.restype = i32
         lib.attn_fwd_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, i32, i32, vp]
         lib.attn_fwd_fp8.restype = i32
+        i64 = ctypes.c_longlong
+        lib.attn_kv_tables.argtypes = [vp, vp, vp, i32, vp, i32, i32, vp, vp, vp, vp, vp, i32, i32, vp]
+        lib.attn_kv_tables.restype = i32
+        lib.attn_kv_append_fp8.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp]
+        lib.attn_kv_append_fp8.restype = i32
+        lib.attn_fwd_paged_fp8.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32,
+                                           i32, i32, f32, i32, i32, vp, sz, vp]
+        lib.attn_fwd_paged_fp8.restype = i32
+        lib.attn_fwd_paged_workspace_size.argtypes = [i32, i32, i32, i32]
+        lib.attn_fwd_paged_workspace_size.restype = sz
         lib.attn_bwd_workspace_size.argtypes = [i32, i32, i32, i32, i32]
         lib.attn_bwd_workspace_size.restype = sz
         lib.attn_status_string.argtypes = [i32]
@@ -352,6 +369,149 @@ def attn_fwd_fp8(Qc, q_scale, Kc, k_scale, Vtc, v_scale, scale=None, causal=Fals
                               _stream(stream))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_fwd_fp8")
+    return O, LSE
+
+
+# ---------------------------------------------------------------- paged 8-bit cache
+def _check_tokens(name, t, heads, d, device=None):
+    """A bf16 [T, heads, d] tensor whose tokens may be apart (a slice of a packed
+    projection); returns the elements between tokens."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError(f"{name} must have shape (T, {heads}, {d}), got {tuple(t.shape)}")
+    if t.shape[0] <= 1:  # the stride of a single token says nothing
+        if t.shape[0] == 1 and not t[0].is_contiguous():
+            raise ValueError(f"{name}: the rows of a token must be contiguous")
+        return heads * d
+    st = t.stride()
+    if (d > 1 and st[2] != 1) or (heads > 1 and st[1] != d) or st[0] < heads * d or st[0] % 8:
+        raise ValueError(f"{name}: the rows of a token must be contiguous and tokens a multiple of 8 elements apart")
+    return st[0]
+
+
+def _check_cache(k_pages, k_scale, v_pages, v_scale, device):
+    """Checks the pages and scales; returns (num_pages, Hkv, page_size, d)."""
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+        raise TypeError("k_pages must be a 4-dimensional CUDA tensor")
+    shape = k_pages.shape
+    _check_tensor("k_pages", k_pages, torch.uint8, shape, device)
+    _check_tensor("v_pages", v_pages, torch.uint8, shape, device)
+    _check_tensor("k_scale", k_scale, torch.float32, shape[:2], device)
+    _check_tensor("v_scale", v_scale, torch.float32, shape[:2], device)
+    return shape
+
+
+def attn_kv_tables(cached, added, free_pages, block_table, page_size, T, kv_lens=None, cu_tokens=None, slots=None,
+                   positions=None, taken=None, stream=None):
+    """Block table entries and slot map of a step from the requests' lengths.
+
+    cached, added int32 [R]; free_pages int32 [F]; block_table int32 [R, max_pages]
+    (updated in place); T places for new tokens.  Returns (kv_lens [R], cu_tokens
+    [R + 1], slots [T] int64, positions [T], taken [2]: pages taken from the head
+    of free_pages, requests refused)."""
+    lib = load_library()
+    i32 = torch.int32
+    R = cached.shape[0]
+    _check_tensor("cached", cached, i32, (R,))
+    dev = cached.device
+    _check_tensor("added", added, i32, (R,), dev)
+    _check_tensor("free_pages", free_pages, i32, (free_pages.numel(),), dev)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [R, max_pages]")
+    max_pages = block_table.shape[1]
+    _check_tensor("block_table", block_table, i32, (R, max_pages), dev)
+    kv_lens = torch.empty(R, dtype=i32, device=dev) if kv_lens is None else kv_lens
+    cu_tokens = torch.empty(R + 1, dtype=i32, device=dev) if cu_tokens is None else cu_tokens
+    slots = torch.empty(T, dtype=torch.int64, device=dev) if slots is None else slots
+    positions = torch.empty(T, dtype=i32, device=dev) if positions is None else positions
+    taken = torch.empty(2, dtype=i32, device=dev) if taken is None else taken
+    _check_tensor("kv_lens", kv_lens, i32, (R,), dev)
+    _check_tensor("cu_tokens", cu_tokens, i32, (R + 1,), dev)
+    _check_tensor("slots", slots, torch.int64, (T,), dev)
+    _check_tensor("positions", positions, i32, (T,), dev)
+    _check_tensor("taken", taken, i32, (2,), dev)
+    with torch.cuda.device(dev):
+        rc = lib.attn_kv_tables(_ptr(cached), _ptr(added), _ptr(free_pages), free_pages.numel(), _ptr(block_table),
+                                max_pages, int(page_size), _ptr(kv_lens), _ptr(cu_tokens), _ptr(slots),
+                                _ptr(positions), _ptr(taken), R, T, _stream(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_kv_tables")
+    return kv_lens, cu_tokens, slots, positions, taken
+
+
+def attn_kv_append_fp8(K, V, slots, k_pages, k_scale, v_pages, v_scale, stream=None):
+    """Quantizes the new tokens' K, V [T, Hkv, d] (bf16) into the pages their slots name.
+
+    k_pages, v_pages uint8 [num_pages, Hkv, page_size, d] and k_scale, v_scale fp32
+    [num_pages, Hkv] are updated in place, and returned."""
+    lib = load_library()
+    dev = K.device
+    num_pages, Hkv, page_size, d = _check_cache(k_pages, k_scale, v_pages, v_scale, dev)
+    k_stride = _check_tokens("K", K, Hkv, d)
+    v_stride = _check_tokens("V", V, Hkv, d, dev)
+    T = K.shape[0]
+    if V.shape[0] != T:
+        raise ValueError(f"V has {V.shape[0]} tokens, K has {T}")
+    _check_tensor("slots", slots, torch.int64, (T,), dev)
+    with torch.cuda.device(dev):
+        rc = lib.attn_kv_append_fp8(_ptr(K), k_stride, _ptr(V), v_stride, _ptr(slots), _ptr(k_pages), _ptr(k_scale),
+                                    _ptr(v_pages), _ptr(v_scale), T, Hkv, d, num_pages, page_size, _stream(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_kv_append_fp8")
+    return k_pages, k_scale, v_pages, v_scale
+
+
+def attn_fwd_paged_workspace_size(T: int, Hq: int, Hkv: int, d: int) -> int:
+    return int(load_library().attn_fwd_paged_workspace_size(T, Hq, Hkv, d))
+
+
+def attn_fwd_paged_fp8(Q, k_pages, k_scale, v_pages, v_scale, block_table, cu_q, kv_lens, scale=None, causal=False,
+                       out_dtype=None, O=None, LSE=None, workspace=None, stream=None):
+    """O [T, Hq, d], LSE [T, Hq] of ragged queries over the paged cache.
+
+    Q bf16 [T, Hq, d]; request r's queries are tokens cu_q[r] .. cu_q[r + 1] - 1 and
+    its keys the first kv_lens[r] tokens of the pages that block_table[r] names
+    (bottom-right causal alignment).  Rows behind cu_q[R] are not written."""
+    lib = load_library()
+    if not isinstance(Q, torch.Tensor) or Q.dim() != 3:
+        raise TypeError("Q must be a CUDA tensor [T, Hq, d]")
+    T, Hq, d = Q.shape
+    dev = Q.device
+    q_stride = _check_tokens("Q", Q, Hq, d)
+    num_pages, Hkv, page_size, dk = _check_cache(k_pages, k_scale, v_pages, v_scale, dev)
+    if dk != d:
+        raise ValueError(f"the pages have d = {dk}, Q has {d}")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [R, max_pages]")
+    R, max_pages = block_table.shape
+    i32 = torch.int32
+    _check_tensor("block_table", block_table, i32, (R, max_pages), dev)
+    _check_tensor("cu_q", cu_q, i32, (R + 1,), dev)
+    _check_tensor("kv_lens", kv_lens, i32, (R,), dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+    out_dt = {torch.bfloat16: ATTN_BF16, torch.float32: ATTN_F32}[out_dtype]
+    O = torch.empty((T, Hq, d), dtype=out_dtype, device=dev) if O is None else O
+    LSE = torch.empty((T, Hq), dtype=torch.float32, device=dev) if LSE is None else LSE
+    _check_tensor("O", O, out_dtype, (T, Hq, d), dev)
+    _check_tensor("LSE", LSE, torch.float32, (T, Hq), dev)
+    with torch.cuda.device(dev):
+        ws_bytes = int(lib.attn_fwd_paged_workspace_size(T, Hq, Hkv, d))
+        if workspace is None:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        _check_workspace(workspace, ws_bytes, dev)
+        rc = lib.attn_fwd_paged_fp8(_ptr(Q), q_stride, _ptr(k_pages), _ptr(k_scale), _ptr(v_pages), _ptr(v_scale),
+                                    _ptr(block_table), _ptr(cu_q), _ptr(kv_lens), _ptr(O), _ptr(LSE), R, T, Hq, Hkv,
+                                    d, num_pages, page_size, max_pages, float(scale), int(bool(causal)), out_dt,
+                                    _ptr(workspace), workspace.numel(), _stream(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_fwd_paged_fp8")
     return O, LSE
 
 

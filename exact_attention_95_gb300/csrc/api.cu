@@ -188,6 +188,15 @@ bool make_map_u8(CUtensorMap* m, const void* base, long long planes, int rows, i
   return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// 3-D map over page codes, one page of one head to a box.
+bool make_map_pages(CUtensorMap* m, const void* base, long long planes, int page, int d) {
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)page, (cuuint64_t)planes};
+  const cuuint64_t strides[2] = {(cuuint64_t)d, (cuuint64_t)d * page};
+  const cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)page, 1};
+  return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box,
+                      d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Shape checks shared by forward and backward.  Returns ATTN_OK or an error.
@@ -216,6 +225,17 @@ int head_group_for(size_t bytes_per_head, long long heads, size_t budget) {
   if (g > heads) g = heads;
   return (int)g;
 }
+
+}  // namespace
+
+int* device_status_word() { return status_ptr(); }
+int device_sms() { return sm_count(); }
+unsigned long long device_wait_limit() { return wait_limit(); }
+bool make_page_map(CUtensorMap* m, const void* base, long long planes, int page, int d) {
+  return make_map_pages(m, base, planes, page, d);
+}
+
+namespace {
 
 // Diagnostic kernel: one thread waits on an mbarrier that is never completed.
 __global__ void selftest_wait_kernel(int* status, unsigned long long limit_ns) {

@@ -137,4 +137,67 @@ cudaError_t launch_bwd_bf16(int d, const CUtensorMap& tmQ, const CUtensorMap& tm
                             const CUtensorMap& tmV, const CUtensorMap& tmdO, const CUtensorMap& tmDQ,
                             const BwdParams& p, unsigned stages, cudaStream_t stream);
 
+// Host services of api.cu for the other files of entry points.
+int* device_status_word();               // the status word of the current device
+int device_sms();                        // its SM count (0 if it cannot be read)
+unsigned long long device_wait_limit();  // nanoseconds one wait may take
+// 3-D uint8 map over page codes [num_pages * Hkv][page][d]: a box is one page
+// of one head, rows swizzled over their own length (128 or 64 bytes).
+bool make_page_map(CUtensorMap* m, const void* base, long long planes, int page, int d);
+
+// Tables of a step of a paged cache (paged_cache.cu); see attn_kv_tables.
+struct KvTablesParams {
+  const int* cached;      // [R]
+  const int* added;       // [R]
+  const int* free_pages;  // [n_free]
+  int* block_table;       // [R, max_pages]
+  int* kv_lens;           // [R]
+  int* cu_tokens;         // [R + 1]
+  long long* slots;       // [T]
+  int* positions;         // [T]
+  int* taken;             // [2]
+  int R, n_free, max_pages, page_log2, T;
+};
+cudaError_t launch_kv_tables(const KvTablesParams& p, int sms, cudaStream_t stream);
+
+// Append of new tokens to a paged 8-bit cache; see attn_kv_append_fp8.
+struct KvAppendParams {
+  const uint16_t* K;  // [T, Hkv, d] bf16, k_stride elements between tokens
+  const uint16_t* V;
+  long long k_stride, v_stride;
+  const long long* slots;  // [T]
+  uint8_t* k_pages;        // [num_pages, Hkv, page, d]
+  uint8_t* v_pages;
+  float* k_scale;          // [num_pages, Hkv]
+  float* v_scale;
+  long long T;
+  int Hkv, num_pages, page_log2;
+};
+cudaError_t launch_kv_append(int d, const KvAppendParams& p, int sms, cudaStream_t stream);
+
+// Attention over a paged 8-bit cache (paged_fwd.cu); see attn_fwd_paged_fp8.
+struct PagedFwdParams {
+  const uint16_t* Q;     // [T, Hq, d] bf16, q_stride elements between tokens
+  long long q_stride;
+  const float* k_scale;  // [num_pages, Hkv]
+  const float* v_scale;
+  const int* block_table;  // [R, max_pages]
+  const int* cu_q;         // [R + 1]
+  const int* kv_lens;      // [R]
+  void* O;                 // [T, Hq, d] bf16 or fp32
+  float* LSE;              // [T, Hq]
+  float* part_o;           // workspace: [workers][2][rows of a tile][d] partial sums
+  float* part_ml;          // workspace: [workers][2][rows of a tile][2] their maxima and sums
+  int* desc;               // workspace: [workers][8] what the merge has to do
+  int* status;
+  int R, T, Hq, Hkv, G, num_pages, page_log2, max_pages;
+  float scale_log2;
+  int causal, out_f32;
+  unsigned long long wait_limit_ns;
+};
+size_t paged_fwd_workspace_bytes(int d, int sms);
+// Fills in the workspace pointers of p from `workspace` and launches.
+cudaError_t launch_fwd_paged(int d, const CUtensorMap& tmK, const CUtensorMap& tmV, PagedFwdParams& p, void* workspace,
+                             int sms, cudaStream_t stream);
+
 }  // namespace attn

@@ -1,0 +1,171 @@
+// paged_api.cu -- entry points of the paged 8-bit key/value cache declared in
+// include/attn.h: argument checks, tensor maps, launches.
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/attn.h"
+#include "kernels.h"
+
+namespace {
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// log2 of a supported page size, else -1.
+int page_log2(int page_size) {
+  switch (page_size) {
+    case 16: return 4;
+    case 32: return 5;
+    case 64: return 6;
+    case 128: return 7;
+  }
+  return -1;
+}
+
+constexpr int kMaxRequests = 16384;  // the attention's table of sums holds as many
+
+// Checks shared by the calls that take pages.
+attn_status check_cache(const void* kp, const float* ks, const void* vp, const float* vs, int Hkv, int d,
+                        int num_pages, int page_size) {
+  if (!kp || !ks || !vp || !vs) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(kp, 16) || !aligned(vp, 16) || !aligned(ks, 4) || !aligned(vs, 4)) return ATTN_ERR_INVALID_ARG;
+  if (Hkv < 1 || d < 1 || num_pages < 1 || page_size < 1) return ATTN_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128) || page_log2(page_size) < 0) return ATTN_ERR_UNSUPPORTED;
+  // Heads are a grid dimension, (page, head) a 31-bit tensor coordinate.
+  if (Hkv > 65535 || (long long)num_pages * Hkv > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+// Tokens of `heads` rows of d elements, `stride` elements apart.
+bool token_stride_ok(long long stride, long long heads, int d) { return stride >= heads * d && stride % 8 == 0; }
+
+int sms_or_default() {
+  const int n = attn::device_sms();
+  return n > 0 ? n : 152;
+}
+
+}  // namespace
+
+extern "C" {
+
+attn_status attn_kv_tables(const int32_t* cached, const int32_t* added, const int32_t* free_pages, int n_free,
+                           int32_t* block_table, int max_pages, int page_size, int32_t* kv_lens,
+                           int32_t* cu_tokens, int64_t* slots, int32_t* positions, int32_t* taken, int R, int T,
+                           void* stream) {
+  if (!cached || !added || !block_table || !kv_lens || !cu_tokens || !taken) return ATTN_ERR_INVALID_ARG;
+  if (R < 1 || T < 0 || n_free < 0 || max_pages < 1 || page_size < 1) return ATTN_ERR_INVALID_ARG;
+  if ((n_free > 0 && !free_pages) || (T > 0 && (!slots || !positions))) return ATTN_ERR_INVALID_ARG;
+  const void* words[] = {cached, added, free_pages, block_table, kv_lens, cu_tokens, positions, taken};
+  for (const void* q : words)
+    if (!aligned(q, 4)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(slots, 8)) return ATTN_ERR_INVALID_ARG;
+  const int pl = page_log2(page_size);
+  if (pl < 0 || (long long)max_pages * page_size > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  // The kernel's sums saturate at 2^31 - 1, which has to exceed both limits.
+  if (T >= 0x7fffffff || n_free >= 0x7fffffff) return ATTN_ERR_UNSUPPORTED;
+  attn::KvTablesParams p{};
+  p.cached = cached;
+  p.added = added;
+  p.free_pages = free_pages;
+  p.block_table = block_table;
+  p.kv_lens = kv_lens;
+  p.cu_tokens = cu_tokens;
+  p.slots = reinterpret_cast<long long*>(slots);
+  p.positions = positions;
+  p.taken = taken;
+  p.R = R;
+  p.n_free = n_free;
+  p.max_pages = max_pages;
+  p.page_log2 = pl;
+  p.T = T;
+  cudaError_t e = attn::launch_kv_tables(p, sms_or_default(), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+attn_status attn_kv_append_fp8(const void* K, long long k_stride, const void* V, long long v_stride,
+                               const int64_t* slots, void* k_pages, float* k_scale, void* v_pages, float* v_scale,
+                               int T, int Hkv, int d, int num_pages, int page_size, void* stream) {
+  attn_status st = check_cache(k_pages, k_scale, v_pages, v_scale, Hkv, d, num_pages, page_size);
+  if (st != ATTN_OK) return st;
+  if (T < 0) return ATTN_ERR_INVALID_ARG;
+  if (T == 0) return ATTN_OK;
+  if (!K || !V || !slots) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(K, 16) || !aligned(V, 16) || !aligned(slots, 8)) return ATTN_ERR_INVALID_ARG;
+  if (!token_stride_ok(k_stride, Hkv, d) || !token_stride_ok(v_stride, Hkv, d)) return ATTN_ERR_INVALID_ARG;
+  attn::KvAppendParams p{};
+  p.K = static_cast<const uint16_t*>(K);
+  p.V = static_cast<const uint16_t*>(V);
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.slots = reinterpret_cast<const long long*>(slots);
+  p.k_pages = static_cast<uint8_t*>(k_pages);
+  p.v_pages = static_cast<uint8_t*>(v_pages);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.T = T;
+  p.Hkv = Hkv;
+  p.num_pages = num_pages;
+  p.page_log2 = page_log2(page_size);
+  cudaError_t e = attn::launch_kv_append(d, p, sms_or_default(), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+size_t attn_fwd_paged_workspace_size(int T, int Hq, int Hkv, int d) {
+  if (T < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (d != 64 && d != 128)) return 0;
+  return attn::paged_fwd_workspace_bytes(d, sms_or_default());
+}
+
+attn_status attn_fwd_paged_fp8(const void* Q, long long q_stride, const void* k_pages, const float* k_scale,
+                               const void* v_pages, const float* v_scale, const int32_t* block_table,
+                               const int32_t* cu_q, const int32_t* kv_lens, void* O, float* LSE, int R, int T, int Hq,
+                               int Hkv, int d, int num_pages, int page_size, int max_pages, float scale, int causal,
+                               attn_dtype out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  attn_status st = check_cache(k_pages, k_scale, v_pages, v_scale, Hkv, d, num_pages, page_size);
+  if (st != ATTN_OK) return st;
+  if (!block_table || !cu_q || !kv_lens) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(block_table, 4) || !aligned(cu_q, 4) || !aligned(kv_lens, 4)) return ATTN_ERR_INVALID_ARG;
+  if (out_dtype != ATTN_BF16 && out_dtype != ATTN_F32) return ATTN_ERR_INVALID_ARG;
+  if (R < 1 || T < 0 || Hq < 1 || Hq % Hkv != 0 || max_pages < 1) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.f) || (causal != 0 && causal != 1)) return ATTN_ERR_INVALID_ARG;
+  if (T == 0) return ATTN_OK;
+  if (!Q || !O || !LSE || !workspace) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(Q, 16) || !aligned(O, 16) || !aligned(LSE, 4) || !aligned(workspace, 256)) return ATTN_ERR_INVALID_ARG;
+  if (!token_stride_ok(q_stride, Hq, d)) return ATTN_ERR_INVALID_ARG;
+  if (R > kMaxRequests || (long long)T * Hq > 0x7fffff00LL || (long long)max_pages * page_size > 0x7fffff00LL)
+    return ATTN_ERR_UNSUPPORTED;
+  const int sms = attn::device_sms();
+  int* status = attn::device_status_word();
+  if (sms < 1 || !status) return ATTN_ERR_CUDA;
+  if (workspace_bytes < attn::paged_fwd_workspace_bytes(d, sms)) return ATTN_ERR_INVALID_ARG;
+  CUtensorMap tk, tv;
+  const long long planes = (long long)num_pages * Hkv;
+  if (!attn::make_page_map(&tk, k_pages, planes, page_size, d) ||
+      !attn::make_page_map(&tv, v_pages, planes, page_size, d))
+    return ATTN_ERR_CUDA;
+  attn::PagedFwdParams p{};
+  p.Q = static_cast<const uint16_t*>(Q);
+  p.q_stride = q_stride;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.block_table = block_table;
+  p.cu_q = cu_q;
+  p.kv_lens = kv_lens;
+  p.O = O;
+  p.LSE = LSE;
+  p.status = status;
+  p.R = R;
+  p.T = T;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.num_pages = num_pages;
+  p.page_log2 = page_log2(page_size);
+  p.max_pages = max_pages;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.causal = causal;
+  p.out_f32 = out_dtype == ATTN_F32;
+  p.wait_limit_ns = attn::device_wait_limit();
+  cudaError_t e = attn::launch_fwd_paged(d, tk, tv, p, workspace, sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -262,6 +262,104 @@ attn_status attn_bwd_noalloc(const void* Q, const void* K, const void* V, const 
  * per-row vectors (D = rowsum(dO * O) and LSE in log2 units).  0 on bad sizes. */
 size_t attn_bwd_workspace_size(int B, int Hq, int Hkv, int N, int d);
 
+/*
+ * Paged 8-bit key/value cache, for serving many requests of growing length.
+ *
+ * The cache is caller-owned device memory: pages of page_size tokens (16, 32,
+ * 64 or 128), for keys and for values
+ *   pages  [num_pages, Hkv, page_size, d] uint8 e4m3 codes (d in {64, 128}),
+ *   scale  [num_pages, Hkv] fp32, > 0: an element's value is code * scale.
+ * Token i of request r lies in page block_table[r][i / page_size], at offset
+ * i % page_size.  num_pages * Hkv < 2^31, max_pages * page_size < 2^31.
+ * The notes this library follows name paged attention and FP8 without an
+ * interface ("02 FlashAttention" §12.1, §12.2); the one below is this
+ * library's own.
+ */
+
+/*
+ * Tables of a step, built on the device from the requests' lengths.  Request r
+ * holds cached[r] tokens and takes added[r] more; the new tokens of all
+ * requests, in request order, are tokens 0, 1, ... of the step's arrays.
+ *   need_r = ceil((cached[r] + added[r]) / page_size) - ceil(cached[r] / page_size)
+ * pages are taken from the head of free_pages in request order.  A request is
+ * refused when its pages exceed max_pages, when its last new token lies behind
+ * place T, or when need_r > 0 and need_0 + ... + need_r > n_free (needs of
+ * requests refused for max_pages count as 0).  Negative lengths count as 0.
+ *   cached, added  [R]          free_pages [n_free] (NULL when n_free is 0)
+ *   block_table    [R, max_pages]: entries of the new pages are written, no
+ *                  other; entries of the cached tokens are read
+ *   kv_lens        [R]    cached + added, or cached where refused
+ *   cu_tokens      [R+1]  first new token of each request, and the total (at most T)
+ *   slots          [T] int64  page * page_size + offset of each new token; -1
+ *                  for those of refused requests and behind the last token
+ *   positions      [T]    index of the token in its request; -1 likewise
+ *   taken          [2]    pages taken from the head of free_pages; requests refused
+ * All outputs but block_table are fully overwritten.  R >= 1, T >= 0 (slots
+ * and positions may be NULL when T is 0).  slots is 8-byte aligned, the rest
+ * 4-byte.  Page ids are copied as they are.
+ */
+attn_status attn_kv_tables(const int32_t* cached, const int32_t* added, const int32_t* free_pages, int n_free,
+                           int32_t* block_table, int max_pages, int page_size, int32_t* kv_lens,
+                           int32_t* cu_tokens, int64_t* slots, int32_t* positions, int32_t* taken, int R, int T,
+                           void* stream);
+
+/*
+ * Quantizes new keys and values into their pages.  Token t goes to slots[t]
+ * (as attn_kv_tables writes them); a slot outside [0, num_pages * page_size)
+ * is skipped.  The tokens of one page have to be consecutive in the call, at
+ * consecutive offsets, and no page may occur twice otherwise: what such a page
+ * then holds is undefined (nothing else is touched).  For the tokens of one
+ * page and a kv head, with off the first one's offset:
+ *   want = the smallest power of two 2^k, k >= -126, with |x| <= 448 * 2^k for
+ *          every finite element x of the new tokens,
+ *   scale' = max(scale, want) if off > 0, else want;
+ *   offsets below off: code' = e4m3(code * scale / scale') if scale' > scale;
+ *   new tokens:        code = e4m3(x / scale')  (round to nearest even,
+ *   infinities to +-448, NaN to the NaN code);
+ *   offsets behind the new tokens keep their codes (they hold no token).
+ * A power of two costs e4m3 no precision, and raising it shifts exponents:
+ * only codes that become subnormal are rounded a second time.
+ *   K, V  [T, Hkv, d] bf16, 16-byte aligned, k_stride / v_stride elements
+ *         between tokens (>= Hkv * d, a multiple of 8: slices of a packed
+ *         projection do)
+ *   slots [T] int64;  pages and scales as above, updated in place.
+ * T >= 0; Hkv <= 65535.
+ */
+attn_status attn_kv_append_fp8(const void* K, long long k_stride, const void* V, long long v_stride,
+                               const int64_t* slots, void* k_pages, float* k_scale, void* v_pages, float* v_scale,
+                               int T, int Hkv, int d, int num_pages, int page_size, void* stream);
+
+/*
+ * Attention of ragged queries over the paged cache.  Request r has the query
+ * tokens cu_q[r] <= t < cu_q[r+1] and the keys 0 .. kv_lens[r]-1; with causal
+ * the mask is aligned to the bottom-right corner (its last query sees all its
+ * keys), as in attn_fwd_split; kept keys give
+ *   s_ij = scale * <Q_i, k_j>, O_i = sum_j softmax_j(s_i) v_j, LSE_i = ln sum_j e^{s_ij},
+ * k_j and v_j being code * scale of their page.  A row with no kept key gets
+ * O = 0 and LSE = -inf.  Rows t >= cu_q[R] are left as they were.  Products
+ * run in f16 with fp32 sums (codes are exact in f16; so are bf16 queries down
+ * to 2^-29 of their row's largest element); the weights are rounded to f16,
+ * the sums of the softmax are not.
+ *   Q   [T, Hq, d] bf16, 16-byte aligned, q_stride elements between tokens
+ *       (>= Hq * d, a multiple of 8);  Hq % Hkv == 0
+ *   block_table [R, max_pages], cu_q [R+1] (non-decreasing), kv_lens [R]
+ *   O   [T, Hq, d] out_dtype (bf16 or fp32), LSE [T, Hq] fp32
+ *   workspace: attn_fwd_paged_workspace_size(T, Hq, Hkv, d) bytes, 256-byte
+ *       aligned, owned by the caller, not shared with a concurrent call.
+ * Lengths past the table and page ids outside [0, num_pages) in it are
+ * reported as ATTN_ERR_DEVICE by attn_last_device_status; such keys take no
+ * part.  cu_q is clipped to [0, T].  R <= 16384 and T * Hq < 2^31 - 256, else
+ * ATTN_ERR_UNSUPPORTED.  T may be 0 (nothing is done).
+ */
+attn_status attn_fwd_paged_fp8(const void* Q, long long q_stride, const void* k_pages, const float* k_scale,
+                               const void* v_pages, const float* v_scale, const int32_t* block_table,
+                               const int32_t* cu_q, const int32_t* kv_lens, void* O, float* LSE, int R, int T, int Hq,
+                               int Hkv, int d, int num_pages, int page_size, int max_pages, float scale, int causal,
+                               attn_dtype out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace attn_fwd_paged_fp8 needs on the current device; 0 on bad sizes. */
+size_t attn_fwd_paged_workspace_size(int T, int Hq, int Hkv, int d);
+
 /* Static string naming a status code. */
 const char* attn_status_string(attn_status s);
 
