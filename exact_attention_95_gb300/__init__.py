@@ -373,25 +373,54 @@ def attn_fwd_fp8(Qc, q_scale, Kc, k_scale, Vtc, v_scale, scale=None, causal=Fals
 
 
 # ---------------------------------------------------------------- paged 8-bit cache
-def _check_tokens(name, t, heads, d, device=None):
+# A decoding step makes these calls once a layer, on kernels of a few
+# microseconds: the checks below cost as little as they can (one expression a
+# tensor; _check_tensor words the error), and pointers go to ctypes as ints.
+def _check_fast(name, t, dtype, shape, device):
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        _check_tensor(name, t, dtype, shape, device)
+
+
+def _cuda_device(name, t):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _call(fn, dev, stream, *args):
+    """fn(*args, stream) with `dev` current; `stream` None is dev's current stream."""
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev.index)
+    elif stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
+    else:
+        handle = stream.cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, handle)
+    if rc != ATTN_OK:
+        raise AttnError(rc, fn.__name__)
+
+
+def _check_tokens(name, t, heads, d, device):
     """A bf16 [T, heads, d] tensor whose tokens may be apart (a slice of a packed
     projection); returns the elements between tokens."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
+    if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
         raise ValueError(f"{name} must have shape (T, {heads}, {d}), got {tuple(t.shape)}")
-    if t.shape[0] <= 1:  # the stride of a single token says nothing
-        if t.shape[0] == 1 and not t[0].is_contiguous():
-            raise ValueError(f"{name}: the rows of a token must be contiguous")
-        return heads * d
     st = t.stride()
-    if (d > 1 and st[2] != 1) or (heads > 1 and st[1] != d) or st[0] < heads * d or st[0] % 8:
+    apart = st[0] if t.shape[0] > 1 else heads * d  # the stride of a single token says nothing
+    if st[2] != 1 or (heads > 1 and st[1] != d) or apart < heads * d or apart % 8:
         raise ValueError(f"{name}: the rows of a token must be contiguous and tokens a multiple of 8 elements apart")
-    return st[0]
+    return apart
 
 
 def _check_cache(k_pages, k_scale, v_pages, v_scale, device):
@@ -399,11 +428,19 @@ def _check_cache(k_pages, k_scale, v_pages, v_scale, device):
     if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
         raise TypeError("k_pages must be a 4-dimensional CUDA tensor")
     shape = k_pages.shape
-    _check_tensor("k_pages", k_pages, torch.uint8, shape, device)
-    _check_tensor("v_pages", v_pages, torch.uint8, shape, device)
-    _check_tensor("k_scale", k_scale, torch.float32, shape[:2], device)
-    _check_tensor("v_scale", v_scale, torch.float32, shape[:2], device)
+    scales = shape[:2]
+    _check_fast("k_pages", k_pages, torch.uint8, shape, device)
+    _check_fast("v_pages", v_pages, torch.uint8, shape, device)
+    _check_fast("k_scale", k_scale, torch.float32, scales, device)
+    _check_fast("v_scale", v_scale, torch.float32, scales, device)
     return shape
+
+
+def _check_table(block_table, device):
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise TypeError("block_table must be a CUDA tensor [R, max_pages]")
+    _check_fast("block_table", block_table, torch.int32, block_table.shape, device)
+    return block_table.shape
 
 
 def attn_kv_tables(cached, added, free_pages, block_table, page_size, T, kv_lens=None, cu_tokens=None, slots=None,
@@ -416,31 +453,36 @@ def attn_kv_tables(cached, added, free_pages, block_table, page_size, T, kv_lens
     of free_pages, requests refused)."""
     lib = load_library()
     i32 = torch.int32
-    R = cached.shape[0]
-    _check_tensor("cached", cached, i32, (R,))
-    dev = cached.device
-    _check_tensor("added", added, i32, (R,), dev)
-    _check_tensor("free_pages", free_pages, i32, (free_pages.numel(),), dev)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [R, max_pages]")
-    max_pages = block_table.shape[1]
-    _check_tensor("block_table", block_table, i32, (R, max_pages), dev)
-    kv_lens = torch.empty(R, dtype=i32, device=dev) if kv_lens is None else kv_lens
-    cu_tokens = torch.empty(R + 1, dtype=i32, device=dev) if cu_tokens is None else cu_tokens
-    slots = torch.empty(T, dtype=torch.int64, device=dev) if slots is None else slots
-    positions = torch.empty(T, dtype=i32, device=dev) if positions is None else positions
-    taken = torch.empty(2, dtype=i32, device=dev) if taken is None else taken
-    _check_tensor("kv_lens", kv_lens, i32, (R,), dev)
-    _check_tensor("cu_tokens", cu_tokens, i32, (R + 1,), dev)
-    _check_tensor("slots", slots, torch.int64, (T,), dev)
-    _check_tensor("positions", positions, i32, (T,), dev)
-    _check_tensor("taken", taken, i32, (2,), dev)
-    with torch.cuda.device(dev):
-        rc = lib.attn_kv_tables(_ptr(cached), _ptr(added), _ptr(free_pages), free_pages.numel(), _ptr(block_table),
-                                max_pages, int(page_size), _ptr(kv_lens), _ptr(cu_tokens), _ptr(slots),
-                                _ptr(positions), _ptr(taken), R, T, _stream(stream))
-    if rc != ATTN_OK:
-        raise AttnError(rc, "attn_kv_tables")
+    dev = _cuda_device("cached", cached)
+    R, max_pages = _check_table(block_table, dev)
+    _check_fast("cached", cached, i32, (R,), dev)
+    _check_fast("added", added, i32, (R,), dev)
+    F = _cuda_device("free_pages", free_pages) and free_pages.numel()
+    _check_fast("free_pages", free_pages, i32, (F,), dev)
+    empty = torch.empty
+    if kv_lens is None:
+        kv_lens = empty(R, dtype=i32, device=dev)
+    else:
+        _check_fast("kv_lens", kv_lens, i32, (R,), dev)
+    if cu_tokens is None:
+        cu_tokens = empty(R + 1, dtype=i32, device=dev)
+    else:
+        _check_fast("cu_tokens", cu_tokens, i32, (R + 1,), dev)
+    if slots is None:
+        slots = empty(T, dtype=torch.int64, device=dev)
+    else:
+        _check_fast("slots", slots, torch.int64, (T,), dev)
+    if positions is None:
+        positions = empty(T, dtype=i32, device=dev)
+    else:
+        _check_fast("positions", positions, i32, (T,), dev)
+    if taken is None:
+        taken = empty(2, dtype=i32, device=dev)
+    else:
+        _check_fast("taken", taken, i32, (2,), dev)
+    _call(lib.attn_kv_tables, dev, stream, cached.data_ptr(), added.data_ptr(), free_pages.data_ptr(), F,
+          block_table.data_ptr(), max_pages, page_size, kv_lens.data_ptr(), cu_tokens.data_ptr(), slots.data_ptr(),
+          positions.data_ptr(), taken.data_ptr(), R, T)
     return kv_lens, cu_tokens, slots, positions, taken
 
 
@@ -450,19 +492,17 @@ def attn_kv_append_fp8(K, V, slots, k_pages, k_scale, v_pages, v_scale, stream=N
     k_pages, v_pages uint8 [num_pages, Hkv, page_size, d] and k_scale, v_scale fp32
     [num_pages, Hkv] are updated in place, and returned."""
     lib = load_library()
-    dev = K.device
+    dev = _cuda_device("K", K)
     num_pages, Hkv, page_size, d = _check_cache(k_pages, k_scale, v_pages, v_scale, dev)
-    k_stride = _check_tokens("K", K, Hkv, d)
+    k_stride = _check_tokens("K", K, Hkv, d, dev)
     v_stride = _check_tokens("V", V, Hkv, d, dev)
     T = K.shape[0]
     if V.shape[0] != T:
         raise ValueError(f"V has {V.shape[0]} tokens, K has {T}")
-    _check_tensor("slots", slots, torch.int64, (T,), dev)
-    with torch.cuda.device(dev):
-        rc = lib.attn_kv_append_fp8(_ptr(K), k_stride, _ptr(V), v_stride, _ptr(slots), _ptr(k_pages), _ptr(k_scale),
-                                    _ptr(v_pages), _ptr(v_scale), T, Hkv, d, num_pages, page_size, _stream(stream))
-    if rc != ATTN_OK:
-        raise AttnError(rc, "attn_kv_append_fp8")
+    _check_fast("slots", slots, torch.int64, (T,), dev)
+    _call(lib.attn_kv_append_fp8, dev, stream, K.data_ptr(), k_stride, V.data_ptr(), v_stride, slots.data_ptr(),
+          k_pages.data_ptr(), k_scale.data_ptr(), v_pages.data_ptr(), v_scale.data_ptr(), T, Hkv, d, num_pages,
+          page_size)
     return k_pages, k_scale, v_pages, v_scale
 
 
@@ -478,40 +518,40 @@ def attn_fwd_paged_fp8(Q, k_pages, k_scale, v_pages, v_scale, block_table, cu_q,
     its keys the first kv_lens[r] tokens of the pages that block_table[r] names
     (bottom-right causal alignment).  Rows behind cu_q[R] are not written."""
     lib = load_library()
-    if not isinstance(Q, torch.Tensor) or Q.dim() != 3:
-        raise TypeError("Q must be a CUDA tensor [T, Hq, d]")
+    dev = _cuda_device("Q", Q)
+    if Q.dim() != 3:
+        raise ValueError(f"Q must have shape (T, Hq, d), got {tuple(Q.shape)}")
     T, Hq, d = Q.shape
-    dev = Q.device
-    q_stride = _check_tokens("Q", Q, Hq, d)
+    q_stride = _check_tokens("Q", Q, Hq, d, dev)
     num_pages, Hkv, page_size, dk = _check_cache(k_pages, k_scale, v_pages, v_scale, dev)
     if dk != d:
         raise ValueError(f"the pages have d = {dk}, Q has {d}")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [R, max_pages]")
-    R, max_pages = block_table.shape
+    R, max_pages = _check_table(block_table, dev)
     i32 = torch.int32
-    _check_tensor("block_table", block_table, i32, (R, max_pages), dev)
-    _check_tensor("cu_q", cu_q, i32, (R + 1,), dev)
-    _check_tensor("kv_lens", kv_lens, i32, (R,), dev)
+    _check_fast("cu_q", cu_q, i32, (R + 1,), dev)
+    _check_fast("kv_lens", kv_lens, i32, (R,), dev)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+    if out_dtype is None:
+        out_dtype = torch.bfloat16
     out_dt = {torch.bfloat16: ATTN_BF16, torch.float32: ATTN_F32}[out_dtype]
-    O = torch.empty((T, Hq, d), dtype=out_dtype, device=dev) if O is None else O
-    LSE = torch.empty((T, Hq), dtype=torch.float32, device=dev) if LSE is None else LSE
-    _check_tensor("O", O, out_dtype, (T, Hq, d), dev)
-    _check_tensor("LSE", LSE, torch.float32, (T, Hq), dev)
-    with torch.cuda.device(dev):
-        ws_bytes = int(lib.attn_fwd_paged_workspace_size(T, Hq, Hkv, d))
-        if workspace is None:
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-        _check_workspace(workspace, ws_bytes, dev)
-        rc = lib.attn_fwd_paged_fp8(_ptr(Q), q_stride, _ptr(k_pages), _ptr(k_scale), _ptr(v_pages), _ptr(v_scale),
-                                    _ptr(block_table), _ptr(cu_q), _ptr(kv_lens), _ptr(O), _ptr(LSE), R, T, Hq, Hkv,
-                                    d, num_pages, page_size, max_pages, float(scale), int(bool(causal)), out_dt,
-                                    _ptr(workspace), workspace.numel(), _stream(stream))
-    if rc != ATTN_OK:
-        raise AttnError(rc, "attn_fwd_paged_fp8")
+    if O is None:
+        O = torch.empty((T, Hq, d), dtype=out_dtype, device=dev)
+    else:
+        _check_fast("O", O, out_dtype, (T, Hq, d), dev)
+    if LSE is None:
+        LSE = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    else:
+        _check_fast("LSE", LSE, torch.float32, (T, Hq), dev)
+    if workspace is None:
+        # The size is the current device's; all devices of a process are GB300s.
+        workspace = torch.empty(lib.attn_fwd_paged_workspace_size(T, Hq, Hkv, d), dtype=torch.uint8, device=dev)
+    else:
+        _check_workspace(workspace, 0, dev)
+    _call(lib.attn_fwd_paged_fp8, dev, stream, Q.data_ptr(), q_stride, k_pages.data_ptr(), k_scale.data_ptr(),
+          v_pages.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), cu_q.data_ptr(), kv_lens.data_ptr(),
+          O.data_ptr(), LSE.data_ptr(), R, T, Hq, Hkv, d, num_pages, page_size, max_pages, scale,
+          1 if causal else 0, out_dt, workspace.data_ptr(), workspace.numel())
     return O, LSE
 
 

@@ -23,9 +23,11 @@
 // (m, l, O) in the workspace for the merge kernel.  Every CTA finds its range
 // from the lengths on the device; nothing is planned on the host.
 //
-// A CTA: eight warps that each take 16 keys of a unit, with their own running
-// maximum, sum and accumulators, merged at the item's end; one producer warp
-// that walks the block table and loads whole (page, head) boxes by TMA.
+// A CTA: a producer warp that walks its range and loads whole (page, head)
+// boxes by TMA into a ring of units, and sets of four consumer warps that take
+// the units in turn, 32 keys a warp.  Every warp keeps its own running
+// maximum, sum and accumulators of the item; they meet in shared memory at the
+// item's end.
 #include <algorithm>
 
 #include "kernels.h"
@@ -34,43 +36,54 @@
 namespace attn {
 namespace {
 
-constexpr int kRows = 16;          // query rows of a tile
+constexpr int kRows = 8;           // query rows of a tile
 constexpr int kUnit = 128;         // keys of a unit
-constexpr int kWarps = 8;          // consumer warps, 16 keys of a unit each
+constexpr int kSets = 3;           // sets of four consumer warps
+constexpr int kWarps = 4 * kSets;
+constexpr int kHalf = 8;           // warps whose sums the exchange buffer holds
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kMaxGroups = 512;    // 32 requests each
+constexpr int kItems = 4;          // items announced ahead
 constexpr float kPScale = 16384.f;
 
-// What a stage holds, written by the producer.
-struct StageMeta {
-  int flags;      // kBegin, kEnd, kStop
-  int key0;       // first key
-  int len;        // keys of the request
-  int start, n;   // the request's query rows: tokens [start, start + n)
-  int tile, h;    // row tile, kv head
-  int slot;       // where the item's result goes: -1 output, else partial slot of this worker
-  float ks[8], vs[8];  // scales of the unit's pages
-  int pages;      // bit i: page i of the unit was loaded
+// An item of the CTA's range, announced by the producer.
+struct Item {
+  int start, n, len;  // the request's query rows, tokens [start, start + n), and its keys
+  int tile, h;        // row tile, kv head
+  int k0;             // first unit's number in the item
+  int first, count;   // the units in the CTA's line of units; count < 0: no more items
+  int slot;           // where the result goes: -1 output, else partial slot of this worker
   int pad[3];
 };
-enum : int { kBegin = 1, kEnd = 2, kStop = 4 };
+// What a unit's stage holds besides the codes.
+struct UnitMeta {
+  float ks[8], vs[8];  // scales of its pages
+  int pages;           // bit i: page i was loaded
+  int pad[3];
+};
 
 template <int D>
 struct PC {
-  static constexpr int STAGES = D == 128 ? 4 : 8;
+  static constexpr int STAGES = D == 128 ? 6 : 12;
   static constexpr int KBYTES = kUnit * D;
   static constexpr int SBYTES = 2 * KBYTES;
   static constexpr int OFF_RING = 0;
-  static constexpr int OFF_O = STAGES * SBYTES;                   // [warps][16][D] fp32
-  static constexpr int OFF_ML = OFF_O + kWarps * kRows * D * 4;   // [warps][16][2] fp32
-  static constexpr int OFF_META = OFF_ML + kWarps * kRows * 8;
-  static constexpr int OFF_SUMS = OFF_META + STAGES * (int)sizeof(StageMeta);  // [kMaxGroups] int64
-  static constexpr int OFF_BAR = OFF_SUMS + kMaxGroups * 8;
-  static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_WRITTEN = 2 * STAGES, B_READ = 2 * STAGES + 1;
-  static constexpr int OFF_ABORT = OFF_BAR + (2 * STAGES + 2) * 8;
+  static constexpr int OFF_O = STAGES * SBYTES;                   // [kHalf][8][D] fp32
+  static constexpr int OFF_SUMS = OFF_O;                          // [kMaxGroups] int64, until the first item
+  static constexpr int OFF_ML = OFF_O + kHalf * kRows * D * 4;    // [2][kHalf][8][2] fp32
+  static constexpr int OFF_ITEM = OFF_ML + 2 * kHalf * kRows * 8;
+  static constexpr int OFF_META = OFF_ITEM + kItems * (int)sizeof(Item);
+  static constexpr int OFF_BAR = OFF_META + STAGES * (int)sizeof(UnitMeta);
+  static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_IFULL = 2 * STAGES, B_IEMPTY = B_IFULL + kItems;
+  static constexpr int B_GIVEN = B_IEMPTY + kItems, B_WRITTEN = B_GIVEN + 1, B_READ = B_GIVEN + 2;
+  static constexpr int OFF_ABORT = OFF_BAR + (B_READ + 1) * 8;
   static constexpr int SMEM = OFF_ABORT + 8 + 1024;
 };
 static_assert(PC<128>::SMEM <= 232448 && PC<64>::SMEM <= 232448, "shared memory");
+// A parity names a phase only to a waiter that has seen every phase before it:
+// all units of a stage have to go to the same set.
+static_assert(PC<128>::STAGES % kSets == 0 && PC<64>::STAGES % kSets == 0, "stages and sets");
+static_assert(kMaxGroups * 8 <= kHalf * kRows * 64 * 4, "the sums fit the exchange buffer");
 
 __device__ __forceinline__ uint32_t widen(uint32_t two) {
   uint32_t h;
@@ -87,6 +100,12 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The transpose of an 8 x 8 matrix of 16-bit elements, two of a row in a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 __device__ __forceinline__ uint2 lds_u2(uint32_t addr) {
   uint2 v;
@@ -140,16 +159,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sb = smem_u32(smem);
   auto bar = [&](int i) -> uint32_t { return sb + C::OFF_BAR + 8 * i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
-  StageMeta* metas = reinterpret_cast<StageMeta*>(smem + C::OFF_META);
+  UnitMeta* metas = reinterpret_cast<UnitMeta*>(smem + C::OFF_META);
+  Item* items = reinterpret_cast<Item*>(smem + C::OFF_ITEM);
   long long* sums = reinterpret_cast<long long*>(smem + C::OFF_SUMS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(bar(C::B_FULL + s), 1);
-      mbar_init(bar(C::B_EMPTY + s), kWarps);
+      mbar_init(bar(C::B_EMPTY + s), 4);  // the warps of the set that took the unit
     }
-    mbar_init(bar(C::B_WRITTEN), kWarps);
-    mbar_init(bar(C::B_READ), kWarps);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(bar(C::B_IFULL + i), 1);
+      mbar_init(bar(C::B_IEMPTY + i), kWarps);
+    }
+    mbar_init(bar(C::B_GIVEN), kWarps - kHalf);
+    mbar_init(bar(C::B_WRITTEN), kHalf);
+    mbar_init(bar(C::B_READ), kHalf);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -179,13 +204,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long long end = min(total, begin + per);
     int merge_parts = 0, merge_start = 0, merge_n = 0, merge_tile = 0, merge_h = 0;
     const int npg = kUnit >> p.page_log2;  // pages of a unit
-    int it = 0;                            // stages filled
+    int it = 0;                            // units loaded
+    int items_out = 0;                     // items announced
     bool ok = true;
-    // Take a stage: returns its index once the consumers have left it.
-    auto take = [&]() -> int {
-      const int s = it % C::STAGES;
-      if (it >= C::STAGES) ok = mbar_wait_warp(bar(C::B_EMPTY + s), ((it / C::STAGES) & 1) ^ 1, wc);
-      return s;
+    auto item_place = [&]() -> Item* {
+      const int i = items_out % kItems;
+      if (items_out >= kItems) ok = mbar_wait_warp(bar(C::B_IEMPTY + i), ((items_out / kItems) & 1) ^ 1, wc);
+      return items + i;
+    };
+    auto announce = [&]() {  // by lane 0, which wrote the item
+      mbar_arrive(bar(C::B_IFULL + items_out % kItems));
     };
     if (begin < end) {
       // The group, then the request, that holds unit `begin`.
@@ -231,7 +259,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int last_tok = (min(n * (long long)p.G, (long long)(tile + 1) * kRows) - 1) / p.G;
             seen = max(0, min(len, len - n + last_tok + 1));
           }
-          const int ke = min(k1, max(k0 + 1, (seen + kUnit - 1) / kUnit));
+          const int ke = max(k0, min(k1, (seen + kUnit - 1) / kUnit));
+          Item* im = item_place();
+          if (!ok) break;
+          if (lane == 0) {
+            im->start = start;
+            im->n = n;
+            im->len = len;
+            im->tile = tile;
+            im->h = h;
+            im->k0 = k0;
+            im->first = it;
+            im->count = ke - k0;
+            im->slot = slot;
+            announce();
+          }
+          __syncwarp();
+          ++items_out;
           int id = -1;
           float ks = 0.f, vs = 0.f;
           for (int k = k0; k < ke; ++k) {
@@ -240,6 +284,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (in_batch == 0) {
               const int pg = k * npg + lane;
               id = -1;
+              ks = 1.f;
+              vs = 0.f;
               if (((long long)pg << p.page_log2) < seen) {
                 id = row[pg];
                 if (id < 0 || id >= p.num_pages) {
@@ -251,9 +297,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
             }
-            const int s = take();
+            const int s = it % C::STAGES;
+            if (it >= C::STAGES) ok = mbar_wait_warp(bar(C::B_EMPTY + s), ((it / C::STAGES) & 1) ^ 1, wc);
             if (!ok) break;
-            StageMeta* m = metas + s;
+            UnitMeta* m = metas + s;
             const int my = __shfl_sync(0xffffffffu, id, in_batch + (lane & 7));
             const float mk = __shfl_sync(0xffffffffu, ks, in_batch + (lane & 7));
             const float mv = __shfl_sync(0xffffffffu, vs, in_batch + (lane & 7));
@@ -263,17 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               m->ks[lane] = mk;
               m->vs[lane] = mv;
             }
-            if (lane == 0) {
-              m->flags = (k == k0 ? kBegin : 0) | (k + 1 == ke ? kEnd : 0);
-              m->key0 = k * kUnit;
-              m->len = len;
-              m->start = start;
-              m->n = n;
-              m->tile = tile;
-              m->h = h;
-              m->slot = slot;
-              m->pages = (int)mask;
-            }
+            if (lane == 0) m->pages = (int)mask;
             __syncwarp();
             const uint32_t page_bytes = (uint32_t)D << p.page_log2;
             if (lane == 0) mbar_arrive_expect_tx(bar(C::B_FULL + s), 2 * page_bytes * __popc(mask));
@@ -313,12 +350,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       d[4] = merge_h;
     }
     if (ok) {
-      const int s = take();
-      if (ok) {
-        if (lane == 0) {
-          metas[s].flags = kStop;
-          mbar_arrive(bar(C::B_FULL + s));
-        }
+      Item* im = item_place();
+      if (ok && lane == 0) {
+        im->count = -1;
+        announce();
       }
     }
     // Copies in flight land before the CTA leaves (the consumers have waited
@@ -332,237 +367,285 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // -------------------------------------------------------------- consumers
   const int g = lane >> 2, c = lane & 3;
-  const int ko = key_of<D>(g);                       // this lane's key as a column
-  const int kv0 = key_of<D>(2 * c), kv1 = key_of<D>(2 * c + 1);  // its keys as rows of V
+  const int set = warp >> 2, part = 32 * (warp & 3);  // the units it takes, its keys in them
+  const int ko = key_of<D>(g);                        // its key as a row of the first product (and 8 more)
+  const int kv0 = key_of<D>(2 * c), kv1 = key_of<D>(2 * c + 1);  // its keys as a column of the second
   const int cg = D == 128 ? (g >> 1) | ((g & 1) << 2) : g >> 1;  // its 16-byte piece of a V row
   constexpr int QI = D / 64;   // 64-column parts of the contraction over d
-  constexpr int NT = D / 8;    // 8-column tiles of O
-  uint32_t qa[QI][4][4];
-  float o[NT][4];
+  constexpr int MT = D / 16;   // 16-column tiles of O
+  uint32_t qb[QI][4][2];
+  float o[MT][4];
+  // Rows 2c and 2c + 1: running maximum, sum, factor of the products, limit of the keys.
   float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f, f0 = 0.f, f1 = 0.f, vref = 0.f;
   int lim0 = 0, lim1 = 0, lim_all = 0, lim_any = 0;
-  int ends = 0;  // items finished
-  for (int it = 0;; ++it) {
-    const int s = it % C::STAGES;
-    if (!mbar_wait_warp(bar(C::B_FULL + s), (it / C::STAGES) & 1, wc)) break;
-    const StageMeta* mt = metas + s;
-    const int flags = mt->flags;
-    if (flags & kStop) break;
-    const int start = mt->start, n = mt->n, tile = mt->tile, h = mt->h, len = mt->len, slot = mt->slot;
+  // Places of its pieces in a unit's K and V: rows 8 further on are 8 * D bytes
+  // on; the other half of a row's pieces (d = 128) is 64 bytes away, by the
+  // swizzle in the direction that flips bit 6.
+  const uint32_t koff = piece<D>(0, part + ko, c);
+  const uint32_t voff0 = piece<D>(0, part + kv0, cg) + (D == 64 ? 8 * (g & 1) : 0);
+  const uint32_t voff1 = piece<D>(0, part + kv1, cg) + (D == 64 ? 8 * (g & 1) : 0);
+  for (int i = 0;; ++i) {
+    if (!mbar_wait_warp(bar(C::B_IFULL + i % kItems), (i / kItems) & 1, wc)) return;
+    const Item* im = items + i % kItems;
+    const int count = im->count;
+    if (count < 0) return;
+    const int tile = im->tile, h = im->h, len = im->len, n = im->n, start = im->start;
     const int rows = (int)min((long long)kRows, (long long)n * p.G - (long long)tile * kRows);
-    if (flags & kBegin) {
-      // Queries, as f16 after a power of two of the row; limits of the rows' keys.
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int i = g + 8 * half;
-        const int rho = tile * kRows + min(i, rows - 1);
-        const int tok = rho / p.G;
-        const uint4* src = reinterpret_cast<const uint4*>(p.Q + (long long)(start + tok) * p.q_stride +
-                                                          (long long)(h * p.G + rho - tok * p.G) * D);
-        uint4 w[QI][2];
-        uint32_t am = 0;
-#pragma unroll
-        for (int q = 0; q < QI; ++q)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            w[q][e] = __ldg(src + (64 * q + 16 * c) / 8 + e);
-            const uint32_t ws[4] = {w[q][e].x, w[q][e].y, w[q][e].z, w[q][e].w};
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              uint32_t lo = ws[x] & 0x7fffu, hi = (ws[x] >> 16) & 0x7fffu;
-              am = max(am, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-            }
-          }
-        am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
-        am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
-        // 2^-e with the row's largest at 2^14 (its exponent's floor); e within what fp32 can undo.
-        const int e = min(max((int)(am >> 7) - 127, -100), 126) - 14;
-        const float up = __int_as_float((127 - e) << 23);
-        const float f = __int_as_float((127 + e) << 23) * p.scale_log2;
-#pragma unroll
-        for (int q = 0; q < QI; ++q)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint4 v = w[q][j >> 1];
-            const uint32_t a = (j & 1) ? v.z : v.x, b = (j & 1) ? v.w : v.y;
-            qa[q][j][half] = pack_f16(__uint_as_float(a << 16) * up, __uint_as_float(a & 0xffff0000u) * up);
-            qa[q][j][2 + half] = pack_f16(__uint_as_float(b << 16) * up, __uint_as_float(b & 0xffff0000u) * up);
-          }
-        const int lim = p.causal ? max(0, min(len, len - n + tok + 1)) : len;
-        if (half == 0) {
-          f0 = f;
-          lim0 = lim;
-        } else {
-          f1 = f;
-          lim1 = lim;
-        }
-      }
-      const int first_tok = tile * kRows / p.G, last_tok = (tile * kRows + rows - 1) / p.G;
-      lim_all = p.causal ? max(0, min(len, len - n + first_tok + 1)) : len;
-      lim_any = p.causal ? max(0, min(len, len - n + last_tok + 1)) : len;
-      m0 = m1 = -INFINITY;
-      l0 = l1 = vref = 0.f;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    }
-    const int key0 = mt->key0 + 16 * warp;
-    const int pg = (16 * warp) >> p.page_log2;
-    if (key0 < lim_any && ((mt->pages >> pg) & 1)) {
-      const uint32_t kb = sb + C::OFF_RING + s * C::SBYTES, vb = kb + C::KBYTES;
-      const float ks = mt->ks[pg], vs = mt->vs[pg];
-      float acc[2][4] = {};
+    {
+      // Queries (row g), as f16 after a power of two of the row; limits of the rows' keys.
+      const int rho = tile * kRows + min(g, rows - 1);
+      const int tok = rho / p.G;
+      const uint4* src = reinterpret_cast<const uint4*>(p.Q + (long long)(start + tok) * p.q_stride +
+                                                        (long long)(h * p.G + rho - tok * p.G) * D);
+      uint4 w[QI][2];
+      uint32_t am = 0;
 #pragma unroll
       for (int q = 0; q < QI; ++q)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint4 w = lds_u4(piece<D>(kb, 16 * warp + 8 * u + ko, c + 4 * q));
-          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+        for (int e = 0; e < 2; ++e) {
+          w[q][e] = __ldg(src + (64 * q + 16 * c) / 8 + e);
+          const uint32_t ws[4] = {w[q][e].x, w[q][e].y, w[q][e].z, w[q][e].w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mma_f16(acc[u], qa[q][j], widen(ws[j] & 0xffffu), widen(ws[j] >> 16));
+          for (int x = 0; x < 4; ++x) {
+            uint32_t lo = ws[x] & 0x7fffu, hi = (ws[x] >> 16) & 0x7fffu;
+            am = max(am, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+          }
         }
-      // Columns 2c and 2c + 1 of the two products: keys kv0, kv1 (+ 8).
-      const float c0 = f0 * ks, c1 = f1 * ks;
-      float x0[4] = {acc[0][0] * c0, acc[0][1] * c0, acc[1][0] * c0, acc[1][1] * c0};
-      float x1[4] = {acc[0][2] * c1, acc[0][3] * c1, acc[1][2] * c1, acc[1][3] * c1};
-      if (key0 + 16 > lim_all) {
+      am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+      am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+      // 2^-e takes the row's largest to [2^14, 2^15); e within what fp32 can undo.
+      const int e = min(max((int)(am >> 7) - 127, -100), 126) - 14;
+      const float up = __int_as_float((127 - e) << 23);
+      const float f = __int_as_float((127 + e) << 23) * p.scale_log2;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = key0 + 8 * (e >> 1) + ((e & 1) ? kv1 : kv0);
-          if (key >= lim0) x0[e] = -INFINITY;
-          if (key >= lim1) x1[e] = -INFINITY;
+      for (int q = 0; q < QI; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 v = w[q][j >> 1];
+          const uint32_t x = (j & 1) ? v.z : v.x, y = (j & 1) ? v.w : v.y;
+          qb[q][j][0] = pack_f16(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up);
+          qb[q][j][1] = pack_f16(__uint_as_float(y << 16) * up, __uint_as_float(y & 0xffff0000u) * up);
         }
-      }
-      float mx0 = fmaxf(fmaxf(x0[0], x0[1]), fmaxf(x0[2], x0[3]));
-      float mx1 = fmaxf(fmaxf(x1[0], x1[1]), fmaxf(x1[2], x1[3]));
-      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-      const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
-      if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1) || vs > vref) {
-        const float vnew = fmaxf(vref, vs);
-        const float rv = vref > 0.f ? __fdiv_rn(vref, vnew) : 0.f;
-        const float a0 = n0 > m0 ? ex2(m0 - n0) : 1.f, a1 = n1 > m1 ? ex2(m1 - n1) : 1.f;
-        l0 *= a0;
-        l1 *= a1;
-        const float b0 = a0 * rv, b1 = a1 * rv;
+      const int lim = p.causal ? max(0, min(len, len - n + tok + 1)) : len;
+      f0 = __shfl_sync(0xffffffffu, f, 8 * c);
+      f1 = __shfl_sync(0xffffffffu, f, 8 * c + 4);
+      lim0 = __shfl_sync(0xffffffffu, lim, 8 * c);
+      lim1 = __shfl_sync(0xffffffffu, lim, 8 * c + 4);
+      lim_all = __shfl_sync(0xffffffffu, lim, 0);   // the first token's
+      lim_any = __shfl_sync(0xffffffffu, lim, 28);  // the last one's
+      m0 = m1 = -INFINITY;
+      l0 = l1 = vref = 0.f;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          o[j][0] *= b0;
-          o[j][1] *= b0;
-          o[j][2] *= b1;
-          o[j][3] *= b1;
-        }
-        m0 = n0;
-        m1 = n1;
-        vref = vnew;
-      }
-      const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
-      const float rr = vref > 0.f ? __fdiv_rn(vs, vref) * kPScale : vs;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x0[e] = ex2(x0[e] - u0);
-        x1[e] = ex2(x1[e] - u1);
-      }
-      l0 += (x0[0] + x0[1]) + (x0[2] + x0[3]);
-      l1 += (x1[0] + x1[1]) + (x1[2] + x1[3]);
-      uint32_t pa[4];
-      pa[0] = pack_f16(x0[0] * rr, x0[1] * rr);
-      pa[1] = pack_f16(x1[0] * rr, x1[1] * rr);
-      pa[2] = pack_f16(x0[2] * rr, x0[3] * rr);
-      pa[3] = pack_f16(x1[2] * rr, x1[3] * rr);
-      const int vrow = 16 * warp;
-      uint32_t w[4][D / 32];  // four V rows' piece: keys kv0, kv1, kv0 + 8, kv1 + 8
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int rr_ = vrow + 8 * (e >> 1) + ((e & 1) ? kv1 : kv0);
-        if constexpr (D == 128) {
-          const uint4 v = lds_u4(piece<D>(vb, rr_, cg));
-          w[e][0] = v.x;
-          w[e][1] = v.y;
-          w[e][2] = v.z;
-          w[e][3] = v.w;
-        } else {
-          const uint2 v = lds_u2(piece<D>(vb, rr_, cg) + 8 * (g & 1));
-          w[e][0] = v.x;
-          w[e][1] = v.y;
-        }
-      }
-      if (key0 + 16 > len) {  // rows behind the request's last key hold anything, a NaN too
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (key0 + 8 * (e >> 1) + ((e & 1) ? kv1 : kv0) >= len)
-#pragma unroll
-            for (int x = 0; x < D / 32; ++x) w[e][x] = 0;
-      }
-#pragma unroll
-      for (int x = 0; x < D / 32; ++x) {
-        const uint32_t a01 = __byte_perm(w[0][x], w[1][x], 0x5140), a23 = __byte_perm(w[0][x], w[1][x], 0x7362);
-        const uint32_t b01 = __byte_perm(w[2][x], w[3][x], 0x5140), b23 = __byte_perm(w[2][x], w[3][x], 0x7362);
-        mma_f16(o[4 * x + 0], pa, widen(a01 & 0xffffu), widen(b01 & 0xffffu));
-        mma_f16(o[4 * x + 1], pa, widen(a01 >> 16), widen(b01 >> 16));
-        mma_f16(o[4 * x + 2], pa, widen(a23 & 0xffffu), widen(b23 & 0xffffu));
-        mma_f16(o[4 * x + 3], pa, widen(a23 >> 16), widen(b23 >> 16));
-      }
+      for (int j = 0; j < MT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar(C::B_EMPTY + s));
-    if (!(flags & kEnd)) continue;
+    const int first = im->first;
+    int u = first + (set + kSets - first % kSets) % kSets;
+    for (; u < first + count; u += kSets) {
+      const int s = u % C::STAGES;
+      if (!mbar_wait_warp(bar(C::B_FULL + s), (u / C::STAGES) & 1, wc)) return;
+      const int key0 = (im->k0 + u - first) * kUnit + part;
+      const UnitMeta* mt = metas + s;
+      const int pa = part >> p.page_log2, pb = (part + 16) >> p.page_log2;  // pages of its two 16 keys
+      const bool la = (mt->pages >> pa) & 1, lb = (mt->pages >> pb) & 1;
+      if (key0 < lim_any && (la || lb)) {
+        const uint32_t kb = sb + C::OFF_RING + s * C::SBYTES, vb = kb + C::KBYTES;
+        // S^T = K Q^T: twice 16 keys by 8 rows.
+        float acc[2][4] = {};
+#pragma unroll
+        for (int q = 0; q < QI; ++q) {
+          const uint32_t ka = (kb + koff) ^ (64 * q);
+          const uint4 w0 = lds_u4(ka), w1 = lds_u4(ka + 8 * D), w2 = lds_u4(ka + 16 * D), w3 = lds_u4(ka + 24 * D);
+          const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
+          const uint32_t x2[4] = {w2.x, w2.y, w2.z, w2.w}, x3[4] = {w3.x, w3.y, w3.z, w3.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t a0[4] = {widen(x0[j]), widen(x1[j]), widen(x0[j] >> 16), widen(x1[j] >> 16)};
+            mma_f16(acc[0], a0, qb[q][j][0], qb[q][j][1]);
+            const uint32_t a1[4] = {widen(x2[j]), widen(x3[j]), widen(x2[j] >> 16), widen(x3[j] >> 16)};
+            mma_f16(acc[1], a1, qb[q][j][0], qb[q][j][1]);
+          }
+        }
+        // Keys ko, ko + 8 (and 16 on) of rows 2c, 2c + 1.
+        const float vsa = mt->vs[pa], vsb = mt->vs[pb];
+        float ca0 = f0 * mt->ks[pa], ca1 = f1 * mt->ks[pa], cb0 = f0 * mt->ks[pb], cb1 = f1 * mt->ks[pb];
+        const bool edge = key0 + 32 > lim_all || !la || !lb;
+        if (edge) {
+          // A factor that underflowed must not meet the infinities (any sum times 1e-37 is 0 as well).
+          ca0 = fmaxf(ca0, 1e-37f);
+          ca1 = fmaxf(ca1, 1e-37f);
+          cb0 = fmaxf(cb0, 1e-37f);
+          cb1 = fmaxf(cb1, 1e-37f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (key0 + 8 * (e >> 1) + ko >= ((e & 1) ? lim1 : lim0) || !(e < 4 ? la : lb)) acc[e >> 2][e & 3] = -INFINITY;
+        }
+        float mx0 = fmaxf(fmaxf(acc[0][0], acc[0][2]) * ca0, fmaxf(acc[1][0], acc[1][2]) * cb0);
+        float mx1 = fmaxf(fmaxf(acc[0][1], acc[0][3]) * ca1, fmaxf(acc[1][1], acc[1][3]) * cb1);
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
+        }
+        const float vsm = fmaxf(la ? vsa : 0.f, lb ? vsb : 0.f);
+        if (__any_sync(0xffffffffu, mx0 > m0 || mx1 > m1) || vsm > vref) {
+          const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
+          const float vnew = fmaxf(vref, vsm);
+          const float rv = vref > 0.f ? __fdiv_rn(vref, vnew) : 0.f;
+          const float a0 = n0 > m0 ? ex2(m0 - n0) : 1.f, a1 = n1 > m1 ? ex2(m1 - n1) : 1.f;
+          l0 *= a0;
+          l1 *= a1;
+          const float b0 = a0 * rv, b1 = a1 * rv;
+#pragma unroll
+          for (int j = 0; j < MT; ++j) {
+            o[j][0] *= b0;
+            o[j][1] *= b1;
+            o[j][2] *= b0;
+            o[j][3] *= b1;
+          }
+          m0 = n0;
+          m1 = n1;
+          vref = vnew;
+        }
+        const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
+        uint32_t pt[4];  // P^T with row g and the keys of a column pair in a lane
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const float vs = b ? vsb : vsa;
+          const float rr = vs == vref ? kPScale : vref > 0.f ? __fdiv_rn(vs, vref) * kPScale : vs;
+          const float c0 = b ? cb0 : ca0, c1 = b ? cb1 : ca1;
+          const float x0 = ex2(fmaf(acc[b][0], c0, -u0)), x1 = ex2(fmaf(acc[b][1], c1, -u1));
+          const float x2 = ex2(fmaf(acc[b][2], c0, -u0)), x3 = ex2(fmaf(acc[b][3], c1, -u1));
+          l0 += x0 + x2;
+          l1 += x1 + x3;
+          pt[2 * b] = transpose8(pack_f16(x0 * rr, x1 * rr));
+          pt[2 * b + 1] = transpose8(pack_f16(x2 * rr, x3 * rr));
+        }
+        // O^T += V^T P^T: row g of tile t is column 16 cg + 2t (d = 64: 8g + 2t), row g + 8 the one after.
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          uint32_t w[4][D / 32];  // four V rows' piece: keys kv0, kv1, kv0 + 8, kv1 + 8
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t va = vb + ((e & 1) ? voff1 : voff0) + (16 * b + 8 * (e >> 1)) * D;
+            if constexpr (D == 128) {
+              const uint4 v = lds_u4(va);
+              w[e][0] = v.x;
+              w[e][1] = v.y;
+              w[e][2] = v.z;
+              w[e][3] = v.w;
+            } else {
+              const uint2 v = lds_u2(va);
+              w[e][0] = v.x;
+              w[e][1] = v.y;
+            }
+          }
+          if (edge) {  // V rows that no row of the tile sees hold anything, a NaN too
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (key0 + 16 * b + 8 * (e >> 1) + ((e & 1) ? kv1 : kv0) >= lim_any || !(b ? lb : la))
+#pragma unroll
+                for (int y = 0; y < D / 32; ++y) w[e][y] = 0;
+          }
+#pragma unroll
+          for (int y = 0; y < D / 32; ++y) {
+            const uint32_t a01 = __byte_perm(w[0][y], w[1][y], 0x5140), a23 = __byte_perm(w[0][y], w[1][y], 0x7362);
+            const uint32_t b01 = __byte_perm(w[2][y], w[3][y], 0x5140), b23 = __byte_perm(w[2][y], w[3][y], 0x7362);
+            const uint32_t t0[4] = {widen(a01), widen(a01 >> 16), widen(b01), widen(b01 >> 16)};
+            const uint32_t t1[4] = {widen(a23), widen(a23 >> 16), widen(b23), widen(b23 >> 16)};
+            mma_f16(o[2 * y], t0, pt[2 * b], pt[2 * b + 1]);
+            mma_f16(o[2 * y + 1], t1, pt[2 * b], pt[2 * b + 1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::B_EMPTY + s));
+    }
 
-    // The item's end: the eight warps' sums meet in shared memory.
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-    float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
-    if (c == 0) {
-      ml[warp * kRows + g] = make_float2(m0, l0);
-      ml[warp * kRows + g + 8] = make_float2(m1, l1);
+    // The item's end: the warps' sums meet in shared memory.
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, d);
     }
+    float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
     float4* so = reinterpret_cast<float4*>(smem + C::OFF_O);
     const float back = vref * (1.f / kPScale);
-    // Column 2c of tile j is column 16c + j of the row (d = 128; column 2c + 1:
-    // 64 + 16c + j), or 16c + j and 16c + 8 + j (d = 64): a lane holds runs of
-    // 16 columns.  16-byte pieces are exchanged within a run so that the
-    // lanes of a store meet no bank twice.
+    // Place of 16-byte piece q4 of a row: exchanged with its neighbours so that
+    // the eight lanes of a store (four rows, two pieces) meet no bank twice.
     auto at = [&](int w_, int row, int q4) {
-      const int run = q4 >> 2, x = (q4 & 3) ^ (((run >> 1) & 1) | ((row & 1) << 1));
-      return (w_ * kRows + row) * (D / 4) + run * 4 + x;
+      const int c2 = row >> 1;
+      const int x = D == 128 ? c2 | ((q4 >> 4) << 2) : (c2 & 1) | ((c2 >> 1) << 2);
+      return (w_ * kRows + row) * (D / 4) + (q4 ^ x);
     };
+    if (warp >= kHalf) {
+      // Hand over to warp - kHalf, lane by lane, once the last item's sums have been read.
+      if (i > 0 && !mbar_wait_warp(bar(C::B_READ), (i - 1) & 1, wc)) return;
+      float4* to = so + (warp - kHalf) * kRows * (D / 4) + lane;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int row = g + 8 * half;
-      if constexpr (D == 128) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            so[at(warp, row, (c + 4 * e) * 4 + x)] =
-                make_float4(o[4 * x][2 * half + e] * back, o[4 * x + 1][2 * half + e] * back,
-                            o[4 * x + 2][2 * half + e] * back, o[4 * x + 3][2 * half + e] * back);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            so[at(warp, row, c * 4 + 2 * e + x)] =
-                make_float4(o[4 * x][2 * half + e] * back, o[4 * x + 1][2 * half + e] * back,
-                            o[4 * x + 2][2 * half + e] * back, o[4 * x + 3][2 * half + e] * back);
+      for (int j = 0; j < MT; ++j)
+        to[32 * j] = make_float4(o[j][0] * back, o[j][1] * back, o[j][2] * back, o[j][3] * back);
+      if (g == 0) {
+        ml[(warp - kHalf) * kRows + 2 * c] = make_float2(m0, l0);
+        ml[(warp - kHalf) * kRows + 2 * c + 1] = make_float2(m1, l1);
       }
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(C::B_GIVEN));
+        mbar_arrive(bar(C::B_IEMPTY + i % kItems));
+      }
+      continue;
+    }
+    const int slot = im->slot;
+    if (!mbar_wait_warp(bar(C::B_GIVEN), i & 1, wc)) return;
+    if (warp < kWarps - kHalf) {
+      const float2 g0 = ml[warp * kRows + 2 * c], g1 = ml[warp * kRows + 2 * c + 1];
+      const float n0 = fmaxf(m0, g0.x), n1 = fmaxf(m1, g1.x);
+      const float r0 = n0 == -INFINITY ? 0.f : n0, r1 = n1 == -INFINITY ? 0.f : n1;
+      const float a0 = ex2(m0 - r0), a1 = ex2(m1 - r1), b0 = ex2(g0.x - r0), b1 = ex2(g1.x - r1);
+      const float4* from = so + warp * kRows * (D / 4) + lane;
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        const float4 v = from[32 * j];
+        o[j][0] = fmaf(o[j][0] * back, a0, v.x * b0);
+        o[j][1] = fmaf(o[j][1] * back, a1, v.y * b1);
+        o[j][2] = fmaf(o[j][2] * back, a0, v.z * b0);
+        o[j][3] = fmaf(o[j][3] * back, a1, v.w * b1);
+      }
+      l0 = l0 * a0 + g0.y * b0;
+      l1 = l1 * a1 + g1.y * b1;
+      m0 = n0;
+      m1 = n1;
+    } else {
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][e] *= back;
     }
     __syncwarp();
+    ml += kHalf * kRows;
+    if (g == 0) {
+      ml[warp * kRows + 2 * c] = make_float2(m0, l0);
+      ml[warp * kRows + 2 * c + 1] = make_float2(m1, l1);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int x = 0; x < MT / 2; ++x)
+        so[at(warp, 2 * c + e, (D == 128 ? 4 * cg : 2 * g) + x)] =
+            make_float4(o[2 * x][e], o[2 * x][2 + e], o[2 * x + 1][e], o[2 * x + 1][2 + e]);
+    __syncwarp();
     if (lane == 0) mbar_arrive(bar(C::B_WRITTEN));
-    if (!mbar_wait_warp(bar(C::B_WRITTEN), ends & 1, wc)) break;
-    for (int x = threadIdx.x; x < rows * (D / 4); x += 32 * kWarps) {
+    if (!mbar_wait_warp(bar(C::B_WRITTEN), i & 1, wc)) return;
+    for (int x = threadIdx.x; x < rows * (D / 4); x += 32 * kHalf) {
       const int row = x / (D / 4), q4 = x % (D / 4);
       float M = -INFINITY;
-#pragma unroll
-      for (int w_ = 0; w_ < kWarps; ++w_) M = fmaxf(M, ml[w_ * kRows + row].x);
+#pragma unroll 4
+      for (int w_ = 0; w_ < kHalf; ++w_) M = fmaxf(M, ml[w_ * kRows + row].x);
       const float ref = M == -INFINITY ? 0.f : M;
       float L = 0.f;
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w_ = 0; w_ < kWarps; ++w_) {
+#pragma unroll 4
+      for (int w_ = 0; w_ < kHalf; ++w_) {
         const float2 st = ml[w_ * kRows + row];
         const float wgt = ex2(st.x - ref);
         const float4 v = so[at(w_, row, q4)];
@@ -590,9 +673,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(bar(C::B_READ));
-    if (!mbar_wait_warp(bar(C::B_READ), ends & 1, wc)) break;
-    ++ends;
+    if (lane == 0) {
+      mbar_arrive(bar(C::B_READ));
+      mbar_arrive(bar(C::B_IEMPTY + i % kItems));
+    }
+    // The next item's writes come after all of these reads.
+    if (!mbar_wait_warp(bar(C::B_READ), i & 1, wc)) return;
   }
 }
 

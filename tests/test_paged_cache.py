@@ -356,6 +356,15 @@ def test_attention_of_many_requests_some_idle(R):
 
 
 @gpu
+@pytest.mark.parametrize("d,page", [(64, 32), (128, 16), (128, 128)])
+def test_attention_of_many_units_a_worker(d, page):
+    """Several times more 128-key units than the GPU has SMs times ring stages."""
+    rng = np.random.default_rng(d + page)
+    lens = rng.integers(1, 9000, 40)
+    _check_attention(rng, lens, np.ones(40, int), 8, 4, d, page, True)
+
+
+@gpu
 def test_attention_padded_strided_and_with_a_callers_workspace():
     rng = np.random.default_rng(21)
     ws = torch.full((pkg.attn_fwd_paged_workspace_size(20, 8, 2, 128),), 255, dtype=torch.uint8, device="cuda")
