@@ -25,7 +25,7 @@ Functions carry the C names:
   ``attn_fwd_paged_fp8(Q, k_pages, k_scale, v_pages, v_scale, block_table, cu_q, kv_lens, ...)``:
   a paged e4m3 key/value cache -- its block table and slot map from the requests'
   lengths, the quantizing append, and ragged attention over it;
-  ``attn_fwd_paged_workspace_size(T, Hq, Hkv, d)``
+  ``attn_fwd_paged_workspace_size(R, T, Hq, Hkv, d)``
 * ``attn_bwd(Q, K, V, O, dO, LSE, scale, causal) -> (dQ, dK, dV)``
 * ``attn_bwd_workspace_size(B, Hq, Hkv, N, d)``
 * ``attn_last_device_status(stream=None)``, ``attn_status_string(code)``
@@ -117,7 +117,7 @@ def load_library(path: str = LIB_PATH):
         lib.attn_fwd_paged_fp8.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32,
                                            i32, i32, f32, i32, i32, vp, sz, vp]
         lib.attn_fwd_paged_fp8.restype = i32
-        lib.attn_fwd_paged_workspace_size.argtypes = [i32, i32, i32, i32]
+        lib.attn_fwd_paged_workspace_size.argtypes = [i32, i32, i32, i32, i32]
         lib.attn_fwd_paged_workspace_size.restype = sz
         lib.attn_bwd_workspace_size.argtypes = [i32, i32, i32, i32, i32]
         lib.attn_bwd_workspace_size.restype = sz
@@ -506,8 +506,8 @@ def attn_kv_append_fp8(K, V, slots, k_pages, k_scale, v_pages, v_scale, stream=N
     return k_pages, k_scale, v_pages, v_scale
 
 
-def attn_fwd_paged_workspace_size(T: int, Hq: int, Hkv: int, d: int) -> int:
-    return int(load_library().attn_fwd_paged_workspace_size(T, Hq, Hkv, d))
+def attn_fwd_paged_workspace_size(R: int, T: int, Hq: int, Hkv: int, d: int) -> int:
+    return int(load_library().attn_fwd_paged_workspace_size(R, T, Hq, Hkv, d))
 
 
 def attn_fwd_paged_fp8(Q, k_pages, k_scale, v_pages, v_scale, block_table, cu_q, kv_lens, scale=None, causal=False,
@@ -545,7 +545,7 @@ def attn_fwd_paged_fp8(Q, k_pages, k_scale, v_pages, v_scale, block_table, cu_q,
         _check_fast("LSE", LSE, torch.float32, (T, Hq), dev)
     if workspace is None:
         # The size is the current device's; all devices of a process are GB300s.
-        workspace = torch.empty(lib.attn_fwd_paged_workspace_size(T, Hq, Hkv, d), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(lib.attn_fwd_paged_workspace_size(R, T, Hq, Hkv, d), dtype=torch.uint8, device=dev)
     else:
         _check_workspace(workspace, 0, dev)
     _call(lib.attn_fwd_paged_fp8, dev, stream, Q.data_ptr(), q_stride, k_pages.data_ptr(), k_scale.data_ptr(),

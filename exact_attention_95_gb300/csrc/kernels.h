@@ -191,13 +191,17 @@ struct PagedFwdParams {
   int* desc;               // workspace: [workers][8] what the merge has to do
   int* status;
   int R, T, Hq, Hkv, G, num_pages, page_log2, max_pages;
+  int rows_min, rows_max;  // the launch takes the requests with rows_min < n * G <= rows_max
   float scale_log2;
   int causal, out_f32;
   unsigned long long wait_limit_ns;
 };
-size_t paged_fwd_workspace_bytes(int d, int sms);
-// Fills in the workspace pointers of p from `workspace` and launches.
-cudaError_t launch_fwd_paged(int d, const CUtensorMap& tmK, const CUtensorMap& tmV, PagedFwdParams& p, void* workspace,
-                             int sms, cudaStream_t stream);
+// The two kernels, each followed by its merge: eight query rows of a kv head
+// to a tile (paged_fwd.cu), and 256 (paged_wide.cu).
+constexpr int kPagedNarrowRows = 8, kPagedWideRows = 256;
+cudaError_t launch_paged_narrow(int d, const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedFwdParams& p,
+                                int workers, cudaStream_t stream);
+cudaError_t launch_paged_wide(int d, const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedFwdParams& p,
+                              int workers, cudaStream_t stream);
 
 }  // namespace attn

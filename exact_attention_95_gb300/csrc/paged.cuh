@@ -1,0 +1,290 @@
+// paged.cuh -- what the two kernels of attention over a paged cache share
+// (paged_fwd.cu: few query rows of a kv head; paged_wide.cu: many): the
+// division of a ragged batch between the CTAs, and the merge of items that
+// were cut.
+//
+// An item is a tile of ROWS query rows of a request and kv head (rows
+// token-major, the G heads of a token side by side) against the keys of the
+// request, kUnit keys to a unit.  The units of all items, in one line, are cut
+// into equal ranges, one for each CTA (worker), which finds its own from the
+// lengths on the device; nothing is planned on the host.  Equal ranges keep
+// every SM's memory traffic the same whatever the lengths are.
+#pragma once
+
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace attn {
+namespace paged {
+
+constexpr int kUnit = 128;       // keys of a unit
+constexpr int kMaxGroups = 512;  // 32 requests each
+
+// An item, or the part of it that a worker has.
+struct Item {
+  int start, n, len;  // the request's query rows, tokens [start, start + n), and its keys
+  int req;            // the request
+  int tile, h;        // row tile, kv head
+  int k0;             // first unit's number in the item
+  int first, count;   // the units' numbers in the worker's line of units; count < 0: no more items
+  int slot;           // where the result goes: -1 output, else partial slot of this worker
+  int pad[2];
+};
+
+// The request's query rows and keys, clipped to the arrays, and its units
+// (none where its rows are not this launch's: p.rows_min < n * G <= p.rows_max).
+struct Req {
+  int start, n, len;
+  long long units;
+};
+template <int ROWS>
+__device__ __forceinline__ Req load_req(const PagedFwdParams& p, int r) {
+  Req q{0, 0, 0, 0};
+  if (r < p.R) {
+    const int a = min(max(p.cu_q[r], 0), p.T), b = min(max(p.cu_q[r + 1], 0), p.T);
+    q.start = a;
+    q.n = max(b - a, 0);
+    q.len = max(p.kv_lens[r], 0);
+    const long long room = (long long)p.max_pages << p.page_log2;
+    if (q.len > room) {
+      q.len = (int)room;
+      atomicCAS(p.status, kDevOk, kDevBounds);
+    }
+    const int rows = q.n * p.G;
+    if (rows > p.rows_min && rows <= p.rows_max)
+      q.units = (long long)((rows + ROWS - 1) / ROWS) * p.Hkv * max(1, (q.len + kUnit - 1) / kUnit);
+  }
+  return q;
+}
+
+// Units of every 32 requests, by `warps` warps; synchronise before reading.
+template <int ROWS>
+__device__ __forceinline__ void sum_units(const PagedFwdParams& p, long long* sums, int warp, int warps, int lane) {
+  for (int g = warp; g < (p.R + 31) >> 5; g += warps) {
+    long long u = load_req<ROWS>(p, g * 32 + lane).units;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+    if (lane == 0) sums[g] = u;
+  }
+}
+
+// Keys that a query token may see.
+__device__ __forceinline__ int key_limit(const PagedFwdParams& p, int len, int n, int tok) {
+  return p.causal ? max(0, min(len, len - n + tok + 1)) : len;
+}
+
+// Walks this worker's range (a whole warp).  item(Item, seen) announces an
+// item, of whose keys its rows see the first `seen`; unit(k, lane's page id or
+// -1, its K and V scale, place of the unit's first page among the lanes) loads
+// unit k of it.  Both return false to stop.  Writes the worker's merge
+// descriptor.  Returns false if it was stopped.
+template <int ROWS, class ItemFn, class UnitFn>
+__device__ __forceinline__ bool walk_range(const PagedFwdParams& p, const long long* sums, int lane, ItemFn item_fn,
+                                           UnitFn unit_fn) {
+  const int groups = (p.R + 31) >> 5;
+  long long total = 0;
+  for (int g = lane; g < groups; g += 32) total += sums[g];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long begin = min(total, per * blockIdx.x);
+  const long long end = min(total, begin + per);
+  int merge_parts = 0, merge_start = 0, merge_n = 0, merge_tile = 0, merge_h = 0;
+  const int npg = kUnit >> p.page_log2;  // pages of a unit
+  int line = 0;                          // units walked
+  bool ok = true;
+  if (begin < end) {
+    // The group, then the request, that holds unit `begin`.
+    long long before = 0;
+    int g = 0;
+    while (g + 1 < groups && before + sums[g] <= begin) before += sums[g++];
+    Req rq = load_req<ROWS>(p, g * 32 + lane);
+    long long incl = rq.units;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    incl += before;
+    int l = __ffs(__ballot_sync(0xffffffffu, incl > begin)) - 1;
+    long long off = begin - (__shfl_sync(0xffffffffu, incl, l) - __shfl_sync(0xffffffffu, rq.units, l));
+    long long pos = begin;
+    while (pos < end && ok) {
+      Item im;
+      im.req = g * 32 + l;
+      im.start = __shfl_sync(0xffffffffu, rq.start, l);
+      im.n = __shfl_sync(0xffffffffu, rq.n, l);
+      im.len = __shfl_sync(0xffffffffu, rq.len, l);
+      const long long units = __shfl_sync(0xffffffffu, rq.units, l);
+      const int kt = max(1, (im.len + kUnit - 1) / kUnit);
+      const int tiles = (im.n * p.G + ROWS - 1) / ROWS;
+      const int* row = p.block_table + (size_t)im.req * p.max_pages;
+      int item = (int)(off / kt);
+      int k0 = (int)(off - (long long)item * kt);
+      for (; off < units && pos < end && ok; ++item) {
+        im.h = item / tiles;
+        // First and last tiles in turn: under the causal mask a tile's share
+        // of its kt units grows with its place, and a worker's range then
+        // holds early and late ones alike.
+        const int at = item - im.h * tiles;
+        im.tile = (at & 1) ? tiles - 1 - (at >> 1) : at >> 1;
+        const int k1 = (int)min((long long)kt, k0 + (end - pos));
+        im.slot = k0 == 0 && k1 == kt ? -1 : k0 == 0 ? 1 : 0;
+        if (im.slot == 1) {
+          const long long last = pos + kt - 1;  // the item's last unit
+          merge_parts = (int)(last / per - blockIdx.x) + 1;
+          merge_start = im.start;
+          merge_n = im.n;
+          merge_tile = im.tile;
+          merge_h = im.h;
+        }
+        const int seen = key_limit(p, im.len, im.n, (min(im.n * p.G, (im.tile + 1) * ROWS) - 1) / p.G);
+        const int ke = max(k0, min(k1, (seen + kUnit - 1) / kUnit));
+        im.k0 = k0;
+        im.first = line;
+        im.count = ke - k0;
+        ok = item_fn(im, seen);
+        int id = -1;
+        float ks = 1.f, vs = 0.f;
+        for (int k = k0; k < ke && ok; ++k) {
+          // Page ids and scales, 32 pages at a time (lane i: page i of the batch).
+          const int in_batch = ((k - k0) * npg) & 31;
+          if (in_batch == 0) {
+            const int pg = k * npg + lane;
+            id = -1;
+            ks = 1.f;
+            vs = 0.f;
+            if (((long long)pg << p.page_log2) < seen) {
+              id = row[pg];
+              if (id < 0 || id >= p.num_pages) {
+                id = -1;
+                atomicCAS(p.status, kDevOk, kDevBounds);
+              } else {
+                ks = p.k_scale[(size_t)id * p.Hkv + im.h];
+                vs = p.v_scale[(size_t)id * p.Hkv + im.h];
+              }
+            }
+          }
+          ok = unit_fn(im, k, id, ks, vs, in_batch);
+          ++line;
+        }
+        pos += k1 - k0;
+        off += k1 - k0;
+        k0 = 0;
+      }
+      // The next request that has units.
+      if (pos < end && ok) {
+        off = 0;
+        uint32_t more = __ballot_sync(0xffffffffu, rq.units > 0) & ~(0xffffffffu >> (31 - l));
+        while (!more && g + 1 < groups) {
+          ++g;
+          rq = load_req<ROWS>(p, g * 32 + lane);
+          more = __ballot_sync(0xffffffffu, rq.units > 0);
+        }
+        if (!more) break;
+        l = __ffs(more) - 1;
+      }
+    }
+  }
+  if (lane == 0) {
+    int* d = p.desc + blockIdx.x * 8;
+    d[0] = merge_parts;
+    d[1] = merge_start;
+    d[2] = merge_n;
+    d[3] = merge_tile;
+    d[4] = merge_h;
+  }
+  return ok;
+}
+
+// Row `row` of a tile in the output arrays.
+__device__ __forceinline__ size_t output_row(const PagedFwdParams& p, int start, int h, int rho) {
+  const int tok = rho / p.G;
+  return (size_t)(start + tok) * p.Hq + h * p.G + (rho - tok * p.G);
+}
+
+// 1 / l for the output: 0 for a row without keys, NaN stays.
+__device__ __forceinline__ float output_factor(float l) { return l > 0.f ? __fdiv_rn(1.f, l) : l == 0.f ? 0.f : l; }
+// ln of the sum of a row with maximum m (log2 units).
+__device__ __forceinline__ float output_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// Merge of the items cut between workers: worker w's descriptor names the
+// item that begins in its range and goes on in the next parts - 1 workers'.
+// A warp per row, four rows to a CTA.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(128) paged_merge_kernel(const PagedFwdParams p) {
+  griddep_wait();
+  const int w = blockIdx.x;
+  const int* d = p.desc + w * 8;
+  const int parts = d[0];
+  if (parts < 2) return;
+  const int start = d[1], n = d[2], tile = d[3], h = d[4];
+  const int lane = threadIdx.x & 31, row = blockIdx.y * 4 + (threadIdx.x >> 5);
+  if (row >= n * p.G - tile * ROWS) return;
+  auto part = [&](int s) -> size_t { return (size_t)(s == 0 ? 2 * w + 1 : 2 * (w + s)) * ROWS + row; };
+  constexpr int V = D / 32;  // columns of a lane
+  float M = -INFINITY;
+  for (int s = lane; s < parts; s += 32) M = fmaxf(M, p.part_ml[part(s) * 2]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float ref = M == -INFINITY ? 0.f : M;
+  float L = 0.f, acc[V] = {};
+  for (int s0 = 0; s0 < parts; s0 += 32) {
+    float wl = 0.f;
+    if (s0 + lane < parts) {
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + part(s0 + lane) * 2);
+      wl = ex2(ml.x - ref);
+      L += wl * ml.y;
+    }
+    const int cnt = min(32, parts - s0);
+#pragma unroll 4
+    for (int s = 0; s < cnt; ++s) {
+      const float wgt = __shfl_sync(0xffffffffu, wl, s);
+      const float* src = p.part_o + part(s0 + s) * D + lane * V;
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] += wgt * src[v];
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  const size_t orow = output_row(p, start, h, tile * ROWS + row);
+  const float inv = output_factor(L);
+#pragma unroll
+  for (int v = 0; v < V; v += 2) {
+    if (p.out_f32) {
+      float* dst = static_cast<float*>(p.O) + orow * D + lane * V + v;
+      dst[0] = acc[v] * inv;
+      dst[1] = acc[v + 1] * inv;
+    } else {
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.O) + orow * D + lane * V + v) =
+          pack_bf16(acc[v] * inv, acc[v + 1] * inv);
+    }
+  }
+  if (lane == 0) p.LSE[orow] = output_lse(M, L);
+}
+
+// Launches `kern` and the merge behind it (its launch overlaps the kernel's end).
+template <int D, int ROWS, class Kernel>
+cudaError_t launch_with_merge(Kernel kern, int threads, int smem, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                              const PagedFwdParams& p, int workers, cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<workers, threads, smem, stream>>>(tmK, tmV, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)workers, ROWS / 4);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, ROWS>, p);
+}
+
+}  // namespace paged
+}  // namespace attn

@@ -38,6 +38,21 @@ attn_status check_cache(const void* kp, const float* ks, const void* vp, const f
 // Tokens of `heads` rows of d elements, `stride` elements apart.
 bool token_stride_ok(long long stride, long long heads, int d) { return stride >= heads * d && stride % 8 == 0; }
 
+// Which kernels a call runs, and its workspace: partial sums (O, then maxima
+// and sums, then merge descriptors) of one worker per SM, two slots each.
+// A request goes to the narrow kernel with up to kNarrowMost query rows of a
+// kv head, else to the wide one; without a wide one (T <= R and small groups:
+// a decoding step, where the wide launch would find nothing to do) to the
+// narrow one in any case.
+constexpr int kNarrowMost = 8;
+bool runs_wide(int R, int T, int G) { return T > R || G > kNarrowMost; }
+size_t part_o_bytes(int rows, int d, int sms) { return (size_t)sms * 2 * rows * d * 4; }
+size_t part_ml_bytes(int rows, int sms) { return (size_t)sms * 2 * rows * 8; }
+size_t workspace_bytes_for(bool wide, int d, int sms) {
+  const int rows = wide ? attn::kPagedWideRows : attn::kPagedNarrowRows;
+  return part_o_bytes(rows, d, sms) + part_ml_bytes(rows, sms) + ((size_t)sms * 32 + 255) / 256 * 256;
+}
+
 int sms_or_default() {
   const int n = attn::device_sms();
   return n > 0 ? n : 152;
@@ -109,9 +124,9 @@ attn_status attn_kv_append_fp8(const void* K, long long k_stride, const void* V,
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-size_t attn_fwd_paged_workspace_size(int T, int Hq, int Hkv, int d) {
-  if (T < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (d != 64 && d != 128)) return 0;
-  return attn::paged_fwd_workspace_bytes(d, sms_or_default());
+size_t attn_fwd_paged_workspace_size(int R, int T, int Hq, int Hkv, int d) {
+  if (R < 1 || T < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (d != 64 && d != 128)) return 0;
+  return workspace_bytes_for(runs_wide(R, T, Hq / Hkv), d, sms_or_default());
 }
 
 attn_status attn_fwd_paged_fp8(const void* Q, long long q_stride, const void* k_pages, const float* k_scale,
@@ -135,7 +150,9 @@ attn_status attn_fwd_paged_fp8(const void* Q, long long q_stride, const void* k_
   const int sms = attn::device_sms();
   int* status = attn::device_status_word();
   if (sms < 1 || !status) return ATTN_ERR_CUDA;
-  if (workspace_bytes < attn::paged_fwd_workspace_bytes(d, sms)) return ATTN_ERR_INVALID_ARG;
+  const int G = Hq / Hkv;
+  const bool wide = runs_wide(R, T, G);
+  if (workspace_bytes < workspace_bytes_for(wide, d, sms)) return ATTN_ERR_INVALID_ARG;
   CUtensorMap tk, tv;
   const long long planes = (long long)num_pages * Hkv;
   if (!attn::make_page_map(&tk, k_pages, planes, page_size, d) ||
@@ -156,7 +173,7 @@ attn_status attn_fwd_paged_fp8(const void* Q, long long q_stride, const void* k_
   p.T = T;
   p.Hq = Hq;
   p.Hkv = Hkv;
-  p.G = Hq / Hkv;
+  p.G = G;
   p.num_pages = num_pages;
   p.page_log2 = page_log2(page_size);
   p.max_pages = max_pages;
@@ -164,7 +181,27 @@ attn_status attn_fwd_paged_fp8(const void* Q, long long q_stride, const void* k_
   p.causal = causal;
   p.out_f32 = out_dtype == ATTN_F32;
   p.wait_limit_ns = attn::device_wait_limit();
-  cudaError_t e = attn::launch_fwd_paged(d, tk, tv, p, workspace, sms, static_cast<cudaStream_t>(stream));
+  const cudaStream_t st_ = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  // The two kernels run one after the other and use the workspace in turn.
+  auto place = [&](int rows) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.part_o = reinterpret_cast<float*>(ws);
+    p.part_ml = reinterpret_cast<float*>(ws + part_o_bytes(rows, d, sms));
+    p.desc = reinterpret_cast<int*>(ws + part_o_bytes(rows, d, sms) + part_ml_bytes(rows, sms));
+  };
+  if (wide) {
+    place(attn::kPagedWideRows);
+    p.rows_min = kNarrowMost;
+    p.rows_max = 0x7fffffff;
+    e = attn::launch_paged_wide(d, tk, tv, p, sms, st_);
+  }
+  if (e == cudaSuccess && (!wide || G <= kNarrowMost)) {
+    place(attn::kPagedNarrowRows);
+    p.rows_min = 0;
+    p.rows_max = wide ? kNarrowMost : 0x7fffffff;
+    e = attn::launch_paged_narrow(d, tk, tv, p, sms, st_);
+  }
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

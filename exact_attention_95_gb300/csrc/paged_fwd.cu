@@ -12,49 +12,30 @@
 // f16, relative to the largest V scale seen, times 2^14: 2^-11 relative for
 // every weight down to 2^-28 of the row's largest, which a long tail behind
 // one dominant key needs (an 8-bit weight, even as a sum of two, would lose
-// it).  mma.sync m16n8k16 rather than tcgen05: a 16-row tile of queries
-// against codes that have to be widened in registers anyway leaves the tensor
+// it).  mma.sync m16n8k16 rather than tcgen05: a tile of eight query
+// rows against codes that have to be widened in registers anyway leaves the tensor
 // pipe mostly idle at HBM speed, and no accumulator leaves the registers.
-//
-// Work: a tile of 16 query rows (token-major, the G heads of a kv head of one
-// token side by side) against the keys of its request, 128 keys to a unit.
-// The units of all (request, kv head, row tile) items, in one line, are cut
-// into equal ranges, one per CTA; an item cut between CTAs leaves partial
-// (m, l, O) in the workspace for the merge kernel.  Every CTA finds its range
-// from the lengths on the device; nothing is planned on the host.
 //
 // A CTA: a producer warp that walks its range and loads whole (page, head)
 // boxes by TMA into a ring of units, and sets of four consumer warps that take
 // the units in turn, 32 keys a warp.  Every warp keeps its own running
 // maximum, sum and accumulators of the item; they meet in shared memory at the
 // item's end.
-#include <algorithm>
-
-#include "kernels.h"
-#include "ptx.cuh"
+#include "paged.cuh"
 
 namespace attn {
 namespace {
 
+using namespace paged;
+
 constexpr int kRows = 8;           // query rows of a tile
-constexpr int kUnit = 128;         // keys of a unit
 constexpr int kSets = 3;           // sets of four consumer warps
 constexpr int kWarps = 4 * kSets;
 constexpr int kHalf = 8;           // warps whose sums the exchange buffer holds
 constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kMaxGroups = 512;    // 32 requests each
 constexpr int kItems = 4;          // items announced ahead
 constexpr float kPScale = 16384.f;
 
-// An item of the CTA's range, announced by the producer.
-struct Item {
-  int start, n, len;  // the request's query rows, tokens [start, start + n), and its keys
-  int tile, h;        // row tile, kv head
-  int k0;             // first unit's number in the item
-  int first, count;   // the units in the CTA's line of units; count < 0: no more items
-  int slot;           // where the result goes: -1 output, else partial slot of this worker
-  int pad[3];
-};
 // What a unit's stage holds besides the codes.
 struct UnitMeta {
   float ks[8], vs[8];  // scales of its pages
@@ -113,29 +94,6 @@ __device__ __forceinline__ uint2 lds_u2(uint32_t addr) {
   return v;
 }
 
-// The request's query rows and keys, clipped to the arrays.
-struct Req {
-  int start, n, len;
-  long long units;
-};
-__device__ __forceinline__ Req load_req(const PagedFwdParams& p, int r) {
-  Req q{0, 0, 0, 0};
-  if (r < p.R) {
-    const int a = min(max(p.cu_q[r], 0), p.T), b = min(max(p.cu_q[r + 1], 0), p.T);
-    q.start = a;
-    q.n = max(b - a, 0);
-    q.len = max(p.kv_lens[r], 0);
-    const long long room = (long long)p.max_pages << p.page_log2;
-    if (q.len > room) {
-      q.len = (int)room;
-      atomicCAS(p.status, kDevOk, kDevBounds);
-    }
-    const long long tiles = ((long long)q.n * p.G + kRows - 1) / kRows;
-    q.units = tiles * p.Hkv * max(1, (q.len + kUnit - 1) / kUnit);
-  }
-  return q;
-}
-
 // Key index within eight that column n of a product stands for.  The order is
 // free; these make the 16-byte (8-byte) shared-memory reads of a swizzled
 // page free of bank conflicts.
@@ -178,14 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  // Units of every 32 requests.
-  const int groups = (p.R + 31) >> 5;
-  for (int g = warp; g < groups; g += kWarps + 1) {
-    long long u = load_req(p, g * 32 + lane).units;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-    if (lane == 0) sums[g] = u;
-  }
+  sum_units<kRows>(p, sums, warp, kWarps + 1, lane);
   __syncthreads();
   const WaitCtx wc{abort_flag, p.status, p.wait_limit_ns};
 
@@ -195,166 +146,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
     }
-    long long total = 0;
-    for (int g = lane; g < groups; g += 32) total += sums[g];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    const long long per = (total + gridDim.x - 1) / gridDim.x;
-    const long long begin = min(total, per * blockIdx.x);
-    const long long end = min(total, begin + per);
-    int merge_parts = 0, merge_start = 0, merge_n = 0, merge_tile = 0, merge_h = 0;
     const int npg = kUnit >> p.page_log2;  // pages of a unit
-    int it = 0;                            // units loaded
-    int items_out = 0;                     // items announced
-    bool ok = true;
-    auto item_place = [&]() -> Item* {
+    const uint32_t page_bytes = (uint32_t)D << p.page_log2;
+    int it = 0;         // units loaded
+    int items_out = 0;  // items announced
+    auto announce = [&](const Item& im) -> bool {
       const int i = items_out % kItems;
-      if (items_out >= kItems) ok = mbar_wait_warp(bar(C::B_IEMPTY + i), ((items_out / kItems) & 1) ^ 1, wc);
-      return items + i;
-    };
-    auto announce = [&]() {  // by lane 0, which wrote the item
-      mbar_arrive(bar(C::B_IFULL + items_out % kItems));
-    };
-    if (begin < end) {
-      // The group, then the request, that holds unit `begin`.
-      long long before = 0;
-      int g = 0;
-      while (g + 1 < groups && before + sums[g] <= begin) before += sums[g++];
-      Req rq = load_req(p, g * 32 + lane);
-      long long incl = rq.units;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
+      if (items_out >= kItems && !mbar_wait_warp(bar(C::B_IEMPTY + i), ((items_out / kItems) & 1) ^ 1, wc)) return false;
+      if (lane == 0) {
+        items[i] = im;
+        mbar_arrive(bar(C::B_IFULL + i));
       }
-      incl += before;
-      int l = __ffs(__ballot_sync(0xffffffffu, incl > begin)) - 1;
-      long long off = begin - (__shfl_sync(0xffffffffu, incl, l) - __shfl_sync(0xffffffffu, rq.units, l));
-      long long pos = begin;
-      while (pos < end && ok) {
-        const int r = g * 32 + l;
-        const int start = __shfl_sync(0xffffffffu, rq.start, l), n = __shfl_sync(0xffffffffu, rq.n, l);
-        const int len = __shfl_sync(0xffffffffu, rq.len, l);
-        const long long units = __shfl_sync(0xffffffffu, rq.units, l);
-        const int kt = max(1, (len + kUnit - 1) / kUnit);
-        const int tiles = (int)(((long long)n * p.G + kRows - 1) / kRows);
-        const int* row = p.block_table + (size_t)r * p.max_pages;
-        long long item = off / kt;
-        int k0 = (int)(off - item * kt);
-        for (; off < units && pos < end && ok; ++item) {
-          const int h = (int)(item / tiles), tile = (int)(item - (long long)h * tiles);
-          const int k1 = (int)min((long long)kt, k0 + (end - pos));
-          const int slot = k0 == 0 && k1 == kt ? -1 : k0 == 0 ? 1 : 0;
-          if (slot == 1) {
-            const long long last = pos + kt - 1;  // the item's last unit
-            merge_parts = (int)(last / per - blockIdx.x) + 1;
-            merge_start = start;
-            merge_n = n;
-            merge_tile = tile;
-            merge_h = h;
+      __syncwarp();
+      ++items_out;
+      return true;
+    };
+    bool ok = walk_range<kRows>(
+        p, sums, lane, [&](const Item& im, int) { return announce(im); },
+        [&](const Item& im, int, int id, float ks, float vs, int in_batch) -> bool {
+          const int s = it % C::STAGES;
+          if (it >= C::STAGES && !mbar_wait_warp(bar(C::B_EMPTY + s), ((it / C::STAGES) & 1) ^ 1, wc)) return false;
+          const int my = __shfl_sync(0xffffffffu, id, in_batch + (lane & 7));
+          const bool load = lane < npg && my >= 0;
+          const uint32_t mask = __ballot_sync(0xffffffffu, load);
+          // The copies are issued first: the barrier's phase cannot end before
+          // the arrival below, which waits for the scales.
+          if (load) {
+            const uint32_t dst = sb + C::OFF_RING + s * C::SBYTES + lane * page_bytes;
+            const int plane = my * p.Hkv + im.h;
+            tma_load_3d(dst, &tmK, bar(C::B_FULL + s), 0, 0, plane);
+            tma_load_3d(dst + C::KBYTES, &tmV, bar(C::B_FULL + s), 0, 0, plane);
           }
-          // Keys that some row of the tile may see.
-          int seen = len;
-          if (p.causal) {
-            const int last_tok = (min(n * (long long)p.G, (long long)(tile + 1) * kRows) - 1) / p.G;
-            seen = max(0, min(len, len - n + last_tok + 1));
+          UnitMeta* m = metas + s;
+          const float mk = __shfl_sync(0xffffffffu, ks, in_batch + (lane & 7));
+          const float mv = __shfl_sync(0xffffffffu, vs, in_batch + (lane & 7));
+          if (lane < 8) {
+            m->ks[lane] = mk;
+            m->vs[lane] = mv;
           }
-          const int ke = max(k0, min(k1, (seen + kUnit - 1) / kUnit));
-          Item* im = item_place();
-          if (!ok) break;
-          if (lane == 0) {
-            im->start = start;
-            im->n = n;
-            im->len = len;
-            im->tile = tile;
-            im->h = h;
-            im->k0 = k0;
-            im->first = it;
-            im->count = ke - k0;
-            im->slot = slot;
-            announce();
-          }
+          if (lane == 0) m->pages = (int)mask;
           __syncwarp();
-          ++items_out;
-          int id = -1;
-          float ks = 0.f, vs = 0.f;
-          for (int k = k0; k < ke; ++k) {
-            // Page ids and scales, 32 pages at a time (lane i: page i of the batch).
-            const int in_batch = ((k - k0) * npg) & 31;
-            if (in_batch == 0) {
-              const int pg = k * npg + lane;
-              id = -1;
-              ks = 1.f;
-              vs = 0.f;
-              if (((long long)pg << p.page_log2) < seen) {
-                id = row[pg];
-                if (id < 0 || id >= p.num_pages) {
-                  id = -1;
-                  atomicCAS(p.status, kDevOk, kDevBounds);
-                } else {
-                  ks = p.k_scale[(size_t)id * p.Hkv + h];
-                  vs = p.v_scale[(size_t)id * p.Hkv + h];
-                }
-              }
-            }
-            const int s = it % C::STAGES;
-            if (it >= C::STAGES) ok = mbar_wait_warp(bar(C::B_EMPTY + s), ((it / C::STAGES) & 1) ^ 1, wc);
-            if (!ok) break;
-            UnitMeta* m = metas + s;
-            const int my = __shfl_sync(0xffffffffu, id, in_batch + (lane & 7));
-            const float mk = __shfl_sync(0xffffffffu, ks, in_batch + (lane & 7));
-            const float mv = __shfl_sync(0xffffffffu, vs, in_batch + (lane & 7));
-            const bool load = lane < npg && my >= 0;
-            const uint32_t mask = __ballot_sync(0xffffffffu, load);
-            if (lane < 8) {
-              m->ks[lane] = mk;
-              m->vs[lane] = mv;
-            }
-            if (lane == 0) m->pages = (int)mask;
-            __syncwarp();
-            const uint32_t page_bytes = (uint32_t)D << p.page_log2;
-            if (lane == 0) mbar_arrive_expect_tx(bar(C::B_FULL + s), 2 * page_bytes * __popc(mask));
-            __syncwarp();
-            if (load) {
-              const uint32_t dst = sb + C::OFF_RING + s * C::SBYTES + lane * page_bytes;
-              const long long plane = (long long)my * p.Hkv + h;
-              tma_load_3d(dst, &tmK, bar(C::B_FULL + s), 0, 0, (int)plane);
-              tma_load_3d(dst + C::KBYTES, &tmV, bar(C::B_FULL + s), 0, 0, (int)plane);
-            }
-            ++it;
-          }
-          pos += k1 - k0;
-          off += k1 - k0;
-          k0 = 0;
-        }
-        // The next request that has units.
-        if (pos < end && ok) {
-          off = 0;
-          uint32_t more = __ballot_sync(0xffffffffu, rq.units > 0) & ~(0xffffffffu >> (31 - l));
-          while (!more && g + 1 < groups) {
-            ++g;
-            rq = load_req(p, g * 32 + lane);
-            more = __ballot_sync(0xffffffffu, rq.units > 0);
-          }
-          if (!more) break;
-          l = __ffs(more) - 1;
-        }
-      }
-    }
-    if (lane == 0) {
-      int* d = p.desc + blockIdx.x * 8;
-      d[0] = merge_parts;
-      d[1] = merge_start;
-      d[2] = merge_n;
-      d[3] = merge_tile;
-      d[4] = merge_h;
-    }
+          if (lane == 0) mbar_arrive_expect_tx(bar(C::B_FULL + s), 2 * page_bytes * __popc(mask));
+          ++it;
+          return true;
+        });
     if (ok) {
-      Item* im = item_place();
-      if (ok && lane == 0) {
-        im->count = -1;
-        announce();
-      }
+      Item im{};
+      im.count = -1;
+      ok = announce(im);
     }
     // Copies in flight land before the CTA leaves (the consumers have waited
     // for all of them unless a wait gave up).
@@ -390,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int count = im->count;
     if (count < 0) return;
     const int tile = im->tile, h = im->h, len = im->len, n = im->n, start = im->start;
-    const int rows = (int)min((long long)kRows, (long long)n * p.G - (long long)tile * kRows);
+    const int rows = min(kRows, n * p.G - tile * kRows);
     {
       // Queries (row g), as f16 after a power of two of the row; limits of the rows' keys.
       const int rho = tile * kRows + min(g, rows - 1);
@@ -426,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           qb[q][j][0] = pack_f16(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up);
           qb[q][j][1] = pack_f16(__uint_as_float(y << 16) * up, __uint_as_float(y & 0xffff0000u) * up);
         }
-      const int lim = p.causal ? max(0, min(len, len - n + tok + 1)) : len;
+      const int lim = key_limit(p, len, n, tok);
       f0 = __shfl_sync(0xffffffffu, f, 8 * c);
       f1 = __shfl_sync(0xffffffffu, f, 8 * c + 4);
       lim0 = __shfl_sync(0xffffffffu, lim, 8 * c);
@@ -660,16 +499,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<float4*>(p.part_o + base * D + q4 * 4) = sum;
         if (q4 == 0) *reinterpret_cast<float2*>(p.part_ml + base * 2) = make_float2(M, L);
       } else {
-        const int rho = tile * kRows + row, tok = rho / p.G;
-        const size_t orow = (size_t)(start + tok) * p.Hq + h * p.G + (rho - tok * p.G);
-        const float inv = L > 0.f ? __fdiv_rn(1.f, L) : L == 0.f ? 0.f : L;  // NaN stays
+        const size_t orow = output_row(p, start, h, tile * kRows + row);
+        const float inv = output_factor(L);
         if (p.out_f32)
           *reinterpret_cast<float4*>(static_cast<float*>(p.O) + orow * D + q4 * 4) =
               make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
         else
           *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) + orow * D + q4 * 4) =
               make_uint2(pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
-        if (q4 == 0) p.LSE[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+        if (q4 == 0) p.LSE[orow] = output_lse(M, L);
       }
     }
     __syncwarp();
@@ -682,98 +520,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Merge of the items cut between workers: worker w's descriptor names the
-// item that begins in its range and goes on in the next parts - 1 workers'.
-// A warp per row, four rows to a CTA.
-template <int D>
-__global__ void __launch_bounds__(128) paged_merge_kernel(const PagedFwdParams p) {
-  griddep_wait();
-  const int w = blockIdx.x;
-  const int* d = p.desc + w * 8;
-  const int parts = d[0];
-  if (parts < 2) return;
-  const int start = d[1], n = d[2], tile = d[3], h = d[4];
-  const int lane = threadIdx.x & 31, row = blockIdx.y * 4 + (threadIdx.x >> 5);
-  if (row >= (long long)n * p.G - (long long)tile * kRows) return;
-  auto part = [&](int s) -> size_t { return (size_t)(s == 0 ? 2 * w + 1 : 2 * (w + s)) * kRows + row; };
-  constexpr int V = D / 32;  // columns of a lane
-  float M = -INFINITY;
-  for (int s = lane; s < parts; s += 32) M = fmaxf(M, p.part_ml[part(s) * 2]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float ref = M == -INFINITY ? 0.f : M;
-  float L = 0.f, acc[V] = {};
-  for (int s0 = 0; s0 < parts; s0 += 32) {
-    float wl = 0.f;
-    if (s0 + lane < parts) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + part(s0 + lane) * 2);
-      wl = ex2(ml.x - ref);
-      L += wl * ml.y;
-    }
-    const int cnt = min(32, parts - s0);
-#pragma unroll 4
-    for (int s = 0; s < cnt; ++s) {
-      const float wgt = __shfl_sync(0xffffffffu, wl, s);
-      const float* src = p.part_o + part(s0 + s) * D + lane * V;
-#pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] += wgt * src[v];
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  const int rho = tile * kRows + row, tok = rho / p.G;
-  const size_t orow = (size_t)(start + tok) * p.Hq + h * p.G + (rho - tok * p.G);
-  const float inv = L > 0.f ? __fdiv_rn(1.f, L) : L == 0.f ? 0.f : L;
-#pragma unroll
-  for (int v = 0; v < V; v += 2) {
-    if (p.out_f32) {
-      float* dst = static_cast<float*>(p.O) + orow * D + lane * V + v;
-      dst[0] = acc[v] * inv;
-      dst[1] = acc[v + 1] * inv;
-    } else {
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.O) + orow * D + lane * V + v) =
-          pack_bf16(acc[v] * inv, acc[v + 1] * inv);
-    }
-  }
-  if (lane == 0) p.LSE[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-}
-
-template <int D>
-cudaError_t launch_paged(const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedFwdParams& p, int workers,
-                         cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(fwd_paged_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PC<D>::SMEM);
-  if (e != cudaSuccess) return e;
-  fwd_paged_kernel<D><<<workers, kThreads, PC<D>::SMEM, stream>>>(tmK, tmV, p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)workers, kRows / 4);
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D>, p);
-}
-
-size_t part_o_bytes(int d, int sms) { return (size_t)sms * 2 * kRows * d * 4; }
-size_t part_ml_bytes(int sms) { return ((size_t)sms * 2 * kRows * 8 + 255) / 256 * 256; }
-
 }  // namespace
 
-size_t paged_fwd_workspace_bytes(int d, int sms) {
-  return part_o_bytes(d, sms) + part_ml_bytes(sms) + ((size_t)sms * 32 + 255) / 256 * 256;
-}
-
-cudaError_t launch_fwd_paged(int d, const CUtensorMap& tmK, const CUtensorMap& tmV, PagedFwdParams& p, void* workspace,
-                             int sms, cudaStream_t stream) {
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.part_o = reinterpret_cast<float*>(ws);
-  p.part_ml = reinterpret_cast<float*>(ws + part_o_bytes(d, sms));
-  p.desc = reinterpret_cast<int*>(ws + part_o_bytes(d, sms) + part_ml_bytes(sms));
-  return d == 128 ? launch_paged<128>(tmK, tmV, p, sms, stream) : launch_paged<64>(tmK, tmV, p, sms, stream);
+cudaError_t launch_paged_narrow(int d, const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedFwdParams& p,
+                                int workers, cudaStream_t stream) {
+  return d == 128 ? launch_with_merge<128, kRows>(fwd_paged_kernel<128>, kThreads, PC<128>::SMEM, tmK, tmV, p, workers,
+                                                  stream)
+                  : launch_with_merge<64, kRows>(fwd_paged_kernel<64>, kThreads, PC<64>::SMEM, tmK, tmV, p, workers,
+                                                 stream);
 }
 
 }  // namespace attn

@@ -344,7 +344,7 @@ attn_status attn_kv_append_fp8(const void* K, long long k_stride, const void* V,
  *       (>= Hq * d, a multiple of 8);  Hq % Hkv == 0
  *   block_table [R, max_pages], cu_q [R+1] (non-decreasing), kv_lens [R]
  *   O   [T, Hq, d] out_dtype (bf16 or fp32), LSE [T, Hq] fp32
- *   workspace: attn_fwd_paged_workspace_size(T, Hq, Hkv, d) bytes, 256-byte
+ *   workspace: attn_fwd_paged_workspace_size(R, T, Hq, Hkv, d) bytes, 256-byte
  *       aligned, owned by the caller, not shared with a concurrent call.
  * Lengths past the table and page ids outside [0, num_pages) in it are
  * reported as ATTN_ERR_DEVICE by attn_last_device_status; such keys take no
@@ -358,7 +358,7 @@ attn_status attn_fwd_paged_fp8(const void* Q, long long q_stride, const void* k_
                                attn_dtype out_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of workspace attn_fwd_paged_fp8 needs on the current device; 0 on bad sizes. */
-size_t attn_fwd_paged_workspace_size(int T, int Hq, int Hkv, int d);
+size_t attn_fwd_paged_workspace_size(int R, int T, int Hq, int Hkv, int d);
 
 /* Static string naming a status code. */
 const char* attn_status_string(attn_status s);

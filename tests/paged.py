@@ -90,12 +90,13 @@ def dequantize(codes, scales, row, length):
 
 def attention(Q, kc, ks, vc, vs, table, cu, lens, scale, causal):
     """O, LSE, and the sums that bound the kernel's error: A = sum_j p_j |v_j| (per
-    column) and B = max_j scale * sum_c |q_c k_jc| (per row).  Rows of no request: NaN."""
+    column); B = max_j scale * sum_c |q_c k_jc| and B[1] the same with max |q| for
+    every q_c (per row).  Rows of no request: NaN."""
     T, Hq, d = Q.shape
     Hkv = kc.shape[1]
     G = Hq // Hkv
     O, A = np.full((T, Hq, d), np.nan), np.full((T, Hq, d), np.nan)
-    LSE, B = np.full((T, Hq), np.nan), np.full((T, Hq), np.nan)
+    LSE, B = np.full((T, Hq), np.nan), np.full((2, T, Hq), np.nan)
     for r in range(len(lens)):
         a, b, L = int(cu[r]), int(cu[r + 1]), int(lens[r])
         if b == a:
@@ -107,7 +108,7 @@ def attention(Q, kc, ks, vc, vs, table, cu, lens, scale, causal):
                 q = Q[i, h * G:(h + 1) * G]
                 out = slice(h * G, (h + 1) * G)
                 if n == 0:
-                    O[i, out], A[i, out], B[i, out], LSE[i, out] = 0.0, 0.0, 0.0, -np.inf
+                    O[i, out], A[i, out], B[:, i, out], LSE[i, out] = 0.0, 0.0, 0.0, -np.inf
                     continue
                 x = scale * (q @ k[h, :n].T)
                 m = x.max(1, keepdims=True)
@@ -116,21 +117,24 @@ def attention(Q, kc, ks, vc, vs, table, cu, lens, scale, causal):
                 O[i, out] = e @ v[h, :n] / z
                 A[i, out] = e @ np.abs(v[h, :n]) / z
                 LSE[i, out] = (m + np.log(z))[:, 0]
-                B[i, out] = scale * (np.abs(q) @ np.abs(k[h, :n]).T).max(1)
+                B[0, i, out] = scale * (np.abs(q) @ np.abs(k[h, :n]).T).max(1)
+                B[1, i, out] = scale * np.abs(q).max(1) * np.abs(k[h, :n]).sum(1).max()
     return O, LSE, A, B
 
 
 def bounds(O, LSE, A, B, d, bf16_out):
-    """How far the kernel's O and LSE may be off.
+    """How far the kernels' O and LSE may be off.
 
     The products q k are exact in f16 operands; their fp32 sum over d terms is
     off by at most d * 2^-23 of the sum of magnitudes, the scaled logit in log2
     units by a few more half steps (2^-24 each) of its own size, together
-    e <= (d + 8) * 2^-23 * B.  A weight is then off by 2 e relative (its own
+    (d + 8) * 2^-23 * B[0].  Where q is the sum of two e4m3 numbers, an element
+    is off by at most half of e4m3's smallest step, 2^-10, with the row's largest
+    scaled above 224: 2^-10 / 224 * B[1].  e is the sum of the two.  A weight is then off by 2 e relative (its own
     logit and the maximum's), by the exponential's 2^-21, and by f16's half
     step 2^-11; the weights' sum by the first two.  fp32 sums of positive
     terms over lanes and warps add less than 2^-16.  bf16 output: 2^-8."""
-    e = (d + 8) * 2.0 ** -23 * B
+    e = (d + 8) * 2.0 ** -23 * B[0] + 2.0 ** -10 / 224 * B[1]
     w = (2.0 ** -11 + 4 * e + 2.0 ** -20 + 2.0 ** -16)[..., None]
     tol_o = w * A + (2.0 ** -8 * (np.abs(O) + w * A) if bf16_out else 2.0 ** -23 * np.abs(O)) + 1e-30
     fin = np.where(np.isfinite(LSE), np.abs(LSE), 0.0)

@@ -66,7 +66,7 @@ def test_plain_attention_equals_the_oracle_on_one_page():
     v = paged.dequantize(codes[::-1], scales, [1, 0], 19)[None]
     Or, Lr = oracle.fwd(np.ascontiguousarray(Q.transpose(1, 0, 2)[None]), k, v, 0.2, True)
     assert np.abs(O - Or[0].transpose(1, 0, 2)).max() < 1e-12 and np.abs(L - Lr[0].T).max() < 1e-12
-    assert (A >= np.abs(O) - 1e-12).all() and (B > 0).all()
+    assert (A >= np.abs(O) - 1e-12).all() and (B[0] > 0).all()
 
 
 # ------------------------------------------------------------------ tables
@@ -288,8 +288,10 @@ def _cache(rng, lens, page, Hkv, d, spread=2, width_extra=1):
 
 
 def _check_attention(rng, lens, news, Hq, Hkv, d, page, causal, out=torch.bfloat16, q_mul=1.0, pad=0, packed=0,
-                     spread=2, **kw):
+                     spread=2, uneven=False, **kw):
     kc, ks, vc, vs, table = _cache(rng, lens, page, Hkv, d, spread)
+    if uneven:
+        ks, vs = (s * rng.uniform(1, 2, s.shape).astype(np.float32) for s in (ks, vs))
     cu = np.concatenate([[0], np.cumsum(news)]).astype(I32)
     T = int(cu[-1]) + pad
     q = paged.bf16_bits((q_mul * rng.standard_normal((T, Hq, d))).astype(np.float32))
@@ -334,6 +336,14 @@ ATTENTION = [
     ([90, 513], [2, 3], 40, 1, 64, 16, True),         # 40 heads a kv head: three row tiles a token
     ([4000], [1], 2, 2, 128, 128, True),
     ([9000], [3], 12, 4, 64, 16, False),
+    # More than eight query rows of a kv head.
+    ([600], [300], 4, 2, 128, 64, True),
+    ([600, 0, 130], [300, 0, 130], 8, 2, 64, 16, True),
+    ([1500, 20, 1], [7, 20, 1], 8, 1, 128, 32, True),   # wide and narrow requests in one call
+    ([6000], [33], 8, 2, 128, 128, False),
+    ([2100, 300], [1, 1], 32, 2, 128, 64, True),        # 16 heads a kv head, one token
+    ([128, 129, 127], [128, 129, 127], 2, 2, 64, 128, True),
+    ([200], [257], 1, 1, 128, 16, True),
 ]
 
 
@@ -367,15 +377,23 @@ def test_attention_of_many_units_a_worker(d, page):
 @gpu
 def test_attention_padded_strided_and_with_a_callers_workspace():
     rng = np.random.default_rng(21)
-    ws = torch.full((pkg.attn_fwd_paged_workspace_size(20, 8, 2, 128),), 255, dtype=torch.uint8, device="cuda")
+    ws = torch.full((pkg.attn_fwd_paged_workspace_size(2, 8, 8, 2, 128),), 255, dtype=torch.uint8, device="cuda")
     _check_attention(rng, [500, 77], [2, 1], 8, 2, 128, 64, True, pad=5, packed=4, workspace=ws)
 
 
 @gpu
 def test_attention_large_logits_and_uneven_page_scales():
     rng = np.random.default_rng(22)
-    _check_attention(rng, [2000, 300], [1, 4], 8, 2, 128, 16, True, torch.float32, q_mul=8.0)
-    _check_attention(rng, [2000, 300], [1, 4], 8, 2, 128, 16, True, torch.float32, q_mul=0.05, spread=8)
+    for news in ([1, 1], [1, 4], [40, 9]):
+        _check_attention(rng, [2000, 300], news, 8, 2, 128, 16, True, torch.float32, q_mul=8.0)
+        _check_attention(rng, [2000, 300], news, 8, 2, 128, 16, True, torch.float32, q_mul=0.05, spread=8)
+
+
+@gpu
+def test_attention_scales_that_are_no_powers_of_two():
+    rng = np.random.default_rng(25)
+    for news in ([1, 1], [40, 9]):
+        _check_attention(rng, [700, 300], news, 8, 2, 64, 32, True, torch.float32, uneven=True)
 
 
 @gpu
@@ -388,15 +406,16 @@ def test_attention_keeps_a_tail_behind_a_dominant_key():
     kc[0, 0, 0, 0] = 0x38  # K_0 = (1, 0, ...)
     vc[0, 0, 0, :] = 0  # V_0 = 0
     one = np.ones((n, 1), np.float32)
-    q = np.zeros((1, 1, d), np.float32)
-    q[0, 0, 0] = 12.0
-    g = [dev(a) for a in (kc, one, vc, one, np.arange(n, dtype=I32)[None], np.array([0, 1], I32), np.array([L], I32))]
-    O, Ls = pkg.attn_fwd_paged_fp8(dev_bf16(paged.bf16_bits(q)), *g, 1.0, True, torch.float32)
-    ok()
-    z = np.exp(12.0) + L - 1
-    want = (L - 1) / z
-    assert abs(O.cpu().numpy() - want).max() <= want * (2.0 ** -11 + 2.0 ** -15)
-    assert abs(float(Ls) - np.log(z)) <= 1e-4
+    for T in (1, 20):  # a decoding step; many rows
+        q = np.zeros((T, 1, d), np.float32)
+        q[:, 0, 0] = 12.0
+        g = [dev(a) for a in (kc, one, vc, one, np.arange(n, dtype=I32)[None], np.array([0, T], I32), np.array([L], I32))]
+        O, Ls = pkg.attn_fwd_paged_fp8(dev_bf16(paged.bf16_bits(q)), *g, 1.0, False, torch.float32)
+        ok()
+        z = np.exp(12.0) + L - 1
+        want = (L - 1) / z
+        assert abs(O.cpu().numpy() - want).max() <= want * (2.0 ** -11 + 2.0 ** -15)
+        assert abs(Ls.cpu().numpy() - np.log(z)).max() <= 1e-4
 
 
 @gpu
@@ -486,7 +505,7 @@ def test_a_step_captured_and_replayed():
     g = [x.clone() for x in start]
     cached, added, free = dev(lens[0]), dev(np.ones(3, I32)), dev(np.arange(kc.shape[0] - 3, kc.shape[0], dtype=I32))
     tb = dev(table)
-    ws = torch.empty(pkg.attn_fwd_paged_workspace_size(T, Hq, Hkv, d), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(pkg.attn_fwd_paged_workspace_size(R, T, Hq, Hkv, d), dtype=torch.uint8, device="cuda")
 
     def step():
         kv, cu, slots, _, _ = pkg.attn_kv_tables(cached, added, free, tb, page, T)
