@@ -196,11 +196,11 @@ struct PagedFwdParams {
   int causal, out_f32;
   unsigned long long wait_limit_ns;
 };
-// The two kernels, each followed by its merge: eight query rows of a kv head
-// to a tile (paged_fwd.cu), and 256 (paged_wide.cu).
-constexpr int kPagedNarrowRows = 8, kPagedWideRows = 256;
-cudaError_t launch_paged_narrow(int d, const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedFwdParams& p,
-                                int workers, cudaStream_t stream);
+// The kernels, each followed by its merge: 8 or 16 query rows of a kv head to
+// a tile (paged_fwd.cu), and 256 (paged_wide.cu).
+constexpr int kPagedWideRows = 256;
+cudaError_t launch_paged_narrow(int d, int rows, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                const PagedFwdParams& p, int workers, cudaStream_t stream);
 cudaError_t launch_paged_wide(int d, const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedFwdParams& p,
                               int workers, cudaStream_t stream);
 

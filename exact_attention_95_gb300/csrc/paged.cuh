@@ -212,7 +212,8 @@ __device__ __forceinline__ float output_lse(float m, float l) {
 
 // Merge of the items cut between workers: worker w's descriptor names the
 // item that begins in its range and goes on in the next parts - 1 workers'.
-// A warp per row, four rows to a CTA.
+// A warp per row, kMergeCtas CTAs of four to an item.
+constexpr int kMergeCtas = 8;
 template <int D, int ROWS>
 __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedFwdParams p) {
   griddep_wait();
@@ -221,48 +222,50 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedFwdParams p
   const int parts = d[0];
   if (parts < 2) return;
   const int start = d[1], n = d[2], tile = d[3], h = d[4];
-  const int lane = threadIdx.x & 31, row = blockIdx.y * 4 + (threadIdx.x >> 5);
-  if (row >= n * p.G - tile * ROWS) return;
-  auto part = [&](int s) -> size_t { return (size_t)(s == 0 ? 2 * w + 1 : 2 * (w + s)) * ROWS + row; };
-  constexpr int V = D / 32;  // columns of a lane
-  float M = -INFINITY;
-  for (int s = lane; s < parts; s += 32) M = fmaxf(M, p.part_ml[part(s) * 2]);
+  const int lane = threadIdx.x & 31;
+  const int rows = min(ROWS, n * p.G - tile * ROWS);
+  for (int row = blockIdx.y * 4 + (threadIdx.x >> 5); row < rows; row += 4 * gridDim.y) {
+auto part = [&](int s) -> size_t { return (size_t)(s == 0 ? 2 * w + 1 : 2 * (w + s)) * ROWS + row; };
+    constexpr int V = D / 32;  // columns of a lane
+    float M = -INFINITY;
+    for (int s = lane; s < parts; s += 32) M = fmaxf(M, p.part_ml[part(s) * 2]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float ref = M == -INFINITY ? 0.f : M;
-  float L = 0.f, acc[V] = {};
-  for (int s0 = 0; s0 < parts; s0 += 32) {
-    float wl = 0.f;
-    if (s0 + lane < parts) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + part(s0 + lane) * 2);
-      wl = ex2(ml.x - ref);
-      L += wl * ml.y;
-    }
-    const int cnt = min(32, parts - s0);
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float ref = M == -INFINITY ? 0.f : M;
+    float L = 0.f, acc[V] = {};
+    for (int s0 = 0; s0 < parts; s0 += 32) {
+      float wl = 0.f;
+      if (s0 + lane < parts) {
+        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + part(s0 + lane) * 2);
+        wl = ex2(ml.x - ref);
+        L += wl * ml.y;
+      }
+      const int cnt = min(32, parts - s0);
 #pragma unroll 4
-    for (int s = 0; s < cnt; ++s) {
-      const float wgt = __shfl_sync(0xffffffffu, wl, s);
-      const float* src = p.part_o + part(s0 + s) * D + lane * V;
+      for (int s = 0; s < cnt; ++s) {
+        const float wgt = __shfl_sync(0xffffffffu, wl, s);
+        const float* src = p.part_o + part(s0 + s) * D + lane * V;
 #pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] += wgt * src[v];
+        for (int v = 0; v < V; ++v) acc[v] += wgt * src[v];
+      }
     }
-  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  const size_t orow = output_row(p, start, h, tile * ROWS + row);
-  const float inv = output_factor(L);
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    const size_t orow = output_row(p, start, h, tile * ROWS + row);
+    const float inv = output_factor(L);
 #pragma unroll
-  for (int v = 0; v < V; v += 2) {
-    if (p.out_f32) {
-      float* dst = static_cast<float*>(p.O) + orow * D + lane * V + v;
-      dst[0] = acc[v] * inv;
-      dst[1] = acc[v + 1] * inv;
-    } else {
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.O) + orow * D + lane * V + v) =
-          pack_bf16(acc[v] * inv, acc[v + 1] * inv);
+    for (int v = 0; v < V; v += 2) {
+      if (p.out_f32) {
+        float* dst = static_cast<float*>(p.O) + orow * D + lane * V + v;
+        dst[0] = acc[v] * inv;
+        dst[1] = acc[v + 1] * inv;
+      } else {
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.O) + orow * D + lane * V + v) =
+            pack_bf16(acc[v] * inv, acc[v + 1] * inv);
+      }
     }
+    if (lane == 0) p.LSE[orow] = output_lse(M, L);
   }
-  if (lane == 0) p.LSE[orow] = output_lse(M, L);
 }
 
 // Launches `kern` and the merge behind it (its launch overlaps the kernel's end).
@@ -275,7 +278,7 @@ cudaError_t launch_with_merge(Kernel kern, int threads, int smem, const CUtensor
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)workers, ROWS / 4);
+  cfg.gridDim = dim3((unsigned)workers, (unsigned)min(ROWS / 4, kMergeCtas));
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute at{};

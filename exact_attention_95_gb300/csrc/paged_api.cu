@@ -38,18 +38,19 @@ attn_status check_cache(const void* kp, const float* ks, const void* vp, const f
 // Tokens of `heads` rows of d elements, `stride` elements apart.
 bool token_stride_ok(long long stride, long long heads, int d) { return stride >= heads * d && stride % 8 == 0; }
 
-// Which kernels a call runs, and its workspace: partial sums (O, then maxima
-// and sums, then merge descriptors) of one worker per SM, two slots each.
-// A request goes to the narrow kernel with up to kNarrowMost query rows of a
-// kv head, else to the wide one; without a wide one (T <= R and small groups:
-// a decoding step, where the wide launch would find nothing to do) to the
-// narrow one in any case.
-constexpr int kNarrowMost = 8;
-bool runs_wide(int R, int T, int G) { return T > R || G > kNarrowMost; }
+// Which kernels a call runs.  A decoding step (T <= R: on average a token a
+// request at most) with groups of up to eight heads runs the eight-row kernel
+// alone, whatever the requests' rows are: a launch for wider ones would find
+// nothing to do.  Any other call runs the 16-row kernel for the requests with
+// up to kNarrowMost query rows of a kv head and the 256-row kernel for the rest.
+constexpr int kNarrowMost = 48;
+bool runs_wide(int R, int T, int G) { return T > R || G > 8; }
+// Workspace: partial sums (O, then maxima and sums, then merge descriptors) of
+// one worker per SM, two slots each.
 size_t part_o_bytes(int rows, int d, int sms) { return (size_t)sms * 2 * rows * d * 4; }
 size_t part_ml_bytes(int rows, int sms) { return (size_t)sms * 2 * rows * 8; }
 size_t workspace_bytes_for(bool wide, int d, int sms) {
-  const int rows = wide ? attn::kPagedWideRows : attn::kPagedNarrowRows;
+  const int rows = wide ? attn::kPagedWideRows : 8;
   return part_o_bytes(rows, d, sms) + part_ml_bytes(rows, sms) + ((size_t)sms * 32 + 255) / 256 * 256;
 }
 
@@ -190,17 +191,18 @@ attn_status attn_fwd_paged_fp8(const void* Q, long long q_stride, const void* k_
     p.part_ml = reinterpret_cast<float*>(ws + part_o_bytes(rows, d, sms));
     p.desc = reinterpret_cast<int*>(ws + part_o_bytes(rows, d, sms) + part_ml_bytes(rows, sms));
   };
-  if (wide) {
+  if (wide && (long long)T * G > kNarrowMost) {
     place(attn::kPagedWideRows);
     p.rows_min = kNarrowMost;
     p.rows_max = 0x7fffffff;
     e = attn::launch_paged_wide(d, tk, tv, p, sms, st_);
   }
   if (e == cudaSuccess && (!wide || G <= kNarrowMost)) {
-    place(attn::kPagedNarrowRows);
+    const int rows = wide ? 16 : 8;
+    place(rows);
     p.rows_min = 0;
     p.rows_max = wide ? kNarrowMost : 0x7fffffff;
-    e = attn::launch_paged_narrow(d, tk, tv, p, sms, st_);
+    e = attn::launch_paged_narrow(d, rows, tk, tv, p, sms, st_);
   }
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }

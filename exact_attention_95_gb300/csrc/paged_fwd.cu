@@ -28,11 +28,6 @@ namespace {
 
 using namespace paged;
 
-constexpr int kRows = 8;           // query rows of a tile
-constexpr int kSets = 3;           // sets of four consumer warps
-constexpr int kWarps = 4 * kSets;
-constexpr int kHalf = 8;           // warps whose sums the exchange buffer holds
-constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kItems = 4;          // items announced ahead
 constexpr float kPScale = 16384.f;
 
@@ -43,28 +38,36 @@ struct UnitMeta {
   int pad[3];
 };
 
-template <int D>
+// NB: eight-row blocks of a tile.  Three sets of four consumer warps for one
+// block; two, with half as many registers more, for two.
+template <int D, int NB>
 struct PC {
+  static constexpr int ROWS = 8 * NB;
+  static constexpr int SETS = NB == 1 ? 3 : 2;
+  static constexpr int WARPS = 4 * SETS;
+  static constexpr int HALF = 8 / NB;  // warps whose sums the exchange buffer holds
+  static constexpr int THREADS = 32 * (WARPS + 1);
   static constexpr int STAGES = D == 128 ? 6 : 12;
   static constexpr int KBYTES = kUnit * D;
   static constexpr int SBYTES = 2 * KBYTES;
   static constexpr int OFF_RING = 0;
-  static constexpr int OFF_O = STAGES * SBYTES;                   // [kHalf][8][D] fp32
+  static constexpr int OFF_O = STAGES * SBYTES;                   // [HALF][ROWS][D] fp32
   static constexpr int OFF_SUMS = OFF_O;                          // [kMaxGroups] int64, until the first item
-  static constexpr int OFF_ML = OFF_O + kHalf * kRows * D * 4;    // [2][kHalf][8][2] fp32
-  static constexpr int OFF_ITEM = OFF_ML + 2 * kHalf * kRows * 8;
+  static constexpr int OFF_ML = OFF_O + HALF * ROWS * D * 4;      // [2][HALF][ROWS][2] fp32
+  static constexpr int OFF_ITEM = OFF_ML + 2 * HALF * ROWS * 8;
   static constexpr int OFF_META = OFF_ITEM + kItems * (int)sizeof(Item);
   static constexpr int OFF_BAR = OFF_META + STAGES * (int)sizeof(UnitMeta);
   static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_IFULL = 2 * STAGES, B_IEMPTY = B_IFULL + kItems;
   static constexpr int B_GIVEN = B_IEMPTY + kItems, B_WRITTEN = B_GIVEN + 1, B_READ = B_GIVEN + 2;
   static constexpr int OFF_ABORT = OFF_BAR + (B_READ + 1) * 8;
   static constexpr int SMEM = OFF_ABORT + 8 + 1024;
+  static_assert(SMEM <= 232448, "shared memory");
+  // A parity names a phase only to a waiter that has seen every phase before
+  // it: all units of a stage have to go to the same set.
+  static_assert(STAGES % SETS == 0, "stages and sets");
+  static_assert(WARPS > HALF && WARPS - HALF <= HALF, "the other warps hand over to as many");
+  static_assert(kMaxGroups * 8 <= HALF * ROWS * D * 4, "the sums fit the exchange buffer");
 };
-static_assert(PC<128>::SMEM <= 232448 && PC<64>::SMEM <= 232448, "shared memory");
-// A parity names a phase only to a waiter that has seen every phase before it:
-// all units of a stage have to go to the same set.
-static_assert(PC<128>::STAGES % kSets == 0 && PC<64>::STAGES % kSets == 0, "stages and sets");
-static_assert(kMaxGroups * 8 <= kHalf * kRows * 64 * 4, "the sums fit the exchange buffer");
 
 __device__ __forceinline__ uint32_t widen(uint32_t two) {
   uint32_t h;
@@ -107,11 +110,12 @@ __device__ __forceinline__ uint32_t piece(uint32_t base, int row, int c) {
   return D == 128 ? base + row * 128 + ((c ^ (row & 7)) << 4) : base + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, int NB>
+__global__ void __launch_bounds__(PC<D, NB>::THREADS, 1)
     fwd_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const PagedFwdParams p) {
-  using C = PC<D>;
+  using C = PC<D, NB>;
+  constexpr int kRows = C::ROWS, kSets = C::SETS, kWarps = C::WARPS, kHalf = C::HALF;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
@@ -212,11 +216,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int cg = D == 128 ? (g >> 1) | ((g & 1) << 2) : g >> 1;  // its 16-byte piece of a V row
   constexpr int QI = D / 64;   // 64-column parts of the contraction over d
   constexpr int MT = D / 16;   // 16-column tiles of O
-  uint32_t qb[QI][4][2];
-  float o[MT][4];
-  // Rows 2c and 2c + 1: running maximum, sum, factor of the products, limit of the keys.
-  float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f, f0 = 0.f, f1 = 0.f, vref = 0.f;
-  int lim0 = 0, lim1 = 0, lim_all = 0, lim_any = 0;
+  uint32_t qb[NB][QI][4][2];
+  float o[NB][MT][4];
+  // Of each block rows 2c and 2c + 1: running maximum, sum, factor of the products, limit of the keys.
+  float m[NB][2], l[NB][2], f[NB][2], vref = 0.f;
+  int lim[NB][2], lim_all = 0, lim_any = 0;
   // Places of its pieces in a unit's K and V: rows 8 further on are 8 * D bytes
   // on; the other half of a row's pieces (d = 128) is 64 bytes away, by the
   // swizzle in the direction that flips bit 6.
@@ -230,9 +234,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (count < 0) return;
     const int tile = im->tile, h = im->h, len = im->len, n = im->n, start = im->start;
     const int rows = min(kRows, n * p.G - tile * kRows);
-    {
-      // Queries (row g), as f16 after a power of two of the row; limits of the rows' keys.
-      const int rho = tile * kRows + min(g, rows - 1);
+    // Queries (row g of a block), as f16 after a power of two of the row; limits of the rows' keys.
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int rho = tile * kRows + min(8 * b + g, rows - 1);
       const int tok = rho / p.G;
       const uint4* src = reinterpret_cast<const uint4*>(p.Q + (long long)(start + tok) * p.q_stride +
                                                         (long long)(h * p.G + rho - tok * p.G) * D);
@@ -255,28 +260,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       // 2^-e takes the row's largest to [2^14, 2^15); e within what fp32 can undo.
       const int e = min(max((int)(am >> 7) - 127, -100), 126) - 14;
       const float up = __int_as_float((127 - e) << 23);
-      const float f = __int_as_float((127 + e) << 23) * p.scale_log2;
+      const float fr = __int_as_float((127 + e) << 23) * p.scale_log2;
 #pragma unroll
       for (int q = 0; q < QI; ++q)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint4 v = w[q][j >> 1];
           const uint32_t x = (j & 1) ? v.z : v.x, y = (j & 1) ? v.w : v.y;
-          qb[q][j][0] = pack_f16(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up);
-          qb[q][j][1] = pack_f16(__uint_as_float(y << 16) * up, __uint_as_float(y & 0xffff0000u) * up);
+          qb[b][q][j][0] = pack_f16(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up);
+          qb[b][q][j][1] = pack_f16(__uint_as_float(y << 16) * up, __uint_as_float(y & 0xffff0000u) * up);
         }
-      const int lim = key_limit(p, len, n, tok);
-      f0 = __shfl_sync(0xffffffffu, f, 8 * c);
-      f1 = __shfl_sync(0xffffffffu, f, 8 * c + 4);
-      lim0 = __shfl_sync(0xffffffffu, lim, 8 * c);
-      lim1 = __shfl_sync(0xffffffffu, lim, 8 * c + 4);
-      lim_all = __shfl_sync(0xffffffffu, lim, 0);   // the first token's
-      lim_any = __shfl_sync(0xffffffffu, lim, 28);  // the last one's
-      m0 = m1 = -INFINITY;
-      l0 = l1 = vref = 0.f;
+      const int lr = key_limit(p, len, n, tok);
 #pragma unroll
-      for (int j = 0; j < MT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+      for (int e2 = 0; e2 < 2; ++e2) {
+        f[b][e2] = __shfl_sync(0xffffffffu, fr, 8 * c + 4 * e2);
+        lim[b][e2] = __shfl_sync(0xffffffffu, lr, 8 * c + 4 * e2);
+        m[b][e2] = -INFINITY;
+        l[b][e2] = 0.f;
+      }
+      if (b == 0) lim_all = __shfl_sync(0xffffffffu, lr, 0);        // the first token's
+      if (b == NB - 1) lim_any = __shfl_sync(0xffffffffu, lr, 28);  // the last one's
+#pragma unroll
+      for (int j = 0; j < MT; ++j) o[b][j][0] = o[b][j][1] = o[b][j][2] = o[b][j][3] = 0.f;
     }
+    vref = 0.f;
     const int first = im->first;
     int u = first + (set + kSets - first % kSets) % kSets;
     for (; u < first + count; u += kSets) {
@@ -288,8 +295,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool la = (mt->pages >> pa) & 1, lb = (mt->pages >> pb) & 1;
       if (key0 < lim_any && (la || lb)) {
         const uint32_t kb = sb + C::OFF_RING + s * C::SBYTES, vb = kb + C::KBYTES;
-        // S^T = K Q^T: twice 16 keys by 8 rows.
-        float acc[2][4] = {};
+        // S^T = K Q^T: twice 16 keys by 8 rows of a block.
+        float acc[NB][2][4] = {};
 #pragma unroll
         for (int q = 0; q < QI; ++q) {
           const uint32_t ka = (kb + koff) ^ (64 * q);
@@ -299,73 +306,80 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint32_t a0[4] = {widen(x0[j]), widen(x1[j]), widen(x0[j] >> 16), widen(x1[j] >> 16)};
-            mma_f16(acc[0], a0, qb[q][j][0], qb[q][j][1]);
             const uint32_t a1[4] = {widen(x2[j]), widen(x3[j]), widen(x2[j] >> 16), widen(x3[j] >> 16)};
-            mma_f16(acc[1], a1, qb[q][j][0], qb[q][j][1]);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              mma_f16(acc[b][0], a0, qb[b][q][j][0], qb[b][q][j][1]);
+              mma_f16(acc[b][1], a1, qb[b][q][j][0], qb[b][q][j][1]);
+            }
           }
         }
         // Keys ko, ko + 8 (and 16 on) of rows 2c, 2c + 1.
         const float vsa = mt->vs[pa], vsb = mt->vs[pb];
-        float ca0 = f0 * mt->ks[pa], ca1 = f1 * mt->ks[pa], cb0 = f0 * mt->ks[pb], cb1 = f1 * mt->ks[pb];
+        const float ksa = mt->ks[pa], ksb = mt->ks[pb];
         const bool edge = key0 + 32 > lim_all || !la || !lb;
-        if (edge) {
-          // A factor that underflowed must not meet the infinities (any sum times 1e-37 is 0 as well).
-          ca0 = fmaxf(ca0, 1e-37f);
-          ca1 = fmaxf(ca1, 1e-37f);
-          cb0 = fmaxf(cb0, 1e-37f);
-          cb1 = fmaxf(cb1, 1e-37f);
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (key0 + 8 * (e >> 1) + ko >= ((e & 1) ? lim1 : lim0) || !(e < 4 ? la : lb)) acc[e >> 2][e & 3] = -INFINITY;
-        }
-        float mx0 = fmaxf(fmaxf(acc[0][0], acc[0][2]) * ca0, fmaxf(acc[1][0], acc[1][2]) * cb0);
-        float mx1 = fmaxf(fmaxf(acc[0][1], acc[0][3]) * ca1, fmaxf(acc[1][1], acc[1][3]) * cb1);
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
-          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
-        }
         const float vsm = fmaxf(la ? vsa : 0.f, lb ? vsb : 0.f);
-        if (__any_sync(0xffffffffu, mx0 > m0 || mx1 > m1) || vsm > vref) {
-          const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
-          const float vnew = fmaxf(vref, vsm);
-          const float rv = vref > 0.f ? __fdiv_rn(vref, vnew) : 0.f;
-          const float a0 = n0 > m0 ? ex2(m0 - n0) : 1.f, a1 = n1 > m1 ? ex2(m1 - n1) : 1.f;
-          l0 *= a0;
-          l1 *= a1;
-          const float b0 = a0 * rv, b1 = a1 * rv;
+        const float vnew = fmaxf(vref, vsm);
+        const float rv = vnew > vref && vref > 0.f ? __fdiv_rn(vref, vnew) : vnew > vref ? 0.f : 1.f;
+        vref = vnew;
+        const float rra = vsa == vref ? kPScale : vref > 0.f ? __fdiv_rn(vsa, vref) * kPScale : vsa;
+        const float rrb = vsb == vref ? kPScale : vref > 0.f ? __fdiv_rn(vsb, vref) * kPScale : vsb;
+        uint32_t pt[NB][4];  // P^T with row g and the keys of a column pair in a lane
 #pragma unroll
-          for (int j = 0; j < MT; ++j) {
-            o[j][0] *= b0;
-            o[j][1] *= b1;
-            o[j][2] *= b0;
-            o[j][3] *= b1;
+        for (int b = 0; b < NB; ++b) {
+          float ca0 = f[b][0] * ksa, ca1 = f[b][1] * ksa, cb0 = f[b][0] * ksb, cb1 = f[b][1] * ksb;
+          if (edge) {
+            // A factor that underflowed must not meet the infinities (any sum times 1e-37 is 0 as well).
+            ca0 = fmaxf(ca0, 1e-37f);
+            ca1 = fmaxf(ca1, 1e-37f);
+            cb0 = fmaxf(cb0, 1e-37f);
+            cb1 = fmaxf(cb1, 1e-37f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (key0 + 8 * (e >> 1) + ko >= lim[b][e & 1] || !(e < 4 ? la : lb)) acc[b][e >> 2][e & 3] = -INFINITY;
           }
-          m0 = n0;
-          m1 = n1;
-          vref = vnew;
-        }
-        const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
-        uint32_t pt[4];  // P^T with row g and the keys of a column pair in a lane
+          float mx0 = fmaxf(fmaxf(acc[b][0][0], acc[b][0][2]) * ca0, fmaxf(acc[b][1][0], acc[b][1][2]) * cb0);
+          float mx1 = fmaxf(fmaxf(acc[b][0][1], acc[b][0][3]) * ca1, fmaxf(acc[b][1][1], acc[b][1][3]) * cb1);
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const float vs = b ? vsb : vsa;
-          const float rr = vs == vref ? kPScale : vref > 0.f ? __fdiv_rn(vs, vref) * kPScale : vs;
-          const float c0 = b ? cb0 : ca0, c1 = b ? cb1 : ca1;
-          const float x0 = ex2(fmaf(acc[b][0], c0, -u0)), x1 = ex2(fmaf(acc[b][1], c1, -u1));
-          const float x2 = ex2(fmaf(acc[b][2], c0, -u0)), x3 = ex2(fmaf(acc[b][3], c1, -u1));
-          l0 += x0 + x2;
-          l1 += x1 + x3;
-          pt[2 * b] = transpose8(pack_f16(x0 * rr, x1 * rr));
-          pt[2 * b + 1] = transpose8(pack_f16(x2 * rr, x3 * rr));
+          for (int d = 4; d < 32; d <<= 1) {
+            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
+          }
+          if (__any_sync(0xffffffffu, mx0 > m[b][0] || mx1 > m[b][1]) || rv != 1.f) {
+            const float n0 = fmaxf(m[b][0], mx0), n1 = fmaxf(m[b][1], mx1);
+            const float a0 = n0 > m[b][0] ? ex2(m[b][0] - n0) : 1.f, a1 = n1 > m[b][1] ? ex2(m[b][1] - n1) : 1.f;
+            l[b][0] *= a0;
+            l[b][1] *= a1;
+            const float b0 = a0 * rv, b1 = a1 * rv;
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+              o[b][j][0] *= b0;
+              o[b][j][1] *= b1;
+              o[b][j][2] *= b0;
+              o[b][j][3] *= b1;
+            }
+            m[b][0] = n0;
+            m[b][1] = n1;
+          }
+          const float u0 = m[b][0] == -INFINITY ? 0.f : m[b][0], u1 = m[b][1] == -INFINITY ? 0.f : m[b][1];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float rr = e ? rrb : rra, c0 = e ? cb0 : ca0, c1 = e ? cb1 : ca1;
+            const float x0 = ex2(fmaf(acc[b][e][0], c0, -u0)), x1 = ex2(fmaf(acc[b][e][1], c1, -u1));
+            const float x2 = ex2(fmaf(acc[b][e][2], c0, -u0)), x3 = ex2(fmaf(acc[b][e][3], c1, -u1));
+            l[b][0] += x0 + x2;
+            l[b][1] += x1 + x3;
+            pt[b][2 * e] = transpose8(pack_f16(x0 * rr, x1 * rr));
+            pt[b][2 * e + 1] = transpose8(pack_f16(x2 * rr, x3 * rr));
+          }
         }
         // O^T += V^T P^T: row g of tile t is column 16 cg + 2t (d = 64: 8g + 2t), row g + 8 the one after.
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int hf = 0; hf < 2; ++hf) {
           uint32_t w[4][D / 32];  // four V rows' piece: keys kv0, kv1, kv0 + 8, kv1 + 8
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint32_t va = vb + ((e & 1) ? voff1 : voff0) + (16 * b + 8 * (e >> 1)) * D;
+            const uint32_t va = vb + ((e & 1) ? voff1 : voff0) + (16 * hf + 8 * (e >> 1)) * D;
             if constexpr (D == 128) {
               const uint4 v = lds_u4(va);
               w[e][0] = v.x;
@@ -381,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (edge) {  // V rows that no row of the tile sees hold anything, a NaN too
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (key0 + 16 * b + 8 * (e >> 1) + ((e & 1) ? kv1 : kv0) >= lim_any || !(b ? lb : la))
+              if (key0 + 16 * hf + 8 * (e >> 1) + ((e & 1) ? kv1 : kv0) >= lim_any || !(hf ? lb : la))
 #pragma unroll
                 for (int y = 0; y < D / 32; ++y) w[e][y] = 0;
           }
@@ -391,8 +405,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t b01 = __byte_perm(w[2][y], w[3][y], 0x5140), b23 = __byte_perm(w[2][y], w[3][y], 0x7362);
             const uint32_t t0[4] = {widen(a01), widen(a01 >> 16), widen(b01), widen(b01 >> 16)};
             const uint32_t t1[4] = {widen(a23), widen(a23 >> 16), widen(b23), widen(b23 >> 16)};
-            mma_f16(o[2 * y], t0, pt[2 * b], pt[2 * b + 1]);
-            mma_f16(o[2 * y + 1], t1, pt[2 * b], pt[2 * b + 1]);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              mma_f16(o[b][2 * y], t0, pt[b][2 * hf], pt[b][2 * hf + 1]);
+              mma_f16(o[b][2 * y + 1], t1, pt[b][2 * hf], pt[b][2 * hf + 1]);
+            }
           }
         }
       }
@@ -402,17 +419,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // The item's end: the warps' sums meet in shared memory.
 #pragma unroll
-    for (int d = 4; d < 32; d <<= 1) {
-      l0 += __shfl_xor_sync(0xffffffffu, l0, d);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, d);
-    }
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], d);
     float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
     float4* so = reinterpret_cast<float4*>(smem + C::OFF_O);
     const float back = vref * (1.f / kPScale);
     // Place of 16-byte piece q4 of a row: exchanged with its neighbours so that
     // the eight lanes of a store (four rows, two pieces) meet no bank twice.
     auto at = [&](int w_, int row, int q4) {
-      const int c2 = row >> 1;
+      const int c2 = (row >> 1) & 3;
       const int x = D == 128 ? c2 | ((q4 >> 4) << 2) : (c2 & 1) | ((c2 >> 1) << 2);
       return (w_ * kRows + row) * (D / 4) + (q4 ^ x);
     };
@@ -421,12 +439,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i > 0 && !mbar_wait_warp(bar(C::B_READ), (i - 1) & 1, wc)) return;
       float4* to = so + (warp - kHalf) * kRows * (D / 4) + lane;
 #pragma unroll
-      for (int j = 0; j < MT; ++j)
-        to[32 * j] = make_float4(o[j][0] * back, o[j][1] * back, o[j][2] * back, o[j][3] * back);
-      if (g == 0) {
-        ml[(warp - kHalf) * kRows + 2 * c] = make_float2(m0, l0);
-        ml[(warp - kHalf) * kRows + 2 * c + 1] = make_float2(m1, l1);
-      }
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+          to[32 * (b * MT + j)] =
+              make_float4(o[b][j][0] * back, o[b][j][1] * back, o[b][j][2] * back, o[b][j][3] * back);
+      if (g == 0)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            ml[(warp - kHalf) * kRows + 8 * b + 2 * c + e] = make_float2(m[b][e], l[b][e]);
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(bar(C::B_GIVEN));
@@ -436,42 +459,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int slot = im->slot;
     if (!mbar_wait_warp(bar(C::B_GIVEN), i & 1, wc)) return;
-    if (warp < kWarps - kHalf) {
-      const float2 g0 = ml[warp * kRows + 2 * c], g1 = ml[warp * kRows + 2 * c + 1];
-      const float n0 = fmaxf(m0, g0.x), n1 = fmaxf(m1, g1.x);
-      const float r0 = n0 == -INFINITY ? 0.f : n0, r1 = n1 == -INFINITY ? 0.f : n1;
-      const float a0 = ex2(m0 - r0), a1 = ex2(m1 - r1), b0 = ex2(g0.x - r0), b1 = ex2(g1.x - r1);
-      const float4* from = so + warp * kRows * (D / 4) + lane;
+    const bool takes = warp < kWarps - kHalf;
+    const float4* from = so + warp * kRows * (D / 4) + lane;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      float wa[2] = {back, back}, wb[2] = {0.f, 0.f};
+      if (takes) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 gv = ml[warp * kRows + 8 * b + 2 * c + e];
+          const float mn = fmaxf(m[b][e], gv.x), r = mn == -INFINITY ? 0.f : mn;
+          const float x = ex2(m[b][e] - r);
+          wb[e] = ex2(gv.x - r);
+          wa[e] = back * x;
+          l[b][e] = l[b][e] * x + gv.y * wb[e];
+          m[b][e] = mn;
+        }
+      }
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
-        const float4 v = from[32 * j];
-        o[j][0] = fmaf(o[j][0] * back, a0, v.x * b0);
-        o[j][1] = fmaf(o[j][1] * back, a1, v.y * b1);
-        o[j][2] = fmaf(o[j][2] * back, a0, v.z * b0);
-        o[j][3] = fmaf(o[j][3] * back, a1, v.w * b1);
+        const float4 v = takes ? from[32 * (b * MT + j)] : make_float4(0.f, 0.f, 0.f, 0.f);
+        o[b][j][0] = fmaf(o[b][j][0], wa[0], v.x * wb[0]);
+        o[b][j][1] = fmaf(o[b][j][1], wa[1], v.y * wb[1]);
+        o[b][j][2] = fmaf(o[b][j][2], wa[0], v.z * wb[0]);
+        o[b][j][3] = fmaf(o[b][j][3], wa[1], v.w * wb[1]);
       }
-      l0 = l0 * a0 + g0.y * b0;
-      l1 = l1 * a1 + g1.y * b1;
-      m0 = n0;
-      m1 = n1;
-    } else {
-#pragma unroll
-      for (int j = 0; j < MT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[j][e] *= back;
     }
     __syncwarp();
     ml += kHalf * kRows;
-    if (g == 0) {
-      ml[warp * kRows + 2 * c] = make_float2(m0, l0);
-      ml[warp * kRows + 2 * c + 1] = make_float2(m1, l1);
-    }
+    if (g == 0)
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int x = 0; x < MT / 2; ++x)
-        so[at(warp, 2 * c + e, (D == 128 ? 4 * cg : 2 * g) + x)] =
-            make_float4(o[2 * x][e], o[2 * x][2 + e], o[2 * x + 1][e], o[2 * x + 1][2 + e]);
+        for (int e = 0; e < 2; ++e) ml[warp * kRows + 8 * b + 2 * c + e] = make_float2(m[b][e], l[b][e]);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int x = 0; x < MT / 2; ++x)
+          so[at(warp, 8 * b + 2 * c + e, (D == 128 ? 4 * cg : 2 * g) + x)] =
+              make_float4(o[b][2 * x][e], o[b][2 * x][2 + e], o[b][2 * x + 1][e], o[b][2 * x + 1][2 + e]);
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(C::B_WRITTEN));
     if (!mbar_wait_warp(bar(C::B_WRITTEN), i & 1, wc)) return;
@@ -522,12 +550,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-cudaError_t launch_paged_narrow(int d, const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedFwdParams& p,
-                                int workers, cudaStream_t stream) {
-  return d == 128 ? launch_with_merge<128, kRows>(fwd_paged_kernel<128>, kThreads, PC<128>::SMEM, tmK, tmV, p, workers,
-                                                  stream)
-                  : launch_with_merge<64, kRows>(fwd_paged_kernel<64>, kThreads, PC<64>::SMEM, tmK, tmV, p, workers,
-                                                 stream);
+namespace {
+
+template <int D, int NB>
+cudaError_t launch_narrow(const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedFwdParams& p, int workers,
+                          cudaStream_t stream) {
+  using C = PC<D, NB>;
+  return launch_with_merge<D, C::ROWS>(fwd_paged_kernel<D, NB>, C::THREADS, C::SMEM, tmK, tmV, p, workers, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_narrow(int d, int rows, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                const PagedFwdParams& p, int workers, cudaStream_t stream) {
+  if (rows == 8)
+    return d == 128 ? launch_narrow<128, 1>(tmK, tmV, p, workers, stream)
+                    : launch_narrow<64, 1>(tmK, tmV, p, workers, stream);
+  return d == 128 ? launch_narrow<128, 2>(tmK, tmV, p, workers, stream)
+                  : launch_narrow<64, 2>(tmK, tmV, p, workers, stream);
 }
 
 }  // namespace attn

@@ -50,8 +50,8 @@ constexpr float kThreshold = 6.f;
 constexpr float kLowRatio = -60.f;  // log2 of the smallest V scale ratio that is told from zero
 
 struct UnitMeta {
-  float ks[8];  // K scales of its pages
-  float lv[8];  // log2 of their V scales
+  float ks[8];  // for every 16 keys: K scale of their page
+  float lv[8];  // log2 of its V scale, -infinity where the page was not loaded
   int pages;    // bit i: page i was loaded
   int pad[3];
 };
@@ -236,8 +236,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive_expect_tx(bar(C::B_KFULL + sk), bytes);
             if (!reuse(C::B_MEMPTY, u, kMetas)) return false;
             UnitMeta* m = metas + u % kMetas;
-            const float mk = __shfl_sync(0xffffffffu, ks, in_batch + (lane & 7));
-            const float mv = __shfl_sync(0xffffffffu, vs, in_batch + (lane & 7));
+            const int seg = ((lane & 7) * 16) >> p.page_log2;
+            const float mk = __shfl_sync(0xffffffffu, ks, in_batch + seg);
+            const float mv = __shfl_sync(0xffffffffu, vs, in_batch + seg);
             if (lane < 8) {
               m->ks[lane] = mk;
               m->lv[lane] = lg2(mv);
@@ -519,25 +520,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (key0 + c * 32 + x >= lim || !((pages >> ((c * 32 + (x & 16)) >> p.page_log2)) & 1))
                   sr[c][x] = __float_as_uint(-INFINITY);
           }
-          // A factor that underflowed must not meet an infinity (a sum times
+          float cf[8], lv[8];
+#pragma unroll
+          for (int x = 0; x < 8; x += 4) {
+            const float4 a = *reinterpret_cast<const float4*>(mt->ks + x);
+            const float4 b = *reinterpret_cast<const float4*>(mt->lv + x);
+            cf[x] = f * a.x, cf[x + 1] = f * a.y, cf[x + 2] = f * a.z, cf[x + 3] = f * a.w;
+            lv[x] = b.x, lv[x + 1] = b.y, lv[x + 2] = b.z, lv[x + 3] = b.w;
+          }
+          // Largest logit and V scale of the unit; 16 keys are of one page.  A
+          // factor that underflowed must not meet an infinity (a sum times
           // 1e-37 is 0 as well); a NaN stays.
-          auto factor = [&](int pg) -> float {
-            const float x = f * mt->ks[pg];
-            return x < 1e-37f ? 1e-37f : x;
-          };
-          // Largest logit and V scale of the unit; 16 keys are of one page.
           float mx = -INFINITY, lvm = -INFINITY;
 #pragma unroll
           for (int sgm = 0; sgm < 8; ++sgm) {
-            const int pg = (16 * sgm) >> p.page_log2, c = sgm >> 1, x0 = 16 * (sgm & 1);
+            const int c = sgm >> 1, x0 = 16 * (sgm & 1);
+            if (cf[sgm] < 1e-37f) cf[sgm] = 1e-37f;
             float a = -INFINITY, b = -INFINITY;
 #pragma unroll
             for (int x = 0; x < 8; x += 2) {
               a = fmax3(a, __uint_as_float(sr[c][x0 + x]), __uint_as_float(sr[c][x0 + x + 1]));
               b = fmax3(b, __uint_as_float(sr[c][x0 + 8 + x]), __uint_as_float(sr[c][x0 + 9 + x]));
             }
-            mx = fmaxf(mx, fmaxf(a, b) * factor(pg));
-            if ((pages >> pg) & 1) lvm = fmaxf(lvm, mt->lv[pg]);
+            mx = fmaxf(mx, fmaxf(a, b) * cf[sgm]);
+            lvm = fmaxf(lvm, lv[sgm]);
           }
           move = mx > m + kThreshold || lvm > lvref;
           if (move) {
@@ -553,10 +559,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           float lsum = 0.f;
 #pragma unroll
           for (int sgm = 0; sgm < 8; ++sgm) {
-            const int pg = (16 * sgm) >> p.page_log2, c = sgm >> 1, x0 = 16 * (sgm & 1);
-            const float ratio = fmaxf(mt->lv[pg] - lvref, kLowRatio) + kShift;
-            const float cf = factor(pg);
-            const uint64_t c2 = f2pack(cf, cf), off2 = f2pack(ratio - m_use, ratio - m_use);
+            const int c = sgm >> 1, x0 = 16 * (sgm & 1);
+            const float ratio = fmaxf(lv[sgm] - lvref, kLowRatio) + kShift;
+            const uint64_t c2 = f2pack(cf[sgm], cf[sgm]), off2 = f2pack(ratio - m_use, ratio - m_use);
             uint64_t rs = 0, rs1 = 0;
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
