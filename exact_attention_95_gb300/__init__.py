@@ -66,6 +66,7 @@ _BWD_STAGES = {"all": "attn_bwd", "preprocess": "attn_bwd_preprocess", "main": "
 
 _lock = threading.Lock()
 _lib = None
+_fast = None  # the extension module, bound to the loaded library
 
 
 class AttnError(RuntimeError):
@@ -76,7 +77,7 @@ class AttnError(RuntimeError):
 
 def load_library(path: str = LIB_PATH):
     """Load the CUDA library (raises if it has not been built)."""
-    global _lib
+    global _lib, _fast
     with _lock:
         if _lib is not None:
             return _lib
@@ -127,8 +128,19 @@ def load_library(path: str = LIB_PATH):
         lib.attn_last_device_status.restype = i32
         lib.attn_selftest_wait_timeout.argtypes = [ctypes.c_ulonglong, vp]
         lib.attn_selftest_wait_timeout.restype = i32
+        from . import _binding
+        _binding.bind(*(ctypes.cast(f, vp).value for f in (
+            lib.attn_kv_tables, lib.attn_kv_append_fp8, lib.attn_fwd_paged_fp8, lib.attn_fwd_paged_workspace_size)))
+        _fast = _binding
         _lib = lib
         return lib
+
+
+def _bound():
+    """The extension module (csrc/binding.cpp), with the library loaded."""
+    if _fast is None:
+        load_library()
+    return _fast
 
 
 def _stream(stream):
@@ -374,35 +386,36 @@ def attn_fwd_fp8(Qc, q_scale, Kc, k_scale, Vtc, v_scale, scale=None, causal=Fals
 
 # ---------------------------------------------------------------- paged 8-bit cache
 # A decoding step makes these calls once a layer, on kernels of a few
-# microseconds: the checks below cost as little as they can (one expression a
-# tensor; _check_tensor words the error), and pointers go to ctypes as ints.
-def _check_fast(name, t, dtype, shape, device):
-    if not (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == device
-            and t.is_contiguous()):
-        _check_tensor(name, t, dtype, shape, device)
-
-
+# microseconds, so the extension module checks, allocates and calls first; where
+# it finds an argument that is not as it has to be it returns None, and the
+# checks below say what is wrong.  A call on a named stream takes this way too.
 def _cuda_device(name, t):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     return t.device
 
 
-def _call(fn, dev, stream, *args):
-    """fn(*args, stream) with `dev` current; `stream` None is dev's current stream."""
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(dev.index)
-    elif stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
-    else:
-        handle = stream.cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        rc = fn(*args, handle)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, handle)
+def _call(fn, *args):
+    """fn(*args, current stream) of the current device."""
+    rc = fn(*args, torch.cuda.current_stream().cuda_stream)
     if rc != ATTN_OK:
         raise AttnError(rc, fn.__name__)
+
+
+def _on(dev, stream):
+    """A context with `dev` and `stream` (None: dev's current one) current, so
+    that what a call allocates belongs to the stream that it runs on."""
+    if stream is None:
+        return torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
+    return torch.cuda.stream(stream)
+
+
+def _result(r, where):
+    if type(r) is int:
+        raise AttnError(r, where)
+    return r
 
 
 def _check_tokens(name, t, heads, d, device):
@@ -429,17 +442,17 @@ def _check_cache(k_pages, k_scale, v_pages, v_scale, device):
         raise TypeError("k_pages must be a 4-dimensional CUDA tensor")
     shape = k_pages.shape
     scales = shape[:2]
-    _check_fast("k_pages", k_pages, torch.uint8, shape, device)
-    _check_fast("v_pages", v_pages, torch.uint8, shape, device)
-    _check_fast("k_scale", k_scale, torch.float32, scales, device)
-    _check_fast("v_scale", v_scale, torch.float32, scales, device)
+    _check_tensor("k_pages", k_pages, torch.uint8, shape, device)
+    _check_tensor("v_pages", v_pages, torch.uint8, shape, device)
+    _check_tensor("k_scale", k_scale, torch.float32, scales, device)
+    _check_tensor("v_scale", v_scale, torch.float32, scales, device)
     return shape
 
 
 def _check_table(block_table, device):
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise TypeError("block_table must be a CUDA tensor [R, max_pages]")
-    _check_fast("block_table", block_table, torch.int32, block_table.shape, device)
+    _check_tensor("block_table", block_table, torch.int32, block_table.shape, device)
     return block_table.shape
 
 
@@ -451,38 +464,35 @@ def attn_kv_tables(cached, added, free_pages, block_table, page_size, T, kv_lens
     (updated in place); T places for new tokens.  Returns (kv_lens [R], cu_tokens
     [R + 1], slots [T] int64, positions [T], taken [2]: pages taken from the head
     of free_pages, requests refused)."""
+    if stream is None:
+        r = _bound().kv_tables(cached, added, free_pages, block_table, page_size, T, kv_lens, cu_tokens, slots,
+                               positions, taken)
+        if r is not None:
+            return _result(r, "attn_kv_tables")
     lib = load_library()
     i32 = torch.int32
     dev = _cuda_device("cached", cached)
     R, max_pages = _check_table(block_table, dev)
-    _check_fast("cached", cached, i32, (R,), dev)
-    _check_fast("added", added, i32, (R,), dev)
-    F = _cuda_device("free_pages", free_pages) and free_pages.numel()
-    _check_fast("free_pages", free_pages, i32, (F,), dev)
-    empty = torch.empty
-    if kv_lens is None:
-        kv_lens = empty(R, dtype=i32, device=dev)
-    else:
-        _check_fast("kv_lens", kv_lens, i32, (R,), dev)
-    if cu_tokens is None:
-        cu_tokens = empty(R + 1, dtype=i32, device=dev)
-    else:
-        _check_fast("cu_tokens", cu_tokens, i32, (R + 1,), dev)
-    if slots is None:
-        slots = empty(T, dtype=torch.int64, device=dev)
-    else:
-        _check_fast("slots", slots, torch.int64, (T,), dev)
-    if positions is None:
-        positions = empty(T, dtype=i32, device=dev)
-    else:
-        _check_fast("positions", positions, i32, (T,), dev)
-    if taken is None:
-        taken = empty(2, dtype=i32, device=dev)
-    else:
-        _check_fast("taken", taken, i32, (2,), dev)
-    _call(lib.attn_kv_tables, dev, stream, cached.data_ptr(), added.data_ptr(), free_pages.data_ptr(), F,
-          block_table.data_ptr(), max_pages, page_size, kv_lens.data_ptr(), cu_tokens.data_ptr(), slots.data_ptr(),
-          positions.data_ptr(), taken.data_ptr(), R, T)
+    _check_tensor("cached", cached, i32, (R,), dev)
+    _check_tensor("added", added, i32, (R,), dev)
+    _cuda_device("free_pages", free_pages)
+    F = free_pages.numel()
+    _check_tensor("free_pages", free_pages, i32, (F,), dev)
+    with _on(dev, stream):
+        empty = torch.empty
+        kv_lens = empty(R, dtype=i32, device=dev) if kv_lens is None else kv_lens
+        cu_tokens = empty(R + 1, dtype=i32, device=dev) if cu_tokens is None else cu_tokens
+        slots = empty(T, dtype=torch.int64, device=dev) if slots is None else slots
+        positions = empty(T, dtype=i32, device=dev) if positions is None else positions
+        taken = empty(2, dtype=i32, device=dev) if taken is None else taken
+        _check_tensor("kv_lens", kv_lens, i32, (R,), dev)
+        _check_tensor("cu_tokens", cu_tokens, i32, (R + 1,), dev)
+        _check_tensor("slots", slots, torch.int64, (T,), dev)
+        _check_tensor("positions", positions, i32, (T,), dev)
+        _check_tensor("taken", taken, i32, (2,), dev)
+        _call(lib.attn_kv_tables, cached.data_ptr(), added.data_ptr(), free_pages.data_ptr(), F,
+              block_table.data_ptr(), max_pages, int(page_size), kv_lens.data_ptr(), cu_tokens.data_ptr(),
+              slots.data_ptr(), positions.data_ptr(), taken.data_ptr(), R, int(T))
     return kv_lens, cu_tokens, slots, positions, taken
 
 
@@ -491,6 +501,10 @@ def attn_kv_append_fp8(K, V, slots, k_pages, k_scale, v_pages, v_scale, stream=N
 
     k_pages, v_pages uint8 [num_pages, Hkv, page_size, d] and k_scale, v_scale fp32
     [num_pages, Hkv] are updated in place, and returned."""
+    if stream is None:
+        r = _bound().kv_append_fp8(K, V, slots, k_pages, k_scale, v_pages, v_scale)
+        if r is not None:
+            return _result(r, "attn_kv_append_fp8")
     lib = load_library()
     dev = _cuda_device("K", K)
     num_pages, Hkv, page_size, d = _check_cache(k_pages, k_scale, v_pages, v_scale, dev)
@@ -499,10 +513,11 @@ def attn_kv_append_fp8(K, V, slots, k_pages, k_scale, v_pages, v_scale, stream=N
     T = K.shape[0]
     if V.shape[0] != T:
         raise ValueError(f"V has {V.shape[0]} tokens, K has {T}")
-    _check_fast("slots", slots, torch.int64, (T,), dev)
-    _call(lib.attn_kv_append_fp8, dev, stream, K.data_ptr(), k_stride, V.data_ptr(), v_stride, slots.data_ptr(),
-          k_pages.data_ptr(), k_scale.data_ptr(), v_pages.data_ptr(), v_scale.data_ptr(), T, Hkv, d, num_pages,
-          page_size)
+    _check_tensor("slots", slots, torch.int64, (T,), dev)
+    with _on(dev, stream):
+        _call(lib.attn_kv_append_fp8, K.data_ptr(), k_stride, V.data_ptr(), v_stride, slots.data_ptr(),
+              k_pages.data_ptr(), k_scale.data_ptr(), v_pages.data_ptr(), v_scale.data_ptr(), T, Hkv, d, num_pages,
+              page_size)
     return k_pages, k_scale, v_pages, v_scale
 
 
@@ -517,6 +532,14 @@ def attn_fwd_paged_fp8(Q, k_pages, k_scale, v_pages, v_scale, block_table, cu_q,
     Q bf16 [T, Hq, d]; request r's queries are tokens cu_q[r] .. cu_q[r + 1] - 1 and
     its keys the first kv_lens[r] tokens of the pages that block_table[r] names
     (bottom-right causal alignment).  Rows behind cu_q[R] are not written."""
+    if out_dtype is None:
+        out_dtype = torch.bfloat16
+    out_dt = {torch.bfloat16: ATTN_BF16, torch.float32: ATTN_F32}[out_dtype]
+    if stream is None:
+        r = _bound().fwd_paged_fp8(Q, k_pages, k_scale, v_pages, v_scale, block_table, cu_q, kv_lens, scale, causal,
+                                   out_dt, O, LSE, workspace)
+        if r is not None:
+            return _result(r, "attn_fwd_paged_fp8")
     lib = load_library()
     dev = _cuda_device("Q", Q)
     if Q.dim() != 3:
@@ -528,30 +551,23 @@ def attn_fwd_paged_fp8(Q, k_pages, k_scale, v_pages, v_scale, block_table, cu_q,
         raise ValueError(f"the pages have d = {dk}, Q has {d}")
     R, max_pages = _check_table(block_table, dev)
     i32 = torch.int32
-    _check_fast("cu_q", cu_q, i32, (R + 1,), dev)
-    _check_fast("kv_lens", kv_lens, i32, (R,), dev)
+    _check_tensor("cu_q", cu_q, i32, (R + 1,), dev)
+    _check_tensor("kv_lens", kv_lens, i32, (R,), dev)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    if out_dtype is None:
-        out_dtype = torch.bfloat16
-    out_dt = {torch.bfloat16: ATTN_BF16, torch.float32: ATTN_F32}[out_dtype]
-    if O is None:
-        O = torch.empty((T, Hq, d), dtype=out_dtype, device=dev)
-    else:
-        _check_fast("O", O, out_dtype, (T, Hq, d), dev)
-    if LSE is None:
-        LSE = torch.empty((T, Hq), dtype=torch.float32, device=dev)
-    else:
-        _check_fast("LSE", LSE, torch.float32, (T, Hq), dev)
-    if workspace is None:
-        # The size is the current device's; all devices of a process are GB300s.
-        workspace = torch.empty(lib.attn_fwd_paged_workspace_size(R, T, Hq, Hkv, d), dtype=torch.uint8, device=dev)
-    else:
-        _check_workspace(workspace, 0, dev)
-    _call(lib.attn_fwd_paged_fp8, dev, stream, Q.data_ptr(), q_stride, k_pages.data_ptr(), k_scale.data_ptr(),
-          v_pages.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), cu_q.data_ptr(), kv_lens.data_ptr(),
-          O.data_ptr(), LSE.data_ptr(), R, T, Hq, Hkv, d, num_pages, page_size, max_pages, scale,
-          1 if causal else 0, out_dt, workspace.data_ptr(), workspace.numel())
+    with _on(dev, stream):
+        O = torch.empty((T, Hq, d), dtype=out_dtype, device=dev) if O is None else O
+        LSE = torch.empty((T, Hq), dtype=torch.float32, device=dev) if LSE is None else LSE
+        _check_tensor("O", O, out_dtype, (T, Hq, d), dev)
+        _check_tensor("LSE", LSE, torch.float32, (T, Hq), dev)
+        need = int(lib.attn_fwd_paged_workspace_size(R, T, Hq, Hkv, d))
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        _check_workspace(workspace, need, dev)
+        _call(lib.attn_fwd_paged_fp8, Q.data_ptr(), q_stride, k_pages.data_ptr(), k_scale.data_ptr(),
+              v_pages.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), cu_q.data_ptr(), kv_lens.data_ptr(),
+              O.data_ptr(), LSE.data_ptr(), R, T, Hq, Hkv, d, num_pages, page_size, max_pages, float(scale),
+              int(bool(causal)), out_dt, workspace.data_ptr(), workspace.numel())
     return O, LSE
 
 

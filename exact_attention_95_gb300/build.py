@@ -2,7 +2,8 @@
 
 Each .cu file under csrc/ is compiled by its own nvcc process (in parallel)
 and linked into ``libattn_sm103.so`` next to this file.  nvcc cross-compiles,
-so this runs on a machine without a GPU.
+so this runs on a machine without a GPU.  csrc/binding.cpp becomes the
+extension module ``_binding.so`` (host compiler, PyTorch's headers).
 """
 
 from __future__ import annotations
@@ -12,6 +13,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -51,12 +53,40 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+# The extension module of the paged calls; it does not depend on which variant
+# of the library is loaded.
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(HERE, "_binding.so")
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile the extension module with the host compiler."""
+    deps = (BINDING_SRC, os.path.join(ROOT, "include", "attn.h"), __file__)
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
+        return BINDING
+    import torch
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc())) or "/usr/local/cuda"
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(t, "include"),
+           "-I", os.path.join(t, "include", "torch", "csrc", "api", "include"), "-I", os.path.join(cuda, "include"),
+           BINDING_SRC, "-o", tmp, "-L", os.path.join(t, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: bool = False) -> str:
     """Compile and link the library; with debug=True the -DATTN_DEBUG variant."""
     lib, bdir = (DEBUG_LIB, DEBUG_BUILD) if debug else (LIB, BUILD)
     if debug:
         extra_flags = tuple(extra_flags) + ("-DATTN_DEBUG",)
     if not force and up_to_date(lib):
+        build_binding()
         return lib
     os.makedirs(bdir, exist_ok=True)
     nvcc = _nvcc()
@@ -72,7 +102,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+        binding = ex.submit(build_binding, force)
         objs = list(ex.map(compile_one, _sources()))
+        binding.result()
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -186,9 +186,11 @@ struct PagedFwdParams {
   const int* kv_lens;      // [R]
   void* O;                 // [T, Hq, d] bf16 or fp32
   float* LSE;              // [T, Hq]
-  float* part_o;           // workspace: [workers][2][rows of a tile][d] partial sums
-  float* part_ml;          // workspace: [workers][2][rows of a tile][2] their maxima and sums
-  int* desc;               // workspace: [workers][8] what the merge has to do
+  // Workspace: [workers][2][rows of a tile][d] partial sums, their maxima and
+  // sums [workers][2][rows of a tile][2], and what the merge has to do [workers][8].
+  float* part_o;
+  float* part_ml;
+  int* desc;
   int* status;
   int R, T, Hq, Hkv, G, num_pages, page_log2, max_pages;
   int rows_min, rows_max;  // the launch takes the requests with rows_min < n * G <= rows_max
@@ -196,12 +198,17 @@ struct PagedFwdParams {
   int causal, out_f32;
   unsigned long long wait_limit_ns;
 };
-// The kernels, each followed by its merge: 8 or 16 query rows of a kv head to
-// a tile (paged_fwd.cu), and 256 (paged_wide.cu).
+// The kernels: 8 or 16 query rows of a kv head to a tile (paged_fwd.cu), and
+// 256 (paged_wide.cu).  `behind`: launched behind the other one, whose end it
+// overlaps and which it outlasts.
 constexpr int kPagedWideRows = 256;
 cudaError_t launch_paged_narrow(int d, int rows, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                const PagedFwdParams& p, int workers, cudaStream_t stream);
+                                const PagedFwdParams& p, int workers, bool behind, cudaStream_t stream);
 cudaError_t launch_paged_wide(int d, const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedFwdParams& p,
                               int workers, cudaStream_t stream);
+// Merge of the items that the one or two launches (given by their parameters
+// and rows of a tile; the second may be null) have cut.
+cudaError_t launch_paged_merge(int d, const PagedFwdParams& p, int rows, const PagedFwdParams* p2, int rows2,
+                               int workers, cudaStream_t stream);
 
 }  // namespace attn

@@ -11,6 +11,8 @@
 // every SM's memory traffic the same whatever the lengths are.
 #pragma once
 
+#include <atomic>
+
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -58,8 +60,10 @@ __device__ __forceinline__ Req load_req(const PagedFwdParams& p, int r) {
 }
 
 // Units of every 32 requests, by `warps` warps; synchronise before reading.
+// (Of a single group walk_range sums them itself.)
 template <int ROWS>
 __device__ __forceinline__ void sum_units(const PagedFwdParams& p, long long* sums, int warp, int warps, int lane) {
+  if (p.R <= 32) return;
   for (int g = warp; g < (p.R + 31) >> 5; g += warps) {
     long long u = load_req<ROWS>(p, g * 32 + lane).units;
 #pragma unroll
@@ -82,8 +86,11 @@ template <int ROWS, class ItemFn, class UnitFn>
 __device__ __forceinline__ bool walk_range(const PagedFwdParams& p, const long long* sums, int lane, ItemFn item_fn,
                                            UnitFn unit_fn) {
   const int groups = (p.R + 31) >> 5;
+  Req rq = load_req<ROWS>(p, lane);
   long long total = 0;
-  for (int g = lane; g < groups; g += 32) total += sums[g];
+  if (groups == 1) total = rq.units;
+  else
+    for (int g = lane; g < groups; g += 32) total += sums[g];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   const long long per = (total + gridDim.x - 1) / gridDim.x;
@@ -98,7 +105,7 @@ __device__ __forceinline__ bool walk_range(const PagedFwdParams& p, const long l
     long long before = 0;
     int g = 0;
     while (g + 1 < groups && before + sums[g] <= begin) before += sums[g++];
-    Req rq = load_req<ROWS>(p, g * 32 + lane);
+    if (g > 0) rq = load_req<ROWS>(p, g * 32 + lane);
     long long incl = rq.units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -210,83 +217,37 @@ __device__ __forceinline__ float output_lse(float m, float l) {
   return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-// Merge of the items cut between workers: worker w's descriptor names the
-// item that begins in its range and goes on in the next parts - 1 workers'.
-// A warp per row, kMergeCtas CTAs of four to an item.
-constexpr int kMergeCtas = 8;
-template <int D, int ROWS>
-__global__ void __launch_bounds__(128) paged_merge_kernel(const PagedFwdParams p) {
-  griddep_wait();
-  const int w = blockIdx.x;
-  const int* d = p.desc + w * 8;
-  const int parts = d[0];
-  if (parts < 2) return;
-  const int start = d[1], n = d[2], tile = d[3], h = d[4];
-  const int lane = threadIdx.x & 31;
-  const int rows = min(ROWS, n * p.G - tile * ROWS);
-  for (int row = blockIdx.y * 4 + (threadIdx.x >> 5); row < rows; row += 4 * gridDim.y) {
-auto part = [&](int s) -> size_t { return (size_t)(s == 0 ? 2 * w + 1 : 2 * (w + s)) * ROWS + row; };
-    constexpr int V = D / 32;  // columns of a lane
-    float M = -INFINITY;
-    for (int s = lane; s < parts; s += 32) M = fmaxf(M, p.part_ml[part(s) * 2]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float ref = M == -INFINITY ? 0.f : M;
-    float L = 0.f, acc[V] = {};
-    for (int s0 = 0; s0 < parts; s0 += 32) {
-      float wl = 0.f;
-      if (s0 + lane < parts) {
-        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + part(s0 + lane) * 2);
-        wl = ex2(ml.x - ref);
-        L += wl * ml.y;
-      }
-      const int cnt = min(32, parts - s0);
-#pragma unroll 4
-      for (int s = 0; s < cnt; ++s) {
-        const float wgt = __shfl_sync(0xffffffffu, wl, s);
-        const float* src = p.part_o + part(s0 + s) * D + lane * V;
-#pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] += wgt * src[v];
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    const size_t orow = output_row(p, start, h, tile * ROWS + row);
-    const float inv = output_factor(L);
-#pragma unroll
-    for (int v = 0; v < V; v += 2) {
-      if (p.out_f32) {
-        float* dst = static_cast<float*>(p.O) + orow * D + lane * V + v;
-        dst[0] = acc[v] * inv;
-        dst[1] = acc[v + 1] * inv;
-      } else {
-        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.O) + orow * D + lane * V + v) =
-            pack_bf16(acc[v] * inv, acc[v + 1] * inv);
-      }
-    }
-    if (lane == 0) p.LSE[orow] = output_lse(M, L);
-  }
-}
-
-// Launches `kern` and the merge behind it (its launch overlaps the kernel's end).
-template <int D, int ROWS, class Kernel>
-cudaError_t launch_with_merge(Kernel kern, int threads, int smem, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                              const PagedFwdParams& p, int workers, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  kern<<<workers, threads, smem, stream>>>(tmK, tmV, p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)workers, (unsigned)min(ROWS / 4, kMergeCtas));
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute at{};
+// Launch attribute: may start while the kernel before it in the stream ends.
+__host__ inline void overlap_with_previous(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& at) {
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, ROWS>, p);
+}
+
+// Launches a kernel of `workers` CTAs with `smem` bytes of dynamic shared
+// memory.  ID tells the kernels of one signature apart: the attribute is set
+// once on a device.
+template <int ID, class Kernel>
+cudaError_t launch_workers(Kernel kern, int threads, int smem, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                           const PagedFwdParams& p, int workers, bool overlap, cudaStream_t stream) {
+  static std::atomic<bool> ready[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)workers);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  if (overlap) overlap_with_previous(cfg, at);
+  return cudaLaunchKernelEx(&cfg, kern, tmK, tmV, p);
 }
 
 }  // namespace paged

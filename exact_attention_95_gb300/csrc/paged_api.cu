@@ -49,9 +49,17 @@ bool runs_wide(int R, int T, int G) { return T > R || G > 8; }
 // one worker per SM, two slots each.
 size_t part_o_bytes(int rows, int d, int sms) { return (size_t)sms * 2 * rows * d * 4; }
 size_t part_ml_bytes(int rows, int sms) { return (size_t)sms * 2 * rows * 8; }
-size_t workspace_bytes_for(bool wide, int d, int sms) {
-  const int rows = wide ? attn::kPagedWideRows : 8;
+size_t part_bytes(int rows, int d, int sms) {
   return part_o_bytes(rows, d, sms) + part_ml_bytes(rows, sms) + ((size_t)sms * 32 + 255) / 256 * 256;
+}
+size_t workspace_bytes_for(bool wide, int d, int sms) {
+  return wide ? part_bytes(16, d, sms) + part_bytes(attn::kPagedWideRows, d, sms) : part_bytes(8, d, sms);
+}
+// The partial sums of tiles of `rows` rows at `ws`.
+void place(attn::PagedFwdParams& p, uint8_t* ws, int rows, int d, int sms) {
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + part_o_bytes(rows, d, sms));
+  p.desc = reinterpret_cast<int*>(ws + part_o_bytes(rows, d, sms) + part_ml_bytes(rows, sms));
 }
 
 int sms_or_default() {
@@ -182,28 +190,23 @@ attn_status attn_fwd_paged_fp8(const void* Q, long long q_stride, const void* k_
   p.causal = causal;
   p.out_f32 = out_dtype == ATTN_F32;
   p.wait_limit_ns = attn::device_wait_limit();
-  const cudaStream_t st_ = static_cast<cudaStream_t>(stream);
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const int rows = wide ? 16 : 8;
+  const bool big = wide && (long long)T * G > kNarrowMost, small = !wide || G <= kNarrowMost;
+  attn::PagedFwdParams pw = p;
+  place(p, ws, rows, d, sms);
+  p.rows_min = 0;
+  p.rows_max = wide ? kNarrowMost : 0x7fffffff;
+  place(pw, ws + part_bytes(rows, d, sms), attn::kPagedWideRows, d, sms);
+  pw.rows_min = kNarrowMost;
+  pw.rows_max = 0x7fffffff;
   cudaError_t e = cudaSuccess;
-  // The two kernels run one after the other and use the workspace in turn.
-  auto place = [&](int rows) {
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    p.part_o = reinterpret_cast<float*>(ws);
-    p.part_ml = reinterpret_cast<float*>(ws + part_o_bytes(rows, d, sms));
-    p.desc = reinterpret_cast<int*>(ws + part_o_bytes(rows, d, sms) + part_ml_bytes(rows, sms));
-  };
-  if (wide && (long long)T * G > kNarrowMost) {
-    place(attn::kPagedWideRows);
-    p.rows_min = kNarrowMost;
-    p.rows_max = 0x7fffffff;
-    e = attn::launch_paged_wide(d, tk, tv, p, sms, st_);
-  }
-  if (e == cudaSuccess && (!wide || G <= kNarrowMost)) {
-    const int rows = wide ? 16 : 8;
-    place(rows);
-    p.rows_min = 0;
-    p.rows_max = wide ? kNarrowMost : 0x7fffffff;
-    e = attn::launch_paged_narrow(d, rows, tk, tv, p, sms, st_);
-  }
+  if (big) e = attn::launch_paged_wide(d, tk, tv, pw, sms, cs);
+  if (e == cudaSuccess && small) e = attn::launch_paged_narrow(d, rows, tk, tv, p, sms, big, cs);
+  if (e == cudaSuccess)
+    e = small ? attn::launch_paged_merge(d, p, rows, big ? &pw : nullptr, attn::kPagedWideRows, sms, cs)
+              : attn::launch_paged_merge(d, pw, attn::kPagedWideRows, nullptr, 0, sms, cs);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

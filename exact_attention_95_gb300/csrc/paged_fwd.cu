@@ -205,6 +205,8 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, 1)
       for (int k = max(0, it - C::STAGES); k < it; ++k)
         mbar_wait_drain_warp(bar(C::B_FULL + k % C::STAGES), (k / C::STAGES) & 1, wc);
     griddep_launch_dependents();
+    // Behind the wide kernel: this one's completion stands for both.
+    griddep_wait();
     return;
   }
 
@@ -554,20 +556,20 @@ namespace {
 
 template <int D, int NB>
 cudaError_t launch_narrow(const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedFwdParams& p, int workers,
-                          cudaStream_t stream) {
+                          bool behind, cudaStream_t stream) {
   using C = PC<D, NB>;
-  return launch_with_merge<D, C::ROWS>(fwd_paged_kernel<D, NB>, C::THREADS, C::SMEM, tmK, tmV, p, workers, stream);
+  return launch_workers<D * 2 + NB>(fwd_paged_kernel<D, NB>, C::THREADS, C::SMEM, tmK, tmV, p, workers, behind, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_narrow(int d, int rows, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                const PagedFwdParams& p, int workers, cudaStream_t stream) {
+                                const PagedFwdParams& p, int workers, bool behind, cudaStream_t stream) {
   if (rows == 8)
-    return d == 128 ? launch_narrow<128, 1>(tmK, tmV, p, workers, stream)
-                    : launch_narrow<64, 1>(tmK, tmV, p, workers, stream);
-  return d == 128 ? launch_narrow<128, 2>(tmK, tmV, p, workers, stream)
-                  : launch_narrow<64, 2>(tmK, tmV, p, workers, stream);
+    return d == 128 ? launch_narrow<128, 1>(tmK, tmV, p, workers, behind, stream)
+                    : launch_narrow<64, 1>(tmK, tmV, p, workers, behind, stream);
+  return d == 128 ? launch_narrow<128, 2>(tmK, tmV, p, workers, behind, stream)
+                  : launch_narrow<64, 2>(tmK, tmV, p, workers, behind, stream);
 }
 
 }  // namespace attn

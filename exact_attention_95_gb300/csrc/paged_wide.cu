@@ -692,8 +692,7 @@ cudaError_t launch_wide(const CUtensorMap& tmK, const CUtensorMap& tmV, const Pa
     regs = fa.numRegs;
   }
   if (regs != kLaunchRegs) return cudaErrorInvalidKernelImage;
-  return launch_with_merge<D, kPagedWideRows>(fwd_paged_wide_kernel<D>, kThreads, WC<D>::SMEM, tmK, tmV, p, workers,
-                                              stream);
+  return launch_workers<D>(fwd_paged_wide_kernel<D>, kThreads, WC<D>::SMEM, tmK, tmV, p, workers, false, stream);
 }
 
 }  // namespace
