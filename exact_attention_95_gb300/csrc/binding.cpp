@@ -65,6 +65,14 @@ bool output(PyObject* o, at::Tensor& t, at::ScalarType type, at::IntArrayRef sha
   t = *given;
   return true;
 }
+// `count` elements of a one-dimensional tensor, from `first` on, sharing its memory.
+at::Tensor part_of(const at::Tensor& t, int64_t first, int64_t count) {
+  at::Tensor v = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(t.storage()), t.key_set(),
+                                                          t.dtype());
+  v.unsafeGetTensorImpl()->set_storage_offset(first);
+  v.unsafeGetTensorImpl()->set_sizes_contiguous({count});
+  return v;
+}
 PyObject* wrap(PyObject* given, at::Tensor& t) {
   if (given != Py_None) {
     Py_INCREF(given);
@@ -127,7 +135,15 @@ PyObject* kv_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
         !is(free_pages, at::kInt, {F}, dev) || !is(table, at::kInt, {R, width}, dev))
       Py_RETURN_NONE;
     at::Tensor lens, cu, slots, positions, taken;
-    if (!output(a[6], lens, at::kInt, {R}, dev) || !output(a[7], cu, at::kInt, {R + 1}, dev) ||
+    if (a[6] == Py_None && a[7] == Py_None && a[9] == Py_None && a[10] == Py_None) {
+      // One allocation for the 32-bit outputs.
+      const at::Tensor all = at::empty({2 * R + 3 + T}, at::TensorOptions().dtype(at::kInt).device(dev));
+      lens = part_of(all, 0, R);
+      cu = part_of(all, R, R + 1);
+      taken = part_of(all, 2 * R + 1, 2);
+      positions = part_of(all, 2 * R + 3, T);
+      if (!output(a[8], slots, at::kLong, {T}, dev)) Py_RETURN_NONE;
+    } else if (!output(a[6], lens, at::kInt, {R}, dev) || !output(a[7], cu, at::kInt, {R + 1}, dev) ||
         !output(a[8], slots, at::kLong, {T}, dev) || !output(a[9], positions, at::kInt, {T}, dev) ||
         !output(a[10], taken, at::kInt, {2}, dev))
       Py_RETURN_NONE;
