@@ -65,12 +65,13 @@ bool output(PyObject* o, at::Tensor& t, at::ScalarType type, at::IntArrayRef sha
   t = *given;
   return true;
 }
-// `count` elements of a one-dimensional tensor, from `first` on, sharing its memory.
-at::Tensor part_of(const at::Tensor& t, int64_t first, int64_t count) {
+// A contiguous tensor of this type and shape in the memory of a new tensor t,
+// from element `first` (of this type) on.
+at::Tensor part_of(const at::Tensor& t, at::ScalarType type, int64_t first, at::IntArrayRef shape) {
   at::Tensor v = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(t.storage()), t.key_set(),
-                                                          t.dtype());
+                                                          c10::scalarTypeToTypeMeta(type));
   v.unsafeGetTensorImpl()->set_storage_offset(first);
-  v.unsafeGetTensorImpl()->set_sizes_contiguous({count});
+  v.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
   return v;
 }
 PyObject* wrap(PyObject* given, at::Tensor& t) {
@@ -138,10 +139,10 @@ PyObject* kv_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[6] == Py_None && a[7] == Py_None && a[9] == Py_None && a[10] == Py_None) {
       // One allocation for the 32-bit outputs.
       const at::Tensor all = at::empty({2 * R + 3 + T}, at::TensorOptions().dtype(at::kInt).device(dev));
-      lens = part_of(all, 0, R);
-      cu = part_of(all, R, R + 1);
-      taken = part_of(all, 2 * R + 1, 2);
-      positions = part_of(all, 2 * R + 3, T);
+      lens = part_of(all, at::kInt, 0, {R});
+      cu = part_of(all, at::kInt, R, {R + 1});
+      taken = part_of(all, at::kInt, 2 * R + 1, {2});
+      positions = part_of(all, at::kInt, 2 * R + 3, {T});
       if (!output(a[8], slots, at::kLong, {T}, dev)) Py_RETURN_NONE;
     } else if (!output(a[6], lens, at::kInt, {R}, dev) || !output(a[7], cu, at::kInt, {R + 1}, dev) ||
         !output(a[8], slots, at::kLong, {T}, dev) || !output(a[9], positions, at::kInt, {T}, dev) ||
@@ -202,9 +203,16 @@ PyObject* fwd_paged_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int causal = PyObject_IsTrue(a[9]), f32 = PyObject_IsTrue(a[10]);
     if (causal < 0 || f32 < 0) return nullptr;
     at::Tensor O, LSE, ws;
-    if (!output(a[11], O, f32 ? at::kFloat : at::kBFloat16, {T, Hq, c.d}, dev) ||
-        !output(a[12], LSE, at::kFloat, {T, Hq}, dev))
+    const at::ScalarType type = f32 ? at::kFloat : at::kBFloat16;
+    if (a[11] == Py_None && a[12] == Py_None) {
+      // One allocation for both outputs (O's rows are 128 bytes at least).
+      const int64_t bytes = T * Hq * c.d * (f32 ? 4 : 2);
+      const at::Tensor all = at::empty({bytes / 4 + T * Hq}, at::TensorOptions().dtype(at::kFloat).device(dev));
+      O = part_of(all, type, 0, {T, Hq, c.d});
+      LSE = part_of(all, at::kFloat, bytes / 4, {T, Hq});
+    } else if (!output(a[11], O, type, {T, Hq, c.d}, dev) || !output(a[12], LSE, at::kFloat, {T, Hq}, dev)) {
       Py_RETURN_NONE;
+    }
     const size_t need = g_workspace((int)R, (int)T, (int)Hq, (int)c.Hkv, (int)c.d);
     if (a[13] == Py_None) {
       ws = at::empty({(int64_t)need}, at::TensorOptions().dtype(at::kByte).device(dev));

@@ -202,13 +202,15 @@ struct PagedFwdParams {
 // 256 (paged_wide.cu).  `behind`: launched behind the other one, whose end it
 // overlaps and which it outlasts.
 constexpr int kPagedWideRows = 256;
+// CTAs of an SM, each a worker, by the rows of a tile.
+constexpr int paged_ctas(int rows) { return rows == 8 ? 3 : rows == 16 ? 2 : 1; }
 cudaError_t launch_paged_narrow(int d, int rows, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                 const PagedFwdParams& p, int workers, bool behind, cudaStream_t stream);
 cudaError_t launch_paged_wide(int d, const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedFwdParams& p,
                               int workers, cudaStream_t stream);
-// Merge of the items that the one or two launches (given by their parameters
-// and rows of a tile; the second may be null) have cut.
-cudaError_t launch_paged_merge(int d, const PagedFwdParams& p, int rows, const PagedFwdParams* p2, int rows2,
-                               int workers, cudaStream_t stream);
+// Merge of the items that the one or two launches (given by their parameters,
+// rows of a tile and workers; the second may be null) have cut.
+cudaError_t launch_paged_merge(int d, const PagedFwdParams& p, int rows, int workers, const PagedFwdParams* p2,
+                               int rows2, int workers2, cudaStream_t stream);
 
 }  // namespace attn

@@ -77,34 +77,56 @@ __device__ __forceinline__ int key_limit(const PagedFwdParams& p, int len, int n
   return p.causal ? max(0, min(len, len - n + tok + 1)) : len;
 }
 
-// Walks this worker's range (a whole warp).  item(Item, seen) announces an
-// item, of whose keys its rows see the first `seen`; unit(k, lane's page id or
-// -1, its K and V scale, place of the unit's first page among the lanes) loads
-// unit k of it.  Both return false to stop.  Writes the worker's merge
-// descriptor.  Returns false if it was stopped.
-template <int ROWS, class ItemFn, class UnitFn>
-__device__ __forceinline__ bool walk_range(const PagedFwdParams& p, const long long* sums, int lane, ItemFn item_fn,
-                                           UnitFn unit_fn) {
-  const int groups = (p.R + 31) >> 5;
-  Req rq = load_req<ROWS>(p, lane);
-  long long total = 0;
-  if (groups == 1) total = rq.units;
-  else
-    for (int g = lane; g < groups; g += 32) total += sums[g];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
-  const long long begin = min(total, per * blockIdx.x);
-  const long long end = min(total, begin + per);
+// a / b for non-negative a; units rarely need more than 32 bits.
+__device__ __forceinline__ long long divide(long long a, int b) {
+  return (a >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// Up to 32 pages of an item: the units whose page ids and scales a warp holds
+// at once (lane i: page i).
+struct Batch {
+  int k, units;  // first unit and how many
+  bool opens;    // the item's first batch
+};
+
+// This worker's range, item by item and batch by batch (a whole warp, every
+// lane with the same state).
+template <int ROWS>
+struct Walker {
+  const PagedFwdParams& p;
+  const long long* sums;
+  int lane;
+  int groups, g, l;        // request: group of 32, lane
+  Req rq;                  // lane's request of the group
+  long long pos, end, per; // units: next, end of the range, of a worker
+  long long off, units;    // of the request: next unit, all
+  Item im;                 // current item
+  int seen, ke;            // keys its rows see, end of its units
+  int kt, tiles, item;     // units of an item, tiles of the request, next item
+  int k, line;             // next unit of the item; units walked
+  bool opened;             // the current item's first batch has been given
   int merge_parts = 0, merge_start = 0, merge_n = 0, merge_tile = 0, merge_h = 0;
-  const int npg = kUnit >> p.page_log2;  // pages of a unit
-  int line = 0;                          // units walked
-  bool ok = true;
-  if (begin < end) {
-    // The group, then the request, that holds unit `begin`.
+
+  __device__ __forceinline__ Walker(const PagedFwdParams& p_, const long long* sums_, int lane_)
+      : p(p_), sums(sums_), lane(lane_) {
+    groups = (p.R + 31) >> 5;
+    rq = load_req<ROWS>(p, lane);
+    long long total = 0;
+    if (groups == 1) total = rq.units;
+    else
+      for (int i = lane; i < groups; i += 32) total += sums[i];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    per = divide(total + gridDim.x - 1, gridDim.x);
+    pos = min(total, per * blockIdx.x);
+    end = min(total, pos + per);
+    g = l = line = k = ke = 0;
+    off = units = 0;
+    opened = true;
+    if (pos >= end) return;
+    // The group, then the request, that holds unit `pos`.
     long long before = 0;
-    int g = 0;
-    while (g + 1 < groups && before + sums[g] <= begin) before += sums[g++];
+    while (g + 1 < groups && before + sums[g] <= pos) before += sums[g++];
     if (g > 0) rq = load_req<ROWS>(p, g * 32 + lane);
     long long incl = rq.units;
 #pragma unroll
@@ -113,94 +135,152 @@ __device__ __forceinline__ bool walk_range(const PagedFwdParams& p, const long l
       if (lane >= o) incl += x;
     }
     incl += before;
-    int l = __ffs(__ballot_sync(0xffffffffu, incl > begin)) - 1;
-    long long off = begin - (__shfl_sync(0xffffffffu, incl, l) - __shfl_sync(0xffffffffu, rq.units, l));
-    long long pos = begin;
-    while (pos < end && ok) {
-      Item im;
-      im.req = g * 32 + l;
-      im.start = __shfl_sync(0xffffffffu, rq.start, l);
-      im.n = __shfl_sync(0xffffffffu, rq.n, l);
-      im.len = __shfl_sync(0xffffffffu, rq.len, l);
-      const long long units = __shfl_sync(0xffffffffu, rq.units, l);
-      const int kt = max(1, (im.len + kUnit - 1) / kUnit);
-      const int tiles = (im.n * p.G + ROWS - 1) / ROWS;
-      const int* row = p.block_table + (size_t)im.req * p.max_pages;
-      int item = (int)(off / kt);
-      int k0 = (int)(off - (long long)item * kt);
-      for (; off < units && pos < end && ok; ++item) {
-        im.h = item / tiles;
-        // First and last tiles in turn: under the causal mask a tile's share
-        // of its kt units grows with its place, and a worker's range then
-        // holds early and late ones alike.
-        const int at = item - im.h * tiles;
-        im.tile = (at & 1) ? tiles - 1 - (at >> 1) : at >> 1;
-        const int k1 = (int)min((long long)kt, k0 + (end - pos));
-        im.slot = k0 == 0 && k1 == kt ? -1 : k0 == 0 ? 1 : 0;
-        if (im.slot == 1) {
-          const long long last = pos + kt - 1;  // the item's last unit
-          merge_parts = (int)(last / per - blockIdx.x) + 1;
-          merge_start = im.start;
-          merge_n = im.n;
-          merge_tile = im.tile;
-          merge_h = im.h;
-        }
-        const int seen = key_limit(p, im.len, im.n, (min(im.n * p.G, (im.tile + 1) * ROWS) - 1) / p.G);
-        const int ke = max(k0, min(k1, (seen + kUnit - 1) / kUnit));
-        im.k0 = k0;
-        im.first = line;
-        im.count = ke - k0;
-        ok = item_fn(im, seen);
-        int id = -1;
-        float ks = 1.f, vs = 0.f;
-        for (int k = k0; k < ke && ok; ++k) {
-          // Page ids and scales, 32 pages at a time (lane i: page i of the batch).
-          const int in_batch = ((k - k0) * npg) & 31;
-          if (in_batch == 0) {
-            const int pg = k * npg + lane;
-            id = -1;
-            ks = 1.f;
-            vs = 0.f;
-            if (((long long)pg << p.page_log2) < seen) {
-              id = row[pg];
-              if (id < 0 || id >= p.num_pages) {
-                id = -1;
-                atomicCAS(p.status, kDevOk, kDevBounds);
-              } else {
-                ks = p.k_scale[(size_t)id * p.Hkv + im.h];
-                vs = p.v_scale[(size_t)id * p.Hkv + im.h];
-              }
-            }
-          }
-          ok = unit_fn(im, k, id, ks, vs, in_batch);
-          ++line;
-        }
-        pos += k1 - k0;
-        off += k1 - k0;
-        k0 = 0;
-      }
-      // The next request that has units.
-      if (pos < end && ok) {
-        off = 0;
+    l = __ffs(__ballot_sync(0xffffffffu, incl > pos)) - 1;
+    open_request();
+    off = pos - (__shfl_sync(0xffffffffu, incl, l) - units);
+    item = (int)divide(off, kt);
+    im.k0 = (int)(off - (long long)item * kt);
+    open_item();
+  }
+  __device__ __forceinline__ void open_request() {
+    im.req = g * 32 + l;
+    im.start = __shfl_sync(0xffffffffu, rq.start, l);
+    im.n = __shfl_sync(0xffffffffu, rq.n, l);
+    im.len = __shfl_sync(0xffffffffu, rq.len, l);
+    units = __shfl_sync(0xffffffffu, rq.units, l);
+    kt = max(1, (im.len + kUnit - 1) / kUnit);
+    tiles = (im.n * p.G + ROWS - 1) / ROWS;
+    off = 0;
+    item = 0;
+    im.k0 = 0;
+  }
+  __device__ __forceinline__ void open_item() {
+    im.h = item / tiles;
+    // First and last tiles in turn: under the causal mask a tile's share of its
+    // kt units grows with its place, and a worker's range then holds early and
+    // late ones alike.
+    const int at = item - im.h * tiles;
+    im.tile = (at & 1) ? tiles - 1 - (at >> 1) : at >> 1;
+    const int k0 = im.k0, k1 = (int)min((long long)kt, k0 + (end - pos));
+    im.slot = k0 == 0 && k1 == kt ? -1 : k0 == 0 ? 1 : 0;
+    if (im.slot == 1) {
+      const long long last = pos + kt - 1;  // the item's last unit
+      merge_parts = (int)((per >> 31) == 0 ? divide(last, (int)per) : last / per) - (int)blockIdx.x + 1;
+      merge_start = im.start;
+      merge_n = im.n;
+      merge_tile = im.tile;
+      merge_h = im.h;
+    }
+    seen = key_limit(p, im.len, im.n, (min(im.n * p.G, (im.tile + 1) * ROWS) - 1) / p.G);
+    ke = max(k0, min(k1, (seen + kUnit - 1) / kUnit));
+    im.first = line;
+    im.count = ke - k0;
+    line += im.count;
+    k = k0;
+    pos += k1 - k0;
+    off += k1 - k0;
+    opened = false;
+  }
+  // The next batch, or false at the range's end.  `im` and `seen` are its item's.
+  __device__ __forceinline__ bool next(Batch& b) {
+    if (opened && k >= ke) {
+      if (pos >= end) return false;
+      if (off >= units) {
+        // The next request that has units.
         uint32_t more = __ballot_sync(0xffffffffu, rq.units > 0) & ~(0xffffffffu >> (31 - l));
         while (!more && g + 1 < groups) {
           ++g;
           rq = load_req<ROWS>(p, g * 32 + lane);
           more = __ballot_sync(0xffffffffu, rq.units > 0);
         }
-        if (!more) break;
+        if (!more) return false;
         l = __ffs(more) - 1;
+        open_request();
+      } else {
+        ++item;
+        im.k0 = 0;
       }
+      open_item();
+    }
+    b.opens = !opened;
+    opened = true;
+    b.k = k;
+    b.units = min(ke - k, 32 >> (7 - p.page_log2));
+    k += b.units;
+    return true;
+  }
+  // Whether the lane has a page of a batch of the current item, and its id.
+  __device__ __forceinline__ bool page_id(const Batch& b, int& id) const {
+    const int pg = (b.k << (7 - p.page_log2)) + lane;
+    if (pg >= ((b.k + b.units) << (7 - p.page_log2)) || ((long long)pg << p.page_log2) >= seen) return false;
+    id = p.block_table[(size_t)im.req * p.max_pages + pg];
+    return true;
+  }
+  __device__ __forceinline__ void write_descriptor() const {
+    if (lane == 0) {
+      int* d = p.desc + blockIdx.x * 8;
+      d[0] = merge_parts;
+      d[1] = merge_start;
+      d[2] = merge_n;
+      d[3] = merge_tile;
+      d[4] = merge_h;
     }
   }
-  if (lane == 0) {
-    int* d = p.desc + blockIdx.x * 8;
-    d[0] = merge_parts;
-    d[1] = merge_start;
-    d[2] = merge_n;
-    d[3] = merge_tile;
-    d[4] = merge_h;
+};
+static_assert(kUnit == 128, "units are 2^7 keys");
+
+// Walks this worker's range (a whole warp): item_fn(Item) announces an item,
+// unit_fn(kv head, lane's page id or negative, its K and V scale, place of the
+// unit's first page among the lanes) loads the next unit.  Both return false
+// to stop; then so does this.  Page ids are read two batches ahead and scales
+// one, so that neither latency is waited for but at the start; an item is
+// announced as soon as its first ids are on their way (up to two items before
+// its units are loaded: the announcements' ring has to hold four).
+template <int ROWS, class ItemFn, class UnitFn>
+__device__ __forceinline__ bool walk_range(const PagedFwdParams& p, const long long* sums, int lane, ItemFn item_fn,
+                                           UnitFn unit_fn) {
+  Walker<ROWS> w(p, sums, lane);
+  struct Held {
+    int units = 0;  // 0: none, or an item without units
+    int id = -1, h = 0;
+    float ks = 1.f, vs = 0.f;
+    bool any = false, page = false;
+  };
+  bool ok = true;
+  auto take = [&]() -> Held {
+    Held x;
+    Batch b;
+    x.any = ok && w.next(b);
+    if (x.any) {
+      x.units = b.units;
+      x.h = w.im.h;
+      x.page = w.page_id(b, x.id);
+      if (b.opens) ok = item_fn(w.im);
+    }
+    return x;
+  };
+  auto scales = [&](Held& x) {
+    if (!x.page) return;
+    if (x.id < 0 || x.id >= p.num_pages) {
+      x.id = -1;
+      atomicCAS(p.status, kDevOk, kDevBounds);
+    } else {
+      x.ks = p.k_scale[(size_t)x.id * p.Hkv + x.h];
+      x.vs = p.v_scale[(size_t)x.id * p.Hkv + x.h];
+    }
+  };
+  const int npg_log2 = 7 - p.page_log2;
+  Held cur = take();
+  scales(cur);
+  Held nxt = take();
+  while (cur.any && ok) {
+    scales(nxt);
+    const Held then = take();
+    for (int j = 0; j < cur.units && ok; ++j) ok = unit_fn(cur.h, cur.id, cur.ks, cur.vs, j << npg_log2);
+    cur = nxt;
+    nxt = then;
   }
+  w.write_descriptor();
   return ok;
 }
 

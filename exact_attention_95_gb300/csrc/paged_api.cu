@@ -46,11 +46,13 @@ bool token_stride_ok(long long stride, long long heads, int d) { return stride >
 constexpr int kNarrowMost = 48;
 bool runs_wide(int R, int T, int G) { return T > R || G > 8; }
 // Workspace: partial sums (O, then maxima and sums, then merge descriptors) of
-// one worker per SM, two slots each.
-size_t part_o_bytes(int rows, int d, int sms) { return (size_t)sms * 2 * rows * d * 4; }
-size_t part_ml_bytes(int rows, int sms) { return (size_t)sms * 2 * rows * 8; }
+// every worker, two slots each.
+int workers_of(int rows, int sms) { return sms * attn::paged_ctas(rows); }
+size_t part_o_bytes(int rows, int d, int sms) { return (size_t)workers_of(rows, sms) * 2 * rows * d * 4; }
+size_t part_ml_bytes(int rows, int sms) { return (size_t)workers_of(rows, sms) * 2 * rows * 8; }
 size_t part_bytes(int rows, int d, int sms) {
-  return part_o_bytes(rows, d, sms) + part_ml_bytes(rows, sms) + ((size_t)sms * 32 + 255) / 256 * 256;
+  return part_o_bytes(rows, d, sms) + part_ml_bytes(rows, sms) +
+         ((size_t)workers_of(rows, sms) * 32 + 255) / 256 * 256;
 }
 size_t workspace_bytes_for(bool wide, int d, int sms) {
   return wide ? part_bytes(16, d, sms) + part_bytes(attn::kPagedWideRows, d, sms) : part_bytes(8, d, sms);
@@ -202,11 +204,12 @@ attn_status attn_fwd_paged_fp8(const void* Q, long long q_stride, const void* k_
   pw.rows_min = kNarrowMost;
   pw.rows_max = 0x7fffffff;
   cudaError_t e = cudaSuccess;
-  if (big) e = attn::launch_paged_wide(d, tk, tv, pw, sms, cs);
-  if (e == cudaSuccess && small) e = attn::launch_paged_narrow(d, rows, tk, tv, p, sms, big, cs);
+  const int wide_rows = attn::kPagedWideRows, w1 = workers_of(rows, sms), w2 = workers_of(wide_rows, sms);
+  if (big) e = attn::launch_paged_wide(d, tk, tv, pw, w2, cs);
+  if (e == cudaSuccess && small) e = attn::launch_paged_narrow(d, rows, tk, tv, p, w1, big, cs);
   if (e == cudaSuccess)
-    e = small ? attn::launch_paged_merge(d, p, rows, big ? &pw : nullptr, attn::kPagedWideRows, sms, cs)
-              : attn::launch_paged_merge(d, pw, attn::kPagedWideRows, nullptr, 0, sms, cs);
+    e = small ? attn::launch_paged_merge(d, p, rows, w1, big ? &pw : nullptr, wide_rows, w2, cs)
+              : attn::launch_paged_merge(d, pw, wide_rows, w2, nullptr, 0, 0, cs);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

@@ -17,10 +17,9 @@
 // pipe mostly idle at HBM speed, and no accumulator leaves the registers.
 //
 // A CTA: a producer warp that walks its range and loads whole (page, head)
-// boxes by TMA into a ring of units, and sets of four consumer warps that take
-// the units in turn, 32 keys a warp.  Every warp keeps its own running
-// maximum, sum and accumulators of the item; they meet in shared memory at the
-// item's end.
+// boxes by TMA into a ring of units, and four consumer warps, 32 keys of a unit
+// each.  Every warp keeps its own running maximum, sum and accumulators of the
+// item; they meet in shared memory at the item's end.
 #include "paged.cuh"
 
 namespace attn {
@@ -38,16 +37,17 @@ struct UnitMeta {
   int pad[3];
 };
 
-// NB: eight-row blocks of a tile.  Three sets of four consumer warps for one
-// block; two, with half as many registers more, for two.
+// NB: eight-row blocks of a tile.  Three CTAs to an SM for one block, two, with
+// a third more registers, for two: they share nothing, so one's waits (the
+// ends of items, page ids, query rows) are the others' time.
 template <int D, int NB>
 struct PC {
   static constexpr int ROWS = 8 * NB;
-  static constexpr int SETS = NB == 1 ? 3 : 2;
-  static constexpr int WARPS = 4 * SETS;
-  static constexpr int HALF = 8 / NB;  // warps whose sums the exchange buffer holds
+  static constexpr int CTAS = NB == 1 ? 3 : 2;
+  static constexpr int WARPS = 4;      // consumer warps, 32 keys of a unit each
+  static constexpr int HALF = 2;       // warps whose sums the exchange buffer holds
   static constexpr int THREADS = 32 * (WARPS + 1);
-  static constexpr int STAGES = D == 128 ? 6 : 12;
+  static constexpr int STAGES = D == 128 ? 2 : 4;
   static constexpr int KBYTES = kUnit * D;
   static constexpr int SBYTES = 2 * KBYTES;
   static constexpr int OFF_RING = 0;
@@ -61,11 +61,8 @@ struct PC {
   static constexpr int B_GIVEN = B_IEMPTY + kItems, B_WRITTEN = B_GIVEN + 1, B_READ = B_GIVEN + 2;
   static constexpr int OFF_ABORT = OFF_BAR + (B_READ + 1) * 8;
   static constexpr int SMEM = OFF_ABORT + 8 + 1024;
-  static_assert(SMEM <= 232448, "shared memory");
-  // A parity names a phase only to a waiter that has seen every phase before
-  // it: all units of a stage have to go to the same set.
-  static_assert(STAGES % SETS == 0, "stages and sets");
-  static_assert(WARPS > HALF && WARPS - HALF <= HALF, "the other warps hand over to as many");
+  static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory");
+  static_assert(WARPS == 2 * HALF, "half of the warps hand over to the others");
   static_assert(kMaxGroups * 8 <= HALF * ROWS * D * 4, "the sums fit the exchange buffer");
 };
 
@@ -111,11 +108,11 @@ __device__ __forceinline__ uint32_t piece(uint32_t base, int row, int c) {
 }
 
 template <int D, int NB>
-__global__ void __launch_bounds__(PC<D, NB>::THREADS, 1)
+__global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
     fwd_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const PagedFwdParams p) {
   using C = PC<D, NB>;
-  constexpr int kRows = C::ROWS, kSets = C::SETS, kWarps = C::WARPS, kHalf = C::HALF;
+  constexpr int kRows = C::ROWS, kWarps = C::WARPS, kHalf = C::HALF;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
@@ -128,7 +125,7 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(bar(C::B_FULL + s), 1);
-      mbar_init(bar(C::B_EMPTY + s), 4);  // the warps of the set that took the unit
+      mbar_init(bar(C::B_EMPTY + s), kWarps);
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(bar(C::B_IFULL + i), 1);
@@ -152,7 +149,7 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, 1)
     }
     const int npg = kUnit >> p.page_log2;  // pages of a unit
     const uint32_t page_bytes = (uint32_t)D << p.page_log2;
-    int it = 0;         // units loaded
+    int it = 0, stage = 0, turn = 0;  // units loaded; place and round of the next in the ring
     int items_out = 0;  // items announced
     auto announce = [&](const Item& im) -> bool {
       const int i = items_out % kItems;
@@ -161,15 +158,23 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, 1)
         items[i] = im;
         mbar_arrive(bar(C::B_IFULL + i));
       }
+      // The item's query rows, on their way to L1 before the warps ask for them.
+      constexpr int LINES = D * 2 / 128;  // of a row
+      const int rows = min(kRows, im.n * p.G - im.tile * kRows);
+      for (int x = lane; x < rows * LINES; x += 32) {
+        const int rho = im.tile * kRows + x / LINES, tok = rho / p.G;
+        const uint16_t* q = p.Q + (long long)(im.start + tok) * p.q_stride +
+                            (long long)(im.h * p.G + rho - tok * p.G) * D + x % LINES * 64;
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(q));
+      }
       __syncwarp();
       ++items_out;
       return true;
     };
     bool ok = walk_range<kRows>(
-        p, sums, lane, [&](const Item& im, int) { return announce(im); },
-        [&](const Item& im, int, int id, float ks, float vs, int in_batch) -> bool {
-          const int s = it % C::STAGES;
-          if (it >= C::STAGES && !mbar_wait_warp(bar(C::B_EMPTY + s), ((it / C::STAGES) & 1) ^ 1, wc)) return false;
+        p, sums, lane, announce, [&](int h, int id, float ks, float vs, int in_batch) -> bool {
+          const int s = stage;
+          if (it >= C::STAGES && !mbar_wait_warp(bar(C::B_EMPTY + s), turn ^ 1, wc)) return false;
           const int my = __shfl_sync(0xffffffffu, id, in_batch + (lane & 7));
           const bool load = lane < npg && my >= 0;
           const uint32_t mask = __ballot_sync(0xffffffffu, load);
@@ -177,7 +182,7 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, 1)
           // the arrival below, which waits for the scales.
           if (load) {
             const uint32_t dst = sb + C::OFF_RING + s * C::SBYTES + lane * page_bytes;
-            const int plane = my * p.Hkv + im.h;
+            const int plane = my * p.Hkv + h;
             tma_load_3d(dst, &tmK, bar(C::B_FULL + s), 0, 0, plane);
             tma_load_3d(dst + C::KBYTES, &tmV, bar(C::B_FULL + s), 0, 0, plane);
           }
@@ -192,10 +197,14 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_expect_tx(bar(C::B_FULL + s), 2 * page_bytes * __popc(mask));
           ++it;
+          if (++stage == C::STAGES) {
+            stage = 0;
+            turn ^= 1;
+          }
           return true;
         });
     if (ok) {
-      Item im{};
+      Item im{};  // (no rows)
       im.count = -1;
       ok = announce(im);
     }
@@ -212,8 +221,8 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, 1)
 
   // -------------------------------------------------------------- consumers
   const int g = lane >> 2, c = lane & 3;
-  const int set = warp >> 2, part = 32 * (warp & 3);  // the units it takes, its keys in them
-  const int ko = key_of<D>(g);                        // its key as a row of the first product (and 8 more)
+  const int part = 32 * warp;   // its keys in a unit
+  const int ko = key_of<D>(g);  // its key as a row of the first product (and 8 more)
   const int kv0 = key_of<D>(2 * c), kv1 = key_of<D>(2 * c + 1);  // its keys as a column of the second
   const int cg = D == 128 ? (g >> 1) | ((g & 1) << 2) : g >> 1;  // its 16-byte piece of a V row
   constexpr int QI = D / 64;   // 64-column parts of the contraction over d
@@ -229,6 +238,7 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, 1)
   const uint32_t koff = piece<D>(0, part + ko, c);
   const uint32_t voff0 = piece<D>(0, part + kv0, cg) + (D == 64 ? 8 * (g & 1) : 0);
   const uint32_t voff1 = piece<D>(0, part + kv1, cg) + (D == 64 ? 8 * (g & 1) : 0);
+  int stage = 0, turn = 0;  // place and round of the next unit in the ring
   for (int i = 0;; ++i) {
     if (!mbar_wait_warp(bar(C::B_IFULL + i % kItems), (i / kItems) & 1, wc)) return;
     const Item* im = items + i % kItems;
@@ -286,12 +296,10 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, 1)
       for (int j = 0; j < MT; ++j) o[b][j][0] = o[b][j][1] = o[b][j][2] = o[b][j][3] = 0.f;
     }
     vref = 0.f;
-    const int first = im->first;
-    int u = first + (set + kSets - first % kSets) % kSets;
-    for (; u < first + count; u += kSets) {
-      const int s = u % C::STAGES;
-      if (!mbar_wait_warp(bar(C::B_FULL + s), (u / C::STAGES) & 1, wc)) return;
-      const int key0 = (im->k0 + u - first) * kUnit + part;
+    int key0 = im->k0 * kUnit + part;
+    for (int u = 0; u < count; ++u, key0 += kUnit) {
+      const int s = stage;
+      if (!mbar_wait_warp(bar(C::B_FULL + s), turn, wc)) return;
       const UnitMeta* mt = metas + s;
       const int pa = part >> p.page_log2, pb = (part + 16) >> p.page_log2;  // pages of its two 16 keys
       const bool la = (mt->pages >> pa) & 1, lb = (mt->pages >> pb) & 1;
@@ -417,6 +425,10 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(C::B_EMPTY + s));
+      if (++stage == C::STAGES) {
+        stage = 0;
+        turn ^= 1;
+      }
     }
 
     // The item's end: the warps' sums meet in shared memory.
@@ -436,9 +448,10 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, 1)
       const int x = D == 128 ? c2 | ((q4 >> 4) << 2) : (c2 & 1) | ((c2 >> 1) << 2);
       return (w_ * kRows + row) * (D / 4) + (q4 ^ x);
     };
+    // The last item's sums have been read.
+    if (i > 0 && !mbar_wait_warp(bar(C::B_READ), (i - 1) & 1, wc)) return;
     if (warp >= kHalf) {
-      // Hand over to warp - kHalf, lane by lane, once the last item's sums have been read.
-      if (i > 0 && !mbar_wait_warp(bar(C::B_READ), (i - 1) & 1, wc)) return;
+      // Hand over to warp - kHalf, lane by lane.
       float4* to = so + (warp - kHalf) * kRows * (D / 4) + lane;
 #pragma unroll
       for (int b = 0; b < NB; ++b)
@@ -461,26 +474,23 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, 1)
     }
     const int slot = im->slot;
     if (!mbar_wait_warp(bar(C::B_GIVEN), i & 1, wc)) return;
-    const bool takes = warp < kWarps - kHalf;
     const float4* from = so + warp * kRows * (D / 4) + lane;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      float wa[2] = {back, back}, wb[2] = {0.f, 0.f};
-      if (takes) {
+      float wa[2], wb[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float2 gv = ml[warp * kRows + 8 * b + 2 * c + e];
-          const float mn = fmaxf(m[b][e], gv.x), r = mn == -INFINITY ? 0.f : mn;
-          const float x = ex2(m[b][e] - r);
-          wb[e] = ex2(gv.x - r);
-          wa[e] = back * x;
-          l[b][e] = l[b][e] * x + gv.y * wb[e];
-          m[b][e] = mn;
-        }
+      for (int e = 0; e < 2; ++e) {
+        const float2 gv = ml[warp * kRows + 8 * b + 2 * c + e];
+        const float mn = fmaxf(m[b][e], gv.x), r = mn == -INFINITY ? 0.f : mn;
+        const float x = ex2(m[b][e] - r);
+        wb[e] = ex2(gv.x - r);
+        wa[e] = back * x;
+        l[b][e] = l[b][e] * x + gv.y * wb[e];
+        m[b][e] = mn;
       }
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
-        const float4 v = takes ? from[32 * (b * MT + j)] : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 v = from[32 * (b * MT + j)];
         o[b][j][0] = fmaf(o[b][j][0], wa[0], v.x * wb[0]);
         o[b][j][1] = fmaf(o[b][j][1], wa[1], v.y * wb[1]);
         o[b][j][2] = fmaf(o[b][j][2], wa[0], v.z * wb[0]);
@@ -545,8 +555,6 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, 1)
       mbar_arrive(bar(C::B_READ));
       mbar_arrive(bar(C::B_IEMPTY + i % kItems));
     }
-    // The next item's writes come after all of these reads.
-    if (!mbar_wait_warp(bar(C::B_READ), i & 1, wc)) return;
   }
 }
 
@@ -558,6 +566,7 @@ template <int D, int NB>
 cudaError_t launch_narrow(const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedFwdParams& p, int workers,
                           bool behind, cudaStream_t stream) {
   using C = PC<D, NB>;
+  static_assert(C::CTAS == paged_ctas(C::ROWS), "workers of an SM");
   return launch_workers<D * 2 + NB>(fwd_paged_kernel<D, NB>, C::THREADS, C::SMEM, tmK, tmV, p, workers, behind, stream);
 }
 

@@ -4,8 +4,9 @@
 // Worker w's descriptor names the item that begins in its range and goes on in
 // the next parts - 1 workers': with M = max_s m_s,
 //   l = sum_s 2^{m_s - M} l_s,  O = sum_s 2^{m_s - M} O_s / l.
-// Latency bound: launched so that its start overlaps the kernel's end.  A warp
-// per row, kMergeCtas CTAs of four warps to an item.
+// Latency bound: launched so that its start overlaps the kernel's end.  Of a
+// small tile a CTA takes a row at a time, its eight warps the parts in turn (a
+// long context cut over all workers has dozens); of a large one a warp does.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -15,13 +16,14 @@ namespace {
 
 using namespace paged;
 
-constexpr int kMergeCtas = 8;
+constexpr int kMergeCtas = 8;   // of an item
+constexpr int kMergeWarps = 8;
 
 struct MergeSet {
   const float* part_o;
   const float* part_ml;
   const int* desc;
-  int rows;
+  int rows, workers;
 };
 struct MergeParams {
   MergeSet set[2];
@@ -29,72 +31,89 @@ struct MergeParams {
 };
 
 template <int D>
-__global__ void __launch_bounds__(128) paged_merge_kernel(const MergeParams q) {
+__global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const MergeParams q) {
+  constexpr int V = D / 32;  // columns of a lane
+  __shared__ float s_acc[kMergeWarps][D], s_l[kMergeWarps];
   griddep_wait();
   const MergeSet& t = q.set[blockIdx.z];
   const PagedFwdParams& p = q.p;
   const int w = blockIdx.x;
+  if (w >= t.workers) return;
   const int* d = t.desc + w * 8;
   const int parts = d[0];
   if (parts < 2) return;
   const int start = d[1], n = d[2], tile = d[3], h = d[4];
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = min(t.rows, n * p.G - tile * t.rows);
-  for (int row = blockIdx.y * 4 + (threadIdx.x >> 5); row < rows; row += 4 * gridDim.y) {
+  // Warps that share a row, and this one's number among them.
+  const int team = t.rows > 16 ? 1 : kMergeWarps, mate = warp % team;
+  const int step = gridDim.y * (kMergeWarps / team);
+  const int rounds = (rows + step - 1) / step;
+  for (int i = 0; i < rounds; ++i) {
+    const int row = i * step + blockIdx.y * (kMergeWarps / team) + warp / team;
+    if (row >= rows) break;  // (a whole team)
     auto part = [&](int s) -> size_t { return (size_t)(s == 0 ? 2 * w + 1 : 2 * (w + s)) * t.rows + row; };
-    constexpr int V = D / 32;  // columns of a lane
     float M = -INFINITY;
     for (int s = lane; s < parts; s += 32) M = fmaxf(M, t.part_ml[part(s) * 2]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     const float ref = M == -INFINITY ? 0.f : M;
     float L = 0.f, acc[V] = {};
-    for (int s0 = 0; s0 < parts; s0 += 32) {
-      float wl = 0.f;
-      if (s0 + lane < parts) {
-        const float2 ml = *reinterpret_cast<const float2*>(t.part_ml + part(s0 + lane) * 2);
-        wl = ex2(ml.x - ref);
-        L += wl * ml.y;
-      }
-      const int cnt = min(32, parts - s0);
 #pragma unroll 4
-      for (int s = 0; s < cnt; ++s) {
-        const float wgt = __shfl_sync(0xffffffffu, wl, s);
-        const float* src = t.part_o + part(s0 + s) * D + lane * V;
+    for (int s = mate; s < parts; s += team) {
+      const float2 ml = *reinterpret_cast<const float2*>(t.part_ml + part(s) * 2);
+      const float wgt = ex2(ml.x - ref);
+      L += wgt * ml.y;
+      const float* src = t.part_o + part(s) * D + lane * V;
 #pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] += wgt * src[v];
-      }
+      for (int v = 0; v < V; ++v) acc[v] += wgt * src[v];
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     const size_t orow = output_row(p, start, h, tile * t.rows + row);
-    const float inv = output_factor(L);
+    // Columns c, c + 1 of the row.
+    auto put = [&](int c, float x, float y, float inv) {
+      if (p.out_f32)
+        *reinterpret_cast<float2*>(static_cast<float*>(p.O) + orow * D + c) = make_float2(x * inv, y * inv);
+      else
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.O) + orow * D + c) = pack_bf16(x * inv, y * inv);
+    };
+    if (team == 1) {
 #pragma unroll
-    for (int v = 0; v < V; v += 2) {
-      if (p.out_f32) {
-        float* dst = static_cast<float*>(p.O) + orow * D + lane * V + v;
-        dst[0] = acc[v] * inv;
-        dst[1] = acc[v + 1] * inv;
-      } else {
-        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.O) + orow * D + lane * V + v) =
-            pack_bf16(acc[v] * inv, acc[v + 1] * inv);
-      }
+      for (int v = 0; v < V; v += 2) put(lane * V + v, acc[v], acc[v + 1], output_factor(L));
+      if (lane == 0) p.LSE[orow] = output_lse(M, L);
+      continue;
     }
-    if (lane == 0) p.LSE[orow] = output_lse(M, L);
+#pragma unroll
+    for (int v = 0; v < V; ++v) s_acc[warp][lane * V + v] = acc[v];
+    if (lane == 0) s_l[warp] = L;
+    __syncthreads();
+    if (threadIdx.x < D / 2) {
+      const int c = 2 * threadIdx.x;
+      float x = 0.f, y = 0.f;
+      L = 0.f;
+#pragma unroll
+      for (int j = 0; j < kMergeWarps; ++j) {
+        x += s_acc[j][c];
+        y += s_acc[j][c + 1];
+        L += s_l[j];
+      }
+      put(c, x, y, output_factor(L));
+      if (c == 0) p.LSE[orow] = output_lse(M, L);
+    }
+    __syncthreads();
   }
 }
 
 }  // namespace
 
-cudaError_t launch_paged_merge(int d, const PagedFwdParams& p, int rows, const PagedFwdParams* p2, int rows2,
-                               int workers, cudaStream_t stream) {
+cudaError_t launch_paged_merge(int d, const PagedFwdParams& p, int rows, int workers, const PagedFwdParams* p2,
+                               int rows2, int workers2, cudaStream_t stream) {
   MergeParams q{};
   q.p = p;
-  q.set[0] = {p.part_o, p.part_ml, p.desc, rows};
-  if (p2) q.set[1] = {p2->part_o, p2->part_ml, p2->desc, rows2};
+  q.set[0] = {p.part_o, p.part_ml, p.desc, rows, workers};
+  if (p2) q.set[1] = {p2->part_o, p2->part_ml, p2->desc, rows2, workers2};
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)workers, (unsigned)std::min(std::max(rows, p2 ? rows2 : 0) / 4, kMergeCtas), p2 ? 2u : 1u);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3((unsigned)std::max(workers, p2 ? workers2 : 0), (unsigned)(p2 || rows > 8 ? kMergeCtas : kMergeCtas / 2), p2 ? 2u : 1u);
+  cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.stream = stream;
   cudaLaunchAttribute at{};
   overlap_with_previous(cfg, at);

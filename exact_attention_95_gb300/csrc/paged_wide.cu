@@ -223,13 +223,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       bool ok = walk_range<kPagedWideRows>(
-          p, sums, lane, [&](const Item& im, int) { return announce(im); },
-          [&](const Item& im, int, int id, float ks, float vs, int in_batch) -> bool {
+          p, sums, lane, announce, [&](int h, int id, float ks, float vs, int in_batch) -> bool {
             const int my = __shfl_sync(0xffffffffu, id, in_batch + (lane & 7));
             const bool load = lane < npg && my >= 0;
             const uint32_t mask = __ballot_sync(0xffffffffu, load);
             const uint32_t bytes = page_bytes * __popc(mask);
-            const int plane = my * p.Hkv + im.h;
+            const int plane = my * p.Hkv + h;
             if (!reuse(C::B_KEMPTY, u, C::KS)) return false;
             const int sk = u % C::KS;
             if (load) tma_load_3d(sb + C::OFF_K + sk * C::T8 + lane * page_bytes, &tmK, bar(C::B_KFULL + sk), 0, 0, plane);
