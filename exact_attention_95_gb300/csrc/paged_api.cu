@@ -43,7 +43,7 @@ bool token_stride_ok(long long stride, long long heads, int d) { return stride >
 // alone, whatever the requests' rows are: a launch for wider ones would find
 // nothing to do.  Any other call runs the 16-row kernel for the requests with
 // up to kNarrowMost query rows of a kv head and the 256-row kernel for the rest.
-constexpr int kNarrowMost = 48;
+constexpr int kNarrowMost = 16;
 bool runs_wide(int R, int T, int G) { return T > R || G > 8; }
 // Workspace: partial sums (O, then maxima and sums, then merge descriptors) of
 // every worker, two slots each.
@@ -208,7 +208,7 @@ attn_status attn_fwd_paged_fp8(const void* Q, long long q_stride, const void* k_
   if (big) e = attn::launch_paged_wide(d, tk, tv, pw, w2, cs);
   if (e == cudaSuccess && small) e = attn::launch_paged_narrow(d, rows, tk, tv, p, w1, big, cs);
   if (e == cudaSuccess)
-    e = small ? attn::launch_paged_merge(d, p, rows, w1, big ? &pw : nullptr, wide_rows, w2, cs)
+    e = small ? attn::launch_paged_merge(d, p, rows, w1, big ? &pw : nullptr, wide_rows, big ? w2 : 0, cs)
               : attn::launch_paged_merge(d, pw, wide_rows, w2, nullptr, 0, 0, cs);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }

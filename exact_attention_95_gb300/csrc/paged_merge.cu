@@ -4,11 +4,9 @@
 // Worker w's descriptor names the item that begins in its range and goes on in
 // the next parts - 1 workers': with M = max_s m_s,
 //   l = sum_s 2^{m_s - M} l_s,  O = sum_s 2^{m_s - M} O_s / l.
-// Latency bound: launched so that its start overlaps the kernel's end.  Of a
-// small tile a CTA takes a row at a time, its eight warps the parts in turn (a
-// long context cut over all workers has dozens); of a large one a warp does.
-#include <algorithm>
-
+// Latency bound: launched so that its start overlaps the kernel's end.  Of an
+// item in many parts (a long context cut over all workers has dozens) a CTA
+// takes a row at a time, its eight warps the parts in turn; else a warp does.
 #include "paged.cuh"
 
 namespace attn {
@@ -16,7 +14,7 @@ namespace {
 
 using namespace paged;
 
-constexpr int kMergeCtas = 8;   // of an item
+constexpr int kMergeCtas = 4;   // of an item
 constexpr int kMergeWarps = 8;
 
 struct MergeSet {
@@ -35,10 +33,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Mer
   constexpr int V = D / 32;  // columns of a lane
   __shared__ float s_acc[kMergeWarps][D], s_l[kMergeWarps];
   griddep_wait();
-  const MergeSet& t = q.set[blockIdx.z];
+  const bool second = (int)blockIdx.x >= q.set[0].workers;
+  const MergeSet& t = q.set[second];
   const PagedFwdParams& p = q.p;
-  const int w = blockIdx.x;
-  if (w >= t.workers) return;
+  const int w = blockIdx.x - (second ? q.set[0].workers : 0);
   const int* d = t.desc + w * 8;
   const int parts = d[0];
   if (parts < 2) return;
@@ -46,7 +44,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Mer
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = min(t.rows, n * p.G - tile * t.rows);
   // Warps that share a row, and this one's number among them.
-  const int team = t.rows > 16 ? 1 : kMergeWarps, mate = warp % team;
+  const int team = parts > 2 * kMergeWarps ? kMergeWarps : 1, mate = warp % team;
   const int step = gridDim.y * (kMergeWarps / team);
   const int rounds = (rows + step - 1) / step;
   for (int i = 0; i < rounds; ++i) {
@@ -112,7 +110,7 @@ cudaError_t launch_paged_merge(int d, const PagedFwdParams& p, int rows, int wor
   q.set[0] = {p.part_o, p.part_ml, p.desc, rows, workers};
   if (p2) q.set[1] = {p2->part_o, p2->part_ml, p2->desc, rows2, workers2};
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)std::max(workers, p2 ? workers2 : 0), (unsigned)(p2 || rows > 8 ? kMergeCtas : kMergeCtas / 2), p2 ? 2u : 1u);
+  cfg.gridDim = dim3((unsigned)(workers + workers2), kMergeCtas);
   cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.stream = stream;
   cudaLaunchAttribute at{};

@@ -344,6 +344,10 @@ ATTENTION = [
     ([2100, 300], [1, 1], 32, 2, 128, 64, True),        # 16 heads a kv head, one token
     ([128, 129, 127], [128, 129, 127], 2, 2, 64, 128, True),
     ([200], [257], 1, 1, 128, 16, True),
+    ([5000, 128, 300], [6, 5, 9], 32, 8, 128, 32, True),  # 17 to 128 rows
+    ([5000, 128, 300], [30, 31, 32], 8, 2, 64, 64, True),
+    ([700, 900], [100, 128], 1, 1, 128, 16, False),
+    ([700, 900, 20], [128, 129, 100], 2, 2, 64, 16, True),
 ]
 
 
