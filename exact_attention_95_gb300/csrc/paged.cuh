@@ -20,6 +20,7 @@ namespace attn {
 namespace paged {
 
 constexpr int kUnit = 128;       // keys of a unit
+
 constexpr int kMaxGroups = 512;  // 32 requests each
 
 // An item, or the part of it that a worker has.
@@ -64,6 +65,7 @@ __device__ __forceinline__ Req load_req(const PagedFwdParams& p, int r) {
 template <int ROWS>
 __device__ __forceinline__ void sum_units(const PagedFwdParams& p, long long* sums, int warp, int warps, int lane) {
   if (p.R <= 32) return;
+#pragma unroll 1
   for (int g = warp; g < (p.R + 31) >> 5; g += warps) {
     long long u = load_req<ROWS>(p, g * 32 + lane).units;
 #pragma unroll
@@ -77,9 +79,9 @@ __device__ __forceinline__ int key_limit(const PagedFwdParams& p, int len, int n
   return p.causal ? max(0, min(len, len - n + tok + 1)) : len;
 }
 
-// a / b for non-negative a; units rarely need more than 32 bits.
-__device__ __forceinline__ long long divide(long long a, int b) {
-  return (a >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+// a / b for non-negative a and b > 0; units rarely need more than 32 bits.
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // Up to 32 pages of an item: the units whose page ids and scales a warp holds
@@ -114,6 +116,7 @@ struct Walker {
     long long total = 0;
     if (groups == 1) total = rq.units;
     else
+  #pragma unroll 1
       for (int i = lane; i < groups; i += 32) total += sums[i];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -126,6 +129,7 @@ struct Walker {
     if (pos >= end) return;
     // The group, then the request, that holds unit `pos`.
     long long before = 0;
+#pragma unroll 1
     while (g + 1 < groups && before + sums[g] <= pos) before += sums[g++];
     if (g > 0) rq = load_req<ROWS>(p, g * 32 + lane);
     long long incl = rq.units;
@@ -165,7 +169,7 @@ struct Walker {
     im.slot = k0 == 0 && k1 == kt ? -1 : k0 == 0 ? 1 : 0;
     if (im.slot == 1) {
       const long long last = pos + kt - 1;  // the item's last unit
-      merge_parts = (int)((per >> 31) == 0 ? divide(last, (int)per) : last / per) - (int)blockIdx.x + 1;
+      merge_parts = (int)divide(last, per) - (int)blockIdx.x + 1;
       merge_start = im.start;
       merge_n = im.n;
       merge_tile = im.tile;
@@ -188,6 +192,7 @@ struct Walker {
       if (off >= units) {
         // The next request that has units.
         uint32_t more = __ballot_sync(0xffffffffu, rq.units > 0) & ~(0xffffffffu >> (31 - l));
+#pragma unroll 1
         while (!more && g + 1 < groups) {
           ++g;
           rq = load_req<ROWS>(p, g * 32 + lane);
@@ -270,13 +275,16 @@ __device__ __forceinline__ bool walk_range(const PagedFwdParams& p, const long l
     }
   };
   const int npg_log2 = 7 - p.page_log2;
-  Held cur = take();
-  scales(cur);
-  Held nxt = take();
-  while (cur.any && ok) {
+  // (One place for each step: the code of a walk is long, and instructions are
+  // fetched too.)
+  Held cur, nxt;
+#pragma unroll 1
+  for (;;) {
     scales(nxt);
     const Held then = take();
+#pragma unroll 1
     for (int j = 0; j < cur.units && ok; ++j) ok = unit_fn(cur.h, cur.id, cur.ks, cur.vs, j << npg_log2);
+    if (!ok || !(nxt.any || then.any)) break;
     cur = nxt;
     nxt = then;
   }

@@ -43,7 +43,7 @@ bool token_stride_ok(long long stride, long long heads, int d) { return stride >
 // alone, whatever the requests' rows are: a launch for wider ones would find
 // nothing to do.  Any other call runs the 16-row kernel for the requests with
 // up to kNarrowMost query rows of a kv head and the 256-row kernel for the rest.
-constexpr int kNarrowMost = 16;
+constexpr int kNarrowMost = 48;
 bool runs_wide(int R, int T, int G) { return T > R || G > 8; }
 // Workspace: partial sums (O, then maxima and sums, then merge descriptors) of
 // every worker, two slots each.

@@ -30,6 +30,42 @@ using namespace paged;
 constexpr int kItems = 4;          // items announced ahead
 constexpr float kPScale = 16384.f;
 
+// Bounded waits of this kernel.  As mbar_wait (ptx.cuh), but with all that
+// is not the try itself in a function of its own, called every kTries tries:
+// written out at each of some thirty waits it would be half of the code.
+constexpr uint32_t kTries = 1024;
+struct Waits {
+  volatile int* abort_flag;            // shared: a wait of the CTA gave up
+  volatile unsigned long long* since;  // shared, this warp's: when the wait at hand was first looked at
+  int* status;
+  unsigned long long limit_ns;
+};
+__device__ __noinline__ bool give_up(volatile int* abort_flag, volatile unsigned long long* since, int* status,
+                                     unsigned long long limit_ns, uint32_t tries) {
+  if (*abort_flag) return true;
+  const unsigned long long now = globaltimer_ns();
+  if (tries == kTries) *since = now;
+  else if (now - *since > limit_ns) {
+    *abort_flag = 1;
+    atomicCAS(status, kDevOk, kDevTimeout);
+    return true;
+  }
+  return false;
+}
+// By a whole warp, with one result.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Waits& w) {
+  uint32_t tries = 0;
+  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+    if ((++tries & (kTries - 1)) == 0 &&
+        __any_sync(0xffffffffu, give_up(w.abort_flag, w.since, w.status, w.limit_ns, tries)))
+      return false;
+  return true;
+}
+// The same for copies and products in flight, which have to land whatever else gave up.
+__device__ __noinline__ void drain_bar(uint32_t bar, uint32_t parity, const Waits& w) {
+  const WaitCtx c{w.abort_flag, w.status, w.limit_ns};
+  mbar_wait_drain_warp(bar, parity, c);
+}
 // What a unit's stage holds besides the codes.
 struct UnitMeta {
   float ks[8], vs[8];  // scales of its pages
@@ -59,7 +95,8 @@ struct PC {
   static constexpr int OFF_BAR = OFF_META + STAGES * (int)sizeof(UnitMeta);
   static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_IFULL = 2 * STAGES, B_IEMPTY = B_IFULL + kItems;
   static constexpr int B_GIVEN = B_IEMPTY + kItems, B_WRITTEN = B_GIVEN + 1, B_READ = B_GIVEN + 2;
-  static constexpr int OFF_ABORT = OFF_BAR + (B_READ + 1) * 8;
+  static constexpr int OFF_SINCE = OFF_BAR + (B_READ + 1) * 8;  // of each warp
+  static constexpr int OFF_ABORT = OFF_SINCE + (WARPS + 1) * 8;
   static constexpr int SMEM = OFF_ABORT + 8 + 1024;
   static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory");
   static_assert(WARPS == 2 * HALF, "half of the warps hand over to the others");
@@ -139,7 +176,7 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
   }
   sum_units<kRows>(p, sums, warp, kWarps + 1, lane);
   __syncthreads();
-  const WaitCtx wc{abort_flag, p.status, p.wait_limit_ns};
+  const Waits wc{abort_flag, reinterpret_cast<unsigned long long*>(smem + C::OFF_SINCE) + warp, p.status, p.wait_limit_ns};
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ producer
@@ -153,7 +190,7 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
     int items_out = 0;  // items announced
     auto announce = [&](const Item& im) -> bool {
       const int i = items_out % kItems;
-      if (items_out >= kItems && !mbar_wait_warp(bar(C::B_IEMPTY + i), ((items_out / kItems) & 1) ^ 1, wc)) return false;
+      if (items_out >= kItems && !wait_bar(bar(C::B_IEMPTY + i), ((items_out / kItems) & 1) ^ 1, wc)) return false;
       if (lane == 0) {
         items[i] = im;
         mbar_arrive(bar(C::B_IFULL + i));
@@ -161,6 +198,7 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
       // The item's query rows, on their way to L1 before the warps ask for them.
       constexpr int LINES = D * 2 / 128;  // of a row
       const int rows = min(kRows, im.n * p.G - im.tile * kRows);
+#pragma unroll 1
       for (int x = lane; x < rows * LINES; x += 32) {
         const int rho = im.tile * kRows + x / LINES, tok = rho / p.G;
         const uint16_t* q = p.Q + (long long)(im.start + tok) * p.q_stride +
@@ -174,7 +212,7 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
     bool ok = walk_range<kRows>(
         p, sums, lane, announce, [&](int h, int id, float ks, float vs, int in_batch) -> bool {
           const int s = stage;
-          if (it >= C::STAGES && !mbar_wait_warp(bar(C::B_EMPTY + s), turn ^ 1, wc)) return false;
+          if (it >= C::STAGES && !wait_bar(bar(C::B_EMPTY + s), turn ^ 1, wc)) return false;
           const int my = __shfl_sync(0xffffffffu, id, in_batch + (lane & 7));
           const bool load = lane < npg && my >= 0;
           const uint32_t mask = __ballot_sync(0xffffffffu, load);
@@ -212,7 +250,7 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
     // for all of them unless a wait gave up).
     if (!ok)
       for (int k = max(0, it - C::STAGES); k < it; ++k)
-        mbar_wait_drain_warp(bar(C::B_FULL + k % C::STAGES), (k / C::STAGES) & 1, wc);
+        drain_bar(bar(C::B_FULL + k % C::STAGES), (k / C::STAGES) & 1, wc);
     griddep_launch_dependents();
     // Behind the wide kernel: this one's completion stands for both.
     griddep_wait();
@@ -239,8 +277,9 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
   const uint32_t voff0 = piece<D>(0, part + kv0, cg) + (D == 64 ? 8 * (g & 1) : 0);
   const uint32_t voff1 = piece<D>(0, part + kv1, cg) + (D == 64 ? 8 * (g & 1) : 0);
   int stage = 0, turn = 0;  // place and round of the next unit in the ring
+#pragma unroll 1
   for (int i = 0;; ++i) {
-    if (!mbar_wait_warp(bar(C::B_IFULL + i % kItems), (i / kItems) & 1, wc)) return;
+    if (!wait_bar(bar(C::B_IFULL + i % kItems), (i / kItems) & 1, wc)) return;
     const Item* im = items + i % kItems;
     const int count = im->count;
     if (count < 0) return;
@@ -297,9 +336,10 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
     }
     vref = 0.f;
     int key0 = im->k0 * kUnit + part;
+#pragma unroll 1
     for (int u = 0; u < count; ++u, key0 += kUnit) {
       const int s = stage;
-      if (!mbar_wait_warp(bar(C::B_FULL + s), turn, wc)) return;
+      if (!wait_bar(bar(C::B_FULL + s), turn, wc)) return;
       const UnitMeta* mt = metas + s;
       const int pa = part >> p.page_log2, pb = (part + 16) >> p.page_log2;  // pages of its two 16 keys
       const bool la = (mt->pages >> pa) & 1, lb = (mt->pages >> pb) & 1;
@@ -449,7 +489,7 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
       return (w_ * kRows + row) * (D / 4) + (q4 ^ x);
     };
     // The last item's sums have been read.
-    if (i > 0 && !mbar_wait_warp(bar(C::B_READ), (i - 1) & 1, wc)) return;
+    if (i > 0 && !wait_bar(bar(C::B_READ), (i - 1) & 1, wc)) return;
     if (warp >= kHalf) {
       // Hand over to warp - kHalf, lane by lane.
       float4* to = so + (warp - kHalf) * kRows * (D / 4) + lane;
@@ -473,7 +513,7 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
       continue;
     }
     const int slot = im->slot;
-    if (!mbar_wait_warp(bar(C::B_GIVEN), i & 1, wc)) return;
+    if (!wait_bar(bar(C::B_GIVEN), i & 1, wc)) return;
     const float4* from = so + warp * kRows * (D / 4) + lane;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
@@ -514,7 +554,8 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
               make_float4(o[b][2 * x][e], o[b][2 * x][2 + e], o[b][2 * x + 1][e], o[b][2 * x + 1][2 + e]);
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(C::B_WRITTEN));
-    if (!mbar_wait_warp(bar(C::B_WRITTEN), i & 1, wc)) return;
+    if (!wait_bar(bar(C::B_WRITTEN), i & 1, wc)) return;
+#pragma unroll 1
     for (int x = threadIdx.x; x < rows * (D / 4); x += 32 * kHalf) {
       const int row = x / (D / 4), q4 = x % (D / 4);
       float M = -INFINITY;

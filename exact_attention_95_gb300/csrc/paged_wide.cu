@@ -15,24 +15,15 @@
 //      P is not split into 8-bit terms: below 2^-18 of the row's largest
 //      weight they hold nothing, and the tail behind one dominant key is lost.
 //
-// Two row tiles (256 rows) to an item share every unit.  An item with up to 128
-// rows is taken by both tiles instead, one the even units and one the odd, with
-// the same Q; their sums meet in TMEM, where both tiles' warps reach the same
-// lanes.  A tile's units follow one another (S, the rows' softmax, P V, the next
-// S); the tiles are independent, so one's products run during the other's
-// softmax.
-//
-// Roles (16 warps):
+// Two row tiles (256 rows) to an item share every unit.  Roles (16 warps):
 //   warp 0       producer: walks the range, loads page boxes (TMA).
 //   warps 1, 2   MMA issuers of row tile 0 and 1 (as in fwd_persist.cu).
 //   warp 3       idle.
 //   warps 4-7    widen V: 8-bit tile -> f16 tile, 64-column blocks.
 //   warps 8-11, 12-15  softmax and epilogue of tile 0, 1; a thread is a row.
-// TMEM (512 columns): S_t 128 columns each, over whose first 64 P_t is written;
-// O_t d columns each.  The products of a CTA run in the order of their issue:
-// once S(j) is there P(j - 1) has been used, and S(j + 1) cannot overtake P(j).
-// The softmax reads S twice, 64 columns at a time in loops: held in registers
-// and unrolled it is twice the code, and the warps wait for instructions.
+// TMEM (512 columns): S [0, 128) shared by the tiles in turn, P_t 64 columns
+// each, O_t d columns each.  A tile without rows takes part in every hand-off
+// and skips the work.
 #include "paged.cuh"
 
 namespace attn {
@@ -92,18 +83,17 @@ struct WC {
   static constexpr int B_IEMPTY = B_IFULL + kItems;
   static constexpr int B_QFULL = B_IEMPTY + kItems;  // 2
   static constexpr int B_SFULL = B_QFULL + 2;        // 2
-  static constexpr int B_PFULL = B_SFULL + 2;        // 2
+  static constexpr int B_SREAD = B_SFULL + 2;        // 2
+  static constexpr int B_PFULL = B_SREAD + 2;        // 2
   static constexpr int B_ODONE = B_PFULL + 2;        // 2
   static constexpr int B_DRAIN = B_ODONE + 2;        // 2
-  static constexpr int B_GIVEN = B_DRAIN + 2;        // tile 1's sums of a shared item are in TMEM
-  static constexpr int B_READ = B_GIVEN + 1;         // and have been read
-  static constexpr int OFF_TMEMSLOT = OFF_BAR + (B_READ + 1) * 8;
+  static constexpr int OFF_TMEMSLOT = OFF_BAR + (B_DRAIN + 2) * 8;
   static constexpr int OFF_ABORT = OFF_TMEMSLOT + 4;
   static constexpr int SMEM = OFF_ABORT + 4 + 1024;
   static constexpr uint32_t IDESC_S = idesc_e4m3(kBM, kUnit);
   // f16 A and B (format 0), fp32 sums, B as V's rows (MN-major).
   static constexpr uint32_t IDESC_O = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
-  static constexpr uint32_t TM_S = 0, TM_O = 256;  // + 128 t, + D t
+  static constexpr uint32_t TM_S = 0, TM_P = 128, TM_O = 256;
 };
 static_assert(WC<128>::SMEM <= 232448 && WC<64>::SMEM <= 232448, "shared memory");
 static_assert(kMaxGroups * 8 <= WC<64>::WS * WC<64>::T16, "the sums fit the widened tiles");
@@ -138,24 +128,6 @@ __device__ __forceinline__ void values4(uint32_t c, float (&x)[4]) {
         : "=f"(x[2 * k]), "=f"(x[2 * k + 1])
         : "r"(widen(c >> (16 * k))));
 }
-
-// Four 32-bit columns of a warp's TMEM lanes.
-__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3])
-               : "memory");
-}
-__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3])::"memory");
-}
-// Query rows of an item, and whether its tiles share them.
-__device__ __forceinline__ int item_rows(const PagedFwdParams& p, const Item* im) {
-  return min(kPagedWideRows, im->n * p.G - im->tile * kPagedWideRows);
-}
-__device__ __forceinline__ bool item_shared(int rows) { return rows <= kBM; }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -203,12 +175,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(C::B_QFULL + t), 4);
       mbar_init(bar(C::B_SFULL + t), 1);
+      mbar_init(bar(C::B_SREAD + t), 4);
       mbar_init(bar(C::B_PFULL + t), 4);
       mbar_init(bar(C::B_ODONE + t), 1);
       mbar_init(bar(C::B_DRAIN + t), 1);
     }
-    mbar_init(bar(C::B_GIVEN), 4);
-    mbar_init(bar(C::B_READ), 4);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -303,67 +274,74 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t = warp - 1;
       int u0 = 0;  // units before the item
       int qn = 0;  // items with units
+      int ns = 0;  // S products of this tile issued
       int pf = 0;  // P_t hand-offs waited for
       bool ok = true;
       for (int i = 0; ok; ++i) {
         if (!wait_item(i)) break;
         const Item* im = items + i % kItems;
         const int n = im->count;
-        const bool shared = item_shared(item_rows(p, im));
+        const bool live = im->n * p.G - im->tile * kPagedWideRows > t * kBM;
         release_item(i);
         if (n < 0) break;
         if (n == 0) continue;
         auto wait_ring = [&](int b, int k, int ring) -> bool {
-          return mbar_wait_warp(bar(b + k % ring), (k / ring) & 1, wc);
-        };
-        // Of a shared item the other tile's units pass by here: they are
-        // released for this tile once they are there, in the order of the
-        // units, but no earlier than this tile needs the next.
-        auto pass = [&](int full, int empty, int ring, int v) -> bool {
-          if (v < 0 || v >= n) return true;
-          if (!wait_ring(full, u0 + v, ring)) return false;
-          release(empty + (u0 + v) % ring);
+          if (!mbar_wait_warp(bar(b + k % ring), (k / ring) & 1, wc)) return false;
+          tc_fence_after();
           return true;
         };
-        ok = mbar_wait_warp(bar(C::B_QFULL + t), qn & 1, wc) &&
-             (!shared || t == 0 || mbar_wait_warp(bar(C::B_QFULL), qn & 1, wc));
-        tc_fence_after();
-        const int step = shared ? 2 : 1, first = shared ? t : 0;
-        const uint32_t tm_s = tmem + C::TM_S + t * 128;
-        int v = first;
-        for (; v < n && ok; v += step) {
-          ok = (!shared || pass(C::B_KFULL, C::B_KEMPTY, C::KS, v - 1)) && wait_ring(C::B_KFULL, u0 + v, C::KS);
-          if (!ok) break;
+        // The S buffer is free for this tile's next S once the other tile has
+        // read the S issued before it (S_0(j), S_1(j), S_0(j + 1), ...).
+        auto wait_sbuf = [&]() -> bool {
+          if (t == 0 && ns == 0) return true;
+          const int phase = t == 0 ? ns - 1 : ns;
+          if (!mbar_wait_warp(bar(C::B_SREAD + (t ^ 1)), phase & 1, wc)) return false;
           tc_fence_after();
-          {
-            uint64_t qd = code_desc<D>(sb + C::OFF_Q + (shared ? 0 : t * 2 * C::T8));
+          return true;
+        };
+        auto issue_s = [&](int j) {
+          const int s = (u0 + j) % C::KS;
+          if (live) {
+            uint64_t qd = code_desc<D>(sb + C::OFF_Q + t * 2 * C::T8);
             asm volatile("" : "+l"(qd));
-            const int s = (u0 + v) % C::KS;
             const uint64_t kd = code_desc<D>(sb + C::OFF_K + s * C::T8);
 #pragma unroll
             for (int part = 0; part < 2; ++part)
 #pragma unroll
               for (int kk = 0; kk < D / 32; ++kk)
-                mma_ss_f8_warp(tm_s, qd + ((part * C::T8 + kk * 32) >> 4), kd + (kk * 32 >> 4), C::IDESC_S,
+                mma_ss_f8_warp(tmem + C::TM_S, qd + ((part * C::T8 + kk * 32) >> 4), kd + (kk * 32 >> 4), C::IDESC_S,
                                part + kk > 0 ? 1u : 0u);
-            tc_commit_warp(bar(C::B_SFULL + t));
-            tc_commit_warp(bar(C::B_KEMPTY + s));
           }
-          ok = (!shared || pass(C::B_WFULL, C::B_WEMPTY, C::WS, v - 1)) && wait_ring(C::B_WFULL, u0 + v, C::WS) &&
-               mbar_wait_warp(bar(C::B_PFULL + t), pf & 1, wc);
+          tc_commit_warp(bar(C::B_SFULL + t));
+          tc_commit_warp(bar(C::B_KEMPTY + s));
+          ++ns;
+        };
+        auto issue_pv = [&](int j) {
+          const int s = (u0 + j) % C::WS;
+          if (live) {
+            const uint64_t vd = sdesc_sw128(sb + C::OFF_W + s * C::T16, 16384, 1024);
+#pragma unroll
+            for (int kk = 0; kk < kUnit / 16; ++kk)
+              mma_ts_warp(tmem + C::TM_O + t * D, tmem + C::TM_P + t * 64 + kk * 8, vd + (kk * 2048 >> 4), C::IDESC_O,
+                          (kk > 0 || j > 0) ? 1u : 0u);
+          }
+          tc_commit_warp(bar(C::B_ODONE + t));
+          tc_commit_warp(bar(C::B_WEMPTY + s));
+        };
+        ok = wait_sbuf() && mbar_wait_warp(bar(C::B_QFULL + t), qn & 1, wc) && wait_ring(C::B_KFULL, u0, C::KS);
+        if (ok) issue_s(0);
+        for (int j = 0; j < n && ok; ++j) {
+          if (j + 1 < n) {
+            ok = wait_sbuf() && wait_ring(C::B_KFULL, u0 + j + 1, C::KS);
+            if (!ok) break;
+            issue_s(j + 1);
+          }
+          ok = wait_ring(C::B_WFULL, u0 + j, C::WS) && mbar_wait_warp(bar(C::B_PFULL + t), pf & 1, wc);
           if (!ok) break;
           ++pf;
           tc_fence_after();
-          const int s = (u0 + v) % C::WS;
-          const uint64_t vd = sdesc_sw128(sb + C::OFF_W + s * C::T16, 16384, 1024);
-#pragma unroll
-          for (int kk = 0; kk < kUnit / 16; ++kk)
-            mma_ts_warp(tmem + C::TM_O + t * D, tm_s + kk * 8, vd + (kk * 2048 >> 4), C::IDESC_O,
-                        (kk > 0 || v > first) ? 1u : 0u);
-          tc_commit_warp(bar(C::B_WEMPTY + s));
+          issue_pv(j);
         }
-        if (ok && v > first) tc_commit_warp(bar(C::B_ODONE + t));
-        if (ok && shared) ok = pass(C::B_KFULL, C::B_KEMPTY, C::KS, v - 1) && pass(C::B_WFULL, C::B_WEMPTY, C::WS, v - 1);
         u0 += n;
         ++qn;
       }
@@ -433,25 +411,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------- softmax + epilogue
     const int t = (warp - 8) >> 2, quad = warp & 3, row = quad * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const uint32_t s_t = tmem + lane_off + C::TM_S + t * 128;  // P_t as well
+    const uint32_t s_t = tmem + lane_off + C::TM_S;
+    const uint32_t p_t = tmem + lane_off + C::TM_P + t * 64;
     const uint32_t o_t = tmem + lane_off + C::TM_O + t * D;
     const uint32_t q_hi = sb + C::OFF_Q + t * 2 * C::T8, q_lo = q_hi + C::T8;
-    int u = 0;       // units before the item
-    int sg = 0;      // S tiles waited for
-    int od = 0;      // ends of P V waited for
-    int shares = 0;  // shared items
+    int u = 0;   // units
+    int sg = 0;  // S tiles completed (one per unit; ODONE likewise)
     bool ok = true;
     for (int i = 0; ok; ++i) {
       if (!wait_item(i)) break;
       const Item* im = items + i % kItems;
       const int n = im->count;
       if (n < 0) break;
-      const bool shared = item_shared(item_rows(p, im));
-      const int step = shared ? 2 : 1, first = shared ? t : 0;
-      // Tile 1's O and statistics of the last shared item have been read.
-      if (t == 1 && shares > 0 && !mbar_wait_warp(bar(C::B_READ), (shares - 1) & 1, wc)) break;
-      if (shared && n > 0) ++shares;
-      const int rho = im->tile * kPagedWideRows + (shared ? 0 : t * kBM) + row;
+      const int rho = im->tile * kPagedWideRows + t * kBM + row;
       const int last = im->n * p.G - 1;  // last row of the request
       // A warp without rows takes part in the hand-offs only.
       const bool live = rho - lane <= last;
@@ -461,8 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float f = 0.f;
       if (n > 0) {
         if (live) {
-          // This thread's row of Q as hi + lo (of a shared item tile 0 writes
-          // it; tile 1 only needs its factor).  The products that read the
+          // This thread's row of Q as hi + lo.  The products that read the
           // tile's last Q have completed: their S tiles were waited for.
           const uint4* src = reinterpret_cast<const uint4*>(
               p.Q + (long long)(im->start + tok) * p.q_stride +
@@ -484,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float down = __int_as_float((127 - k) << 23);
           f = odd ? NAN : __int_as_float((127 + k) << 23) * p.scale_log2;
 #pragma unroll 2
-          for (int x = 0; x < (shared && t ? 0 : D / 16); ++x) {
+          for (int x = 0; x < D / 16; ++x) {
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
@@ -511,88 +482,119 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float m = -INFINITY, l = 0.f;
       float lvref = -1e30f;  // log2 of the largest V scale seen
-      auto wait_scales = [&](int v) -> bool {
-        return mbar_wait_warp(bar(C::B_MFULL + (u + v) % kMetas), ((u + v) / kMetas) & 1, wc);
-      };
-      // The scales of the other tile's units of a shared item pass by here.
-      auto pass = [&](int v) -> bool {
-        if (v < 0 || v >= n) return true;
-        if (!wait_scales(v)) return false;
-        release(C::B_MEMPTY + (u + v) % kMetas);
-        return true;
-      };
-      int v = first;
-      for (; v < n; v += step) {
-        if ((shared && !pass(v - 1)) || !wait_scales(v) || !mbar_wait_warp(bar(C::B_SFULL + t), sg & 1, wc)) {
+      for (int j = 0; j < n; ++j, ++u) {
+        const int key0 = (im->k0 + j) * kUnit;
+        if (!mbar_wait_warp(bar(C::B_MFULL + u % kMetas), (u / kMetas) & 1, wc) ||
+            !mbar_wait_warp(bar(C::B_SFULL + t), sg & 1, wc)) {
           ok = false;
           break;
         }
         ++sg;
         tc_fence_after();
-        const int ring = (u + v) % kMetas;
-        const int key0 = (im->k0 + v) * kUnit;
-        if (live) {
-          const UnitMeta* mt = metas + ring;
+        // The hand-off of S(j) back, of the scales, and of P(j) once P(j - 1) has been used.
+        if (!live) {
+          tc_fence_before();
+          release(C::B_SREAD + t);
+          if (lane == 0) mbar_arrive(bar(C::B_MEMPTY + u % kMetas));
+          if (j > 0 && !mbar_wait_warp(bar(C::B_ODONE + t), sg & 1, wc)) {
+            ok = false;
+            break;
+          }
+          release(C::B_PFULL + t);
+          continue;
+        }
+        const UnitMeta* mt = metas + u % kMetas;
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_t + c * 32, sr[c]);
+        tmem_ld_wait(sr[0]);
+        reg_fence32(sr[1]);
+        reg_fence32(sr[2]);
+        reg_fence32(sr[3]);
+        tc_fence_before();
+        release(C::B_SREAD + t);
+        float alpha = 1.f;
+        bool move = false;
+        uint32_t wv[2][32];
+        {
           const uint32_t pages = (uint32_t)mt->pages;
           if (key0 + kUnit > lim_all || pages != (1u << (kUnit >> p.page_log2)) - 1) {
-            // Keys that the row does not see, and pages that are not there.
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t x[32];
-              tmem_ld32(s_t + c * 32, x);
-              tmem_ld_wait(x);
-              const bool p0 = (pages >> ((c * 32) >> p.page_log2)) & 1, p1 = (pages >> ((c * 32 + 16) >> p.page_log2)) & 1;
-              const int left = lim - key0 - c * 32;
 #pragma unroll
-              for (int y = 0; y < 32; ++y)
-                if (y >= left || !(y < 16 ? p0 : p1)) x[y] = __float_as_uint(-INFINITY);
-              tmem_st32(s_t + c * 32, x);
-            }
-            tmem_st_wait();
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                if (key0 + c * 32 + x >= lim || !((pages >> ((c * 32 + (x & 16)) >> p.page_log2)) & 1))
+                  sr[c][x] = __float_as_uint(-INFINITY);
           }
-          // A factor that underflowed must not meet an infinity (a sum times
+          float cf[8], lv[8];
+#pragma unroll
+          for (int x = 0; x < 8; x += 4) {
+            const float4 a = *reinterpret_cast<const float4*>(mt->ks + x);
+            const float4 b = *reinterpret_cast<const float4*>(mt->lv + x);
+            cf[x] = f * a.x, cf[x + 1] = f * a.y, cf[x + 2] = f * a.z, cf[x + 3] = f * a.w;
+            lv[x] = b.x, lv[x + 1] = b.y, lv[x + 2] = b.z, lv[x + 3] = b.w;
+          }
+          // Largest logit and V scale of the unit; 16 keys are of one page.  A
+          // factor that underflowed must not meet an infinity (a sum times
           // 1e-37 is 0 as well); a NaN stays.
-          auto factor = [&](float ks) -> float {
-            const float x = f * ks;
-            return x < 1e-37f ? 1e-37f : x;
-          };
-          // Largest logit and V scale of the unit; 16 keys are of one page.
           float mx = -INFINITY, lvm = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            uint32_t x[2][32];
-            tmem_ld32(s_t + c * 64, x[0]);
-            tmem_ld32(s_t + c * 64 + 32, x[1]);
-            const float4 ks = *reinterpret_cast<const float4*>(mt->ks + 4 * c);
-            const float4 lv = *reinterpret_cast<const float4*>(mt->lv + 4 * c);
-            lvm = fmax3(fmaxf(lvm, lv.x), fmaxf(lv.y, lv.z), lv.w);
-            tmem_ld_wait(x[0]);
-            reg_fence32(x[1]);
-            const float k4[4] = {ks.x, ks.y, ks.z, ks.w};
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              float a = -INFINITY, b = -INFINITY;
+          for (int sgm = 0; sgm < 8; ++sgm) {
+            const int c = sgm >> 1, x0 = 16 * (sgm & 1);
+            if (cf[sgm] < 1e-37f) cf[sgm] = 1e-37f;
+            float a = -INFINITY, b = -INFINITY;
 #pragma unroll
-              for (int y = 0; y < 8; y += 2) {
-                const int z = (g & 1) * 16 + y;
-                a = fmax3(a, __uint_as_float(x[g >> 1][z]), __uint_as_float(x[g >> 1][z + 1]));
-                b = fmax3(b, __uint_as_float(x[g >> 1][z + 8]), __uint_as_float(x[g >> 1][z + 9]));
-              }
-              mx = fmaxf(mx, fmaxf(a, b) * factor(k4[g]));
+            for (int x = 0; x < 8; x += 2) {
+              a = fmax3(a, __uint_as_float(sr[c][x0 + x]), __uint_as_float(sr[c][x0 + x + 1]));
+              b = fmax3(b, __uint_as_float(sr[c][x0 + 8 + x]), __uint_as_float(sr[c][x0 + 9 + x]));
             }
+            mx = fmaxf(mx, fmaxf(a, b) * cf[sgm]);
+            lvm = fmaxf(lvm, lv[sgm]);
           }
-          const bool move = mx > m + kThreshold || lvm > lvref;
-          float alpha = 1.f;
+          move = mx > m + kThreshold || lvm > lvref;
           if (move) {
             const float mn = fmaxf(m, mx), ln = fmaxf(lvref, lvm);
-            alpha = mn == -INFINITY ? 1.f : ex2(m - mn);
+            alpha = ex2(m - mn);
+            if (mn == -INFINITY) alpha = 1.f;
             l *= alpha;
             alpha *= ex2(lvref - ln);
             m = mn;
             lvref = ln;
           }
-          if (v > first && __any_sync(0xffffffffu, move)) {
-            // O_t holds the item's units before this one: their products have completed.
+          const float m_use = m == -INFINITY ? 0.f : m;
+          float lsum = 0.f;
+#pragma unroll
+          for (int sgm = 0; sgm < 8; ++sgm) {
+            const int c = sgm >> 1, x0 = 16 * (sgm & 1);
+            const float ratio = fmaxf(lv[sgm] - lvref, kLowRatio) + kShift;
+            const uint64_t c2 = f2pack(cf[sgm], cf[sgm]), off2 = f2pack(ratio - m_use, ratio - m_use);
+            uint64_t rs = 0, rs1 = 0;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              float y0, y1;
+              f2unpack(ffma2(f2pack(__uint_as_float(sr[c][x0 + 2 * x]), __uint_as_float(sr[c][x0 + 2 * x + 1])), c2, off2),
+                       y0, y1);
+              const float p0 = ex2(y0), p1 = ex2(y1);
+              if (x & 1) rs1 = fadd2(rs1, f2pack(p0, p1));
+              else rs = fadd2(rs, f2pack(p0, p1));
+              wv[c >> 1][(c & 1) * 16 + (x0 >> 1) + x] = pack_f16(p0, p1);
+            }
+            float a0, a1;
+            f2unpack(fadd2(rs, rs1), a0, a1);
+            lsum = fmaf(a0 + a1, ex2(-ratio), lsum);
+          }
+          l += lsum;
+        }
+        release(C::B_MEMPTY + u % kMetas);
+        if (j > 0) {
+          // The item's last P_t V has completed: it read the P_t written below, and O_t may be scaled.
+          if (!mbar_wait_warp(bar(C::B_ODONE + t), sg & 1, wc)) {  // phase sg - 2
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (__any_sync(0xffffffffu, move)) {
+            // 32 columns at a time: P_t's 64 registers are live here.
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
@@ -603,116 +605,30 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st32(o_t + c * 32, o);
             }
           }
-          const float m_use = m == -INFINITY ? 0.f : m;
-#pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            uint32_t x[2][32], w[32];
-            tmem_ld32(s_t + c * 64, x[0]);
-            tmem_ld32(s_t + c * 64 + 32, x[1]);
-            const float4 ks = *reinterpret_cast<const float4*>(mt->ks + 4 * c);
-            const float4 lv = *reinterpret_cast<const float4*>(mt->lv + 4 * c);
-            const float k4[4] = {ks.x, ks.y, ks.z, ks.w}, v4[4] = {lv.x, lv.y, lv.z, lv.w};
-            uint64_t c2[4], off2[4];
-            float back[4];
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const float cf = factor(k4[g]), ratio = fmaxf(v4[g] - lvref, kLowRatio) + kShift;
-              c2[g] = f2pack(cf, cf);
-              off2[g] = f2pack(ratio - m_use, ratio - m_use);
-              back[g] = ex2(-ratio);
-            }
-            tmem_ld_wait(x[0]);
-            reg_fence32(x[1]);
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              uint64_t r0 = 0, r1 = 0;
-#pragma unroll
-              for (int y = 0; y < 8; ++y) {
-                const int z = (g & 1) * 16 + 2 * y;
-                float y0, y1;
-                f2unpack(ffma2(f2pack(__uint_as_float(x[g >> 1][z]), __uint_as_float(x[g >> 1][z + 1])), c2[g], off2[g]),
-                         y0, y1);
-                const float p0 = ex2(y0), p1 = ex2(y1);
-                if (y & 1) r1 = fadd2(r1, f2pack(p0, p1));
-                else r0 = fadd2(r0, f2pack(p0, p1));
-                w[g * 8 + y] = pack_f16(p0, p1);
-              }
-              float a0, a1;
-              f2unpack(fadd2(r0, r1), a0, a1);
-              l = fmaf(a0 + a1, back[g], l);
-            }
-            tmem_st32(s_t + c * 32, w);  // over columns that have been read
-          }
-          tmem_st_wait();
         }
+        tmem_st32(p_t, wv[0]);
+        tmem_st32(p_t + 32, wv[1]);
+        tmem_st_wait();
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(C::B_PFULL + t));
-          mbar_arrive(bar(C::B_MEMPTY + ring));
-        }
+        release(C::B_PFULL + t);
       }
-      if (!ok || (shared && !pass(v - 1))) break;
-      u += n;
-      if (v > first) {
-        if (!mbar_wait_warp(bar(C::B_ODONE + t), od & 1, wc)) break;
-        ++od;
+      if (!ok) break;
+      if (n > 0) {
+        if (!mbar_wait_warp(bar(C::B_ODONE + t), (sg - 1) & 1, wc)) break;
         tc_fence_after();
-      }
-      if (shared && n > 0) {
-        if (t == 1) {
-          // Maximum, sum and O's scale, over S_1, whose last product has completed.
-          const uint32_t st[4] = {__float_as_uint(m), __float_as_uint(l), __float_as_uint(lvref), 0u};
-          tmem_st4(s_t, st);
-          tmem_st_wait();
-          tc_fence_before();
-          release(C::B_GIVEN);
-          release_item(i);
-          continue;
-        }
-        if (!mbar_wait_warp(bar(C::B_GIVEN), (shares - 1) & 1, wc)) break;
-        tc_fence_after();
-      }
-      if (t == 1 && shared) {
-        release_item(i);
-        continue;
       }
       if (live) {
         const bool valid = rho <= last;
-        float back = n > 0 ? ex2(lvref - kShift) : 0.f, back1 = 0.f;
-        const bool two = shared && n > 1;  // tile 1 had a unit
-        if (two) {
-          uint32_t st[4];
-          tmem_ld4(s_t + 128, st);
-          const float m1 = __uint_as_float(st[0]), l1 = __uint_as_float(st[1]);
-          const float mn = fmaxf(m, m1), r = mn == -INFINITY ? 0.f : mn;
-          const float a0 = ex2(m - r), a1 = ex2(m1 - r);
-          back *= a0;
-          back1 = ex2(__uint_as_float(st[2]) - kShift) * a1;
-          l = l * a0 + l1 * a1;
-          m = mn;
-        }
+        const float back = n > 0 ? ex2(lvref - kShift) : 0.f;
         const size_t orow = output_row(p, im->start, im->h, min(rho, last));
-        const float inv = im->slot < 0 ? output_factor(l) : 1.f;
-        const float mul = two ? 1.f : back * inv;
-        back *= inv;
-        back1 *= inv;
+        const float mul = im->slot < 0 ? back * output_factor(l) : back;
         const size_t prow = (size_t)(blockIdx.x * 2 + max(im->slot, 0)) * kPagedWideRows + t * kBM + row;
         // bf16 rows go through the warp's quarter of the Q tile (whose products have completed).
         const uint32_t stage = q_hi + quad * 32 * D;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
-          if (two) {
-            uint32_t o1[32];
-            tmem_ld32(o_t + c * 32, o);
-            tmem_ld32(o_t + D + c * 32, o1);
-            tmem_ld_wait(o);
-            reg_fence32(o1);
-#pragma unroll
-            for (int x = 0; x < 32; ++x)
-              o[x] = __float_as_uint(fmaf(__uint_as_float(o[x]), back, __uint_as_float(o1[x]) * back1));
-          } else if (n > 0) {
+          if (n > 0) {
             tmem_ld32(o_t + c * 32, o);
             tmem_ld_wait(o);
           } else {
@@ -757,10 +673,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (im->slot >= 0) *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m, l);
           else p.LSE[orow] = output_lse(m, l);
         }
-      }
-      if (shared && n > 0) {
-        tc_fence_before();
-        release(C::B_READ);
       }
       release_item(i);
     }
