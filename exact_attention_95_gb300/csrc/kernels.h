@@ -181,6 +181,7 @@ struct PagedFwdParams {
   long long q_stride;
   const float* k_scale;  // [num_pages, Hkv]
   const float* v_scale;
+  const uint8_t* v_pages;  // [num_pages, Hkv, page, d]
   const int* block_table;  // [R, max_pages]
   const int* cu_q;         // [R + 1]
   const int* kv_lens;      // [R]

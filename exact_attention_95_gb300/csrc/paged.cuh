@@ -292,6 +292,20 @@ __device__ __forceinline__ bool walk_range(const PagedFwdParams& p, const long l
   return ok;
 }
 
+// Bytes 0xff where four codes hold a NaN.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t c) { return __vcmpeq4(c & 0x7f7f7f7fu, 0x7f7f7f7fu); }
+// A NaN in V at a key that some rows of a tile see and others do not (a drafted
+// token behind them, say) would reach all of them: 0 * NaN is one.  The kernels
+// take such codes for 0 and note it; at the item's end every row looks up the
+// codes of the keys that it does see.  Four codes of key `key` from column c on:
+__device__ __forceinline__ uint32_t v_codes(const uint8_t* v_pages, const int* block_table, int num_pages, int page_log2,
+                                         int Hkv, int D, size_t row0, int key, int h, int c) {
+  const int id = block_table[row0 + (key >> page_log2)];
+  if (id < 0 || id >= num_pages) return 0;
+  const size_t row = (((size_t)id * Hkv + h) << page_log2) + (key & ((1 << page_log2) - 1));
+  return *reinterpret_cast<const uint32_t*>(v_pages + row * D + c);
+}
+
 // Row `row` of a tile in the output arrays.
 __device__ __forceinline__ size_t output_row(const PagedFwdParams& p, int start, int h, int rho) {
   const int tok = rho / p.G;

@@ -174,6 +174,7 @@ attn_status attn_fwd_paged_fp8(const void* Q, long long q_stride, const void* k_
   p.q_stride = q_stride;
   p.k_scale = k_scale;
   p.v_scale = v_scale;
+  p.v_pages = static_cast<const uint8_t*>(v_pages);
   p.block_table = block_table;
   p.cu_q = cu_q;
   p.kv_lens = kv_lens;

@@ -96,7 +96,8 @@ struct PC {
   static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_IFULL = 2 * STAGES, B_IEMPTY = B_IFULL + kItems;
   static constexpr int B_GIVEN = B_IEMPTY + kItems, B_WRITTEN = B_GIVEN + 1, B_READ = B_GIVEN + 2;
   static constexpr int OFF_SINCE = OFF_BAR + (B_READ + 1) * 8;  // of each warp
-  static constexpr int OFF_ABORT = OFF_SINCE + (WARPS + 1) * 8;
+  static constexpr int OFF_NAN = OFF_SINCE + (WARPS + 1) * 8;   // [kItems]: number + 1 of an item with a NaN put aside
+  static constexpr int OFF_ABORT = OFF_NAN + kItems * 4;
   static constexpr int SMEM = OFF_ABORT + 8 + 1024;
   static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory");
   static_assert(WARPS == 2 * HALF, "half of the warps hand over to the others");
@@ -155,6 +156,7 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
   const uint32_t sb = smem_u32(smem);
   auto bar = [&](int i) -> uint32_t { return sb + C::OFF_BAR + 8 * i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
+  volatile int* nans = reinterpret_cast<volatile int*>(smem + C::OFF_NAN);
   UnitMeta* metas = reinterpret_cast<UnitMeta*>(smem + C::OFF_META);
   Item* items = reinterpret_cast<Item*>(smem + C::OFF_ITEM);
   long long* sums = reinterpret_cast<long long*>(smem + C::OFF_SUMS);
@@ -172,6 +174,7 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
     mbar_init(bar(C::B_WRITTEN), kHalf);
     mbar_init(bar(C::B_READ), kHalf);
     *abort_flag = 0;
+    for (int i = 0; i < kItems; ++i) nans[i] = 0;
     fence_mbar_init();
   }
   sum_units<kRows>(p, sums, warp, kWarps + 1, lane);
@@ -444,10 +447,16 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
           }
           if (edge) {  // V rows that no row of the tile sees hold anything, a NaN too
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (key0 + 16 * hf + 8 * (e >> 1) + ((e & 1) ? kv1 : kv0) >= lim_any || !(hf ? lb : la))
+            for (int e = 0; e < 4; ++e) {
+              const int key = key0 + 16 * hf + 8 * (e >> 1) + ((e & 1) ? kv1 : kv0);
+              const bool seen = key < lim_any && (hf ? lb : la);
 #pragma unroll
-                for (int y = 0; y < D / 32; ++y) w[e][y] = 0;
+              for (int y = 0; y < D / 32; ++y) {
+                const uint32_t bad = seen && key >= lim_all ? nan_codes(w[e][y]) : 0u;
+                if (bad) nans[i % kItems] = i + 1;
+                w[e][y] = seen ? w[e][y] & ~bad : 0u;
+              }
+            }
           }
 #pragma unroll
           for (int y = 0; y < D / 32; ++y) {
@@ -574,6 +583,19 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
         sum.y += wgt * v.y;
         sum.z += wgt * v.z;
         sum.w += wgt * v.w;
+      }
+      if (nans[i % kItems] == i + 1) {
+        const int tok = (tile * kRows + row) / p.G;
+        const int from = max(im->k0 * kUnit, lim_all), to = min((im->k0 + count) * kUnit, key_limit(p, len, n, tok));
+#pragma unroll 1
+        for (int key = from; key < to; ++key) {
+          const uint32_t bad = nan_codes(v_codes(p.v_pages, p.block_table, p.num_pages, p.page_log2, p.Hkv, D,
+                                                 (size_t)im->req * p.max_pages, key, h, q4 * 4));
+          if (bad & 0xffu) sum.x = NAN;
+          if (bad & 0xff00u) sum.y = NAN;
+          if (bad & 0xff0000u) sum.z = NAN;
+          if (bad & 0xff000000u) sum.w = NAN;
+        }
       }
       if (slot >= 0) {
         const size_t base = (size_t)(blockIdx.x * 2 + slot) * kRows + row;

@@ -87,7 +87,8 @@ struct WC {
   static constexpr int B_PFULL = B_SREAD + 2;        // 2
   static constexpr int B_ODONE = B_PFULL + 2;        // 2
   static constexpr int B_DRAIN = B_ODONE + 2;        // 2
-  static constexpr int OFF_TMEMSLOT = OFF_BAR + (B_DRAIN + 2) * 8;
+  static constexpr int OFF_NAN = OFF_BAR + (B_DRAIN + 2) * 8;  // [kItems]: number + 1 of an item with a NaN put aside
+  static constexpr int OFF_TMEMSLOT = OFF_NAN + kItems * 4;
   static constexpr int OFF_ABORT = OFF_TMEMSLOT + 4;
   static constexpr int SMEM = OFF_ABORT + 4 + 1024;
   static constexpr uint32_t IDESC_S = idesc_e4m3(kBM, kUnit);
@@ -140,6 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) -> uint32_t { return sb + C::OFF_BAR + 8 * i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_TMEMSLOT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
+  volatile int* nans = reinterpret_cast<volatile int*>(smem + C::OFF_NAN);
   UnitMeta* metas = reinterpret_cast<UnitMeta*>(smem + C::OFF_META);
   Item* items = reinterpret_cast<Item*>(smem + C::OFF_ITEM);
   long long* sums = reinterpret_cast<long long*>(smem + C::OFF_SUMS);
@@ -181,6 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(C::B_DRAIN + t), 1);
     }
     *abort_flag = 0;
+    for (int i = 0; i < kItems; ++i) nans[i] = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -362,6 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Keys behind the last one that a row of the tile sees hold anything, a NaN code too.
       const int seen =
           key_limit(p, im->len, im->n, (min(im->n * p.G, (im->tile + 1) * kPagedWideRows) - 1) / p.G);
+      const int seen_all = key_limit(p, im->len, im->n, im->tile * kPagedWideRows / p.G);  // by its first row
       release_item(i);
       if (n < 0) break;
       for (int j = 0; j < n; ++j, ++u) {
@@ -374,14 +378,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint32_t pages = (uint32_t)metas[u % kMetas].pages;
         const int valid = min(kUnit, seen - (k0 + j) * kUnit);
-        const bool whole = valid == kUnit && pages == (1u << (kUnit >> p.page_log2)) - 1;
+        const int all = seen_all - (k0 + j) * kUnit;
+        const bool whole = all >= kUnit && pages == (1u << (kUnit >> p.page_log2)) - 1;
         constexpr int PC = D / 16;  // pieces of a row
         const uint32_t src = sb + C::OFF_V + sv * C::T8, dst = sb + C::OFF_W + sw * C::T16;
 #pragma unroll 4
         for (int x = 0; x < kUnit * PC / 128; ++x) {
           const int e = wl + 128 * x, row = e / PC, pc = e % PC;
           uint4 v = lds_u4(piece<D>(src, row, pc));
-          if (!whole && (row >= valid || !((pages >> (row >> p.page_log2)) & 1))) v = make_uint4(0, 0, 0, 0);
+          if (!whole) {
+            if (row >= valid || !((pages >> (row >> p.page_log2)) & 1)) {
+              v = make_uint4(0, 0, 0, 0);
+            } else if (row >= all) {  // some rows do not see it
+              const uint32_t b0 = nan_codes(v.x), b1 = nan_codes(v.y), b2 = nan_codes(v.z), b3 = nan_codes(v.w);
+              if (b0 | b1 | b2 | b3) nans[i % kItems] = i + 1;
+              v = make_uint4(v.x & ~b0, v.y & ~b1, v.z & ~b2, v.w & ~b3);
+            }
+          }
           const uint32_t base = dst + (pc >> 2) * 16384 + row * 128;
           const int c0 = 2 * (pc & 3);
           // The two halves in an order that keeps the eight lanes of a row off each other's banks.
@@ -668,6 +681,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   pack_bf16(__uint_as_float(o[8 * x + 4]) * mul, __uint_as_float(o[8 * x + 5]) * mul),
                                   pack_bf16(__uint_as_float(o[8 * x + 6]) * mul, __uint_as_float(o[8 * x + 7]) * mul));
           }
+        }
+        __syncwarp();
+        if (n > 0 && nans[i % kItems] == i + 1 && valid) {
+          // Over what the warp has stored.
+          const int from = max(im->k0 * kUnit, key_limit(p, im->len, im->n, im->tile * kPagedWideRows / p.G));
+          const int to = min((im->k0 + n) * kUnit, lim);
+#pragma unroll 1
+          for (int key = from; key < to; ++key)
+#pragma unroll 1
+            for (int c = 0; c < D; ++c) {
+              if (!(nan_codes(v_codes(p.v_pages, p.block_table, p.num_pages, p.page_log2, p.Hkv, D,
+                                      (size_t)im->req * p.max_pages, key, im->h, c & ~3)) >> (8 * (c & 3)) & 0xffu))
+                continue;
+              if (im->slot >= 0) p.part_o[prow * D + c] = NAN;
+              else if (p.out_f32) static_cast<float*>(p.O)[orow * D + c] = NAN;
+              else static_cast<uint16_t*>(p.O)[orow * D + c] = 0x7fc0;
+            }
         }
         if (valid) {
           if (im->slot >= 0) *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m, l);

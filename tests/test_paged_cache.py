@@ -562,3 +562,64 @@ def test_calls_on_two_streams_at_once():
     ok()
     for i, x in enumerate(got):
         assert torch.equal(x[0], want[i % 2][0]) and torch.equal(x[1], want[i % 2][1])
+
+
+# ------------------------------------------------------------------ NaN where a row does not look
+@gpu
+@pytest.mark.parametrize("lens,news,Hq,Hkv,page", [([70, 33], [4, 3], 2, 1, 16), ([70, 300], [7, 9], 8, 2, 32),
+                                                   ([700, 300], [40, 100], 4, 2, 64), ([500], [300], 1, 1, 128)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_attention_nan_values_reach_only_the_rows_that_see_them(lens, news, Hq, Hkv, page, d, out):
+    """V holds NaN in some columns of the last tokens: a row before them must not
+    meet it (0 * NaN), a row that sees them must."""
+    rng = np.random.default_rng(sum(lens) + d)
+    kc, ks, vc, vs, table = _cache(rng, lens, page, Hkv, d)
+    cu = np.concatenate([[0], np.cumsum(news)]).astype(I32)
+    T = int(cu[-1])
+    where = []
+    for r, n in enumerate(lens):
+        for back in (1, 2, min(news[r], 3)):
+            key = n - back
+            cols = rng.choice(d, 3, replace=False)
+            vc[table[r, key // page], :, key % page, cols] = 0x7F if back % 2 else 0xFF
+            where.append((r, key, cols))
+    q = _tokens(rng, T, Hq, d, 0)
+    g = [dev(a) for a in (kc, ks, vc, vs, table, cu, np.asarray(lens, I32))]
+    O, L = pkg.attn_fwd_paged_fp8(dev_bf16(q), *g, None, True, out)
+    ok()
+    want = np.zeros((T, Hq, d), bool)
+    for r, key, cols in where:
+        for i in range(news[r]):
+            if key <= lens[r] - news[r] + i:
+                want[cu[r] + i][:, cols] = True
+    assert np.array_equal(torch.isnan(O).cpu().numpy(), want)
+    assert torch.isfinite(L).all()
+    clean = vc.copy()
+    clean[(clean & 0x7F) == 0x7F] = 0
+    Or, _, A, B = paged.attention(paged.bf16_values(q), kc, ks, clean, vs, table, cu, lens,
+                                  float(np.float32(1 / np.sqrt(d))), True)
+    tol, _ = paged.bounds(Or, np.zeros(Or.shape[:2]), A, B, d, out == torch.bfloat16)
+    err = np.abs(np.where(want, 0.0, O.double().cpu().numpy()) - np.where(want, 0.0, Or))
+    assert (err <= tol).all()
+
+
+@gpu
+def test_attention_nan_in_keys_and_queries():
+    rng = np.random.default_rng(41)
+    for news in ([3], [40]):
+        kc, ks, vc, vs, table = _cache(rng, [200], 32, 1, 64)
+        kc[table[0, 199 // 32], 0, 199 % 32, 5] = 0x7F  # the last key: seen by the last query only
+        T = news[0]
+        q = _tokens(rng, T, 2, 64, 0)
+        q[0, 1, 3] = 0x7FC0  # one query row is NaN
+        q[1, 0, 3] = 0x7F80  # one has an infinity
+        cu = np.array([0, T], I32)
+        g = [dev(a) for a in (kc, ks, vc, vs, table, cu, np.array([200], I32))]
+        O, L = pkg.attn_fwd_paged_fp8(dev_bf16(q), *g, None, True, torch.float32)
+        ok()
+        bad = np.zeros((T, 2), bool)
+        bad[T - 1] = bad[0, 1] = bad[1, 0] = True
+        assert np.array_equal(torch.isnan(L).cpu().numpy(), bad)
+        assert np.array_equal(torch.isnan(O).all(-1).cpu().numpy(), bad)
+        assert np.array_equal(torch.isnan(O).any(-1).cpu().numpy(), bad)
