@@ -30,42 +30,6 @@ using namespace paged;
 constexpr int kItems = 4;          // items announced ahead
 constexpr float kPScale = 16384.f;
 
-// Bounded waits of this kernel.  As mbar_wait (ptx.cuh), but with all that
-// is not the try itself in a function of its own, called every kTries tries:
-// written out at each of some thirty waits it would be half of the code.
-constexpr uint32_t kTries = 1024;
-struct Waits {
-  volatile int* abort_flag;            // shared: a wait of the CTA gave up
-  volatile unsigned long long* since;  // shared, this warp's: when the wait at hand was first looked at
-  int* status;
-  unsigned long long limit_ns;
-};
-__device__ __noinline__ bool give_up(volatile int* abort_flag, volatile unsigned long long* since, int* status,
-                                     unsigned long long limit_ns, uint32_t tries) {
-  if (*abort_flag) return true;
-  const unsigned long long now = globaltimer_ns();
-  if (tries == kTries) *since = now;
-  else if (now - *since > limit_ns) {
-    *abort_flag = 1;
-    atomicCAS(status, kDevOk, kDevTimeout);
-    return true;
-  }
-  return false;
-}
-// By a whole warp, with one result.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Waits& w) {
-  uint32_t tries = 0;
-  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
-    if ((++tries & (kTries - 1)) == 0 &&
-        __any_sync(0xffffffffu, give_up(w.abort_flag, w.since, w.status, w.limit_ns, tries)))
-      return false;
-  return true;
-}
-// The same for copies and products in flight, which have to land whatever else gave up.
-__device__ __noinline__ void drain_bar(uint32_t bar, uint32_t parity, const Waits& w) {
-  const WaitCtx c{w.abort_flag, w.status, w.limit_ns};
-  mbar_wait_drain_warp(bar, parity, c);
-}
 // What a unit's stage holds besides the codes.
 struct UnitMeta {
   float ks[8], vs[8];  // scales of its pages
@@ -95,8 +59,7 @@ struct PC {
   static constexpr int OFF_BAR = OFF_META + STAGES * (int)sizeof(UnitMeta);
   static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_IFULL = 2 * STAGES, B_IEMPTY = B_IFULL + kItems;
   static constexpr int B_GIVEN = B_IEMPTY + kItems, B_WRITTEN = B_GIVEN + 1, B_READ = B_GIVEN + 2;
-  static constexpr int OFF_SINCE = OFF_BAR + (B_READ + 1) * 8;  // of each warp
-  static constexpr int OFF_NAN = OFF_SINCE + (WARPS + 1) * 8;   // [kItems]: number + 1 of an item with a NaN put aside
+  static constexpr int OFF_NAN = OFF_BAR + (B_READ + 1) * 8;  // [kItems]: number + 1 of an item with a NaN put aside
   static constexpr int OFF_ABORT = OFF_NAN + kItems * 4;
   static constexpr int SMEM = OFF_ABORT + 8 + 1024;
   static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory");
@@ -179,7 +142,7 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
   }
   sum_units<kRows>(p, sums, warp, kWarps + 1, lane);
   __syncthreads();
-  const Waits wc{abort_flag, reinterpret_cast<unsigned long long*>(smem + C::OFF_SINCE) + warp, p.status, p.wait_limit_ns};
+  volatile int* const wc = abort_flag;
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ producer
@@ -251,9 +214,13 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
     }
     // Copies in flight land before the CTA leaves (the consumers have waited
     // for all of them unless a wait gave up).
-    if (!ok)
+    if (!ok) {
+      const WaitCtx drain{abort_flag, p.status, p.wait_limit_ns};
+#pragma unroll 1
       for (int k = max(0, it - C::STAGES); k < it; ++k)
-        drain_bar(bar(C::B_FULL + k % C::STAGES), (k / C::STAGES) & 1, wc);
+        mbar_wait_drain_warp(bar(C::B_FULL + k % C::STAGES), (k / C::STAGES) & 1, drain);
+    }
+    if (*abort_flag && lane == 0) atomicCAS(p.status, kDevOk, kDevTimeout);
     griddep_launch_dependents();
     // Behind the wide kernel: this one's completion stands for both.
     griddep_wait();
@@ -280,345 +247,350 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
   const uint32_t voff0 = piece<D>(0, part + kv0, cg) + (D == 64 ? 8 * (g & 1) : 0);
   const uint32_t voff1 = piece<D>(0, part + kv1, cg) + (D == 64 ? 8 * (g & 1) : 0);
   int stage = 0, turn = 0;  // place and round of the next unit in the ring
+  auto consume = [&]() {
 #pragma unroll 1
-  for (int i = 0;; ++i) {
-    if (!wait_bar(bar(C::B_IFULL + i % kItems), (i / kItems) & 1, wc)) return;
-    const Item* im = items + i % kItems;
-    const int count = im->count;
-    if (count < 0) return;
-    const int tile = im->tile, h = im->h, len = im->len, n = im->n, start = im->start;
-    const int rows = min(kRows, n * p.G - tile * kRows);
-    // Queries (row g of a block), as f16 after a power of two of the row; limits of the rows' keys.
+    for (int i = 0;; ++i) {
+      if (!wait_bar(bar(C::B_IFULL + i % kItems), (i / kItems) & 1, wc)) return;
+      const Item* im = items + i % kItems;
+      const int count = im->count;
+      if (count < 0) return;
+      const int tile = im->tile, h = im->h, len = im->len, n = im->n, start = im->start;
+      const int rows = min(kRows, n * p.G - tile * kRows);
+      // Queries (row g of a block), as f16 after a power of two of the row; limits of the rows' keys.
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const int rho = tile * kRows + min(8 * b + g, rows - 1);
-      const int tok = rho / p.G;
-      const uint4* src = reinterpret_cast<const uint4*>(p.Q + (long long)(start + tok) * p.q_stride +
-                                                        (long long)(h * p.G + rho - tok * p.G) * D);
-      uint4 w[QI][2];
-      uint32_t am = 0;
+      for (int b = 0; b < NB; ++b) {
+        const int rho = tile * kRows + min(8 * b + g, rows - 1);
+        const int tok = rho / p.G;
+        const uint4* src = reinterpret_cast<const uint4*>(p.Q + (long long)(start + tok) * p.q_stride +
+                                                          (long long)(h * p.G + rho - tok * p.G) * D);
+        uint4 w[QI][2];
+        uint32_t am = 0;
 #pragma unroll
-      for (int q = 0; q < QI; ++q)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          w[q][e] = __ldg(src + (64 * q + 16 * c) / 8 + e);
-          const uint32_t ws[4] = {w[q][e].x, w[q][e].y, w[q][e].z, w[q][e].w};
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t lo = ws[x] & 0x7fffu, hi = (ws[x] >> 16) & 0x7fffu;
-            am = max(am, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-          }
-        }
-      am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
-      am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
-      // 2^-e takes the row's largest to [2^14, 2^15); e within what fp32 can undo.
-      const int e = min(max((int)(am >> 7) - 127, -100), 126) - 14;
-      const float up = __int_as_float((127 - e) << 23);
-      const float fr = __int_as_float((127 + e) << 23) * p.scale_log2;
-#pragma unroll
-      for (int q = 0; q < QI; ++q)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint4 v = w[q][j >> 1];
-          const uint32_t x = (j & 1) ? v.z : v.x, y = (j & 1) ? v.w : v.y;
-          qb[b][q][j][0] = pack_f16(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up);
-          qb[b][q][j][1] = pack_f16(__uint_as_float(y << 16) * up, __uint_as_float(y & 0xffff0000u) * up);
-        }
-      const int lr = key_limit(p, len, n, tok);
-#pragma unroll
-      for (int e2 = 0; e2 < 2; ++e2) {
-        f[b][e2] = __shfl_sync(0xffffffffu, fr, 8 * c + 4 * e2);
-        lim[b][e2] = __shfl_sync(0xffffffffu, lr, 8 * c + 4 * e2);
-        m[b][e2] = -INFINITY;
-        l[b][e2] = 0.f;
-      }
-      if (b == 0) lim_all = __shfl_sync(0xffffffffu, lr, 0);        // the first token's
-      if (b == NB - 1) lim_any = __shfl_sync(0xffffffffu, lr, 28);  // the last one's
-#pragma unroll
-      for (int j = 0; j < MT; ++j) o[b][j][0] = o[b][j][1] = o[b][j][2] = o[b][j][3] = 0.f;
-    }
-    vref = 0.f;
-    int key0 = im->k0 * kUnit + part;
-#pragma unroll 1
-    for (int u = 0; u < count; ++u, key0 += kUnit) {
-      const int s = stage;
-      if (!wait_bar(bar(C::B_FULL + s), turn, wc)) return;
-      const UnitMeta* mt = metas + s;
-      const int pa = part >> p.page_log2, pb = (part + 16) >> p.page_log2;  // pages of its two 16 keys
-      const bool la = (mt->pages >> pa) & 1, lb = (mt->pages >> pb) & 1;
-      if (key0 < lim_any && (la || lb)) {
-        const uint32_t kb = sb + C::OFF_RING + s * C::SBYTES, vb = kb + C::KBYTES;
-        // S^T = K Q^T: twice 16 keys by 8 rows of a block.
-        float acc[NB][2][4] = {};
-#pragma unroll
-        for (int q = 0; q < QI; ++q) {
-          const uint32_t ka = (kb + koff) ^ (64 * q);
-          const uint4 w0 = lds_u4(ka), w1 = lds_u4(ka + 8 * D), w2 = lds_u4(ka + 16 * D), w3 = lds_u4(ka + 24 * D);
-          const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
-          const uint32_t x2[4] = {w2.x, w2.y, w2.z, w2.w}, x3[4] = {w3.x, w3.y, w3.z, w3.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t a0[4] = {widen(x0[j]), widen(x1[j]), widen(x0[j] >> 16), widen(x1[j] >> 16)};
-            const uint32_t a1[4] = {widen(x2[j]), widen(x3[j]), widen(x2[j] >> 16), widen(x3[j] >> 16)};
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-              mma_f16(acc[b][0], a0, qb[b][q][j][0], qb[b][q][j][1]);
-              mma_f16(acc[b][1], a1, qb[b][q][j][0], qb[b][q][j][1]);
-            }
-          }
-        }
-        // Keys ko, ko + 8 (and 16 on) of rows 2c, 2c + 1.
-        const float vsa = mt->vs[pa], vsb = mt->vs[pb];
-        const float ksa = mt->ks[pa], ksb = mt->ks[pb];
-        const bool edge = key0 + 32 > lim_all || !la || !lb;
-        const float vsm = fmaxf(la ? vsa : 0.f, lb ? vsb : 0.f);
-        const float vnew = fmaxf(vref, vsm);
-        const float rv = vnew > vref && vref > 0.f ? __fdiv_rn(vref, vnew) : vnew > vref ? 0.f : 1.f;
-        vref = vnew;
-        const float rra = vsa == vref ? kPScale : vref > 0.f ? __fdiv_rn(vsa, vref) * kPScale : vsa;
-        const float rrb = vsb == vref ? kPScale : vref > 0.f ? __fdiv_rn(vsb, vref) * kPScale : vsb;
-        uint32_t pt[NB][4];  // P^T with row g and the keys of a column pair in a lane
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          float ca0 = f[b][0] * ksa, ca1 = f[b][1] * ksa, cb0 = f[b][0] * ksb, cb1 = f[b][1] * ksb;
-          if (edge) {
-            // A factor that underflowed must not meet the infinities (any sum times 1e-37 is 0 as well).
-            ca0 = fmaxf(ca0, 1e-37f);
-            ca1 = fmaxf(ca1, 1e-37f);
-            cb0 = fmaxf(cb0, 1e-37f);
-            cb1 = fmaxf(cb1, 1e-37f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (key0 + 8 * (e >> 1) + ko >= lim[b][e & 1] || !(e < 4 ? la : lb)) acc[b][e >> 2][e & 3] = -INFINITY;
-          }
-          float mx0 = fmaxf(fmaxf(acc[b][0][0], acc[b][0][2]) * ca0, fmaxf(acc[b][1][0], acc[b][1][2]) * cb0);
-          float mx1 = fmaxf(fmaxf(acc[b][0][1], acc[b][0][3]) * ca1, fmaxf(acc[b][1][1], acc[b][1][3]) * cb1);
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) {
-            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
-            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
-          }
-          if (__any_sync(0xffffffffu, mx0 > m[b][0] || mx1 > m[b][1]) || rv != 1.f) {
-            const float n0 = fmaxf(m[b][0], mx0), n1 = fmaxf(m[b][1], mx1);
-            const float a0 = n0 > m[b][0] ? ex2(m[b][0] - n0) : 1.f, a1 = n1 > m[b][1] ? ex2(m[b][1] - n1) : 1.f;
-            l[b][0] *= a0;
-            l[b][1] *= a1;
-            const float b0 = a0 * rv, b1 = a1 * rv;
-#pragma unroll
-            for (int j = 0; j < MT; ++j) {
-              o[b][j][0] *= b0;
-              o[b][j][1] *= b1;
-              o[b][j][2] *= b0;
-              o[b][j][3] *= b1;
-            }
-            m[b][0] = n0;
-            m[b][1] = n1;
-          }
-          const float u0 = m[b][0] == -INFINITY ? 0.f : m[b][0], u1 = m[b][1] == -INFINITY ? 0.f : m[b][1];
+        for (int q = 0; q < QI; ++q)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float rr = e ? rrb : rra, c0 = e ? cb0 : ca0, c1 = e ? cb1 : ca1;
-            const float x0 = ex2(fmaf(acc[b][e][0], c0, -u0)), x1 = ex2(fmaf(acc[b][e][1], c1, -u1));
-            const float x2 = ex2(fmaf(acc[b][e][2], c0, -u0)), x3 = ex2(fmaf(acc[b][e][3], c1, -u1));
-            l[b][0] += x0 + x2;
-            l[b][1] += x1 + x3;
-            pt[b][2 * e] = transpose8(pack_f16(x0 * rr, x1 * rr));
-            pt[b][2 * e + 1] = transpose8(pack_f16(x2 * rr, x3 * rr));
-          }
-        }
-        // O^T += V^T P^T: row g of tile t is column 16 cg + 2t (d = 64: 8g + 2t), row g + 8 the one after.
+            w[q][e] = __ldg(src + (64 * q + 16 * c) / 8 + e);
+            const uint32_t ws[4] = {w[q][e].x, w[q][e].y, w[q][e].z, w[q][e].w};
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t w[4][D / 32];  // four V rows' piece: keys kv0, kv1, kv0 + 8, kv1 + 8
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t va = vb + ((e & 1) ? voff1 : voff0) + (16 * hf + 8 * (e >> 1)) * D;
-            if constexpr (D == 128) {
-              const uint4 v = lds_u4(va);
-              w[e][0] = v.x;
-              w[e][1] = v.y;
-              w[e][2] = v.z;
-              w[e][3] = v.w;
-            } else {
-              const uint2 v = lds_u2(va);
-              w[e][0] = v.x;
-              w[e][1] = v.y;
+            for (int x = 0; x < 4; ++x) {
+              uint32_t lo = ws[x] & 0x7fffu, hi = (ws[x] >> 16) & 0x7fffu;
+              am = max(am, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
             }
           }
-          if (edge) {  // V rows that no row of the tile sees hold anything, a NaN too
+        am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+        am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+        // 2^-e takes the row's largest to [2^14, 2^15); e within what fp32 can undo.
+        const int e = min(max((int)(am >> 7) - 127, -100), 126) - 14;
+        const float up = __int_as_float((127 - e) << 23);
+        const float fr = __int_as_float((127 + e) << 23) * p.scale_log2;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int key = key0 + 16 * hf + 8 * (e >> 1) + ((e & 1) ? kv1 : kv0);
-              const bool seen = key < lim_any && (hf ? lb : la);
+        for (int q = 0; q < QI; ++q)
 #pragma unroll
-              for (int y = 0; y < D / 32; ++y) {
-                const uint32_t bad = seen && key >= lim_all ? nan_codes(w[e][y]) : 0u;
-                if (bad) nans[i % kItems] = i + 1;
-                w[e][y] = seen ? w[e][y] & ~bad : 0u;
+          for (int j = 0; j < 4; ++j) {
+            const uint4 v = w[q][j >> 1];
+            const uint32_t x = (j & 1) ? v.z : v.x, y = (j & 1) ? v.w : v.y;
+            qb[b][q][j][0] = pack_f16(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up);
+            qb[b][q][j][1] = pack_f16(__uint_as_float(y << 16) * up, __uint_as_float(y & 0xffff0000u) * up);
+          }
+        const int lr = key_limit(p, len, n, tok);
+#pragma unroll
+        for (int e2 = 0; e2 < 2; ++e2) {
+          f[b][e2] = __shfl_sync(0xffffffffu, fr, 8 * c + 4 * e2);
+          lim[b][e2] = __shfl_sync(0xffffffffu, lr, 8 * c + 4 * e2);
+          m[b][e2] = -INFINITY;
+          l[b][e2] = 0.f;
+        }
+        if (b == 0) lim_all = __shfl_sync(0xffffffffu, lr, 0);        // the first token's
+        if (b == NB - 1) lim_any = __shfl_sync(0xffffffffu, lr, 28);  // the last one's
+#pragma unroll
+        for (int j = 0; j < MT; ++j) o[b][j][0] = o[b][j][1] = o[b][j][2] = o[b][j][3] = 0.f;
+      }
+      vref = 0.f;
+      int key0 = im->k0 * kUnit + part;
+#pragma unroll 1
+      for (int u = 0; u < count; ++u, key0 += kUnit) {
+        const int s = stage;
+        if (!wait_bar(bar(C::B_FULL + s), turn, wc)) return;
+        const UnitMeta* mt = metas + s;
+        const int pa = part >> p.page_log2, pb = (part + 16) >> p.page_log2;  // pages of its two 16 keys
+        const bool la = (mt->pages >> pa) & 1, lb = (mt->pages >> pb) & 1;
+        if (key0 < lim_any && (la || lb)) {
+          const uint32_t kb = sb + C::OFF_RING + s * C::SBYTES, vb = kb + C::KBYTES;
+          // S^T = K Q^T: twice 16 keys by 8 rows of a block.
+          float acc[NB][2][4] = {};
+#pragma unroll
+          for (int q = 0; q < QI; ++q) {
+            const uint32_t ka = (kb + koff) ^ (64 * q);
+            const uint4 w0 = lds_u4(ka), w1 = lds_u4(ka + 8 * D), w2 = lds_u4(ka + 16 * D), w3 = lds_u4(ka + 24 * D);
+            const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
+            const uint32_t x2[4] = {w2.x, w2.y, w2.z, w2.w}, x3[4] = {w3.x, w3.y, w3.z, w3.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t a0[4] = {widen(x0[j]), widen(x1[j]), widen(x0[j] >> 16), widen(x1[j] >> 16)};
+              const uint32_t a1[4] = {widen(x2[j]), widen(x3[j]), widen(x2[j] >> 16), widen(x3[j] >> 16)};
+#pragma unroll
+              for (int b = 0; b < NB; ++b) {
+                mma_f16(acc[b][0], a0, qb[b][q][j][0], qb[b][q][j][1]);
+                mma_f16(acc[b][1], a1, qb[b][q][j][0], qb[b][q][j][1]);
               }
             }
           }
+          // Keys ko, ko + 8 (and 16 on) of rows 2c, 2c + 1.
+          const float vsa = mt->vs[pa], vsb = mt->vs[pb];
+          const float ksa = mt->ks[pa], ksb = mt->ks[pb];
+          const bool edge = key0 + 32 > lim_all || !la || !lb;
+          const float vsm = fmaxf(la ? vsa : 0.f, lb ? vsb : 0.f);
+          const float vnew = fmaxf(vref, vsm);
+          const float rv = vnew > vref && vref > 0.f ? __fdiv_rn(vref, vnew) : vnew > vref ? 0.f : 1.f;
+          vref = vnew;
+          const float rra = vsa == vref ? kPScale : vref > 0.f ? __fdiv_rn(vsa, vref) * kPScale : vsa;
+          const float rrb = vsb == vref ? kPScale : vref > 0.f ? __fdiv_rn(vsb, vref) * kPScale : vsb;
+          uint32_t pt[NB][4];  // P^T with row g and the keys of a column pair in a lane
 #pragma unroll
-          for (int y = 0; y < D / 32; ++y) {
-            const uint32_t a01 = __byte_perm(w[0][y], w[1][y], 0x5140), a23 = __byte_perm(w[0][y], w[1][y], 0x7362);
-            const uint32_t b01 = __byte_perm(w[2][y], w[3][y], 0x5140), b23 = __byte_perm(w[2][y], w[3][y], 0x7362);
-            const uint32_t t0[4] = {widen(a01), widen(a01 >> 16), widen(b01), widen(b01 >> 16)};
-            const uint32_t t1[4] = {widen(a23), widen(a23 >> 16), widen(b23), widen(b23 >> 16)};
+          for (int b = 0; b < NB; ++b) {
+            float ca0 = f[b][0] * ksa, ca1 = f[b][1] * ksa, cb0 = f[b][0] * ksb, cb1 = f[b][1] * ksb;
+            if (edge) {
+              // A factor that underflowed must not meet the infinities (any sum times 1e-37 is 0 as well).
+              ca0 = fmaxf(ca0, 1e-37f);
+              ca1 = fmaxf(ca1, 1e-37f);
+              cb0 = fmaxf(cb0, 1e-37f);
+              cb1 = fmaxf(cb1, 1e-37f);
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-              mma_f16(o[b][2 * y], t0, pt[b][2 * hf], pt[b][2 * hf + 1]);
-              mma_f16(o[b][2 * y + 1], t1, pt[b][2 * hf], pt[b][2 * hf + 1]);
+              for (int e = 0; e < 8; ++e)
+                if (key0 + 8 * (e >> 1) + ko >= lim[b][e & 1] || !(e < 4 ? la : lb)) acc[b][e >> 2][e & 3] = -INFINITY;
+            }
+            float mx0 = fmaxf(fmaxf(acc[b][0][0], acc[b][0][2]) * ca0, fmaxf(acc[b][1][0], acc[b][1][2]) * cb0);
+            float mx1 = fmaxf(fmaxf(acc[b][0][1], acc[b][0][3]) * ca1, fmaxf(acc[b][1][1], acc[b][1][3]) * cb1);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+              mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
+              mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
+            }
+            if (__any_sync(0xffffffffu, mx0 > m[b][0] || mx1 > m[b][1]) || rv != 1.f) {
+              const float n0 = fmaxf(m[b][0], mx0), n1 = fmaxf(m[b][1], mx1);
+              const float a0 = n0 > m[b][0] ? ex2(m[b][0] - n0) : 1.f, a1 = n1 > m[b][1] ? ex2(m[b][1] - n1) : 1.f;
+              l[b][0] *= a0;
+              l[b][1] *= a1;
+              const float b0 = a0 * rv, b1 = a1 * rv;
+#pragma unroll
+              for (int j = 0; j < MT; ++j) {
+                o[b][j][0] *= b0;
+                o[b][j][1] *= b1;
+                o[b][j][2] *= b0;
+                o[b][j][3] *= b1;
+              }
+              m[b][0] = n0;
+              m[b][1] = n1;
+            }
+            const float u0 = m[b][0] == -INFINITY ? 0.f : m[b][0], u1 = m[b][1] == -INFINITY ? 0.f : m[b][1];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float rr = e ? rrb : rra, c0 = e ? cb0 : ca0, c1 = e ? cb1 : ca1;
+              const float x0 = ex2(fmaf(acc[b][e][0], c0, -u0)), x1 = ex2(fmaf(acc[b][e][1], c1, -u1));
+              const float x2 = ex2(fmaf(acc[b][e][2], c0, -u0)), x3 = ex2(fmaf(acc[b][e][3], c1, -u1));
+              l[b][0] += x0 + x2;
+              l[b][1] += x1 + x3;
+              pt[b][2 * e] = transpose8(pack_f16(x0 * rr, x1 * rr));
+              pt[b][2 * e + 1] = transpose8(pack_f16(x2 * rr, x3 * rr));
+            }
+          }
+          // O^T += V^T P^T: row g of tile t is column 16 cg + 2t (d = 64: 8g + 2t), row g + 8 the one after.
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t w[4][D / 32];  // four V rows' piece: keys kv0, kv1, kv0 + 8, kv1 + 8
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t va = vb + ((e & 1) ? voff1 : voff0) + (16 * hf + 8 * (e >> 1)) * D;
+              if constexpr (D == 128) {
+                const uint4 v = lds_u4(va);
+                w[e][0] = v.x;
+                w[e][1] = v.y;
+                w[e][2] = v.z;
+                w[e][3] = v.w;
+              } else {
+                const uint2 v = lds_u2(va);
+                w[e][0] = v.x;
+                w[e][1] = v.y;
+              }
+            }
+            if (edge) {  // V rows that no row of the tile sees hold anything, a NaN too
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int key = key0 + 16 * hf + 8 * (e >> 1) + ((e & 1) ? kv1 : kv0);
+                const bool seen = key < lim_any && (hf ? lb : la);
+#pragma unroll
+                for (int y = 0; y < D / 32; ++y) {
+                  const uint32_t bad = seen && key >= lim_all ? nan_codes(w[e][y]) : 0u;
+                  if (bad) nans[i % kItems] = i + 1;
+                  w[e][y] = seen ? w[e][y] & ~bad : 0u;
+                }
+              }
+            }
+#pragma unroll
+            for (int y = 0; y < D / 32; ++y) {
+              const uint32_t a01 = __byte_perm(w[0][y], w[1][y], 0x5140), a23 = __byte_perm(w[0][y], w[1][y], 0x7362);
+              const uint32_t b01 = __byte_perm(w[2][y], w[3][y], 0x5140), b23 = __byte_perm(w[2][y], w[3][y], 0x7362);
+              const uint32_t t0[4] = {widen(a01), widen(a01 >> 16), widen(b01), widen(b01 >> 16)};
+              const uint32_t t1[4] = {widen(a23), widen(a23 >> 16), widen(b23), widen(b23 >> 16)};
+#pragma unroll
+              for (int b = 0; b < NB; ++b) {
+                mma_f16(o[b][2 * y], t0, pt[b][2 * hf], pt[b][2 * hf + 1]);
+                mma_f16(o[b][2 * y + 1], t1, pt[b][2 * hf], pt[b][2 * hf + 1]);
+              }
             }
           }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::B_EMPTY + s));
+        if (++stage == C::STAGES) {
+          stage = 0;
+          turn ^= 1;
+        }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(C::B_EMPTY + s));
-      if (++stage == C::STAGES) {
-        stage = 0;
-        turn ^= 1;
-      }
-    }
 
-    // The item's end: the warps' sums meet in shared memory.
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], d);
-    float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
-    float4* so = reinterpret_cast<float4*>(smem + C::OFF_O);
-    const float back = vref * (1.f / kPScale);
-    // Place of 16-byte piece q4 of a row: exchanged with its neighbours so that
-    // the eight lanes of a store (four rows, two pieces) meet no bank twice.
-    auto at = [&](int w_, int row, int q4) {
-      const int c2 = (row >> 1) & 3;
-      const int x = D == 128 ? c2 | ((q4 >> 4) << 2) : (c2 & 1) | ((c2 >> 1) << 2);
-      return (w_ * kRows + row) * (D / 4) + (q4 ^ x);
-    };
-    // The last item's sums have been read.
-    if (i > 0 && !wait_bar(bar(C::B_READ), (i - 1) & 1, wc)) return;
-    if (warp >= kHalf) {
-      // Hand over to warp - kHalf, lane by lane.
-      float4* to = so + (warp - kHalf) * kRows * (D / 4) + lane;
+      // The item's end: the warps' sums meet in shared memory.
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int j = 0; j < MT; ++j)
-          to[32 * (b * MT + j)] =
-              make_float4(o[b][j][0] * back, o[b][j][1] * back, o[b][j][2] * back, o[b][j][3] * back);
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], d);
+      float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
+      float4* so = reinterpret_cast<float4*>(smem + C::OFF_O);
+      const float back = vref * (1.f / kPScale);
+      // Place of 16-byte piece q4 of a row: exchanged with its neighbours so that
+      // the eight lanes of a store (four rows, two pieces) meet no bank twice.
+      auto at = [&](int w_, int row, int q4) {
+        const int c2 = (row >> 1) & 3;
+        const int x = D == 128 ? c2 | ((q4 >> 4) << 2) : (c2 & 1) | ((c2 >> 1) << 2);
+        return (w_ * kRows + row) * (D / 4) + (q4 ^ x);
+      };
+      // The last item's sums have been read.
+      if (i > 0 && !wait_bar(bar(C::B_READ), (i - 1) & 1, wc)) return;
+      if (warp >= kHalf) {
+        // Hand over to warp - kHalf, lane by lane.
+        float4* to = so + (warp - kHalf) * kRows * (D / 4) + lane;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int j = 0; j < MT; ++j)
+            to[32 * (b * MT + j)] =
+                make_float4(o[b][j][0] * back, o[b][j][1] * back, o[b][j][2] * back, o[b][j][3] * back);
+        if (g == 0)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              ml[(warp - kHalf) * kRows + 8 * b + 2 * c + e] = make_float2(m[b][e], l[b][e]);
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(C::B_GIVEN));
+          mbar_arrive(bar(C::B_IEMPTY + i % kItems));
+        }
+        continue;
+      }
+      const int slot = im->slot;
+      if (!wait_bar(bar(C::B_GIVEN), i & 1, wc)) return;
+      const float4* from = so + warp * kRows * (D / 4) + lane;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        float wa[2], wb[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 gv = ml[warp * kRows + 8 * b + 2 * c + e];
+          const float mn = fmaxf(m[b][e], gv.x), r = mn == -INFINITY ? 0.f : mn;
+          const float x = ex2(m[b][e] - r);
+          wb[e] = ex2(gv.x - r);
+          wa[e] = back * x;
+          l[b][e] = l[b][e] * x + gv.y * wb[e];
+          m[b][e] = mn;
+        }
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          const float4 v = from[32 * (b * MT + j)];
+          o[b][j][0] = fmaf(o[b][j][0], wa[0], v.x * wb[0]);
+          o[b][j][1] = fmaf(o[b][j][1], wa[1], v.y * wb[1]);
+          o[b][j][2] = fmaf(o[b][j][2], wa[0], v.z * wb[0]);
+          o[b][j][3] = fmaf(o[b][j][3], wa[1], v.w * wb[1]);
+        }
+      }
+      __syncwarp();
+      ml += kHalf * kRows;
       if (g == 0)
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            ml[(warp - kHalf) * kRows + 8 * b + 2 * c + e] = make_float2(m[b][e], l[b][e]);
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(C::B_GIVEN));
-        mbar_arrive(bar(C::B_IEMPTY + i % kItems));
-      }
-      continue;
-    }
-    const int slot = im->slot;
-    if (!wait_bar(bar(C::B_GIVEN), i & 1, wc)) return;
-    const float4* from = so + warp * kRows * (D / 4) + lane;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      float wa[2], wb[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float2 gv = ml[warp * kRows + 8 * b + 2 * c + e];
-        const float mn = fmaxf(m[b][e], gv.x), r = mn == -INFINITY ? 0.f : mn;
-        const float x = ex2(m[b][e] - r);
-        wb[e] = ex2(gv.x - r);
-        wa[e] = back * x;
-        l[b][e] = l[b][e] * x + gv.y * wb[e];
-        m[b][e] = mn;
-      }
-#pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        const float4 v = from[32 * (b * MT + j)];
-        o[b][j][0] = fmaf(o[b][j][0], wa[0], v.x * wb[0]);
-        o[b][j][1] = fmaf(o[b][j][1], wa[1], v.y * wb[1]);
-        o[b][j][2] = fmaf(o[b][j][2], wa[0], v.z * wb[0]);
-        o[b][j][3] = fmaf(o[b][j][3], wa[1], v.w * wb[1]);
-      }
-    }
-    __syncwarp();
-    ml += kHalf * kRows;
-    if (g == 0)
+          for (int e = 0; e < 2; ++e) ml[warp * kRows + 8 * b + 2 * c + e] = make_float2(m[b][e], l[b][e]);
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) ml[warp * kRows + 8 * b + 2 * c + e] = make_float2(m[b][e], l[b][e]);
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int x = 0; x < MT / 2; ++x)
-          so[at(warp, 8 * b + 2 * c + e, (D == 128 ? 4 * cg : 2 * g) + x)] =
-              make_float4(o[b][2 * x][e], o[b][2 * x][2 + e], o[b][2 * x + 1][e], o[b][2 * x + 1][2 + e]);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar(C::B_WRITTEN));
-    if (!wait_bar(bar(C::B_WRITTEN), i & 1, wc)) return;
+          for (int x = 0; x < MT / 2; ++x)
+            so[at(warp, 8 * b + 2 * c + e, (D == 128 ? 4 * cg : 2 * g) + x)] =
+                make_float4(o[b][2 * x][e], o[b][2 * x][2 + e], o[b][2 * x + 1][e], o[b][2 * x + 1][2 + e]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::B_WRITTEN));
+      if (!wait_bar(bar(C::B_WRITTEN), i & 1, wc)) return;
 #pragma unroll 1
-    for (int x = threadIdx.x; x < rows * (D / 4); x += 32 * kHalf) {
-      const int row = x / (D / 4), q4 = x % (D / 4);
-      float M = -INFINITY;
+      for (int x = threadIdx.x; x < rows * (D / 4); x += 32 * kHalf) {
+        const int row = x / (D / 4), q4 = x % (D / 4);
+        float M = -INFINITY;
 #pragma unroll 4
-      for (int w_ = 0; w_ < kHalf; ++w_) M = fmaxf(M, ml[w_ * kRows + row].x);
-      const float ref = M == -INFINITY ? 0.f : M;
-      float L = 0.f;
-      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w_ = 0; w_ < kHalf; ++w_) M = fmaxf(M, ml[w_ * kRows + row].x);
+        const float ref = M == -INFINITY ? 0.f : M;
+        float L = 0.f;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-      for (int w_ = 0; w_ < kHalf; ++w_) {
-        const float2 st = ml[w_ * kRows + row];
-        const float wgt = ex2(st.x - ref);
-        const float4 v = so[at(w_, row, q4)];
-        L += wgt * st.y;
-        sum.x += wgt * v.x;
-        sum.y += wgt * v.y;
-        sum.z += wgt * v.z;
-        sum.w += wgt * v.w;
-      }
-      if (nans[i % kItems] == i + 1) {
-        const int tok = (tile * kRows + row) / p.G;
-        const int from = max(im->k0 * kUnit, lim_all), to = min((im->k0 + count) * kUnit, key_limit(p, len, n, tok));
+        for (int w_ = 0; w_ < kHalf; ++w_) {
+          const float2 st = ml[w_ * kRows + row];
+          const float wgt = ex2(st.x - ref);
+          const float4 v = so[at(w_, row, q4)];
+          L += wgt * st.y;
+          sum.x += wgt * v.x;
+          sum.y += wgt * v.y;
+          sum.z += wgt * v.z;
+          sum.w += wgt * v.w;
+        }
+        if (nans[i % kItems] == i + 1) {
+          const int tok = (tile * kRows + row) / p.G;
+          const int from = max(im->k0 * kUnit, lim_all), to = min((im->k0 + count) * kUnit, key_limit(p, len, n, tok));
 #pragma unroll 1
-        for (int key = from; key < to; ++key) {
-          const uint32_t bad = nan_codes(v_codes(p.v_pages, p.block_table, p.num_pages, p.page_log2, p.Hkv, D,
-                                                 (size_t)im->req * p.max_pages, key, h, q4 * 4));
-          if (bad & 0xffu) sum.x = NAN;
-          if (bad & 0xff00u) sum.y = NAN;
-          if (bad & 0xff0000u) sum.z = NAN;
-          if (bad & 0xff000000u) sum.w = NAN;
+          for (int key = from; key < to; ++key) {
+            const uint32_t bad = nan_codes(v_codes(p.v_pages, p.block_table, p.num_pages, p.page_log2, p.Hkv, D,
+                                                   (size_t)im->req * p.max_pages, key, h, q4 * 4));
+            if (bad & 0xffu) sum.x = NAN;
+            if (bad & 0xff00u) sum.y = NAN;
+            if (bad & 0xff0000u) sum.z = NAN;
+            if (bad & 0xff000000u) sum.w = NAN;
+          }
+        }
+        if (slot >= 0) {
+          const size_t base = (size_t)(blockIdx.x * 2 + slot) * kRows + row;
+          *reinterpret_cast<float4*>(p.part_o + base * D + q4 * 4) = sum;
+          if (q4 == 0) *reinterpret_cast<float2*>(p.part_ml + base * 2) = make_float2(M, L);
+        } else {
+          const size_t orow = output_row(p, start, h, tile * kRows + row);
+          const float inv = output_factor(L);
+          if (p.out_f32)
+            *reinterpret_cast<float4*>(static_cast<float*>(p.O) + orow * D + q4 * 4) =
+                make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
+          else
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) + orow * D + q4 * 4) =
+                make_uint2(pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
+          if (q4 == 0) p.LSE[orow] = output_lse(M, L);
         }
       }
-      if (slot >= 0) {
-        const size_t base = (size_t)(blockIdx.x * 2 + slot) * kRows + row;
-        *reinterpret_cast<float4*>(p.part_o + base * D + q4 * 4) = sum;
-        if (q4 == 0) *reinterpret_cast<float2*>(p.part_ml + base * 2) = make_float2(M, L);
-      } else {
-        const size_t orow = output_row(p, start, h, tile * kRows + row);
-        const float inv = output_factor(L);
-        if (p.out_f32)
-          *reinterpret_cast<float4*>(static_cast<float*>(p.O) + orow * D + q4 * 4) =
-              make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
-        else
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) + orow * D + q4 * 4) =
-              make_uint2(pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
-        if (q4 == 0) p.LSE[orow] = output_lse(M, L);
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(C::B_READ));
+        mbar_arrive(bar(C::B_IEMPTY + i % kItems));
       }
     }
-    __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(bar(C::B_READ));
-      mbar_arrive(bar(C::B_IEMPTY + i % kItems));
-    }
-  }
+  };
+  consume();
+  // A wait that gave up.
+  if (*abort_flag && lane == 0) atomicCAS(p.status, kDevOk, kDevTimeout);
 }
 
 }  // namespace

@@ -195,9 +195,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const WaitCtx wc{abort_flag, p.status, p.wait_limit_ns};
+  volatile int* const wc = abort_flag;
+  const WaitCtx drain{abort_flag, p.status, p.wait_limit_ns};
   // Item i, for a consumer warp.
-  auto wait_item = [&](int i) -> bool { return mbar_wait_warp(bar(C::B_IFULL + i % kItems), (i / kItems) & 1, wc); };
+  auto wait_item = [&](int i) -> bool { return wait_bar(bar(C::B_IFULL + i % kItems), (i / kItems) & 1, wc); };
   auto release_item = [&](int i) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(C::B_IEMPTY + i % kItems));
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int u = 0;          // units loaded
       int items_out = 0;  // items announced
       auto reuse = [&](int b, int n, int ring) -> bool {  // wait until place n % ring is free again
-        return n < ring || mbar_wait_warp(bar(b + n % ring), ((n / ring) & 1) ^ 1, wc);
+        return n < ring || wait_bar(bar(b + n % ring), ((n / ring) & 1) ^ 1, wc);
       };
       auto announce = [&](const Item& im) -> bool {
         if (!reuse(C::B_IEMPTY, items_out, kItems)) return false;
@@ -268,9 +269,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // Copies in flight land before the CTA leaves: those of the units loaded
       // whole, and K's of one whose loading was given up.
-      for (int k = max(0, u - C::KS); k < u; ++k) mbar_wait_drain_warp(bar(C::B_KFULL + k % C::KS), (k / C::KS) & 1, wc);
-      for (int k = max(0, u - C::VS); k < u; ++k) mbar_wait_drain_warp(bar(C::B_VFULL + k % C::VS), (k / C::VS) & 1, wc);
-      if (!ok) mbar_wait_drain_warp(bar(C::B_KFULL + u % C::KS), (u / C::KS) & 1, wc);
+      for (int k = max(0, u - C::KS); k < u; ++k) mbar_wait_drain_warp(bar(C::B_KFULL + k % C::KS), (k / C::KS) & 1, drain);
+      for (int k = max(0, u - C::VS); k < u; ++k) mbar_wait_drain_warp(bar(C::B_VFULL + k % C::VS), (k / C::VS) & 1, drain);
+      if (!ok) mbar_wait_drain_warp(bar(C::B_KFULL + u % C::KS), (u / C::KS) & 1, drain);
       griddep_launch_dependents();
     } else if (warp < 3) {
       // ---------------------------------------------------------- MMA issuers
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n < 0) break;
         if (n == 0) continue;
         auto wait_ring = [&](int b, int k, int ring) -> bool {
-          if (!mbar_wait_warp(bar(b + k % ring), (k / ring) & 1, wc)) return false;
+          if (!wait_bar(bar(b + k % ring), (k / ring) & 1, wc)) return false;
           tc_fence_after();
           return true;
         };
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto wait_sbuf = [&]() -> bool {
           if (t == 0 && ns == 0) return true;
           const int phase = t == 0 ? ns - 1 : ns;
-          if (!mbar_wait_warp(bar(C::B_SREAD + (t ^ 1)), phase & 1, wc)) return false;
+          if (!wait_bar(bar(C::B_SREAD + (t ^ 1)), phase & 1, wc)) return false;
           tc_fence_after();
           return true;
         };
@@ -331,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_commit_warp(bar(C::B_ODONE + t));
           tc_commit_warp(bar(C::B_WEMPTY + s));
         };
-        ok = wait_sbuf() && mbar_wait_warp(bar(C::B_QFULL + t), qn & 1, wc) && wait_ring(C::B_KFULL, u0, C::KS);
+        ok = wait_sbuf() && wait_bar(bar(C::B_QFULL + t), qn & 1, wc) && wait_ring(C::B_KFULL, u0, C::KS);
         if (ok) issue_s(0);
         for (int j = 0; j < n && ok; ++j) {
           if (j + 1 < n) {
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             issue_s(j + 1);
           }
-          ok = wait_ring(C::B_WFULL, u0 + j, C::WS) && mbar_wait_warp(bar(C::B_PFULL + t), pf & 1, wc);
+          ok = wait_ring(C::B_WFULL, u0 + j, C::WS) && wait_bar(bar(C::B_PFULL + t), pf & 1, wc);
           if (!ok) break;
           ++pf;
           tc_fence_after();
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // All products of this warp complete before TMEM is released.
       tc_commit_warp(bar(C::B_DRAIN + t));
-      mbar_wait_drain_warp(bar(C::B_DRAIN + t), 0, wc);
+      mbar_wait_drain_warp(bar(C::B_DRAIN + t), 0, drain);
     }
   } else if (warp < 8) {
     regs_dec<kRegsWiden>();
@@ -370,9 +371,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n < 0) break;
       for (int j = 0; j < n; ++j, ++u) {
         const int sv = u % C::VS, sw = u % C::WS;
-        if (!mbar_wait_warp(bar(C::B_MFULL + u % kMetas), (u / kMetas) & 1, wc) ||
-            !mbar_wait_warp(bar(C::B_VFULL + sv), (u / C::VS) & 1, wc) ||
-            (u >= C::WS && !mbar_wait_warp(bar(C::B_WEMPTY + sw), ((u / C::WS) & 1) ^ 1, wc))) {
+        if (!wait_bar(bar(C::B_MFULL + u % kMetas), (u / kMetas) & 1, wc) ||
+            !wait_bar(bar(C::B_VFULL + sv), (u / C::VS) & 1, wc) ||
+            (u >= C::WS && !wait_bar(bar(C::B_WEMPTY + sw), ((u / C::WS) & 1) ^ 1, wc))) {
           ok = false;
           break;
         }
@@ -382,11 +383,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool whole = all >= kUnit && pages == (1u << (kUnit >> p.page_log2)) - 1;
         constexpr int PC = D / 16;  // pieces of a row
         const uint32_t src = sb + C::OFF_V + sv * C::T8, dst = sb + C::OFF_W + sw * C::T16;
-#pragma unroll 4
-        for (int x = 0; x < kUnit * PC / 128; ++x) {
+        // Piece x of this thread, widened.
+        auto put = [&](int x, const uint4& v) {
           const int e = wl + 128 * x, row = e / PC, pc = e % PC;
-          uint4 v = lds_u4(piece<D>(src, row, pc));
-          if (!whole) {
+          const uint32_t base = dst + (pc >> 2) * 16384 + row * 128;
+          const int c0 = 2 * (pc & 3);
+          // The two halves in an order that keeps the eight lanes of a row off each other's banks.
+          const int flip = pc >> 2;
+          const uint32_t first[2] = {flip ? v.z : v.x, flip ? v.w : v.y}, second[2] = {flip ? v.x : v.z, flip ? v.y : v.w};
+          sts_u4(base + (((c0 + flip) ^ (row & 7)) << 4), widen(first[0]), widen(first[0] >> 16), widen(first[1]),
+                 widen(first[1] >> 16));
+          sts_u4(base + (((c0 + 1 - flip) ^ (row & 7)) << 4), widen(second[0]), widen(second[0] >> 16),
+                 widen(second[1]), widen(second[1] >> 16));
+        };
+        constexpr int NX = kUnit * PC / 128;  // pieces of a thread
+        if (whole) {
+#pragma unroll 1
+          for (int x0 = 0; x0 < NX; x0 += 4) {
+            uint4 v[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int e = wl + 128 * (x0 + x);
+              v[x] = lds_u4(piece<D>(src, e / PC, e % PC));
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) put(x0 + x, v[x]);
+          }
+        } else {
+#pragma unroll 1
+          for (int x = 0; x < NX; ++x) {
+            const int e = wl + 128 * x, row = e / PC;
+            uint4 v = lds_u4(piece<D>(src, row, e % PC));
             if (row >= valid || !((pages >> (row >> p.page_log2)) & 1)) {
               v = make_uint4(0, 0, 0, 0);
             } else if (row >= all) {  // some rows do not see it
@@ -394,20 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (b0 | b1 | b2 | b3) nans[i % kItems] = i + 1;
               v = make_uint4(v.x & ~b0, v.y & ~b1, v.z & ~b2, v.w & ~b3);
             }
-          }
-          const uint32_t base = dst + (pc >> 2) * 16384 + row * 128;
-          const int c0 = 2 * (pc & 3);
-          // The two halves in an order that keeps the eight lanes of a row off each other's banks.
-          const int flip = pc >> 2;
-          const uint32_t lo[4] = {widen(v.x), widen(v.x >> 16), widen(v.y), widen(v.y >> 16)};
-          const uint32_t hi[4] = {widen(v.z), widen(v.z >> 16), widen(v.w), widen(v.w >> 16)};
-          const uint32_t a = base + (((c0 + flip) ^ (row & 7)) << 4), b = base + (((c0 + 1 - flip) ^ (row & 7)) << 4);
-          if (flip) {
-            sts_u4(a, hi[0], hi[1], hi[2], hi[3]);
-            sts_u4(b, lo[0], lo[1], lo[2], lo[3]);
-          } else {
-            sts_u4(a, lo[0], lo[1], lo[2], lo[3]);
-            sts_u4(b, hi[0], hi[1], hi[2], hi[3]);
+            put(x, v);
           }
         }
         fence_async_smem();
@@ -453,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               (long long)(im->h * p.G + min(rho, last) - tok * p.G) * D);
           uint32_t am = 0;
           bool odd = false;
-#pragma unroll 4
+#pragma unroll 2
           for (int x = 0; x < D / 8; ++x) {
             const uint4 v = __ldg(src + x);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -467,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           k = min(max(k, -110), 118);
           const float down = __int_as_float((127 - k) << 23);
           f = odd ? NAN : __int_as_float((127 + k) << 23) * p.scale_log2;
-#pragma unroll 2
+#pragma unroll 1
           for (int x = 0; x < D / 16; ++x) {
             uint32_t hi[4], lo[4];
 #pragma unroll
@@ -497,8 +511,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float lvref = -1e30f;  // log2 of the largest V scale seen
       for (int j = 0; j < n; ++j, ++u) {
         const int key0 = (im->k0 + j) * kUnit;
-        if (!mbar_wait_warp(bar(C::B_MFULL + u % kMetas), (u / kMetas) & 1, wc) ||
-            !mbar_wait_warp(bar(C::B_SFULL + t), sg & 1, wc)) {
+        if (!wait_bar(bar(C::B_MFULL + u % kMetas), (u / kMetas) & 1, wc) ||
+            !wait_bar(bar(C::B_SFULL + t), sg & 1, wc)) {
           ok = false;
           break;
         }
@@ -509,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
           release(C::B_SREAD + t);
           if (lane == 0) mbar_arrive(bar(C::B_MEMPTY + u % kMetas));
-          if (j > 0 && !mbar_wait_warp(bar(C::B_ODONE + t), sg & 1, wc)) {
+          if (j > 0 && !wait_bar(bar(C::B_ODONE + t), sg & 1, wc)) {
             ok = false;
             break;
           }
@@ -601,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         release(C::B_MEMPTY + u % kMetas);
         if (j > 0) {
           // The item's last P_t V has completed: it read the P_t written below, and O_t may be scaled.
-          if (!mbar_wait_warp(bar(C::B_ODONE + t), sg & 1, wc)) {  // phase sg - 2
+          if (!wait_bar(bar(C::B_ODONE + t), sg & 1, wc)) {  // phase sg - 2
             ok = false;
             break;
           }
@@ -627,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       if (n > 0) {
-        if (!mbar_wait_warp(bar(C::B_ODONE + t), (sg - 1) & 1, wc)) break;
+        if (!wait_bar(bar(C::B_ODONE + t), (sg - 1) & 1, wc)) break;
         tc_fence_after();
       }
       if (live) {
@@ -638,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const size_t prow = (size_t)(blockIdx.x * 2 + max(im->slot, 0)) * kPagedWideRows + t * kBM + row;
         // bf16 rows go through the warp's quarter of the Q tile (whose products have completed).
         const uint32_t stage = q_hi + quad * 32 * D;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           if (n > 0) {
@@ -714,6 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  if (threadIdx.x == 0 && *abort_flag) atomicCAS(p.status, kDevOk, kDevTimeout);
 }
 
 template <int D>
