@@ -268,7 +268,8 @@ size_t attn_bwd_workspace_size(int B, int Hq, int Hkv, int N, int d);
  * The cache is caller-owned device memory: pages of page_size tokens (16, 32,
  * 64 or 128), for keys and for values
  *   pages  [num_pages, Hkv, page_size, d] uint8 e4m3 codes (d in {64, 128}),
- *   scale  [num_pages, Hkv] fp32, > 0: an element's value is code * scale.
+ *   scale  [num_pages, Hkv] fp32, > 0: an element's value is code * scale
+ * (Hkv <= 32767).
  * Token i of request r lies in page block_table[r][i / page_size], at offset
  * i % page_size.  num_pages * Hkv < 2^31, max_pages * page_size < 2^31.
  * The notes this library follows name paged attention and FP8 without an
@@ -294,9 +295,12 @@ size_t attn_bwd_workspace_size(int B, int Hq, int Hkv, int N, int d);
  *                  for those of refused requests and behind the last token
  *   positions      [T]    index of the token in its request; -1 likewise
  *   taken          [2]    pages taken from the head of free_pages; requests refused
- * All outputs but block_table are fully overwritten.  R >= 1, T >= 0 (slots
- * and positions may be NULL when T is 0).  slots is 8-byte aligned, the rest
- * 4-byte.  Page ids are copied as they are.
+ * All outputs but block_table are fully overwritten; none may overlap cached,
+ * added or free_pages (ATTN_ERR_INVALID_ARG).  R >= 1, T >= 0 (slots and
+ * positions may be NULL when T is 0).  slots is 8-byte aligned, the rest
+ * 4-byte.  Page ids are copied as they are.  A refused request keeps its
+ * places in the step's arrays: its tokens are appended nowhere, and attention
+ * over its rows takes them for the last ones of the cached tokens.
  */
 attn_status attn_kv_tables(const int32_t* cached, const int32_t* added, const int32_t* free_pages, int n_free,
                            int32_t* block_table, int max_pages, int page_size, int32_t* kv_lens,
@@ -323,7 +327,7 @@ attn_status attn_kv_tables(const int32_t* cached, const int32_t* added, const in
  *         between tokens (>= Hkv * d, a multiple of 8: slices of a packed
  *         projection do)
  *   slots [T] int64;  pages and scales as above, updated in place.
- * T >= 0; Hkv <= 65535.
+ * T >= 0.
  */
 attn_status attn_kv_append_fp8(const void* K, long long k_stride, const void* V, long long v_stride,
                                const int64_t* slots, void* k_pages, float* k_scale, void* v_pages, float* v_scale,
@@ -336,10 +340,14 @@ attn_status attn_kv_append_fp8(const void* K, long long k_stride, const void* V,
  * keys), as in attn_fwd_split; kept keys give
  *   s_ij = scale * <Q_i, k_j>, O_i = sum_j softmax_j(s_i) v_j, LSE_i = ln sum_j e^{s_ij},
  * k_j and v_j being code * scale of their page.  A row with no kept key gets
- * O = 0 and LSE = -inf.  Rows t >= cu_q[R] are left as they were.  Products
- * run in f16 with fp32 sums (codes are exact in f16; so are bf16 queries down
- * to 2^-29 of their row's largest element); the weights are rounded to f16,
- * the sums of the softmax are not.
+ * O = 0 and LSE = -inf.  Rows t >= cu_q[R] are left as they were.  A NaN or
+ * infinity in a row of Q makes that row NaN, one in K or V the rows that see
+ * it.  The codes enter the products exactly and sums are fp32.  Queries enter
+ * exactly down to 2^-10 of their row's largest element, and off by at most
+ * 2^-17 of it below.  The weights are rounded to f16 (2^-11 relative, for
+ * weights down to 2^-23 of the row's largest and V scales of like size: the
+ * product of a weight and its page's V scale relative to the largest V scale
+ * of the request and head counts); the sums of the softmax are not rounded.
  *   Q   [T, Hq, d] bf16, 16-byte aligned, q_stride elements between tokens
  *       (>= Hq * d, a multiple of 8);  Hq % Hkv == 0
  *   block_table [R, max_pages], cu_q [R+1] (non-decreasing), kv_lens [R]
