@@ -194,19 +194,20 @@ struct PagedFwdParams {
   int* desc;
   int* status;
   int R, T, Hq, Hkv, G, num_pages, page_log2, max_pages;
+  int behind;              // launched behind the other kernel of the call: its end is waited for, not its start
   int rows_min, rows_max;  // the launch takes the requests with rows_min < n * G <= rows_max
   float scale_log2;
   int causal, out_f32;
   unsigned long long wait_limit_ns;
 };
 // The kernels: 8 or 16 query rows of a kv head to a tile (paged_fwd.cu), and
-// 256 (paged_wide.cu).  `behind`: launched behind the other one, whose end it
+// 256 (paged_wide.cu).  p.behind: launched behind the other one, whose end it
 // overlaps and which it outlasts.
 constexpr int kPagedWideRows = 256;
 // CTAs of an SM, each a worker, by the rows of a tile.
 constexpr int paged_ctas(int rows) { return rows == 8 ? 3 : rows == 16 ? 2 : 1; }
 cudaError_t launch_paged_narrow(int d, int rows, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                const PagedFwdParams& p, int workers, bool behind, cudaStream_t stream);
+                                const PagedFwdParams& p, int workers, cudaStream_t stream);
 cudaError_t launch_paged_wide(int d, const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedFwdParams& p,
                               int workers, cudaStream_t stream);
 // Merge of the items that the one or two launches (given by their parameters,

@@ -343,11 +343,12 @@ __host__ inline void overlap_with_previous(cudaLaunchConfig_t& cfg, cudaLaunchAt
 }
 
 // Launches a kernel of `workers` CTAs with `smem` bytes of dynamic shared
-// memory.  ID tells the kernels of one signature apart: the attribute is set
-// once on a device.
+// memory, behind whatever is in the stream (it waits for that kernel before it
+// reads anything).  ID tells the kernels of one signature apart: the attribute
+// is set once on a device.
 template <int ID, class Kernel>
 cudaError_t launch_workers(Kernel kern, int threads, int smem, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                           const PagedFwdParams& p, int workers, bool overlap, cudaStream_t stream) {
+                           const PagedFwdParams& p, int workers, cudaStream_t stream) {
   static std::atomic<bool> ready[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -363,7 +364,7 @@ cudaError_t launch_workers(Kernel kern, int threads, int smem, const CUtensorMap
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = stream;
   cudaLaunchAttribute at{};
-  if (overlap) overlap_with_previous(cfg, at);
+  overlap_with_previous(cfg, at);
   return cudaLaunchKernelEx(&cfg, kern, tmK, tmV, p);
 }
 

@@ -217,6 +217,7 @@ attn_status attn_fwd_paged_fp8(const void* Q, long long q_stride, const void* k_
   const bool big = wide && (long long)T * G > kNarrowMost, small = !wide || G <= kNarrowMost;
   attn::PagedFwdParams pw = p;
   place(p, ws, rows, d, sms);
+  p.behind = big;
   p.rows_min = 0;
   p.rows_max = wide ? kNarrowMost : 0x7fffffff;
   place(pw, ws + part_bytes(rows, d, sms), attn::kPagedWideRows, d, sms);
@@ -225,7 +226,7 @@ attn_status attn_fwd_paged_fp8(const void* Q, long long q_stride, const void* k_
   cudaError_t e = cudaSuccess;
   const int wide_rows = attn::kPagedWideRows, w1 = workers_of(rows, sms), w2 = workers_of(wide_rows, sms);
   if (big) e = attn::launch_paged_wide(d, tk, tv, pw, w2, cs);
-  if (e == cudaSuccess && small) e = attn::launch_paged_narrow(d, rows, tk, tv, p, w1, big, cs);
+  if (e == cudaSuccess && small) e = attn::launch_paged_narrow(d, rows, tk, tv, p, w1, cs);
   if (e == cudaSuccess)
     e = small ? attn::launch_paged_merge(d, p, rows, w1, big ? &pw : nullptr, wide_rows, big ? w2 : 0, cs)
               : attn::launch_paged_merge(d, pw, wide_rows, w2, nullptr, 0, 0, cs);

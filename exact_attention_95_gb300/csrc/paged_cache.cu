@@ -322,6 +322,7 @@ __global__ void __launch_bounds__(kAppThreads, 4) kv_append_kernel(const KvAppen
   __shared__ long long s_slot[kMaxChunk];                       // of each run: its first slot,
   __shared__ uint16_t s_first[kMaxChunk], s_len[kMaxChunk];     // first token, tokens
   __shared__ uint32_t s_red[kWarps];
+  griddep_launch_dependents();  // the attention's start overlaps this kernel
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int P = 1 << p.page_log2;
   const long long t0 = (long long)blockIdx.x * chunk;

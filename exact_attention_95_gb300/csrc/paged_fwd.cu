@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
     for (int i = 0; i < kItems; ++i) nans[i] = 0;
     fence_mbar_init();
   }
+  if (!p.behind) griddep_wait();  // the lengths, pages and queries of the kernel before
   sum_units<kRows>(p, sums, warp, kWarps + 1, lane);
   __syncthreads();
   volatile int* const wc = abort_flag;
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
     if (*abort_flag && lane == 0) atomicCAS(p.status, kDevOk, kDevTimeout);
     griddep_launch_dependents();
     // Behind the wide kernel: this one's completion stands for both.
-    griddep_wait();
+    if (p.behind) griddep_wait();
     return;
   }
 
@@ -599,21 +600,21 @@ namespace {
 
 template <int D, int NB>
 cudaError_t launch_narrow(const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedFwdParams& p, int workers,
-                          bool behind, cudaStream_t stream) {
+                          cudaStream_t stream) {
   using C = PC<D, NB>;
   static_assert(C::CTAS == paged_ctas(C::ROWS), "workers of an SM");
-  return launch_workers<D * 2 + NB>(fwd_paged_kernel<D, NB>, C::THREADS, C::SMEM, tmK, tmV, p, workers, behind, stream);
+  return launch_workers<D * 2 + NB>(fwd_paged_kernel<D, NB>, C::THREADS, C::SMEM, tmK, tmV, p, workers, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_narrow(int d, int rows, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                const PagedFwdParams& p, int workers, bool behind, cudaStream_t stream) {
+                                const PagedFwdParams& p, int workers, cudaStream_t stream) {
   if (rows == 8)
-    return d == 128 ? launch_narrow<128, 1>(tmK, tmV, p, workers, behind, stream)
-                    : launch_narrow<64, 1>(tmK, tmV, p, workers, behind, stream);
-  return d == 128 ? launch_narrow<128, 2>(tmK, tmV, p, workers, behind, stream)
-                  : launch_narrow<64, 2>(tmK, tmV, p, workers, behind, stream);
+    return d == 128 ? launch_narrow<128, 1>(tmK, tmV, p, workers, stream)
+                    : launch_narrow<64, 1>(tmK, tmV, p, workers, stream);
+  return d == 128 ? launch_narrow<128, 2>(tmK, tmV, p, workers, stream)
+                  : launch_narrow<64, 2>(tmK, tmV, p, workers, stream);
 }
 
 }  // namespace attn

@@ -32,6 +32,7 @@ template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const MergeParams q) {
   constexpr int V = D / 32;  // columns of a lane
   __shared__ float s_acc[kMergeWarps][D], s_l[kMergeWarps];
+  griddep_launch_dependents();  // the next call's start overlaps this end
   griddep_wait();
   const bool second = (int)blockIdx.x >= q.set[0].workers;
   const MergeSet& t = q.set[second];

@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Item* items = reinterpret_cast<Item*>(smem + C::OFF_ITEM);
   long long* sums = reinterpret_cast<long long*>(smem + C::OFF_SUMS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  griddep_wait();  // the lengths, pages and queries of the kernel before
   // A batch without such requests costs a look at their row counts.
   bool any = false;
   for (int r = threadIdx.x; r < p.R; r += kThreads) any |= load_req<kPagedWideRows>(p, r).units > 0;
@@ -743,7 +744,7 @@ cudaError_t launch_wide(const CUtensorMap& tmK, const CUtensorMap& tmV, const Pa
     regs = fa.numRegs;
   }
   if (regs != kLaunchRegs) return cudaErrorInvalidKernelImage;
-  return launch_workers<D>(fwd_paged_wide_kernel<D>, kThreads, WC<D>::SMEM, tmK, tmV, p, workers, false, stream);
+  return launch_workers<D>(fwd_paged_wide_kernel<D>, kThreads, WC<D>::SMEM, tmK, tmV, p, workers, stream);
 }
 
 }  // namespace
