@@ -14,7 +14,6 @@ namespace {
 
 using namespace paged;
 
-constexpr int kMergeCtas = 4;   // of an item
 constexpr int kMergeWarps = 8;
 
 struct MergeSet {
@@ -31,7 +30,7 @@ struct MergeParams {
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const MergeParams q) {
   constexpr int V = D / 32;  // columns of a lane
-  __shared__ float s_acc[kMergeWarps][D], s_l[kMergeWarps];
+  __shared__ float s_acc[kMergeWarps][D], s_l[kMergeWarps], s_m[kMergeWarps];
   griddep_launch_dependents();  // the next call's start overlaps this end
   griddep_wait();
   const bool second = (int)blockIdx.x >= q.set[0].workers;
@@ -46,26 +45,50 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Mer
   const int rows = min(t.rows, n * p.G - tile * t.rows);
   // Warps that share a row, and this one's number among them.
   const int team = parts > 2 * kMergeWarps ? kMergeWarps : 1, mate = warp % team;
-  const int step = gridDim.y * (kMergeWarps / team);
+  const int step = gridDim.y * (kMergeWarps / team);  // rows at once
   const int rounds = (rows + step - 1) / step;
   for (int i = 0; i < rounds; ++i) {
     const int row = i * step + blockIdx.y * (kMergeWarps / team) + warp / team;
     if (row >= rows) break;  // (a whole team)
     auto part = [&](int s) -> size_t { return (size_t)(s == 0 ? 2 * w + 1 : 2 * (w + s)) * t.rows + row; };
-    float M = -INFINITY;
-    for (int s = lane; s < parts; s += 32) M = fmaxf(M, t.part_ml[part(s) * 2]);
+    // One pass with a running maximum: a part's statistics and sums are one
+    // load's wait, four parts at a time.
+    float M = -INFINITY, L = 0.f, acc[V] = {};
+    for (int s0 = mate; s0 < parts; s0 += 4 * team) {
+      float2 ml[4];
+      float o[4][V];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float ref = M == -INFINITY ? 0.f : M;
-    float L = 0.f, acc[V] = {};
-#pragma unroll 4
-    for (int s = mate; s < parts; s += team) {
-      const float2 ml = *reinterpret_cast<const float2*>(t.part_ml + part(s) * 2);
-      const float wgt = ex2(ml.x - ref);
-      L += wgt * ml.y;
-      const float* src = t.part_o + part(s) * D + lane * V;
+      for (int k = 0; k < 4; ++k) {
+        const int s = s0 + k * team;
+        ml[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] += wgt * src[v];
+        for (int v = 0; v < V; ++v) o[k][v] = 0.f;
+        if (s < parts) {
+          ml[k] = *reinterpret_cast<const float2*>(t.part_ml + part(s) * 2);
+          const float* src = t.part_o + part(s) * D + lane * V;
+          if constexpr (V == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(src);
+            o[k][0] = x.x, o[k][1] = x.y, o[k][2] = x.z, o[k][3] = x.w;
+          } else {
+            const float2 x = *reinterpret_cast<const float2*>(src);
+            o[k][0] = x.x, o[k][1] = x.y;
+          }
+        }
+      }
+      const float mn = fmaxf(fmaxf(fmaxf(M, ml[0].x), fmaxf(ml[1].x, ml[2].x)), ml[3].x);
+      const float ref = mn == -INFINITY ? 0.f : mn;
+      const float old = ex2(M - ref);
+      L *= old;
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] *= old;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float wgt = ex2(ml[k].x - ref);
+        L += wgt * ml[k].y;
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] += wgt * o[k][v];
+      }
+      M = mn;
     }
     const size_t orow = output_row(p, start, h, tile * t.rows + row);
     // Columns c, c + 1 of the row.
@@ -83,17 +106,25 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Mer
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) s_acc[warp][lane * V + v] = acc[v];
-    if (lane == 0) s_l[warp] = L;
+    if (lane == 0) {
+      s_l[warp] = L;
+      s_m[warp] = M;
+    }
     __syncthreads();
     if (threadIdx.x < D / 2) {
       const int c = 2 * threadIdx.x;
       float x = 0.f, y = 0.f;
+      M = s_m[0];
+#pragma unroll
+      for (int j = 1; j < kMergeWarps; ++j) M = fmaxf(M, s_m[j]);
+      const float ref = M == -INFINITY ? 0.f : M;
       L = 0.f;
 #pragma unroll
       for (int j = 0; j < kMergeWarps; ++j) {
-        x += s_acc[j][c];
-        y += s_acc[j][c + 1];
-        L += s_l[j];
+        const float wgt = ex2(s_m[j] - ref);
+        x += wgt * s_acc[j][c];
+        y += wgt * s_acc[j][c + 1];
+        L += wgt * s_l[j];
       }
       put(c, x, y, output_factor(L));
       if (c == 0) p.LSE[orow] = output_lse(M, L);
@@ -111,7 +142,14 @@ cudaError_t launch_paged_merge(int d, const PagedFwdParams& p, int rows, int wor
   q.set[0] = {p.part_o, p.part_ml, p.desc, rows, workers};
   if (p2) q.set[1] = {p2->part_o, p2->part_ml, p2->desc, rows2, workers2};
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(workers + workers2), kMergeCtas);
+  // Four CTAs to a worker where items are in many parts (a decoding step with
+  // fewer than an eighth as many items as workers) or tiles are large; one where
+  // a pass of its warps covers the tile.  Measured, four against one (whole
+  // calls, 8 kv heads, d = 128): one request of 131072 keys 51.1 / 56.3 us,
+  // three prompt chunks 458 / 482 us; the other way 64 requests of up to 8192
+  // keys 124.4 / 122.9 us.
+  const bool few = (long long)p.R * p.Hkv * 8 <= workers;
+  cfg.gridDim = dim3((unsigned)(workers + workers2), few || rows > 16 || p2 ? 4u : 1u);
   cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.stream = stream;
   cudaLaunchAttribute at{};
