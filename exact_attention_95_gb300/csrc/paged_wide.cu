@@ -24,6 +24,12 @@
 // TMEM (512 columns): S [0, 128) shared by the tiles in turn, P_t 64 columns
 // each, O_t d columns each.  A tile without rows takes part in every hand-off
 // and skips the work.
+//
+// Measured: three requests with chunks of up to 1000 tokens against up to 16384
+// keys, 32 query and 8 kv heads, d = 128: 456 us, 1160 TFLOPS (61 % of a plain
+// bf16 product's rate); the tensor pipe is busy 54 % of the time, the softmax
+// warps issue the rest.  Dropped: the tiles with an S buffer each, or a unit to
+// each tile in turn where an item has up to 128 rows (477 to 635 us).
 #include "paged.cuh"
 
 namespace attn {
@@ -736,12 +742,13 @@ template <int D>
 cudaError_t launch_wide(const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedFwdParams& p, int workers,
                         cudaStream_t stream) {
   // The register split draws on what the launch allocates: it has to be kLaunchRegs a thread.
-  static int regs = -1;  // one per instantiation
+  static std::atomic<int> known{-1};  // one per instantiation
+  int regs = known.load(std::memory_order_relaxed);
   if (regs < 0) {
     cudaFuncAttributes fa;
     cudaError_t e = cudaFuncGetAttributes(&fa, fwd_paged_wide_kernel<D>);
     if (e != cudaSuccess) return e;
-    regs = fa.numRegs;
+    known.store(regs = fa.numRegs, std::memory_order_relaxed);
   }
   if (regs != kLaunchRegs) return cudaErrorInvalidKernelImage;
   return launch_workers<D>(fwd_paged_wide_kernel<D>, kThreads, WC<D>::SMEM, tmK, tmV, p, workers, stream);

@@ -1,0 +1,152 @@
+"""The paged cache's calls as a server strings them together: step after step
+with nothing between the calls, first calls of a process inside a capture,
+and caches whose offsets pass 32 bits.  Every result is compared bit for bit
+with the same calls made one at a time."""
+
+import os
+import subprocess
+import sys
+
+import pytest
+import torch
+
+import exact_attention_95_gb300 as pkg
+
+pytestmark = pytest.mark.gpu
+
+
+def _randn(g, *shape):
+    return torch.randn(*shape, generator=g, device="cuda").bfloat16()
+
+
+def _empty_cache(num_pages, Hkv, page, d, make=torch.zeros):
+    return [x for _ in range(2) for x in (make(num_pages, Hkv, page, d, dtype=torch.uint8, device="cuda"),
+                                          torch.ones(num_pages, Hkv, device="cuda"))]
+
+
+@pytest.mark.parametrize("R,chunk", [(3, 0), (40, 0), (3, 90)])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 32)])
+def test_steps_with_nothing_between_the_calls(R, chunk, d, page):
+    """Each append changes codes and scales that the attention before it reads
+    (growing elements raise the scales), and each attention reuses the workspace
+    of the one before.  chunk: every third step, request 0 takes that many tokens."""
+    Hq, Hkv, steps, first = 8, 2, 24, 70
+    g = torch.Generator(device="cuda").manual_seed(5)
+    news = [[chunk if chunk and r == 0 and s % 3 == 2 else 1 for r in range(R)] for s in range(steps)]
+    total = [first + sum(n[r] for n in news) for r in range(R)]
+    width = max(-(-n // page) for n in total)
+    num_pages = R * width
+    table = torch.randperm(num_pages, generator=g, device="cuda").int().reshape(R, width).contiguous()
+    steps_in = []
+    lens = [0] * R
+    for n in [[first] * R] + news:
+        T = sum(n)
+        grow = 2.0 ** (len(steps_in) / 4)
+        slots = []
+        for r in range(R):
+            pos = lens[r] + torch.arange(n[r], device="cuda")
+            slots.append(table[r].long()[pos // page] * page + pos % page)
+        lens = [a + b for a, b in zip(lens, n)]
+        steps_in.append((_randn(g, T, Hq, d), grow * _randn(g, T, Hkv, d), grow * _randn(g, T, Hkv, d),
+                         torch.cat(slots), torch.tensor([0] + n, device="cuda").cumsum(0).int(),
+                         torch.tensor(lens, dtype=torch.int32, device="cuda")))
+    ws = torch.empty(max(pkg.attn_fwd_paged_workspace_size(R, x[0].shape[0], Hq, Hkv, d) for x in steps_in),
+                     dtype=torch.uint8, device="cuda")
+
+    def run(wait):
+        cache = _empty_cache(num_pages, Hkv, page, d)
+        outs = [(torch.empty_like(x[0]), torch.empty(x[0].shape[:2], device="cuda")) for x in steps_in]
+        torch.cuda.synchronize()
+        for (q, k, v, slots, cu, kv), (O, L) in zip(steps_in, outs):
+            pkg.attn_kv_append_fp8(k, v, slots, *cache)
+            if wait:
+                torch.cuda.synchronize()
+            pkg.attn_fwd_paged_fp8(q, *cache, table, cu, kv, causal=True, O=O, LSE=L, workspace=ws)
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert pkg.attn_last_device_status() == pkg.ATTN_OK
+        return [x for o in outs for x in o] + cache
+
+    want = run(True)
+    for _ in range(3):
+        for a, b in zip(run(False), want):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("chunk", [1, 40])
+def test_offsets_past_32_bits(chunk):
+    """The same tokens in pages at the end of 5 GB of keys and 5 GB of values and in a small cache."""
+    page, Hkv, d, Hq = 128, 8, 128, 16
+    num_pages, used, lens = 40000, 8, [500, 130]
+    assert num_pages * Hkv * page * d > 2 ** 32
+    g = torch.Generator(device="cuda").manual_seed(6)
+    T = sum(lens)
+    k, v = _randn(g, T, Hkv, d), _randn(g, T, Hkv, d)
+    q = _randn(g, 2 * chunk, Hq, d)
+    cu = torch.tensor([0, chunk, 2 * chunk], dtype=torch.int32, device="cuda")
+    added = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = []
+    for n in (used, num_pages):
+        cache = _empty_cache(n, Hkv, page, d, torch.empty)
+        free = torch.arange(n - used, n, dtype=torch.int32, device="cuda")
+        table = torch.zeros(2, 5, dtype=torch.int32, device="cuda")
+        kv, _, slots, _, _ = pkg.attn_kv_tables(torch.zeros_like(added), added, free, table, page, T)
+        pkg.attn_kv_append_fp8(k, v, slots, *cache)
+        got.append(pkg.attn_fwd_paged_fp8(q, *cache, table, cu, kv, causal=True))
+        torch.cuda.synchronize()
+        assert pkg.attn_last_device_status() == pkg.ATTN_OK
+        assert int(slots.max()) == (n - used + 5) * page + 130 - page - 1
+        got[-1] += tuple(x[n - used:n - used + 6].clone() for x in cache)
+        del cache
+    rows = torch.arange(page, device="cuda")
+    for a, b in zip(got[0][:2], got[1][:2]):
+        assert torch.equal(a, b)
+    for i in (2, 3, 4, 5):
+        a, b = got[0][i], got[1][i]
+        if a.dim() == 4:  # codes of the places that hold tokens
+            held = torch.stack([rows < (x - y * page) for x, y in [(500, 0), (500, 1), (500, 2), (500, 3), (130, 0),
+                                                                   (130, 1)]])[:, None, :, None]
+            a, b = (x * held for x in (a, b))
+        assert torch.equal(a, b)
+
+
+FIRST = """
+import torch
+import exact_attention_95_gb300 as pkg
+dev = "cuda"
+R, Hq, Hkv, d, page = 3, 8, 2, %d, 32
+g = torch.Generator(device=dev).manual_seed(1)
+new = %d
+T = R * new
+q, k, v = (torch.randn(T, h, d, generator=g, device=dev).bfloat16() for h in (Hq, Hkv, Hkv))
+cache = [x for _ in range(2) for x in (torch.zeros(40, Hkv, page, d, dtype=torch.uint8, device=dev),
+                                       torch.ones(40, Hkv, device=dev))]
+cached = torch.zeros(R, dtype=torch.int32, device=dev)
+added = torch.full((R,), new, dtype=torch.int32, device=dev)
+free = torch.arange(40, dtype=torch.int32, device=dev)
+table = torch.zeros(R, 8, dtype=torch.int32, device=dev)
+def step():
+    kv, cu, slots, _, _ = pkg.attn_kv_tables(cached, added, free, table, page, T)
+    pkg.attn_kv_append_fp8(k, v, slots, *cache)
+    return pkg.attn_fwd_paged_fp8(q, *cache, table, cu, kv, causal=True)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = step()
+graph.replay()
+torch.cuda.synchronize()
+got = [x.clone() for x in out]
+want = step()
+torch.cuda.synchronize()
+assert pkg.attn_last_device_status() == pkg.ATTN_OK
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+assert float(got[0].float().abs().max()) > 0
+print("captured first")
+"""
+
+
+@pytest.mark.parametrize("d,new", [(64, 1), (128, 50)])
+def test_the_first_calls_of_a_process_inside_a_capture(d, new):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST % (d, new)], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
