@@ -104,11 +104,13 @@ struct Cache {
 
 template <class F>
 int on_device(at::Device device, F call) {
-  int rc;
-  Py_BEGIN_ALLOW_THREADS;
+  // (What may throw comes before Python's lock is let go.)
   c10::cuda::OptionalCUDAGuard guard;
   if (c10::cuda::current_device() != device.index()) guard.set_device(device);
-  rc = call((void*)c10::cuda::getCurrentCUDAStream(device.index()).stream());
+  void* const stream = (void*)c10::cuda::getCurrentCUDAStream(device.index()).stream();
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = call(stream);
   Py_END_ALLOW_THREADS;
   return rc;
 }

@@ -29,7 +29,9 @@
 // tokens of four heads each, two tiles of 16 rows: 54 us, bound by what the
 // warps issue for a tile.  Dropped: a tile of 24 rows, whose sums leave no
 // registers for the queries (16 requests of 4096 keys, 24 rows: 71 us against
-// 64 by two tiles of 16).
+// 64 by two tiles of 16); three CTAs to an SM for 16 rows too, with the queries
+// in shared memory and K's and V's tiles in one ring (49 us against 45 at 16
+// rows, 127 against 121 for the 64 requests above: the ring's hand-offs double).
 #include "paged.cuh"
 
 namespace attn {
