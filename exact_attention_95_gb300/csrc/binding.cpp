@@ -13,6 +13,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -65,15 +66,30 @@ bool output(PyObject* o, at::Tensor& t, at::ScalarType type, at::IntArrayRef sha
   t = *given;
   return true;
 }
-// A contiguous tensor of this type and shape in the memory of a new tensor t,
-// from element `first` (of this type) on.
-at::Tensor part_of(const at::Tensor& t, at::ScalarType type, int64_t first, at::IntArrayRef shape) {
-  at::Tensor v = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(t.storage()), t.key_set(),
+// New device memory on the current device and stream, from torch's allocator.
+// Called directly: the dispatcher's code on the way to an at::empty, cold after
+// a kernel launch, takes longer than the allocation (tables 6.7 us a call with
+// two of them, 4.9 like this; attention 9.3 and 6.0).
+at::Storage memory(size_t bytes) {
+  c10::Allocator* from = c10::cuda::CUDACachingAllocator::get();
+  return at::Storage(c10::make_intrusive<c10::StorageImpl>(c10::StorageImpl::use_byte_size_t(), bytes,
+                                                           from->allocate(bytes), from, /*resizable=*/true));
+}
+// A contiguous tensor of this type and shape in it, from element `first` (of this type) on.
+at::Tensor part_of(const at::Storage& s, at::ScalarType type, int64_t first, at::IntArrayRef shape) {
+  at::Tensor v = at::detail::make_tensor<c10::TensorImpl>(at::Storage(s), c10::DispatchKeySet(c10::DispatchKey::CUDA),
                                                           c10::scalarTypeToTypeMeta(type));
   v.unsafeGetTensorImpl()->set_storage_offset(first);
   v.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
   return v;
 }
+// Sets the device, where it is another one, for as long as this lives.
+struct OnDevice {
+  c10::cuda::OptionalCUDAGuard guard;
+  explicit OnDevice(at::Device d) {
+    if (c10::cuda::current_device() != d.index()) guard.set_device(d);
+  }
+};
 PyObject* wrap(PyObject* given, at::Tensor& t) {
   if (given != Py_None) {
     Py_INCREF(given);
@@ -102,17 +118,23 @@ struct Cache {
   }
 };
 
+// The call on the device's current stream, without Python's lock (it throws nothing).
 template <class F>
-int on_device(at::Device device, F call) {
-  // (What may throw comes before Python's lock is let go.)
-  c10::cuda::OptionalCUDAGuard guard;
-  if (c10::cuda::current_device() != device.index()) guard.set_device(device);
+int without_lock(at::Device device, F call) {
   void* const stream = (void*)c10::cuda::getCurrentCUDAStream(device.index()).stream();
   int rc;
   Py_BEGIN_ALLOW_THREADS;
   rc = call(stream);
   Py_END_ALLOW_THREADS;
   return rc;
+}
+// A tuple of new references.
+template <class... P>
+PyObject* tuple(P*... items) {
+  PyObject* t = PyTuple_New(sizeof...(P));
+  Py_ssize_t i = 0;
+  if (t) (PyTuple_SET_ITEM(t, i++, items), ...);
+  return t;
 }
 
 #define ATTN_GUARD(...)                             \
@@ -137,28 +159,29 @@ PyObject* kv_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!fits(R) || !fits(width) || !fits(F) || !is(cached, at::kInt, {R}, dev) || !is(added, at::kInt, {R}, dev) ||
         !is(free_pages, at::kInt, {F}, dev) || !is(table, at::kInt, {R, width}, dev))
       Py_RETURN_NONE;
+    const OnDevice on(dev);
     at::Tensor lens, cu, slots, positions, taken;
-    if (a[6] == Py_None && a[7] == Py_None && a[9] == Py_None && a[10] == Py_None) {
-      // One allocation for the 32-bit outputs.
-      const at::Tensor all = at::empty({2 * R + 3 + T}, at::TensorOptions().dtype(at::kInt).device(dev));
-      lens = part_of(all, at::kInt, 0, {R});
-      cu = part_of(all, at::kInt, R, {R + 1});
-      taken = part_of(all, at::kInt, 2 * R + 1, {2});
-      positions = part_of(all, at::kInt, 2 * R + 3, {T});
-      if (!output(a[8], slots, at::kLong, {T}, dev)) Py_RETURN_NONE;
+    if (a[6] == Py_None && a[7] == Py_None && a[8] == Py_None && a[9] == Py_None && a[10] == Py_None) {
+      // One allocation for all of them.
+      const at::Storage all = memory(8 * (size_t)T + 4 * (size_t)(2 * R + 3 + T));
+      const int64_t at = 2 * (int64_t)T;
+      slots = part_of(all, at::kLong, 0, {T});
+      lens = part_of(all, at::kInt, at, {R});
+      cu = part_of(all, at::kInt, at + R, {R + 1});
+      taken = part_of(all, at::kInt, at + 2 * R + 1, {2});
+      positions = part_of(all, at::kInt, at + 2 * R + 3, {T});
     } else if (!output(a[6], lens, at::kInt, {R}, dev) || !output(a[7], cu, at::kInt, {R + 1}, dev) ||
         !output(a[8], slots, at::kLong, {T}, dev) || !output(a[9], positions, at::kInt, {T}, dev) ||
         !output(a[10], taken, at::kInt, {2}, dev))
       Py_RETURN_NONE;
-    const int rc = on_device(dev, [&](void* stream) {
+    const int rc = without_lock(dev, [&](void* stream) {
       return g_tables((const int32_t*)cached->data_ptr(), (const int32_t*)added->data_ptr(),
                       (const int32_t*)free_pages->data_ptr(), (int)F, (int32_t*)table->data_ptr(), (int)width, page,
                       (int32_t*)lens.data_ptr(), (int32_t*)cu.data_ptr(), (int64_t*)slots.data_ptr(),
                       (int32_t*)positions.data_ptr(), (int32_t*)taken.data_ptr(), (int)R, T, stream);
     });
     if (rc != ATTN_OK) return PyLong_FromLong(rc);
-    return Py_BuildValue("(NNNNN)", wrap(a[6], lens), wrap(a[7], cu), wrap(a[8], slots), wrap(a[9], positions),
-                         wrap(a[10], taken));)
+    return tuple(wrap(a[6], lens), wrap(a[7], cu), wrap(a[8], slots), wrap(a[9], positions), wrap(a[10], taken));)
 }
 
 // K, V, slots, k_pages, k_scale, v_pages, v_scale
@@ -172,7 +195,8 @@ PyObject* kv_append_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const long long ks = token_stride(K, c.Hkv, c.d, dev), vs = token_stride(V, c.Hkv, c.d, dev);
     if (ks < 0 || vs < 0 || K->size(0) != V->size(0) || !fits(K->size(0)) || !is(slots, at::kLong, {K->size(0)}, dev))
       Py_RETURN_NONE;
-    const int rc = on_device(dev, [&](void* stream) {
+    const OnDevice on(dev);
+    const int rc = without_lock(dev, [&](void* stream) {
       return g_append(K->data_ptr(), ks, V->data_ptr(), vs, (const int64_t*)slots->data_ptr(), c.kp->data_ptr(),
                       (float*)c.ks->data_ptr(), c.vp->data_ptr(), (float*)c.vs->data_ptr(), (int)K->size(0), (int)c.Hkv,
                       (int)c.d, (int)c.num_pages, (int)c.page, stream);
@@ -204,34 +228,38 @@ PyObject* fwd_paged_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     const int causal = PyObject_IsTrue(a[9]), f32 = PyObject_IsTrue(a[10]);
     if (causal < 0 || f32 < 0) return nullptr;
-    at::Tensor O, LSE, ws;
+    const OnDevice on(dev);
+    at::Tensor O, LSE;
     const at::ScalarType type = f32 ? at::kFloat : at::kBFloat16;
     if (a[11] == Py_None && a[12] == Py_None) {
       // One allocation for both outputs (O's rows are 128 bytes at least).
       const int64_t bytes = T * Hq * c.d * (f32 ? 4 : 2);
-      const at::Tensor all = at::empty({bytes / 4 + T * Hq}, at::TensorOptions().dtype(at::kFloat).device(dev));
+      const at::Storage all = memory((size_t)bytes + 4 * (size_t)(T * Hq));
       O = part_of(all, type, 0, {T, Hq, c.d});
       LSE = part_of(all, at::kFloat, bytes / 4, {T, Hq});
     } else if (!output(a[11], O, type, {T, Hq, c.d}, dev) || !output(a[12], LSE, at::kFloat, {T, Hq}, dev)) {
       Py_RETURN_NONE;
     }
     const size_t need = g_workspace((int)R, (int)T, (int)Hq, (int)c.Hkv, (int)c.d);
+    c10::DataPtr own;  // freed at the end of this call, for later work of the same stream
+    void* ws = nullptr;
     if (a[13] == Py_None) {
-      ws = at::empty({(int64_t)need}, at::TensorOptions().dtype(at::kByte).device(dev));
+      own = c10::cuda::CUDACachingAllocator::get()->allocate(need);
+      ws = own.get();
     } else {
       const at::Tensor* given = tensor(a[13]);
       if (!given || !is(given, at::kByte, given->sizes(), dev) || (size_t)given->numel() < need) Py_RETURN_NONE;
-      ws = *given;
+      ws = given->data_ptr();
     }
-    const int rc = on_device(dev, [&](void* stream) {
+    const int rc = without_lock(dev, [&](void* stream) {
       return g_fwd(Q->data_ptr(), stride, c.kp->data_ptr(), (const float*)c.ks->data_ptr(), c.vp->data_ptr(),
                    (const float*)c.vs->data_ptr(), (const int32_t*)table->data_ptr(), (const int32_t*)cu->data_ptr(),
                    (const int32_t*)lens->data_ptr(), O.data_ptr(), (float*)LSE.data_ptr(), (int)R, (int)T, (int)Hq,
                    (int)c.Hkv, (int)c.d, (int)c.num_pages, (int)c.page, (int)width, (float)scale, causal,
-                   f32 ? ATTN_F32 : ATTN_BF16, ws.data_ptr(), (size_t)ws.numel(), stream);
+                   f32 ? ATTN_F32 : ATTN_BF16, ws, need, stream);
     });
     if (rc != ATTN_OK) return PyLong_FromLong(rc);
-    return Py_BuildValue("(NN)", wrap(a[11], O), wrap(a[12], LSE));)
+    return tuple(wrap(a[11], O), wrap(a[12], LSE));)
 }
 
 // bind(addresses of attn_kv_tables, attn_kv_append_fp8, attn_fwd_paged_fp8, attn_fwd_paged_workspace_size)
