@@ -176,15 +176,17 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const KvTablesPa
 // looks at `chunk` tokens and `pairs` of the 2 * Hkv (K or V, head) pairs.
 // Measured: 64 requests of one token, 8 kv heads, d = 128: 2.9 us, 500 requests,
 // 16 kv heads, d = 64: 4.1 us (launch and three dependent reads: slot, row and
-// scale, page); nine prompts of up to 4096 tokens 35.6 us, 4.3 TB/s, where the
+// scale, page); nine prompts of up to 4096 tokens 33.8 us, 4.6 TB/s, where the
 // integer pipe is 54 % busy (maxima, packing) and each CTA's first reads are
-// waited for.  Reading the next run while this one is written was no faster.
+// waited for.  Reading the next run while this one is written, prefetching the
+// chunk's rows to L2 while its slots are read, and neighbouring CTAs for the
+// heads of one chunk were no faster.
 constexpr int kAppThreads = 256;
 constexpr int kGroupRun = 4;
 constexpr int kWarpRun = 16;
 constexpr int kMaxPage = 128;
 constexpr int kFewTokens = 1024;
-constexpr int kMaxChunk = 128;
+constexpr int kMaxChunk = 64;
 
 // want for the largest |x| given as bf16 bits (below the infinity's).
 __device__ __forceinline__ float power_scale(uint32_t amax_bits) {
@@ -435,12 +437,13 @@ cudaError_t launch_kv_tables(const KvTablesParams& p, int sms, cudaStream_t stre
 
 cudaError_t launch_kv_append(int d, const KvAppendParams& p, int sms, cudaStream_t stream) {
   // Up to kFewTokens tokens: eight, and as many pairs as give every group of
-  // lanes a run of one token; more: 128 and one pair.  Measured on both sides
-  // of the border, 16 pairs, d = 128, us: 500 tokens of a prompt 6.0 / 4.2, of
-  // 500 requests (32 pairs, d = 64) 4.0 / 5.1; 2000 tokens 10.4 / 6.7 and
-  // 10.5 / 10.0.
+  // lanes a run of one token; more: 64 and two pairs.  Measured on both sides
+  // of the border, 16 pairs, d = 128, us, the few tokens' way first: 500 tokens
+  // of a prompt 6.0 / 4.2, of 500 requests (32 pairs, d = 64) 4.0 / 5.1; 2000
+  // tokens 10.4 / 6.8 and 10.5 / 10.0.  128 tokens and one pair against 64 and
+  // two: 25000 tokens of five prompts 32.9 / 32.3, 8000 requests 25.8 / 24.3.
   const int chunk = p.T <= kFewTokens ? 8 : kMaxChunk;
-  const int pairs = p.T <= kFewTokens ? kAppThreads / (d / 8) / 8 : 1;
+  const int pairs = p.T <= kFewTokens ? kAppThreads / (d / 8) / 8 : 2;
   const long long chunks = (p.T + chunk - 1) / chunk;
   const dim3 grid((unsigned)chunks, (unsigned)((2 * p.Hkv + pairs - 1) / pairs));
   if (d == 128) kv_append_kernel<128><<<grid, kAppThreads, 0, stream>>>(p, chunk, pairs);
