@@ -206,8 +206,10 @@ struct PagedFwdParams {
 constexpr int kPagedWideRows = 256;
 // CTAs of an SM, each a worker, by the rows of a tile.
 constexpr int paged_ctas(int rows) { return rows == 8 ? 3 : rows == 16 ? 2 : 1; }
+// split (8 or 4, tiles of eight rows): a cluster of that many CTAs for every item
+// and no merge; workers is then split times as many items as there may be.
 cudaError_t launch_paged_narrow(int d, int rows, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                const PagedFwdParams& p, int workers, cudaStream_t stream);
+                                const PagedFwdParams& p, int workers, int split, cudaStream_t stream);
 cudaError_t launch_paged_wide(int d, const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedFwdParams& p,
                               int workers, cudaStream_t stream);
 // Merge of the items that the one or two launches (given by their parameters,

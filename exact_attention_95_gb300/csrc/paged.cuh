@@ -57,7 +57,8 @@ struct Req {
   int start, n, len;
   long long units;
 };
-template <int ROWS>
+// SPLIT: an item counts as that many units, whatever its keys are (below).
+template <int ROWS, int SPLIT = 0>
 __device__ __forceinline__ Req load_req(const PagedFwdParams& p, int r) {
   Req q{0, 0, 0, 0};
   if (r < p.R) {
@@ -72,19 +73,19 @@ __device__ __forceinline__ Req load_req(const PagedFwdParams& p, int r) {
     }
     const int rows = q.n * p.G;
     if (rows > p.rows_min && rows <= p.rows_max)
-      q.units = (long long)((rows + ROWS - 1) / ROWS) * p.Hkv * max(1, (q.len + kUnit - 1) / kUnit);
+      q.units = (long long)((rows + ROWS - 1) / ROWS) * p.Hkv * (SPLIT ? SPLIT : max(1, (q.len + kUnit - 1) / kUnit));
   }
   return q;
 }
 
 // Units of every 32 requests, by `warps` warps; synchronise before reading.
 // (Of a single group walk_range sums them itself.)
-template <int ROWS>
+template <int ROWS, int SPLIT = 0>
 __device__ __forceinline__ void sum_units(const PagedFwdParams& p, long long* sums, int warp, int warps, int lane) {
   if (p.R <= 32) return;
 #pragma unroll 1
   for (int g = warp; g < (p.R + 31) >> 5; g += warps) {
-    long long u = load_req<ROWS>(p, g * 32 + lane).units;
+    long long u = load_req<ROWS, SPLIT>(p, g * 32 + lane).units;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
     if (lane == 0) sums[g] = u;
@@ -109,8 +110,10 @@ struct Batch {
 };
 
 // This worker's range, item by item and batch by batch (a whole warp, every
-// lane with the same state).
-template <int ROWS>
+// lane with the same state).  SPLIT: each item has that many workers, the CTAs
+// of a cluster, and each worker an equal part of its units, which may be none;
+// the grid has a cluster for every item.
+template <int ROWS, int SPLIT = 0>
 struct Walker {
   const PagedFwdParams& p;
   const long long* sums;
@@ -129,7 +132,7 @@ struct Walker {
   __device__ __forceinline__ Walker(const PagedFwdParams& p_, const long long* sums_, int lane_)
       : p(p_), sums(sums_), lane(lane_) {
     groups = (p.R + 31) >> 5;
-    rq = load_req<ROWS>(p, lane);
+    rq = load_req<ROWS, SPLIT>(p, lane);
     long long total = 0;
     if (groups == 1) total = rq.units;
     else
@@ -137,7 +140,7 @@ struct Walker {
       for (int i = lane; i < groups; i += 32) total += sums[i];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    per = divide(total + gridDim.x - 1, gridDim.x);
+    per = SPLIT ? 1 : divide(total + gridDim.x - 1, gridDim.x);
     pos = min(total, per * blockIdx.x);
     end = min(total, pos + per);
     g = l = line = k = ke = 0;
@@ -148,7 +151,7 @@ struct Walker {
     long long before = 0;
 #pragma unroll 1
     while (g + 1 < groups && before + sums[g] <= pos) before += sums[g++];
-    if (g > 0) rq = load_req<ROWS>(p, g * 32 + lane);
+    if (g > 0) rq = load_req<ROWS, SPLIT>(p, g * 32 + lane);
     long long incl = rq.units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -169,7 +172,7 @@ struct Walker {
     im.n = __shfl_sync(0xffffffffu, rq.n, l);
     im.len = __shfl_sync(0xffffffffu, rq.len, l);
     units = __shfl_sync(0xffffffffu, rq.units, l);
-    kt = max(1, (im.len + kUnit - 1) / kUnit);
+    kt = SPLIT ? SPLIT : max(1, (im.len + kUnit - 1) / kUnit);
     tiles = (im.n * p.G + ROWS - 1) / ROWS;
     off = 0;
     item = 0;
@@ -182,10 +185,17 @@ struct Walker {
     // late ones alike.
     const int at = item - im.h * tiles;
     im.tile = (at & 1) ? tiles - 1 - (at >> 1) : at >> 1;
-    const int k0 = im.k0, k1 = (int)min((long long)kt, k0 + (end - pos));
+    int k0 = im.k0, k1 = (int)min((long long)kt, k0 + (end - pos));
+    pos += k1 - k0;
+    off += k1 - k0;
+    if constexpr (SPLIT > 0) {
+      const long long all = (im.len + kUnit - 1) / kUnit;
+      im.k0 = k0 = (int)(all * k0 / SPLIT);
+      k1 = (int)(all * k1 / SPLIT);
+    }
     im.slot = k0 == 0 && k1 == kt ? -1 : k0 == 0 ? 1 : 0;
-    if (im.slot == 1) {
-      const long long last = pos + kt - 1;  // the item's last unit
+    if (SPLIT == 0 && im.slot == 1) {
+      const long long last = pos - (k1 - k0) + kt - 1;  // the item's last unit
       merge_parts = (int)divide(last, per) - (int)blockIdx.x + 1;
       merge_start = im.start;
       merge_n = im.n;
@@ -198,8 +208,6 @@ struct Walker {
     im.count = ke - k0;
     line += im.count;
     k = k0;
-    pos += k1 - k0;
-    off += k1 - k0;
     opened = false;
   }
   // The next batch, or false at the range's end.  `im` and `seen` are its item's.
@@ -212,7 +220,7 @@ struct Walker {
 #pragma unroll 1
         while (!more && g + 1 < groups) {
           ++g;
-          rq = load_req<ROWS>(p, g * 32 + lane);
+          rq = load_req<ROWS, SPLIT>(p, g * 32 + lane);
           more = __ballot_sync(0xffffffffu, rq.units > 0);
         }
         if (!more) return false;
@@ -258,10 +266,10 @@ static_assert(kUnit == 128, "units are 2^7 keys");
 // one, so that neither latency is waited for but at the start; an item is
 // announced as soon as its first ids are on their way (up to two items before
 // its units are loaded: the announcements' ring has to hold four).
-template <int ROWS, class ItemFn, class UnitFn>
+template <int ROWS, int SPLIT = 0, class ItemFn, class UnitFn>
 __device__ __forceinline__ bool walk_range(const PagedFwdParams& p, const long long* sums, int lane, ItemFn item_fn,
                                            UnitFn unit_fn) {
-  Walker<ROWS> w(p, sums, lane);
+  Walker<ROWS, SPLIT> w(p, sums, lane);
   struct Held {
     int units = 0;  // 0: none, or an item without units
     int id = -1, h = 0;
@@ -305,7 +313,7 @@ __device__ __forceinline__ bool walk_range(const PagedFwdParams& p, const long l
     cur = nxt;
     nxt = then;
   }
-  w.write_descriptor();
+  if (SPLIT == 0) w.write_descriptor();
   return ok;
 }
 
@@ -346,11 +354,11 @@ __host__ inline void overlap_with_previous(cudaLaunchConfig_t& cfg, cudaLaunchAt
 
 // Launches a kernel of `workers` CTAs with `smem` bytes of dynamic shared
 // memory, behind whatever is in the stream (it waits for that kernel before it
-// reads anything).  ID tells the kernels of one signature apart: the attribute
+// reads anything), in clusters of `cluster` CTAs.  ID tells the kernels of one signature apart: the attribute
 // is set once on a device.
 template <int ID, class Kernel>
 cudaError_t launch_workers(Kernel kern, int threads, int smem, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                           const PagedFwdParams& p, int workers, cudaStream_t stream) {
+                           const PagedFwdParams& p, int workers, cudaStream_t stream, int cluster = 1) {
   static std::atomic<bool> ready[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -365,8 +373,12 @@ cudaError_t launch_workers(Kernel kern, int threads, int smem, const CUtensorMap
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = stream;
-  cudaLaunchAttribute at{};
-  overlap_with_previous(cfg, at);
+  cudaLaunchAttribute at[2] = {};
+  overlap_with_previous(cfg, at[0]);
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  if (cluster > 1) cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, tmK, tmV, p);
 }
 

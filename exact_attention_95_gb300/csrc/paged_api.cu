@@ -47,6 +47,21 @@ bool token_stride_ok(long long stride, long long heads, int d) { return stride >
 // 65 us by two tiles of 16 and 75 us by a tile of 256, 48 rows 93 and 76 us.
 constexpr int kNarrowMost = 32;
 bool runs_wide(int R, int T, int G) { return T > R || G > 8; }
+// CTAs of a cluster for every item of a decoding step, whose sums then meet in
+// shared memory, or 0: the workers' equal ranges and the merge.  Items are tiles
+// of eight rows, and no more than T * Hkv of them as G <= 8.  Clusters where all
+// are resident at once (from 7/8 of the workers on they are not: GPCs leave
+// holes) and where the table is too narrow for a CTA to get more than eight
+// units.  Measured against the ranges, us, 8 kv heads, d = 128, requests of 700 /
+// 4096 / 8192 keys each: clusters of 8, two requests 7.1 / 9.7 / 13.8 against
+// 9.8 / 13.2 / 15.0, six 7.8 / 12.1 / 20.0 against 10.3 / 14.8 / 23.9, one of
+// 16384 keys (beyond the rule) 19.0 against 15.8; clusters of 4, twelve 9.5 / 19.8 / - against
+// 11.1 / 23.5; fourteen (448 CTAs) 15.4 / 34.3 against 11.3 / 26.5.
+int split_of(int T, int Hkv, long long keys, int workers) {
+  for (int s = 8; s >= 4; s /= 2)
+    if ((long long)T * Hkv * s * 7 <= 6LL * workers && keys <= 1024 * s) return s;
+  return 0;
+}
 // Workspace: partial sums (O, then maxima and sums, then merge descriptors) of
 // every worker, two slots each.
 int workers_of(int rows, int sms) { return sms * attn::paged_ctas(rows); }
@@ -225,8 +240,13 @@ attn_status attn_fwd_paged_fp8(const void* Q, long long q_stride, const void* k_
   pw.rows_max = 0x7fffffff;
   cudaError_t e = cudaSuccess;
   const int wide_rows = attn::kPagedWideRows, w1 = workers_of(rows, sms), w2 = workers_of(wide_rows, sms);
+  const int split = wide ? 0 : split_of(T, Hkv, (long long)max_pages * page_size, w1);
+  if (split) {
+    e = attn::launch_paged_narrow(d, rows, tk, tv, p, T * Hkv * split, split, cs);
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  }
   if (big) e = attn::launch_paged_wide(d, tk, tv, pw, w2, cs);
-  if (e == cudaSuccess && small) e = attn::launch_paged_narrow(d, rows, tk, tv, p, w1, cs);
+  if (e == cudaSuccess && small) e = attn::launch_paged_narrow(d, rows, tk, tv, p, w1, 0, cs);
   if (e == cudaSuccess)
     e = small ? attn::launch_paged_merge(d, p, rows, w1, big ? &pw : nullptr, wide_rows, big ? w2 : 0, cs)
               : attn::launch_paged_merge(d, pw, wide_rows, w2, nullptr, 0, 0, cs);

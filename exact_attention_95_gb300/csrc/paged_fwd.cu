@@ -21,10 +21,14 @@
 // each.  Every warp keeps its own running maximum, sum and accumulators of the
 // item; they meet in shared memory at the item's end.
 //
+// SPLIT: a small decoding step gives every item a cluster of SPLIT CTAs, each an
+// equal part of its keys.  Their sums meet through distributed shared memory
+// instead of through the workspace and a second launch.
+//
 // Measured (whole calls, 8 kv heads, d = 128, a token a request): 64 requests of
 // up to 8192 keys 121 us, 6.2 TB/s; one of 131072 keys 51 us, 5.3 TB/s; four of
-// up to 700 keys 9.4 us, of which the merge's launch is 3 (start, page ids,
-// codes, merge: each waits for the one before).  33 requests of up to 3001 keys,
+// up to 700 keys 7.5 us in clusters (start, lengths, page ids, codes, the meeting:
+// each waits for the one before; 9.4 us with the merge's launch).  33 requests of up to 3001 keys,
 // 16 kv heads, d = 64: 34 us, 4.2 TB/s.  16 requests of up to 5000 keys with six
 // tokens of four heads each, two tiles of 16 rows: 54 us, bound by what the
 // warps issue for a tile.  Dropped: a tile of 24 rows, whose sums leave no
@@ -120,7 +124,48 @@ __device__ __forceinline__ uint32_t piece(uint32_t base, int row, int c) {
   return D == 128 ? base + row * 128 + ((c ^ (row & 7)) << 4) : base + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
 }
 
-template <int D, int NB>
+// Piece q4 (four columns) of an output row: its sum, maximum and weights' sum.
+template <int D>
+__device__ __forceinline__ void put_piece(const PagedFwdParams& p, size_t orow, int q4, float4 sum, float M, float L) {
+  const float inv = output_factor(L);
+  if (p.out_f32)
+    *reinterpret_cast<float4*>(static_cast<float*>(p.O) + orow * D + q4 * 4) =
+        make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) + orow * D + q4 * 4) =
+        make_uint2(pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
+  if (q4 == 0) p.LSE[orow] = output_lse(M, L);
+}
+
+// All threads of the cluster's CTAs; what they wrote before is seen after.
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Shared memory of the cluster's CTA r at this CTA's address a.
+__device__ __forceinline__ uint32_t peer(uint32_t a, int r) {
+  uint32_t x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(x) : "r"(a), "r"(r));
+  return x;
+}
+__device__ __forceinline__ uint4 peer_u4(uint32_t a, int r) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(peer(a, r)));
+  return v;
+}
+__device__ __forceinline__ uint2 peer_u2(uint32_t a, int r) {
+  uint2 v;
+  asm volatile("ld.shared::cluster.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(peer(a, r)));
+  return v;
+}
+
+template <int D, int NB, int SPLIT>
 __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
     fwd_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const PagedFwdParams p) {
@@ -153,7 +198,7 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
     fence_mbar_init();
   }
   if (!p.behind) griddep_wait();  // the lengths, pages and queries of the kernel before
-  sum_units<kRows>(p, sums, warp, kWarps + 1, lane);
+  sum_units<kRows, SPLIT>(p, sums, warp, kWarps + 1, lane);
   __syncthreads();
   volatile int* const wc = abort_flag;
 
@@ -188,7 +233,7 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
       ++items_out;
       return true;
     };
-    bool ok = walk_range<kRows>(
+    bool ok = walk_range<kRows, SPLIT>(
         p, sums, lane, announce, [&](int h, int id, float ks, float vs, int in_batch) -> bool {
           const int s = stage;
           if (it >= C::STAGES && !wait_bar(bar(C::B_EMPTY + s), turn ^ 1, wc)) return false;
@@ -237,6 +282,10 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
     griddep_launch_dependents();
     // Behind the wide kernel: this one's completion stands for both.
     if (p.behind) griddep_wait();
+    if constexpr (SPLIT > 0) {
+      cluster_meet();
+      cluster_meet();
+    }
     return;
   }
 
@@ -578,20 +627,16 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
             if (bad & 0xff000000u) sum.w = NAN;
           }
         }
-        if (slot >= 0) {
+        if constexpr (SPLIT > 0) {
+          // For the cluster: where this thread has read its own piece, and where the statistics handed over were.
+          so[at(0, row, q4)] = sum;
+          if (q4 == 0) ml[row - kHalf * kRows] = make_float2(M, L);
+        } else if (slot >= 0) {
           const size_t base = (size_t)(blockIdx.x * 2 + slot) * kRows + row;
           *reinterpret_cast<float4*>(p.part_o + base * D + q4 * 4) = sum;
           if (q4 == 0) *reinterpret_cast<float2*>(p.part_ml + base * 2) = make_float2(M, L);
         } else {
-          const size_t orow = output_row(p, start, h, tile * kRows + row);
-          const float inv = output_factor(L);
-          if (p.out_f32)
-            *reinterpret_cast<float4*>(static_cast<float*>(p.O) + orow * D + q4 * 4) =
-                make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
-          else
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) + orow * D + q4 * 4) =
-                make_uint2(pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
-          if (q4 == 0) p.LSE[orow] = output_lse(M, L);
+          put_piece<D>(p, output_row(p, start, h, tile * kRows + row), q4, sum, M, L);
         }
       }
       __syncwarp();
@@ -604,24 +649,73 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
   consume();
   // A wait that gave up.
   if (*abort_flag && lane == 0) atomicCAS(p.status, kDevOk, kDevTimeout);
+  if constexpr (SPLIT > 0) {
+    // The item's parts, from the shared memory of the cluster's CTAs: each
+    // joins every SPLIT-th 32 pieces.  Without an item there is none in all of them.
+    __syncwarp();
+    cluster_meet();
+    const Item* im = items;  // (the first announcement)
+    if (warp == 0 && im->count >= 0) {
+      const int tile = im->tile, h = im->h, start = im->start, rows = min(kRows, im->n * p.G - tile * kRows);
+#pragma unroll 1
+      for (int x = 32 * (int)cluster_rank() + lane; x < rows * (D / 4); x += 32 * SPLIT) {
+        const int row = x / (D / 4), q4 = x % (D / 4);
+        const int c2 = (row >> 1) & 3, sw = D == 128 ? c2 | ((q4 >> 4) << 2) : (c2 & 1) | ((c2 >> 1) << 2);
+        float2 st[SPLIT];
+        float4 v[SPLIT];
+#pragma unroll
+        for (int r = 0; r < SPLIT; ++r) {
+          const uint4 a = peer_u4(sb + C::OFF_O + (row * (D / 4) + (q4 ^ sw)) * 16, r);
+          const uint2 b = peer_u2(sb + C::OFF_ML + row * 8, r);
+          v[r] = make_float4(__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z), __uint_as_float(a.w));
+          st[r] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y));
+        }
+        float M = st[0].x;
+#pragma unroll
+        for (int r = 1; r < SPLIT; ++r) M = fmaxf(M, st[r].x);
+        const float ref = M == -INFINITY ? 0.f : M;
+        float L = 0.f;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int r = 0; r < SPLIT; ++r) {
+          const float wgt = ex2(st[r].x - ref);
+          L += wgt * st[r].y;
+          sum.x += wgt * v[r].x;
+          sum.y += wgt * v[r].y;
+          sum.z += wgt * v[r].z;
+          sum.w += wgt * v[r].w;
+        }
+        put_piece<D>(p, output_row(p, start, h, tile * kRows + row), q4, sum, M, L);
+      }
+    }
+    __syncwarp();
+    cluster_meet();
+  }
 }
 
 }  // namespace
 
 namespace {
 
-template <int D, int NB>
+template <int D, int NB, int SPLIT = 0>
 cudaError_t launch_narrow(const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedFwdParams& p, int workers,
                           cudaStream_t stream) {
   using C = PC<D, NB>;
   static_assert(C::CTAS == paged_ctas(C::ROWS), "workers of an SM");
-  return launch_workers<D * 2 + NB>(fwd_paged_kernel<D, NB>, C::THREADS, C::SMEM, tmK, tmV, p, workers, stream);
+  return launch_workers<D * 64 + NB * 16 + SPLIT>(fwd_paged_kernel<D, NB, SPLIT>, C::THREADS, C::SMEM, tmK, tmV, p,
+                                                       workers, stream, SPLIT ? SPLIT : 1);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_narrow(int d, int rows, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                const PagedFwdParams& p, int workers, cudaStream_t stream) {
+                                const PagedFwdParams& p, int workers, int split, cudaStream_t stream) {
+  if (split == 8)
+    return d == 128 ? launch_narrow<128, 1, 8>(tmK, tmV, p, workers, stream)
+                    : launch_narrow<64, 1, 8>(tmK, tmV, p, workers, stream);
+  if (split == 4)
+    return d == 128 ? launch_narrow<128, 1, 4>(tmK, tmV, p, workers, stream)
+                    : launch_narrow<64, 1, 4>(tmK, tmV, p, workers, stream);
   if (rows == 8)
     return d == 128 ? launch_narrow<128, 1>(tmK, tmV, p, workers, stream)
                     : launch_narrow<64, 1>(tmK, tmV, p, workers, stream);

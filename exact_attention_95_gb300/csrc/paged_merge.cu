@@ -7,11 +7,11 @@
 // Latency bound: launched so that its start overlaps the kernel's end.  Of an
 // item in many parts (a long context cut over all workers has dozens) a CTA
 // takes a row at a time, its eight warps the parts in turn; else a warp does.
-// Measured by leaving it out: 3 us of a call of 9.4 (four requests of up to 700
-// keys), 4 of 121 (64 of up to 8192 keys), 5 of 51 (one of 131072 keys).  Joining
-// the parts in the main kernel, by the last of an item's workers, would take
-// counters that are zero at every call's start, which a caller's workspace is
-// not.
+// Measured by leaving it out: 4 us of a call of 121 (64 requests of up to 8192
+// keys), 5 of 51 (one of 131072 keys).  Joining the parts in the main kernel, by
+// the last of an item's workers, would take counters that are zero at every
+// call's start, which a caller's workspace is not; clusters do without (small
+// steps, paged_fwd.cu).
 #include "paged.cuh"
 
 namespace attn {

@@ -1,16 +1,21 @@
 """The paged cache's calls as a server strings them together: step after step
 with nothing between the calls, first calls of a process inside a capture,
-and caches whose offsets pass 32 bits.  Every result is compared bit for bit
-with the same calls made one at a time."""
+and caches whose offsets pass 32 bits, compared bit for bit with the same calls
+made one at a time; and small decoding steps, whose tables' width decides how
+the work is divided, against the plain 64-bit implementation."""
 
 import os
 import subprocess
 import sys
 
+import numpy as np
 import pytest
 import torch
 
 import exact_attention_95_gb300 as pkg
+
+import paged
+from test_paged_cache import _cache, dev, dev_bf16
 
 pytestmark = pytest.mark.gpu
 
@@ -150,3 +155,60 @@ def test_the_first_calls_of_a_process_inside_a_capture(d, new):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST % (d, new)], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
+
+
+STEPS = [
+    # lens, new tokens, Hq, Hkv, d, page
+    ([1], [1], 1, 1, 64, 16),
+    ([700, 20, 0, 351], [1, 1, 1, 1], 32, 8, 128, 16),
+    ([5000], [1], 8, 1, 128, 128),              # 40 units of one item
+    ([1023, 1024, 1025, 127, 128, 129], [1] * 6, 16, 8, 64, 32),
+    ([300, 40, 0, 7, 90], [3, 0, 0, 1, 1], 8, 1, 64, 16),   # idle requests; several tokens and tiles of one
+    ([2, 40, 9, 500], [4, 0, 0, 0], 7, 1, 128, 32),  # more queries than keys: the first rows see none
+    ([100 * i for i in range(12)], [1] * 12, 32, 8, 128, 64),
+    ([33] * 60, [0] * 57 + [1] * 3, 12, 2, 64, 16),  # more than 32 requests
+]
+
+
+@pytest.mark.parametrize("case", STEPS, ids=lambda c: "R%d_Hq%d_Hkv%d_d%d_p%d" % (len(c[0]), *c[2:]))
+@pytest.mark.parametrize("keys", [0, 10000])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_small_steps_with_narrow_and_wide_tables(case, keys, out):
+    lens, news, Hq, Hkv, d, page = case
+    rng = np.random.default_rng(51)
+    kc, ks, vc, vs, table = _cache(rng, lens, page, Hkv, d, width_extra=1 + keys // page)
+    cu = np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+    T = int(cu[-1])
+    assert T <= len(lens)
+    q = paged.bf16_bits(rng.standard_normal((T, Hq, d)).astype(np.float32))
+    g = [dev(a) for a in (kc, ks, vc, vs, table, cu, np.asarray(lens, np.int32))]
+    O, L = pkg.attn_fwd_paged_fp8(dev_bf16(q), *g, None, True, out)
+    torch.cuda.synchronize()
+    assert pkg.attn_last_device_status() == pkg.ATTN_OK
+    Or, Lr, A, B = paged.attention(paged.bf16_values(q), kc, ks, vc, vs, table, cu, lens,
+                                   float(np.float32(1 / np.sqrt(d))), True)
+    tol_o, tol_l = paged.bounds(Or, Lr, A, B, d, out == torch.bfloat16)
+    none = np.isneginf(Lr)
+    Og, Lg = O.double().cpu().numpy(), L.double().cpu().numpy()
+    assert np.array_equal(np.isneginf(Lg), none) and (Og[none] == 0.0).all()
+    assert (np.abs(Og - Or) <= tol_o).all()
+    assert (np.abs(np.where(none, 0.0, Lg) - np.where(none, 0.0, Lr)) <= tol_l).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_nan_value_in_a_small_step_with_narrow_and_wide_tables(d):
+    """The NaN lies at the last key, which the last of a request's three tokens sees alone."""
+    rng = np.random.default_rng(52)
+    lens, Hq, Hkv, page = [300, 40, 60], 2, 1, 16
+    cu = np.array([0, 3, 3, 3], np.int32)
+    q = dev_bf16(paged.bf16_bits(rng.standard_normal((3, Hq, d)).astype(np.float32)))
+    for extra in (1, 700):
+        kc, ks, vc, vs, table = _cache(np.random.default_rng(53), lens, page, Hkv, d, width_extra=extra)
+        vc[table[0, 299 // page], 0, 299 % page, 5] = 0x7F
+        g = [dev(a) for a in (kc, ks, vc, vs, table, cu, np.asarray(lens, np.int32))]
+        O, L = pkg.attn_fwd_paged_fp8(q, *g, None, True, torch.float32)
+        torch.cuda.synchronize()
+        assert pkg.attn_last_device_status() == pkg.ATTN_OK
+        want = np.zeros((3, Hq, d), bool)
+        want[2, :, 5] = True
+        assert np.array_equal(torch.isnan(O).cpu().numpy(), want) and torch.isfinite(L).all()
