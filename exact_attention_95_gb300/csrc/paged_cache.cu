@@ -24,8 +24,8 @@ namespace {
 // pass, and then writes its share of the block's tokens and table entries,
 // found by binary search in the block's sums in shared memory; a second
 // launch, or a wait between CTAs, would cost more than the repeated scan.
-// Measured, one step in a captured graph: 8 requests 2.5 us, 777 with up
-// to 200 new tokens each 4.9 us, 64 prompts of up to 8192 tokens 5.2 us.
+// Measured, one step in a captured graph: 8 requests 2.3 us, 777 with up
+// to 200 new tokens each 4.6 us, 64 prompts of up to 8192 tokens 3.4 us.
 // Sums saturate at kCap (associative for non-negative terms), above every
 // limit they are compared with.
 constexpr unsigned kCap = 0x7fffffffu;
@@ -44,6 +44,8 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const KvTablesPa
   const int P = 1 << p.page_log2;
   const unsigned T = (unsigned)p.T, F = (unsigned)p.n_free;
   if (tid == 0) s_taken = s_refused = 0;
+  griddep_launch_dependents();
+  griddep_wait();
   unsigned tok0 = 0, need0 = 0;  // sums over the blocks before this one
   for (int base = 0; base < p.R; base += nthr) {
     const int r = base + tid;
@@ -174,9 +176,9 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const KvTablesPa
 // the D / 8 lanes of one row for up to kGroupRun tokens (a decoding step: four
 // runs or two to a warp), the warp for up to kWarpRun, else the CTA.  A CTA
 // looks at `chunk` tokens and `pairs` of the 2 * Hkv (K or V, head) pairs.
-// Measured: 64 requests of one token, 8 kv heads, d = 128: 2.9 us, 500 requests,
-// 16 kv heads, d = 64: 4.1 us (launch and three dependent reads: slot, row and
-// scale, page); nine prompts of up to 4096 tokens 33.8 us, 4.6 TB/s, where the
+// Measured: 64 requests of one token, 8 kv heads, d = 128: 2.5 us, 500 requests,
+// 16 kv heads, d = 64: 3.7 us (launch and three dependent reads: slot, row and
+// scale, page); nine prompts of up to 4096 tokens 34 us, 4.5 TB/s, where the
 // integer pipe is 54 % busy (maxima, packing) and each CTA's first reads are
 // waited for.  Reading the next run while this one is written, prefetching the
 // chunk's rows to L2 while its slots are read, and neighbouring CTAs for the
@@ -331,7 +333,7 @@ __global__ void __launch_bounds__(kAppThreads, 4) kv_append_kernel(const KvAppen
   __shared__ long long s_slot[kMaxChunk];                       // of each run: its first slot,
   __shared__ uint16_t s_first[kMaxChunk], s_len[kMaxChunk];     // first token, tokens
   __shared__ uint32_t s_red[kWarps];
-  griddep_launch_dependents();  // the attention's start overlaps this kernel
+  griddep_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int P = 1 << p.page_log2;
   const long long t0 = (long long)blockIdx.x * chunk;
@@ -390,6 +392,8 @@ __global__ void __launch_bounds__(kAppThreads, 4) kv_append_kernel(const KvAppen
     const int n = s_len[k];
     return run_of<D>(p, t0 + s_first[k], s_slot[k], task < tasks && n > lo && n <= hi ? n : 0, pair0 + pair);
   };
+  // (No early start of the next kernel: its CTAs would crowd on the SMs that have
+  // fewer of these.  Two appends of 2000 tokens in a row 9.7 us each, with it 13.5.)
   if (any_group) {
     constexpr int GROUPS = kAppThreads / CH;
     for (int base = 0; base < tasks; base += GROUPS) {
@@ -424,15 +428,32 @@ __global__ void __launch_bounds__(kAppThreads, 4) kv_append_kernel(const KvAppen
     }
 }
 
+// Launches a kernel that may start while the one before it in the stream ends
+// (it waits for that one before it reads anything).
+template <class... P, class... A>
+cudaError_t launch_behind(void (*kern)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 }  // namespace
 
 cudaError_t launch_kv_tables(const KvTablesParams& p, int sms, cudaStream_t stream) {
   // Threads for the requests' scan in few blocks, and a CTA for every block of
-  // tokens, up to one per SM.
+  // tokens, up to 1024 threads an SM (64 prompts of up to 8192 tokens, CTAs of
+  // 256 an SM: one 4.7 us, four 3.4, eight 4.4).
   const int thr = p.R <= 256 ? 256 : kTabThreads;
-  const int grid = (int)std::max(1LL, std::min((long long)sms, ((long long)p.T + thr - 1) / thr));
-  kv_tables_kernel<<<grid, thr, 0, stream>>>(p);
-  return cudaGetLastError();
+  const int most = sms * (kTabThreads / thr);
+  const int grid = (int)std::max(1LL, std::min((long long)most, ((long long)p.T + thr - 1) / thr));
+  return launch_behind(kv_tables_kernel, grid, thr, stream, p);
 }
 
 cudaError_t launch_kv_append(int d, const KvAppendParams& p, int sms, cudaStream_t stream) {
@@ -446,9 +467,8 @@ cudaError_t launch_kv_append(int d, const KvAppendParams& p, int sms, cudaStream
   const int pairs = p.T <= kFewTokens ? kAppThreads / (d / 8) / 8 : 2;
   const long long chunks = (p.T + chunk - 1) / chunk;
   const dim3 grid((unsigned)chunks, (unsigned)((2 * p.Hkv + pairs - 1) / pairs));
-  if (d == 128) kv_append_kernel<128><<<grid, kAppThreads, 0, stream>>>(p, chunk, pairs);
-  else kv_append_kernel<64><<<grid, kAppThreads, 0, stream>>>(p, chunk, pairs);
-  return cudaGetLastError();
+  return d == 128 ? launch_behind(kv_append_kernel<128>, grid, kAppThreads, stream, p, chunk, pairs)
+                  : launch_behind(kv_append_kernel<64>, grid, kAppThreads, stream, p, chunk, pairs);
 }
 
 }  // namespace attn
