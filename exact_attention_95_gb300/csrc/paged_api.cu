@@ -150,6 +150,16 @@ attn_status attn_kv_append_fp8(const void* K, long long k_stride, const void* V,
   if (!K || !V || !slots) return ATTN_ERR_INVALID_ARG;
   if (!aligned(K, 16) || !aligned(V, 16) || !aligned(slots, 8)) return ATTN_ERR_INVALID_ARG;
   if (!token_stride_ok(k_stride, Hkv, d) || !token_stride_ok(v_stride, Hkv, d)) return ATTN_ERR_INVALID_ARG;
+  // No updated array may be another array of the call.
+  const size_t codes = (size_t)num_pages * Hkv * page_size * d, scales = (size_t)num_pages * Hkv * 4;
+  const struct {
+    const void* p;
+    size_t n;
+  } all[] = {{k_pages, codes}, {v_pages, codes}, {k_scale, scales}, {v_scale, scales}, {slots, (size_t)T * 8},
+             {K, ((size_t)(T - 1) * k_stride + (size_t)Hkv * d) * 2}, {V, ((size_t)(T - 1) * v_stride + (size_t)Hkv * d) * 2}};
+  for (int o = 0; o < 4; ++o)
+    for (int i = o + 1; i < 7; ++i)
+      if (overlap(all[o].p, all[o].n, all[i].p, all[i].n)) return ATTN_ERR_INVALID_ARG;
   attn::KvAppendParams p{};
   p.K = static_cast<const uint16_t*>(K);
   p.V = static_cast<const uint16_t*>(V);

@@ -326,7 +326,8 @@ attn_status attn_kv_tables(const int32_t* cached, const int32_t* added, const in
  *   K, V  [T, Hkv, d] bf16, 16-byte aligned, k_stride / v_stride elements
  *         between tokens (>= Hkv * d, a multiple of 8: slices of a packed
  *         projection do)
- *   slots [T] int64;  pages and scales as above, updated in place.
+ *   slots [T] int64;  pages and scales as above, updated in place: none of the
+ *         four may overlap another array of the call (ATTN_ERR_INVALID_ARG).
  * T >= 0.
  */
 attn_status attn_kv_append_fp8(const void* K, long long k_stride, const void* V, long long v_stride,

@@ -64,6 +64,14 @@ def test_append_argument_errors(lib, kw, want):
     assert _append(lib, **kw) == want
 
 
+@pytest.mark.parametrize("kw", [
+    dict(vp=at(3)), dict(vsc=at(4)), dict(ksc=P(0x400000 + 10 * 8 * 64 * 128 - 4)), dict(slots=at(6)), dict(K=at(5)),
+    dict(V=P(0x400000 - 2 * (4 * 1024 + 1024) + 16)), dict(vsc=P(0x500000 + 10 * 8 * 4 - 4)),
+], ids=str)
+def test_append_refuses_arrays_that_overlap_what_it_updates(lib, kw):
+    assert _append(lib, **kw) == BAD
+
+
 def _fwd(lib, **kw):
     a = dict(Q=at(0), qs=4096, kp=at(1), ks=at(2), vp=at(3), vs=at(4), table=at(5), cu=at(6), lens=at(7), O=at(8),
              L=at(9), R=3, T=5, Hq=32, Hkv=8, d=128, pages=10, page=64, width=4, scale=0.1, causal=1, out=0, ws=at(10),

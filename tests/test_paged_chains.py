@@ -7,6 +7,7 @@ the work is divided, against the plain 64-bit implementation."""
 import os
 import subprocess
 import sys
+import threading
 
 import numpy as np
 import pytest
@@ -114,6 +115,59 @@ def test_offsets_past_32_bits(chunk):
                                                                    (130, 1)]])[:, None, :, None]
             a, b = (x * held for x in (a, b))
         assert torch.equal(a, b)
+
+
+def test_threads_with_a_stream_each():
+    """Calls of four threads at once (the binding lets Python's lock go) against the same calls in turn."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    Hq, Hkv, d, page = 16, 4, 64, 16
+    work = []
+    for i, (R, new) in enumerate([(2, 1), (5, 3), (40, 1), (1, 60)]):
+        T = R * new
+        cache = _empty_cache(400, Hkv, page, d)
+        free = torch.randperm(400, generator=g, device="cuda").int()
+        added = torch.full((R,), new, dtype=torch.int32, device="cuda")
+        work.append((_randn(g, T, Hq, d), _randn(g, T, Hkv, d), _randn(g, T, Hkv, d), cache, free, added, R, T))
+
+    def steps(w):
+        q, k, v, cache, free, added, R, T = w
+        table = torch.zeros(R, 20, dtype=torch.int32, device="cuda")
+        cached = torch.zeros_like(added)
+        out = []
+        for s in range(5):  # (one request takes four pages a step, the others none after the first)
+            kv, cu, slots, _, _ = pkg.attn_kv_tables(cached, added, free[8 * s:], table, page, T)
+            pkg.attn_kv_append_fp8(k, v, slots, *cache)
+            out += pkg.attn_fwd_paged_fp8(q, *cache, table, cu, kv, causal=True)
+            cached = kv
+        return out
+
+    def reset(w):
+        for x in w[3]:
+            x.fill_(1)
+
+    for w in work:
+        reset(w)
+    want = [steps(w) for w in work]
+    torch.cuda.synchronize()
+    for w in work:
+        reset(w)
+    torch.cuda.synchronize()
+    got, streams = [None] * 4, [torch.cuda.Stream() for _ in work]
+
+    def run(i):
+        with torch.cuda.stream(streams[i]):
+            got[i] = steps(work[i])
+            streams[i].synchronize()
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    torch.cuda.synchronize()
+    assert pkg.attn_last_device_status() == pkg.ATTN_OK
+    for a, b in zip(got, want):
+        assert a is not None and all(torch.equal(x, y) for x, y in zip(a, b))
 
 
 FIRST = """
