@@ -62,6 +62,8 @@ int split_of(int T, int Hkv, long long keys, int workers) {
     if ((long long)T * Hkv * s * 7 <= 6LL * workers && keys <= 1024 * s) return s;
   return 0;
 }
+// A single request runs one of the two only: the wide one if T has more rows than
+// that, even if the request turns out to have fewer.
 // Workspace: partial sums (O, then maxima and sums, then merge descriptors) of
 // every worker, two slots each.
 int workers_of(int rows, int sms) { return sms * attn::paged_ctas(rows); }
@@ -239,14 +241,14 @@ attn_status attn_fwd_paged_fp8(const void* Q, long long q_stride, const void* k_
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const int rows = wide ? 16 : 8;
-  const bool big = wide && (long long)T * G > kNarrowMost, small = !wide || G <= kNarrowMost;
+  const bool big = wide && (long long)T * G > kNarrowMost, small = !wide || (G <= kNarrowMost && !(big && R == 1));
   attn::PagedFwdParams pw = p;
   place(p, ws, rows, d, sms);
   p.behind = big;
   p.rows_min = 0;
   p.rows_max = wide ? kNarrowMost : 0x7fffffff;
   place(pw, ws + part_bytes(rows, d, sms), attn::kPagedWideRows, d, sms);
-  pw.rows_min = kNarrowMost;
+  pw.rows_min = small ? kNarrowMost : 0;
   pw.rows_max = 0x7fffffff;
   cudaError_t e = cudaSuccess;
   const int wide_rows = attn::kPagedWideRows, w1 = workers_of(rows, sms), w2 = workers_of(wide_rows, sms);

@@ -20,12 +20,13 @@ namespace {
 using namespace paged;
 
 constexpr int kMergeWarps = 8;
+constexpr int kTallRows = 128;  // tiles of so many rows keep the warps busy without sharing one
 
 struct MergeSet {
   const float* part_o;
   const float* part_ml;
   const int* desc;
-  int rows, workers;
+  int rows, workers, ctas;  // of a tile; of the launch; of a worker, here
 };
 struct MergeParams {
   MergeSet set[2];
@@ -38,10 +39,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Mer
   __shared__ float s_acc[kMergeWarps][D], s_l[kMergeWarps], s_m[kMergeWarps];
   griddep_launch_dependents();  // the next call's start overlaps this end
   griddep_wait();
-  const bool second = (int)blockIdx.x >= q.set[0].workers;
+  const bool second = (int)blockIdx.x >= q.set[0].workers * q.set[0].ctas;
   const MergeSet& t = q.set[second];
   const PagedFwdParams& p = q.p;
-  const int w = blockIdx.x - (second ? q.set[0].workers : 0);
+  const int cta = blockIdx.x - (second ? q.set[0].workers * q.set[0].ctas : 0);
+  const int w = cta / t.ctas, slice = cta - w * t.ctas;
   const int* d = t.desc + w * 8;
   const int parts = d[0];
   if (parts < 2) return;
@@ -49,11 +51,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Mer
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = min(t.rows, n * p.G - tile * t.rows);
   // Warps that share a row, and this one's number among them.
-  const int team = parts > 2 * kMergeWarps ? kMergeWarps : 1, mate = warp % team;
-  const int step = gridDim.y * (kMergeWarps / team);  // rows at once
+  const int team = parts > 2 * kMergeWarps && t.rows < kTallRows ? kMergeWarps : 1, mate = warp % team;
+  const int step = t.ctas * (kMergeWarps / team);  // rows at once
   const int rounds = (rows + step - 1) / step;
   for (int i = 0; i < rounds; ++i) {
-    const int row = i * step + blockIdx.y * (kMergeWarps / team) + warp / team;
+    const int row = i * step + slice * (kMergeWarps / team) + warp / team;
     if (row >= rows) break;  // (a whole team)
     auto part = [&](int s) -> size_t { return (size_t)(s == 0 ? 2 * w + 1 : 2 * (w + s)) * t.rows + row; };
     // One pass with a running maximum: a part's statistics and sums are one
@@ -144,17 +146,19 @@ cudaError_t launch_paged_merge(int d, const PagedFwdParams& p, int rows, int wor
                                int rows2, int workers2, cudaStream_t stream) {
   MergeParams q{};
   q.p = p;
-  q.set[0] = {p.part_o, p.part_ml, p.desc, rows, workers};
-  if (p2) q.set[1] = {p2->part_o, p2->part_ml, p2->desc, rows2, workers2};
   cudaLaunchConfig_t cfg{};
   // Four CTAs to a worker where items are in many parts (a decoding step with
-  // fewer than an eighth as many items as workers) or tiles are large; one where
-  // a pass of its warps covers the tile.  Measured, four against one (whole
-  // calls, 8 kv heads, d = 128): one request of 131072 keys 51.1 / 56.3 us,
-  // three prompt chunks 458 / 482 us; the other way 64 requests of up to 8192
-  // keys 124.4 / 122.9 us.
+  // fewer than an eighth as many items as workers), else one: a pass of its warps
+  // covers the tile.  Measured, four against one (whole calls, 8 kv heads,
+  // d = 128): one request of 131072 keys 51.1 / 56.3 us; the other way 64 requests
+  // of up to 8192 keys 124.4 / 122.9 us.  Sixteen for tall tiles, against
+  // eight: a chunk of 100 tokens against 4000 keys 31.2 / 37.0 us, of 50 against
+  // 20000 (32 kv heads) 71.3 / 70.3.
   const bool few = (long long)p.R * p.Hkv * 8 <= workers;
-  cfg.gridDim = dim3((unsigned)(workers + workers2), few || rows > 16 || p2 ? 4u : 1u);
+  const int tall = 16;
+  q.set[0] = {p.part_o, p.part_ml, p.desc, rows, workers, rows >= kTallRows ? tall : few ? 4 : 1};
+  if (p2) q.set[1] = {p2->part_o, p2->part_ml, p2->desc, rows2, workers2, tall};
+  cfg.gridDim = dim3((unsigned)(workers * q.set[0].ctas + workers2 * q.set[1].ctas));
   cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.stream = stream;
   cudaLaunchAttribute at{};

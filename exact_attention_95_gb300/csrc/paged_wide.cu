@@ -26,8 +26,8 @@
 // and skips the work.
 //
 // Measured: three requests with chunks of up to 1000 tokens against up to 16384
-// keys, 32 query and 8 kv heads, d = 128: 456 us, 1160 TFLOPS (61 % of a plain
-// bf16 product's rate); the tensor pipe is busy 54 % of the time, the softmax
+// keys, 32 query and 8 kv heads, d = 128: 434 us, 1220 TFLOPS (64 % of a plain
+// bf16 product's rate); the tensor pipe is busy 57 % of the time, the softmax
 // warps issue the rest.  Dropped: the tiles with an S buffer each, or a unit to
 // each tile in turn where an item has up to 128 rows (477 to 635 us).
 #include "paged.cuh"
@@ -474,10 +474,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               (long long)(im->h * p.G + min(rho, last) - tok * p.G) * D);
           uint32_t am = 0;
           bool odd = false;
-#pragma unroll 2
+          uint4 qr[D / 8];  // one wait for all of them
+#pragma unroll
+          for (int x = 0; x < D / 8; ++x) qr[x] = __ldg(src + x);
+#pragma unroll
           for (int x = 0; x < D / 8; ++x) {
-            const uint4 v = __ldg(src + x);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            const uint32_t w[4] = {qr[x].x, qr[x].y, qr[x].z, qr[x].w};
 #pragma unroll
             for (int y = 0; y < 4; ++y) am = __vmaxu2(am, w[y] & 0x7fff7fffu);
           }
@@ -488,12 +490,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           k = min(max(k, -110), 118);
           const float down = __int_as_float((127 - k) << 23);
           f = odd ? NAN : __int_as_float((127 + k) << 23) * p.scale_log2;
-#pragma unroll 1
+#pragma unroll
           for (int x = 0; x < D / 16; ++x) {
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              const uint4 v = __ldg(src + 2 * x + y);
+              const uint4 v = qr[2 * x + y];
               const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
               for (int z = 0; z < 2; ++z) {
