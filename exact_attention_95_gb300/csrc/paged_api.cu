@@ -44,7 +44,7 @@ bool token_stride_ok(long long stride, long long heads, int d) { return stride >
 // nothing to do.  Any other call runs the 16-row kernel for the requests with
 // up to kNarrowMost query rows of a kv head and the 256-row kernel for the
 // rest.  Measured with 16 requests of 4096 keys, 8 kv heads, d = 128: 32 rows
-// 65 us by two tiles of 16 and 75 us by a tile of 256, 48 rows 93 and 76 us.
+// 66 us by two tiles of 16 and 69 us by a tile of 256, 48 rows 94 and 70 us.
 constexpr int kNarrowMost = 32;
 bool runs_wide(int R, int T, int G) { return T > R || G > 8; }
 // CTAs of a cluster for every item of a decoding step, whose sums then meet in

@@ -27,7 +27,7 @@
 //
 // Measured: three requests with chunks of up to 1000 tokens against up to 16384
 // keys, 32 query and 8 kv heads, d = 128: 434 us, 1220 TFLOPS (64 % of a plain
-// bf16 product's rate); the tensor pipe is busy 57 % of the time, the softmax
+// bf16 product's rate); the tensor pipe is busy 56 % of the time, the softmax
 // warps issue the rest.  Dropped: the tiles with an S buffer each, or a unit to
 // each tile in turn where an item has up to 128 rows (477 to 635 us).
 #include "paged.cuh"
