@@ -16,7 +16,7 @@ import torch
 import exact_attention_95_gb300 as pkg
 
 import paged
-from test_paged_cache import _cache, dev, dev_bf16
+from test_paged_cache import _cache, _check_attention, dev, dev_bf16
 
 pytestmark = pytest.mark.gpu
 
@@ -266,3 +266,15 @@ def test_a_nan_value_in_a_small_step_with_narrow_and_wide_tables(d):
         want = np.zeros((3, Hq, d), bool)
         want[2, :, 5] = True
         assert np.array_equal(torch.isnan(O).cpu().numpy(), want) and torch.isfinite(L).all()
+
+
+@pytest.mark.parametrize("lens,news,Hq,Hkv,d,page,pad", [
+    ([500], [3], 8, 2, 128, 32, 60),        # one request of a few rows among many places
+    ([500], [0], 8, 2, 64, 32, 60),         # and of none
+    ([3000, 2900], [12, 11], 16, 1, 128, 32, 0),  # two tall items in two dozen parts each
+    ([3000], [12], 16, 1, 64, 128, 5),
+    ([40, 9000], [2, 70], 8, 1, 64, 16, 0),
+])
+def test_few_tall_items(lens, news, Hq, Hkv, d, page, pad):
+    for out in (torch.bfloat16, torch.float32):
+        _check_attention(np.random.default_rng(61), lens, news, Hq, Hkv, d, page, True, out, pad=pad)
