@@ -45,6 +45,8 @@ bool token_stride_ok(long long stride, long long heads, int d) { return stride >
 // up to kNarrowMost query rows of a kv head and the 256-row kernel for the
 // rest.  Measured with 16 requests of 4096 keys, 8 kv heads, d = 128: 32 rows
 // 66 us by two tiles of 16 and 69 us by a tile of 256, 48 rows 94 and 70 us.
+// A single request runs one of the two only: the wide one if T has more rows than
+// that, even if the request turns out to have fewer.
 constexpr int kNarrowMost = 32;
 bool runs_wide(int R, int T, int G) { return T > R || G > 8; }
 // CTAs of a cluster for every item of a decoding step, whose sums then meet in
@@ -62,8 +64,6 @@ int split_of(int T, int Hkv, long long keys, int workers) {
     if ((long long)T * Hkv * s * 7 <= 6LL * workers && keys <= 1024 * s) return s;
   return 0;
 }
-// A single request runs one of the two only: the wide one if T has more rows than
-// that, even if the request turns out to have fewer.
 // Workspace: partial sums (O, then maxima and sums, then merge descriptors) of
 // every worker, two slots each.
 int workers_of(int rows, int sms) { return sms * attn::paged_ctas(rows); }

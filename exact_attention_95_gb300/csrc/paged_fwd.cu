@@ -28,10 +28,10 @@
 // Measured (whole calls, 8 kv heads, d = 128, a token a request): 64 requests of
 // up to 8192 keys 121 us, 6.2 TB/s; one of 131072 keys 51 us, 5.3 TB/s; four of
 // up to 700 keys 7.5 us in clusters (start, lengths, page ids, codes, the meeting:
-// each waits for the one before; 9.4 us with the merge's launch).  33 requests of up to 3001 keys,
-// 16 kv heads, d = 64: 34 us, 4.2 TB/s.  16 requests of up to 5000 keys with six
-// tokens of four heads each, two tiles of 16 rows: 54 us, bound by what the
-// warps issue for a tile.  Dropped: a tile of 24 rows, whose sums leave no
+// each waits for the one before; 9.4 us with the merge's launch).  33 requests of
+// up to 3001 keys, 16 kv heads, d = 64: 34 us, 4.2 TB/s.  16 requests of up to
+// 5000 keys with six tokens of four heads each, two tiles of 16 rows: 54 us, bound
+// by the latencies of a tile's own instructions.  Dropped: a tile of 24 rows, whose sums leave no
 // registers for the queries (16 requests of 4096 keys, 24 rows: 71 us against
 // 64 by two tiles of 16); three CTAs to an SM for 16 rows too, with the queries
 // in shared memory and K's and V's tiles in one ring (49 us against 45 at 16
