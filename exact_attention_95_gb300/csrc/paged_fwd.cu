@@ -334,16 +334,16 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
             w[q][e] = __ldg(src + (64 * q + 16 * c) / 8 + e);
             const uint32_t ws[4] = {w[q][e].x, w[q][e].y, w[q][e].z, w[q][e].w};
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              uint32_t lo = ws[x] & 0x7fffu, hi = (ws[x] >> 16) & 0x7fffu;
-              am = max(am, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-            }
+            for (int x = 0; x < 4; ++x) am = __vmaxu2(am, ws[x] & 0x7fff7fffu);
           }
+        am = max(am & 0xffffu, am >> 16);
         am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
         am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
         // 2^-e takes the row's largest to [2^14, 2^15); e within what fp32 can undo.
         const int e = min(max((int)(am >> 7) - 127, -100), 126) - 14;
-        const float up = __int_as_float((127 - e) << 23);
+        // An infinity or NaN in the row: NaN for all of it, so that every logit is one (an
+        // infinity times codes of one sign would give -inf alone, a masked key's).
+        const float up = am >= 0x7f80u ? NAN : __int_as_float((127 - e) << 23);
         const float fr = __int_as_float((127 + e) << 23) * p.scale_log2;
 #pragma unroll
         for (int q = 0; q < QI; ++q)

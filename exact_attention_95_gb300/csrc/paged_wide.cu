@@ -473,7 +473,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               p.Q + (long long)(im->start + tok) * p.q_stride +
               (long long)(im->h * p.G + min(rho, last) - tok * p.G) * D);
           uint32_t am = 0;
-          bool odd = false;
           uint4 qr[D / 8];  // one wait for all of them
 #pragma unroll
           for (int x = 0; x < D / 8; ++x) qr[x] = __ldg(src + x);
@@ -484,12 +483,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int y = 0; y < 4; ++y) am = __vmaxu2(am, w[y] & 0x7fff7fffu);
           }
           am = max(am & 0xffffu, am >> 16);
-          odd = am >= 0x7f80u;  // an infinity or NaN: the row's logits are NaN
           // 2^k with the row's largest in (224, 448].
           int k = (int)(am >> 7) - 127 - ((am & 0x7f) <= 0x60 ? 8 : 7);
           k = min(max(k, -110), 118);
-          const float down = __int_as_float((127 - k) << 23);
-          f = odd ? NAN : __int_as_float((127 + k) << 23) * p.scale_log2;
+          // An infinity or NaN in the row: NaN codes for all of it.  Its logits are NaN
+          // then, but for those of masked keys (a row that sees none stays empty).
+          const float down = am >= 0x7f80u ? NAN : __int_as_float((127 - k) << 23);
+          f = __int_as_float((127 + k) << 23) * p.scale_log2;
 #pragma unroll
           for (int x = 0; x < D / 16; ++x) {
             uint32_t hi[4], lo[4];

@@ -342,8 +342,8 @@ attn_status attn_kv_append_fp8(const void* K, long long k_stride, const void* V,
  *   s_ij = scale * <Q_i, k_j>, O_i = sum_j softmax_j(s_i) v_j, LSE_i = ln sum_j e^{s_ij},
  * k_j and v_j being code * scale of their page.  A row with no kept key gets
  * O = 0 and LSE = -inf.  Rows t >= cu_q[R] are left as they were.  A NaN or
- * infinity in a row of Q makes that row NaN, one in K or V the rows that see
- * it.  The codes enter the products exactly and sums are fp32.  Queries enter
+ * infinity in a row of Q makes that row NaN if it has a kept key, one in K or V
+ * the rows that see it.  The codes enter the products exactly and sums are fp32.  Queries enter
  * exactly down to 2^-10 of their row's largest element, and off by at most
  * 2^-17 of it below.  The weights are rounded to f16 (2^-11 relative, for
  * weights down to 2^-23 of the row's largest and V scales of like size: the

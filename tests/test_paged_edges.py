@@ -1,0 +1,59 @@
+"""The paged cache where its kernels could give each other different answers:
+infinite queries, against the plain 64-bit implementation."""
+
+import numpy as np
+import pytest
+import torch
+
+import exact_attention_95_gb300 as pkg
+
+import paged
+from test_paged_cache import I32, _cache, dev, dev_bf16, ok
+
+gpu = pytest.mark.gpu
+
+# What a call runs: new tokens of two requests, heads of a kv head, columns of the table behind the last page.
+KERNELS = {"8 rows, clusters": ([1, 1], 2, 0), "8 rows, ranges": ([1, 1], 2, 700), "16 rows": ([5, 4], 2, 0),
+           "256 rows": ([40, 50], 1, 0), "both": ([5, 50], 2, 0)}
+
+
+# ------------------------------------------------------------------ infinite queries
+@gpu
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("keys", [1, 3, 150])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("d", [64, 128])
+def test_an_infinite_query_makes_its_row_nan_whatever_the_keys_signs(kernel, keys, sign, d):
+    """Every key has a code of one sign in the infinite column, so that all logits are
+    +inf or all -inf; a row that sees no key stays as such rows are."""
+    news, G, extra = KERNELS[kernel]
+    page, Hkv = 16, 2
+    rng = np.random.default_rng(keys + d)
+    kc, ks, vc, vs, table = _cache(rng, [keys, keys], page, Hkv, d, width_extra=1 + extra)
+    kc[..., 3] = 0x38
+    cu = np.concatenate([[0], np.cumsum(news)]).astype(I32)
+    T, Hq = int(cu[-1]), G * Hkv
+    q = paged.bf16_bits(rng.standard_normal((T, Hq, d)).astype(np.float32))
+    bits = q.copy()
+    inf = np.zeros((T, Hq), bool)
+    for r in range(2):
+        for t in (cu[r], cu[r + 1] - 1):  # (the first sees no key where there are more queries)
+            inf[t, r] = inf[t, Hq - 1] = True
+    bits[inf, 3] = 0x7F80 if sign > 0 else 0xFF80
+    q[inf] = 0
+    g = [dev(a) for a in (kc, ks, vc, vs, table, cu, np.array([keys, keys], I32))]
+    for causal in (True, False):
+        O, L = pkg.attn_fwd_paged_fp8(dev_bf16(bits), *g, None, causal, torch.float32)
+        ok()
+        Or, Lr, A, B = paged.attention(paged.bf16_values(q), kc, ks, vc, vs, table, cu, [keys, keys],
+                                       float(np.float32(1 / np.sqrt(d))), causal)
+        Og, Lg = O.double().cpu().numpy(), L.double().cpu().numpy()
+        none = np.isneginf(Lr)
+        assert np.array_equal(np.isnan(Lg), inf & ~none)
+        assert np.isnan(Og[inf & ~none]).all()
+        assert np.isneginf(Lg[none]).all() and (Og[none] == 0.0).all()
+        rest = ~inf & ~none
+        tol_o, tol_l = paged.bounds(Or, Lr, A, B, d, False)
+        assert (np.abs(Og[rest] - Or[rest]) <= tol_o[rest]).all()
+        assert (np.abs(Lg[rest] - Lr[rest]) <= tol_l[rest]).all()
+
