@@ -655,9 +655,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (live) {
         const bool valid = rho <= last;
-        const float back = n > 0 ? ex2(lvref - kShift) : 0.f;
+        // O = sums * part * mul.  (In one factor the smallest V scales would be lost:
+        // 2^-126 * 2^-9 / l is subnormal.)
         const size_t orow = output_row(p, im->start, im->h, min(rho, last));
-        const float mul = im->slot < 0 ? back * output_factor(l) : back;
+        const float part = (im->slot < 0 ? output_factor(l) : 1.f) * (1.f / (1 << (int)kShift));
+        const float mul = n > 0 ? ex2(lvref) : 0.f;
         const size_t prow = (size_t)(blockIdx.x * 2 + max(im->slot, 0)) * kPagedWideRows + t * kBM + row;
         // bf16 rows go through the warp's quarter of the Q tile (whose products have completed).
         const uint32_t stage = q_hi + quad * 32 * D;
@@ -667,6 +669,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (n > 0) {
             tmem_ld32(o_t + c * 32, o);
             tmem_ld_wait(o);
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * part);
           } else {
 #pragma unroll
             for (int x = 0; x < 32; ++x) o[x] = 0u;

@@ -1,5 +1,5 @@
 """The paged cache where its kernels could give each other different answers:
-infinite queries, against the plain 64-bit implementation."""
+infinite queries and the smallest V scales, against the plain 64-bit implementation."""
 
 import numpy as np
 import pytest
@@ -57,3 +57,25 @@ def test_an_infinite_query_makes_its_row_nan_whatever_the_keys_signs(kernel, key
         assert (np.abs(Og[rest] - Or[rest]) <= tol_o[rest]).all()
         assert (np.abs(Lg[rest] - Lr[rest]) <= tol_l[rest]).all()
 
+
+# ------------------------------------------------------------------ the smallest V scales
+@gpu
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_at_the_smallest_scale_are_not_lost(kernel, d):
+    """V = 448 * 2^-126 everywhere (the append's smallest scale): every row's O is V.
+
+    A weight is off by 2^-11 at most.  Sums times the V scale and 1 / l are normal numbers
+    or the result's own size."""
+    news, G, extra = KERNELS[kernel]
+    page, Hkv, lens = 32, 1, [50, 50]
+    rng = np.random.default_rng(d)
+    kc, ks, vc, vs, table = _cache(rng, lens, page, Hkv, d, width_extra=1 + extra)
+    vc[:], vs[:] = 0x7E, 2.0 ** -126
+    cu = np.concatenate([[0], np.cumsum(news)]).astype(I32)
+    q = paged.bf16_bits(rng.standard_normal((int(cu[-1]), G * Hkv, d)).astype(np.float32))
+    g = [dev(a) for a in (kc, ks, vc, vs, table, cu, np.array(lens, I32))]
+    O, _ = pkg.attn_fwd_paged_fp8(dev_bf16(q), *g, None, True, torch.float32)
+    ok()
+    got = O.double().cpu().numpy() / (448.0 * 2.0 ** -126)
+    assert np.abs(got - 1.0).max() <= 2.0 ** -11 + 2.0 ** -15
