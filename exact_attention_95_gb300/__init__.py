@@ -1,10 +1,12 @@
 """Exact softmax attention for NVIDIA GB300 (sm_103a): Python binding.
 
-A thin ctypes layer over the C ABI in ``include/attn.h`` (``libattn_sm103.so``,
-built in-tree by ``exact_attention_95_gb300.build``).  It only marshals
-arguments: PyTorch supplies device memory and the current stream, and every
-step of the computation runs in the library's CUDA kernels.  If the library
-is missing, every call raises; there is no fallback implementation.
+A thin layer over the C ABI in ``include/attn.h`` (``libattn_sm103.so``, built
+in-tree by ``exact_attention_95_gb300.build``): ctypes, and for the paged cache's
+calls an extension module, without which they make their checks in Python and
+take longer.  It only marshals arguments: PyTorch supplies device memory and the
+current stream, and every step of the computation runs in the library's CUDA
+kernels.  If the library is missing, every call raises; there is no fallback
+implementation.
 
 Functions carry the C names:
 
@@ -38,9 +40,11 @@ fp32 forward); ``LSE`` is ``[B, Hq, N]`` fp32.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
 import threading
+import warnings
 
 import torch
 
@@ -66,7 +70,7 @@ _BWD_STAGES = {"all": "attn_bwd", "preprocess": "attn_bwd_preprocess", "main": "
 
 _lock = threading.Lock()
 _lib = None
-_fast = None  # the extension module, bound to the loaded library
+_fast = None  # the extension module, bound to the loaded library; False where there is none
 
 
 class AttnError(RuntimeError):
@@ -77,7 +81,7 @@ class AttnError(RuntimeError):
 
 def load_library(path: str = LIB_PATH):
     """Load the CUDA library (raises if it has not been built)."""
-    global _lib, _fast
+    global _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -128,18 +132,32 @@ def load_library(path: str = LIB_PATH):
         lib.attn_last_device_status.restype = i32
         lib.attn_selftest_wait_timeout.argtypes = [ctypes.c_ulonglong, vp]
         lib.attn_selftest_wait_timeout.restype = i32
-        from . import _binding
-        _binding.bind(*(ctypes.cast(f, vp).value for f in (
-            lib.attn_kv_tables, lib.attn_kv_append_fp8, lib.attn_fwd_paged_fp8, lib.attn_fwd_paged_workspace_size)))
-        _fast = _binding
         _lib = lib
         return lib
 
 
 def _bound():
-    """The extension module (csrc/binding.cpp), with the library loaded."""
-    if _fast is None:
-        load_library()
+    """The extension module (csrc/binding.cpp) with the library loaded, at the first paged
+    call; False, after a warning, where it cannot be loaded."""
+    global _fast
+    if _fast is not None:
+        return _fast
+    lib = load_library()
+    with _lock:
+        if _fast is None:
+            from .build import binding_path
+            try:
+                spec = importlib.util.spec_from_file_location(__name__ + "._binding", binding_path())
+                module = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(module)
+                module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                    lib.attn_kv_tables, lib.attn_kv_append_fp8, lib.attn_fwd_paged_fp8,
+                    lib.attn_fwd_paged_workspace_size)))
+                _fast = module
+            except ImportError as e:
+                _fast = False
+                warnings.warn(f"the paged calls make their checks in Python, which takes longer: {e} "
+                              "(python -m exact_attention_95_gb300.build makes the module)", RuntimeWarning, stacklevel=3)
     return _fast
 
 
@@ -464,9 +482,10 @@ def attn_kv_tables(cached, added, free_pages, block_table, page_size, T, kv_lens
     (updated in place); T places for new tokens.  Returns (kv_lens [R], cu_tokens
     [R + 1], slots [T] int64, positions [T], taken [2]: pages taken from the head
     of free_pages, requests refused)."""
-    if stream is None:
-        r = _bound().kv_tables(cached, added, free_pages, block_table, page_size, T, kv_lens, cu_tokens, slots,
-                               positions, taken)
+    fast = stream is None and _bound()
+    if fast:
+        r = fast.kv_tables(cached, added, free_pages, block_table, page_size, T, kv_lens, cu_tokens, slots,
+                           positions, taken)
         if r is not None:
             return _result(r, "attn_kv_tables")
     lib = load_library()
@@ -501,8 +520,9 @@ def attn_kv_append_fp8(K, V, slots, k_pages, k_scale, v_pages, v_scale, stream=N
 
     k_pages, v_pages uint8 [num_pages, Hkv, page_size, d] and k_scale, v_scale fp32
     [num_pages, Hkv] are updated in place, and returned."""
-    if stream is None:
-        r = _bound().kv_append_fp8(K, V, slots, k_pages, k_scale, v_pages, v_scale)
+    fast = stream is None and _bound()
+    if fast:
+        r = fast.kv_append_fp8(K, V, slots, k_pages, k_scale, v_pages, v_scale)
         if r is not None:
             return _result(r, "attn_kv_append_fp8")
     lib = load_library()
@@ -535,9 +555,10 @@ def attn_fwd_paged_fp8(Q, k_pages, k_scale, v_pages, v_scale, block_table, cu_q,
     if out_dtype is None:
         out_dtype = torch.bfloat16
     out_dt = {torch.bfloat16: ATTN_BF16, torch.float32: ATTN_F32}[out_dtype]
-    if stream is None:
-        r = _bound().fwd_paged_fp8(Q, k_pages, k_scale, v_pages, v_scale, block_table, cu_q, kv_lens, scale, causal,
-                                   out_dt, O, LSE, workspace)
+    fast = stream is None and _bound()
+    if fast:
+        r = fast.fwd_paged_fp8(Q, k_pages, k_scale, v_pages, v_scale, block_table, cu_q, kv_lens, scale, causal,
+                               out_dt, O, LSE, workspace)
         if r is not None:
             return _result(r, "attn_fwd_paged_fp8")
     lib = load_library()

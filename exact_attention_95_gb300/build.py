@@ -2,8 +2,9 @@
 
 Each .cu file under csrc/ is compiled by its own nvcc process (in parallel)
 and linked into ``libattn_sm103.so`` next to this file.  nvcc cross-compiles,
-so this runs on a machine without a GPU.  csrc/binding.cpp becomes the
-extension module ``_binding.so`` (host compiler, PyTorch's headers).
+so this runs on a machine without a GPU.  csrc/binding.cpp becomes an
+extension module (host compiler, PyTorch's headers), for one Python and one
+PyTorch: its file's name has both.  The library does not need it.
 """
 
 from __future__ import annotations
@@ -14,6 +15,7 @@ import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -56,18 +58,26 @@ def up_to_date(lib: str = LIB) -> bool:
 # The extension module of the paged calls; it does not depend on which variant
 # of the library is loaded.
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
-BINDING = os.path.join(HERE, "_binding.so")
+
+
+def binding_path() -> str:
+    """The extension module's file for this Python and PyTorch: one that was built
+    for others has another name, and is neither loaded nor taken for current."""
+    import torch
+    abi = sysconfig.get_config_var("SOABI") or sys.implementation.cache_tag
+    return os.path.join(HERE, f"_binding.{abi}.torch-{torch.__version__}.so")
 
 
 def build_binding(force: bool = False) -> str:
     """Compile the extension module with the host compiler."""
+    path = binding_path()
     deps = (BINDING_SRC, os.path.join(ROOT, "include", "attn.h"), __file__)
-    if not force and os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
-        return BINDING
+    if not force and os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in deps):
+        return path
     import torch
     t = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(_nvcc())) or "/usr/local/cuda"
-    tmp = BINDING + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(t, "include"),
@@ -76,8 +86,17 @@ def build_binding(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING)
-    return BINDING
+    os.replace(tmp, path)
+    return path
+
+
+def _try_binding(force: bool = False) -> None:
+    """The module where the host can build it; a warning where it cannot (no headers
+    of Python's or PyTorch's, say): the paged calls then make their checks in Python."""
+    try:
+        build_binding(force)
+    except Exception as e:
+        warnings.warn(f"the extension module of the paged calls was not built: {e}", RuntimeWarning, stacklevel=3)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: bool = False) -> str:
@@ -86,7 +105,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
     if debug:
         extra_flags = tuple(extra_flags) + ("-DATTN_DEBUG",)
     if not force and up_to_date(lib):
-        build_binding()
+        _try_binding()
         return lib
     os.makedirs(bdir, exist_ok=True)
     nvcc = _nvcc()
@@ -102,7 +121,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
-        binding = ex.submit(build_binding, force)
+        binding = ex.submit(_try_binding, force)
         objs = list(ex.map(compile_one, _sources()))
         binding.result()
     tmp = lib + f".tmp{os.getpid()}"

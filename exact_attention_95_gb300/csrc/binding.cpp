@@ -7,8 +7,10 @@
 // package's functions of the same names, positionally.  They return the
 // outputs, the library's status as an int where a call fails, or None where an
 // argument is not as it has to be (or a stream is named): the package's own
-// checks then word the error.  The library is reached through the addresses
-// that bind() is given, so whichever build of it is loaded is used.
+// checks then word the error.  Without the module (a host that cannot build it, one
+// built for another Python or PyTorch) the package's own checks make the calls.
+// The library is reached through the addresses that bind() is given, so whichever
+// build of it is loaded is used.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
