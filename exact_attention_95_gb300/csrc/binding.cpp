@@ -18,9 +18,11 @@
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <exception>
 
 #include "../../include/attn.h"
 
@@ -139,12 +141,14 @@ PyObject* tuple(P*... items) {
   return t;
 }
 
-#define ATTN_GUARD(...)                             \
-  try {                                             \
-    __VA_ARGS__                                     \
-  } catch (const std::exception& e) {               \
-    PyErr_SetString(PyExc_RuntimeError, e.what());  \
-    return nullptr;                                 \
+// What PyTorch throws is raised as its own calls raise it (an allocation that fails is
+// torch.OutOfMemoryError).
+#define ATTN_GUARD(...)                                             \
+  try {                                                             \
+    __VA_ARGS__                                                     \
+  } catch (const std::exception&) {                                 \
+    torch::translate_exception_to_python(std::current_exception()); \
+    return nullptr;                                                 \
   }
 
 // cached, added, free_pages, block_table, page_size, T, kv_lens, cu_tokens, slots, positions, taken

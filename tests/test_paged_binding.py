@@ -105,3 +105,23 @@ def test_the_calls_give_the_same_without_the_module(R, T, d, monkeypatch):
     with pytest.raises(ValueError, match="workspace"):
         pkg.attn_fwd_paged_fp8(x, pages, one, pages, one, i[:, None].repeat(1, 2).contiguous(), torch.zeros_like(i[:1]).repeat(4),
                                i, workspace=small)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("module", [True, False])
+def test_an_allocation_that_fails_raises_as_torch_raises_it(module, monkeypatch):
+    """Eight gigabytes and more of outputs where the process may have three (nothing is allocated)."""
+    if not module:
+        monkeypatch.setattr(pkg, "_fast", False)
+    i = torch.zeros(3, dtype=torch.int32, device="cuda")
+    table = torch.zeros(3, 2, dtype=torch.int32, device="cuda")
+    torch.cuda.empty_cache()
+    torch.cuda.set_per_process_memory_fraction(0.01)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            pkg.attn_kv_tables(i, i, i, table, 16, 10 ** 9)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    pkg.attn_kv_tables(i, i, i, table, 16, 3)
+    torch.cuda.synchronize()
+    assert pkg.attn_last_device_status() == pkg.ATTN_OK
