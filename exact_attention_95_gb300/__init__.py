@@ -481,7 +481,8 @@ def attn_kv_tables(cached, added, free_pages, block_table, page_size, T, kv_lens
     cached, added int32 [R]; free_pages int32 [F]; block_table int32 [R, max_pages]
     (updated in place); T places for new tokens.  Returns (kv_lens [R], cu_tokens
     [R + 1], slots [T] int64, positions [T], taken [2]: pages taken from the head
-    of free_pages, requests refused)."""
+    of free_pages, requests refused).  kv_lens, cu_tokens and taken may be views of one
+    storage where the call makes them."""
     fast = stream is None and _bound()
     if fast:
         r = fast.kv_tables(cached, added, free_pages, block_table, page_size, T, kv_lens, cu_tokens, slots,

@@ -14,7 +14,6 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -59,33 +58,38 @@ bool small_int(PyObject* o, long long lo, long long hi, int& out) {
 }
 bool fits(int64_t v) { return v >= 0 && v <= 0x7fffffff; }
 
-// An output: the caller's if it is as it has to be, a new one for None.
-bool output(PyObject* o, at::Tensor& t, at::ScalarType type, at::IntArrayRef shape, at::Device device) {
-  if (o == Py_None) {
-    t = at::empty(shape, at::TensorOptions().dtype(type).device(device));
-    return true;
-  }
-  const at::Tensor* given = tensor(o);
-  if (!is(given, type, shape, device)) return false;
-  t = *given;
-  return true;
-}
 // New device memory on the current device and stream, from torch's allocator.
 // Called directly: the dispatcher's code on the way to an at::empty, cold after
-// a kernel launch, takes longer than the allocation (tables 6.7 us a call with
-// two of them, 4.9 like this; attention 9.3 and 6.0).
+// a kernel launch, takes longer than the allocation.
 at::Storage memory(size_t bytes) {
   c10::Allocator* from = c10::cuda::CUDACachingAllocator::get();
   return at::Storage(c10::make_intrusive<c10::StorageImpl>(c10::StorageImpl::use_byte_size_t(), bytes,
                                                            from->allocate(bytes), from, /*resizable=*/true));
 }
 // A contiguous tensor of this type and shape in it, from element `first` (of this type) on.
-at::Tensor part_of(const at::Storage& s, at::ScalarType type, int64_t first, at::IntArrayRef shape) {
-  at::Tensor v = at::detail::make_tensor<c10::TensorImpl>(at::Storage(s), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+at::Tensor part_of(at::Storage s, at::ScalarType type, int64_t first, at::IntArrayRef shape) {
+  at::Tensor v = at::detail::make_tensor<c10::TensorImpl>(std::move(s), c10::DispatchKeySet(c10::DispatchKey::CUDA),
                                                           c10::scalarTypeToTypeMeta(type));
   v.unsafeGetTensorImpl()->set_storage_offset(first);
   v.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
   return v;
+}
+// A tensor with a storage of its own.
+at::Tensor fresh(at::ScalarType type, at::IntArrayRef shape) {
+  size_t bytes = c10::elementSize(type);
+  for (const int64_t n : shape) bytes *= (size_t)n;
+  return part_of(memory(bytes), type, 0, shape);
+}
+// An output: the caller's if it is as it has to be, a new one for None (`device` is the current one).
+bool output(PyObject* o, at::Tensor& t, at::ScalarType type, at::IntArrayRef shape, at::Device device) {
+  if (o == Py_None) {
+    t = fresh(type, shape);
+    return true;
+  }
+  const at::Tensor* given = tensor(o);
+  if (!is(given, type, shape, device)) return false;
+  t = *given;
+  return true;
 }
 // Sets the device, where it is another one, for as long as this lives.
 struct OnDevice {
@@ -167,19 +171,18 @@ PyObject* kv_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
       Py_RETURN_NONE;
     const OnDevice on(dev);
     at::Tensor lens, cu, slots, positions, taken;
-    if (a[6] == Py_None && a[7] == Py_None && a[8] == Py_None && a[9] == Py_None && a[10] == Py_None) {
-      // One allocation for all of them.
-      const at::Storage all = memory(8 * (size_t)T + 4 * (size_t)(2 * R + 3 + T));
-      const int64_t at = 2 * (int64_t)T;
-      slots = part_of(all, at::kLong, 0, {T});
-      lens = part_of(all, at::kInt, at, {R});
-      cu = part_of(all, at::kInt, at + R, {R + 1});
-      taken = part_of(all, at::kInt, at + 2 * R + 1, {2});
-      positions = part_of(all, at::kInt, at + 2 * R + 3, {T});
+    if (a[6] == Py_None && a[7] == Py_None && a[10] == Py_None) {
+      // The small ones in one allocation: each takes 0.35 us of a call.  (The arrays of
+      // the tokens have their own: who keeps `taken` keeps no megabytes.)
+      const at::Storage small = memory(4 * (size_t)(2 * R + 3));
+      lens = part_of(small, at::kInt, 0, {R});
+      cu = part_of(small, at::kInt, R, {R + 1});
+      taken = part_of(small, at::kInt, 2 * R + 1, {2});
     } else if (!output(a[6], lens, at::kInt, {R}, dev) || !output(a[7], cu, at::kInt, {R + 1}, dev) ||
-        !output(a[8], slots, at::kLong, {T}, dev) || !output(a[9], positions, at::kInt, {T}, dev) ||
-        !output(a[10], taken, at::kInt, {2}, dev))
+               !output(a[10], taken, at::kInt, {2}, dev)) {
       Py_RETURN_NONE;
+    }
+    if (!output(a[8], slots, at::kLong, {T}, dev) || !output(a[9], positions, at::kInt, {T}, dev)) Py_RETURN_NONE;
     const int rc = without_lock(dev, [&](void* stream) {
       return g_tables((const int32_t*)cached->data_ptr(), (const int32_t*)added->data_ptr(),
                       (const int32_t*)free_pages->data_ptr(), (int)F, (int32_t*)table->data_ptr(), (int)width, page,
@@ -236,16 +239,9 @@ PyObject* fwd_paged_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (causal < 0 || f32 < 0) return nullptr;
     const OnDevice on(dev);
     at::Tensor O, LSE;
-    const at::ScalarType type = f32 ? at::kFloat : at::kBFloat16;
-    if (a[11] == Py_None && a[12] == Py_None) {
-      // One allocation for both outputs (O's rows are 128 bytes at least).
-      const int64_t bytes = T * Hq * c.d * (f32 ? 4 : 2);
-      const at::Storage all = memory((size_t)bytes + 4 * (size_t)(T * Hq));
-      O = part_of(all, type, 0, {T, Hq, c.d});
-      LSE = part_of(all, at::kFloat, bytes / 4, {T, Hq});
-    } else if (!output(a[11], O, type, {T, Hq, c.d}, dev) || !output(a[12], LSE, at::kFloat, {T, Hq}, dev)) {
+    if (!output(a[11], O, f32 ? at::kFloat : at::kBFloat16, {T, Hq, c.d}, dev) ||
+        !output(a[12], LSE, at::kFloat, {T, Hq}, dev))
       Py_RETURN_NONE;
-    }
     const size_t need = g_workspace((int)R, (int)T, (int)Hq, (int)c.Hkv, (int)c.d);
     c10::DataPtr own;  // freed at the end of this call, for later work of the same stream
     void* ws = nullptr;

@@ -125,3 +125,21 @@ def test_an_allocation_that_fails_raises_as_torch_raises_it(module, monkeypatch)
     pkg.attn_kv_tables(i, i, i, table, 16, 3)
     torch.cuda.synchronize()
     assert pkg.attn_last_device_status() == pkg.ATTN_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("module", [True, False])
+def test_what_outputs_share(module, monkeypatch):
+    """Keeping, saving or resizing an output takes no other along, but for the small ones
+    of the tables (a few bytes a request) among one another."""
+    if not module:
+        monkeypatch.setattr(pkg, "_fast", False)
+    R = 4
+    table, lens, cu, slots, pos, taken, *rest = _step(R, 60, 64)
+    own = [slots, pos, *rest]
+    for t in own:
+        assert t.storage_offset() == 0 and t.untyped_storage().nbytes() == t.numel() * t.element_size()
+    for t in (lens, cu, taken):
+        assert t.untyped_storage().nbytes() <= 4 * (2 * R + 3)
+    at = [t.untyped_storage().data_ptr() for t in own]
+    assert len(set(at)) == len(at) and not {t.untyped_storage().data_ptr() for t in (lens, cu, taken)} & set(at)
