@@ -1,5 +1,6 @@
 """The paged cache where its kernels could give each other different answers:
-infinite queries and the smallest V scales, against the plain 64-bit implementation."""
+infinite queries, the smallest V scales, and ragged batches of more than 32
+requests in every kernel, against the plain 64-bit implementation."""
 
 import numpy as np
 import pytest
@@ -8,7 +9,7 @@ import torch
 import exact_attention_95_gb300 as pkg
 
 import paged
-from test_paged_cache import I32, _cache, dev, dev_bf16, ok
+from test_paged_cache import I32, _cache, _check_attention, dev, dev_bf16, ok
 
 gpu = pytest.mark.gpu
 
@@ -79,3 +80,42 @@ def test_values_at_the_smallest_scale_are_not_lost(kernel, d):
     ok()
     got = O.double().cpu().numpy() / (448.0 * 2.0 ** -126)
     assert np.abs(got - 1.0).max() <= 2.0 ** -11 + 2.0 ** -15
+
+
+# ------------------------------------------------------------------ many requests
+@gpu
+@pytest.mark.parametrize("name,R,counts,Hq,Hkv,d,page", [
+    # Few rows and many in one call, idle requests among them: both kernels' walks over groups of 32 requests.
+    ("mixed", 70, (0, 1, 2, 9, 40, 150), 4, 2, 64, 16),
+    ("mixed", 70, (0, 1, 2, 9, 40, 150), 2, 2, 128, 64),
+    ("mixed, two of the tables' blocks", 1100, (0, 1, 2, 3, 33), 2, 1, 64, 32),
+    # Up to 32 rows of a kv head only: the wide kernel finds nothing.
+    ("16 rows", 100, (1, 2, 3, 6), 8, 2, 128, 32),
+    # More than 32 in each: the 16-row kernel finds nothing.
+    ("256 rows", 45, (40, 77, 130), 1, 1, 128, 16),
+    # Groups above eight heads: a decoding step with 16, and with 40 (the wide kernel alone).
+    ("16 heads", 70, (0, 1), 32, 2, 128, 16),
+    ("40 heads", 70, (0, 1), 40, 1, 64, 16),
+])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_attention_of_more_than_32_requests_in_every_kernel(name, R, counts, Hq, Hkv, d, page, out):
+    rng = np.random.default_rng(R + d + Hq)
+    news = rng.choice(counts, R)
+    news[R // 2] = max(counts)
+    lens = np.where(rng.random(R) < 0.1, 0, news + rng.integers(0, 300, R))
+    _check_attention(rng, lens, news, Hq, Hkv, d, page, True, out, pad=3)
+
+
+@gpu
+@pytest.mark.parametrize("R,tall,Hq,Hkv,d", [(256, 128, 8, 2, 128), (256, 200, 4, 4, 64), (40, 40, 8, 1, 64)])
+@pytest.mark.parametrize("ones", [False, True])
+def test_a_tall_chunk_among_idle_requests(R, tall, Hq, Hkv, d, ones):
+    """No more tokens than requests, most of them one request's: tiles of eight rows only."""
+    rng = np.random.default_rng(R + tall + d)
+    news = np.zeros(R, int)
+    news[R // 3] = tall
+    if ones:
+        news[R // 2:R // 2 + R - tall] = 1
+    assert news.sum() <= R
+    lens = np.where(news > 0, news + rng.integers(0, 400, R), rng.integers(0, 50, R))
+    _check_attention(rng, lens, news, Hq, Hkv, d, 16, True, torch.float32)
