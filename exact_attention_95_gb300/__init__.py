@@ -31,7 +31,7 @@ Functions carry the C names:
 * ``attn_bwd(Q, K, V, O, dO, LSE, scale, causal) -> (dQ, dK, dV)``
 * ``attn_bwd_workspace_size(B, Hq, Hkv, N, d)``
 * ``attn_last_device_status(stream=None)``, ``attn_status_string(code)``
-* ``attn_selftest_wait_timeout(limit_ns)``
+* ``attn_selftest_wait_timeout(limit_ns)``, ``attn_selftest_paged_wait_timeout(limit_ns)``
 
 Tensors are ``[B, H, N, d]`` contiguous CUDA tensors (bf16, or fp32 for the
 fp32 forward); ``LSE`` is ``[B, Hq, N]`` fp32.
@@ -64,7 +64,8 @@ EXPORTED = ("attn_fwd", "attn_fwd_split", "attn_fwd_split_workspace_size", "attn
             "attn_bwd_masked", "attn_quantize_fp8", "attn_fp8_vt_stride", "attn_fwd_fp8", "attn_bwd",
             "attn_bwd_preprocess", "attn_bwd_main", "attn_bwd_convert", "attn_bwd_workspace_size",
             "attn_kv_tables", "attn_kv_append_fp8", "attn_fwd_paged_fp8", "attn_fwd_paged_workspace_size",
-            "attn_status_string", "attn_last_device_status", "attn_selftest_wait_timeout")
+            "attn_status_string", "attn_last_device_status", "attn_selftest_wait_timeout",
+            "attn_selftest_paged_wait_timeout")
 _BWD_STAGES = {"all": "attn_bwd", "preprocess": "attn_bwd_preprocess", "main": "attn_bwd_main",
                "convert": "attn_bwd_convert"}
 
@@ -132,6 +133,8 @@ def load_library(path: str = LIB_PATH):
         lib.attn_last_device_status.restype = i32
         lib.attn_selftest_wait_timeout.argtypes = [ctypes.c_ulonglong, vp]
         lib.attn_selftest_wait_timeout.restype = i32
+        lib.attn_selftest_paged_wait_timeout.argtypes = [ctypes.c_ulonglong, vp]
+        lib.attn_selftest_paged_wait_timeout.restype = i32
         _lib = lib
         return lib
 
@@ -222,6 +225,10 @@ def attn_last_device_status(stream=None) -> int:
 
 def attn_selftest_wait_timeout(limit_ns: int, stream=None) -> int:
     return int(load_library().attn_selftest_wait_timeout(int(limit_ns), _stream(stream)))
+
+
+def attn_selftest_paged_wait_timeout(limit_ns: int, stream=None) -> int:
+    return int(load_library().attn_selftest_paged_wait_timeout(int(limit_ns), _stream(stream)))
 
 
 def attn_fwd(Q, K, V, scale=None, causal=False, out_dtype=None, O=None, LSE=None, stream=None):

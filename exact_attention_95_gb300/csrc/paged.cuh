@@ -21,20 +21,28 @@ namespace paged {
 
 constexpr int kUnit = 128;       // keys of a unit
 
-// Bounded wait of a whole warp, with one result: a failing try gives up its
-// issue slots for 1.3 us (measured), so the limit is about 1.3 s.  As short as
-// it can be: it is written out at some thirty places, and a kernel's warps wait
-// for instructions where there are more than 128 KB of them (three prompt chunks
-// 562 us with waits that look at a clock, 452 us with these).  A wait that runs
-// out sets the CTA's abort flag, which ends the others and is reported at the
-// kernel's end.
-constexpr uint32_t kTries = 1u << 20;
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  for (uint32_t tries = 0; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); ++tries)
-    if (__any_sync(0xffffffffu, *abort_flag != 0 || tries >= kTries)) {
-      *abort_flag = 1;
+// Bounded wait of a whole warp, with one result.  As short as it can be: it is
+// written out at some twenty places, and a kernel's warps wait for instructions
+// where there are more than 128 KB of them (three prompt chunks 562 us with
+// mbar_wait's form, 447 with this; 440 with a count of tries, which is no limit
+// in time).  The clock is read behind a try that failed (one gives up its issue
+// slots for about a microsecond), its low half only: a limit is below 2^32 ns.
+// A wait that runs out sets the CTA's abort flag, which ends the others and is
+// reported at the kernel's end.
+struct Waits {
+  volatile int* abort_flag;
+  uint32_t limit_ns;
+};
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Waits& w) {
+  uint32_t t0 = 0;
+  for (uint32_t first = 1; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); first = 0) {
+    const uint32_t now = globaltimer_low_ns();
+    if (first) t0 = now;
+    if (__any_sync(0xffffffffu, *w.abort_flag != 0 || now - t0 > w.limit_ns)) {
+      *w.abort_flag = 1;
       return false;
     }
+  }
   return true;
 }
 

@@ -1,10 +1,12 @@
 // paged_api.cu -- entry points of the paged 8-bit key/value cache declared in
 // include/attn.h: argument checks, tensor maps, launches.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
 #include "../../include/attn.h"
 #include "kernels.h"
+#include "paged.cuh"
 
 namespace {
 
@@ -21,6 +23,7 @@ int page_log2(int page_size) {
   return -1;
 }
 
+constexpr unsigned long long kMostWaitNs = 4000000000ull;  // the paged kernels' waits count 32 bits of nanoseconds
 constexpr int kMaxRequests = 16384;  // the attention's table of sums holds as many
 
 // Checks shared by the calls that take pages.
@@ -87,6 +90,21 @@ void place(attn::PagedFwdParams& p, uint8_t* ws, int rows, int d, int sms) {
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return na > 0 && nb > 0 && x < y + nb && y < x + na;
+}
+
+// Diagnostic: one warp waits, as the paged kernels do, on an mbarrier that is never completed.
+__global__ void selftest_paged_wait_kernel(int* status, uint32_t limit_ns) {
+  __shared__ __align__(8) uint64_t bar;
+  __shared__ int abort_flag;
+  if (threadIdx.x == 0) {
+    attn::mbar_init(attn::smem_u32(&bar), 1);
+    abort_flag = 0;
+    attn::fence_mbar_init();
+  }
+  __syncthreads();
+  const attn::paged::Waits w{&abort_flag, limit_ns};
+  const bool got = attn::paged::wait_bar(attn::smem_u32(&bar), 0, w);
+  if (!got && threadIdx.x == 0 && *w.abort_flag) atomicCAS(status, attn::kDevOk, attn::kDevTimeout);
 }
 
 int sms_or_default() {
@@ -237,7 +255,7 @@ attn_status attn_fwd_paged_fp8(const void* Q, long long q_stride, const void* k_
   p.scale_log2 = scale * 1.4426950408889634f;
   p.causal = causal;
   p.out_f32 = out_dtype == ATTN_F32;
-  p.wait_limit_ns = attn::device_wait_limit();
+  p.wait_limit_ns = std::min(attn::device_wait_limit(), kMostWaitNs);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const int rows = wide ? 16 : 8;
@@ -263,6 +281,14 @@ attn_status attn_fwd_paged_fp8(const void* Q, long long q_stride, const void* k_
     e = small ? attn::launch_paged_merge(d, p, rows, w1, big ? &pw : nullptr, wide_rows, big ? w2 : 0, cs)
               : attn::launch_paged_merge(d, pw, wide_rows, w2, nullptr, 0, 0, cs);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+attn_status attn_selftest_paged_wait_timeout(unsigned long long limit_ns, void* stream) {
+  if (limit_ns == 0 || limit_ns > 1000000000ull) return ATTN_ERR_INVALID_ARG;
+  int* status = attn::device_status_word();
+  if (!status) return ATTN_ERR_CUDA;
+  selftest_paged_wait_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(status, (uint32_t)limit_ns);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
   if (!p.behind) griddep_wait();  // the lengths, pages and queries of the kernel before
   sum_units<kRows, SPLIT>(p, sums, warp, kWarps + 1, lane);
   __syncthreads();
-  volatile int* const wc = abort_flag;
+  const Waits wc{abort_flag, (uint32_t)p.wait_limit_ns};
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ producer

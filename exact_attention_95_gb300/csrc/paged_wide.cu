@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  volatile int* const wc = abort_flag;
+  const Waits wc{abort_flag, (uint32_t)p.wait_limit_ns};
   const WaitCtx drain{abort_flag, p.status, p.wait_limit_ns};
   // Item i, for a consumer warp.
   auto wait_item = [&](int i) -> bool { return wait_bar(bar(C::B_IFULL + i % kItems), (i / kItems) & 1, wc); };

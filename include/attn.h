@@ -383,6 +383,9 @@ attn_status attn_last_device_status(void* stream);
  * the following attn_last_device_status() report ATTN_ERR_TIMEOUT. */
 attn_status attn_selftest_wait_timeout(unsigned long long limit_ns, void* stream);
 
+/* The same with the bounded wait of the paged cache's attention kernels. */
+attn_status attn_selftest_paged_wait_timeout(unsigned long long limit_ns, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

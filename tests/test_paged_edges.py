@@ -119,3 +119,25 @@ def test_a_tall_chunk_among_idle_requests(R, tall, Hq, Hkv, d, ones):
     assert news.sum() <= R
     lens = np.where(news > 0, news + rng.integers(0, 400, R), rng.integers(0, 50, R))
     _check_attention(rng, lens, news, Hq, Hkv, d, 16, True, torch.float32)
+
+
+# ------------------------------------------------------------------ waits
+def test_the_waits_self_test_refuses_limits_out_of_range():
+    for limit in (0, 10 ** 9 + 1, 2 ** 32):
+        assert pkg.load_library().attn_selftest_paged_wait_timeout(limit, None) == pkg.ATTN_ERR_INVALID_ARG
+
+
+@gpu
+@pytest.mark.parametrize("ms", [5, 50])
+def test_a_wait_ends_at_its_limit_and_is_reported(ms):
+    """The kernels' bounded wait on a barrier that nothing completes: a time, not a number of
+    tries, so it is neither early nor late."""
+    ok()
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    a.record()
+    assert pkg.attn_selftest_paged_wait_timeout(ms * 10 ** 6) == pkg.ATTN_OK
+    b.record()
+    torch.cuda.synchronize()
+    assert pkg.attn_last_device_status() == pkg.ATTN_ERR_TIMEOUT
+    assert pkg.attn_last_device_status() == pkg.ATTN_OK
+    assert 0.9 * ms <= a.elapsed_time(b) <= 2 * ms + 20  # (a try may take a while; launches beside it)
