@@ -86,10 +86,18 @@ void place(attn::PagedFwdParams& p, uint8_t* ws, int rows, int d, int sms) {
   p.desc = reinterpret_cast<int*>(ws + part_o_bytes(rows, d, sms) + part_ml_bytes(rows, sms));
 }
 
-// Whether [a, a + na) and [b, b + nb) share a byte.
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return na > 0 && nb > 0 && x < y + nb && y < x + na;
+// Whether one of the first `written` of `count` arrays shares a byte with another.
+struct Span {
+  const void* p;
+  size_t n;  // bytes
+};
+bool any_overlap(const Span* a, int written, int count) {
+  for (int i = 0; i < written; ++i)
+    for (int j = i + 1; j < count; ++j) {
+      const uintptr_t x = reinterpret_cast<uintptr_t>(a[i].p), y = reinterpret_cast<uintptr_t>(a[j].p);
+      if (a[i].n > 0 && a[j].n > 0 && x < y + a[j].n && y < x + a[i].n) return true;
+    }
+  return false;
 }
 
 // Diagnostic: one warp waits, as the paged kernels do, on an mbarrier that is never completed.
@@ -129,18 +137,13 @@ attn_status attn_kv_tables(const int32_t* cached, const int32_t* added, const in
   if (!aligned(slots, 8)) return ATTN_ERR_INVALID_ARG;
   const int pl = page_log2(page_size);
   if (pl < 0 || (long long)max_pages * page_size > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
-  // Every CTA reads all lengths while others write: no output may be an input.
-  struct {
-    const void* p;
-    size_t n;
-  } const in[] = {{cached, (size_t)R * 4}, {added, (size_t)R * 4}, {free_pages, (size_t)n_free * 4}},
-      out[] = {{kv_lens, (size_t)R * 4}, {cu_tokens, (size_t)R * 4 + 4}, {slots, (size_t)T * 8},
-               {positions, (size_t)T * 4}, {taken, 8}, {block_table, (size_t)R * max_pages * 4}};
-  for (const auto& o : out)
-    for (const auto& i : in)
-      if (overlap(o.p, o.n, i.p, i.n)) return ATTN_ERR_INVALID_ARG;
   // The kernel's sums saturate at 2^31 - 1, which has to exceed both limits.
   if (T >= 0x7fffffff || n_free >= 0x7fffffff) return ATTN_ERR_UNSUPPORTED;
+  // Every CTA reads all lengths and the table while others write: no output may be an input or another output.
+  const Span all[] = {{kv_lens, (size_t)R * 4}, {cu_tokens, (size_t)R * 4 + 4}, {slots, (size_t)T * 8},
+                      {positions, (size_t)T * 4}, {taken, 8}, {block_table, (size_t)R * max_pages * 4},
+                      {cached, (size_t)R * 4}, {added, (size_t)R * 4}, {free_pages, (size_t)n_free * 4}};
+  if (any_overlap(all, 6, 9)) return ATTN_ERR_INVALID_ARG;
   attn::KvTablesParams p{};
   p.cached = cached;
   p.added = added;
@@ -172,14 +175,10 @@ attn_status attn_kv_append_fp8(const void* K, long long k_stride, const void* V,
   if (!token_stride_ok(k_stride, Hkv, d) || !token_stride_ok(v_stride, Hkv, d)) return ATTN_ERR_INVALID_ARG;
   // No updated array may be another array of the call.
   const size_t codes = (size_t)num_pages * Hkv * page_size * d, scales = (size_t)num_pages * Hkv * 4;
-  const struct {
-    const void* p;
-    size_t n;
-  } all[] = {{k_pages, codes}, {v_pages, codes}, {k_scale, scales}, {v_scale, scales}, {slots, (size_t)T * 8},
-             {K, ((size_t)(T - 1) * k_stride + (size_t)Hkv * d) * 2}, {V, ((size_t)(T - 1) * v_stride + (size_t)Hkv * d) * 2}};
-  for (int o = 0; o < 4; ++o)
-    for (int i = o + 1; i < 7; ++i)
-      if (overlap(all[o].p, all[o].n, all[i].p, all[i].n)) return ATTN_ERR_INVALID_ARG;
+  const Span all[] = {{k_pages, codes}, {v_pages, codes}, {k_scale, scales}, {v_scale, scales}, {slots, (size_t)T * 8},
+                      {K, ((size_t)(T - 1) * k_stride + (size_t)Hkv * d) * 2},
+                      {V, ((size_t)(T - 1) * v_stride + (size_t)Hkv * d) * 2}};
+  if (any_overlap(all, 4, 7)) return ATTN_ERR_INVALID_ARG;
   attn::KvAppendParams p{};
   p.K = static_cast<const uint16_t*>(K);
   p.V = static_cast<const uint16_t*>(V);

@@ -295,9 +295,10 @@ size_t attn_bwd_workspace_size(int B, int Hq, int Hkv, int N, int d);
  *                  for those of refused requests and behind the last token
  *   positions      [T]    index of the token in its request; -1 likewise
  *   taken          [2]    pages taken from the head of free_pages; requests refused
- * All outputs but block_table are fully overwritten; none may overlap cached,
- * added or free_pages (ATTN_ERR_INVALID_ARG).  R >= 1, T >= 0 (slots and
- * positions may be NULL when T is 0).  slots is 8-byte aligned, the rest
+ * All outputs but block_table are fully overwritten; none of them, block_table
+ * included, may overlap another or cached, added or free_pages
+ * (ATTN_ERR_INVALID_ARG).  R >= 1, T >= 0 (slots and positions may be NULL when
+ * T is 0).  slots is 8-byte aligned, the rest
  * 4-byte.  Page ids are copied as they are.  A refused request keeps its
  * places in the step's arrays: its tokens are appended nowhere, and attention
  * over its rows takes them for the last ones of the cached tokens.
