@@ -220,12 +220,20 @@ attn_status attn_fwd_paged_fp8(const void* Q, long long q_stride, const void* k_
   if (!token_stride_ok(q_stride, Hq, d)) return ATTN_ERR_INVALID_ARG;
   if (R > kMaxRequests || (long long)T * Hq > 0x7fffff00LL || (long long)max_pages * page_size > 0x7fffff00LL)
     return ATTN_ERR_UNSUPPORTED;
+  const int G = Hq / Hkv;
+  const bool wide = runs_wide(R, T, G);
+  const size_t need = workspace_bytes_for(wide, d, sms_or_default());
+  if (workspace_bytes < need) return ATTN_ERR_INVALID_ARG;
+  // What is written may be no other array of the call: others still read.
+  const size_t codes = (size_t)num_pages * Hkv * page_size * d, scales = (size_t)num_pages * Hkv * 4;
+  const Span all[] = {{O, (size_t)T * Hq * d * (out_dtype == ATTN_F32 ? 4 : 2)}, {LSE, (size_t)T * Hq * 4},
+                      {workspace, need}, {Q, ((size_t)(T - 1) * q_stride + (size_t)Hq * d) * 2}, {k_pages, codes},
+                      {v_pages, codes}, {k_scale, scales}, {v_scale, scales},
+                      {block_table, (size_t)R * max_pages * 4}, {cu_q, (size_t)R * 4 + 4}, {kv_lens, (size_t)R * 4}};
+  if (any_overlap(all, 3, 11)) return ATTN_ERR_INVALID_ARG;
   const int sms = attn::device_sms();
   int* status = attn::device_status_word();
   if (sms < 1 || !status) return ATTN_ERR_CUDA;
-  const int G = Hq / Hkv;
-  const bool wide = runs_wide(R, T, G);
-  if (workspace_bytes < workspace_bytes_for(wide, d, sms)) return ATTN_ERR_INVALID_ARG;
   CUtensorMap tk, tv;
   const long long planes = (long long)num_pages * Hkv;
   if (!attn::make_page_map(&tk, k_pages, planes, page_size, d) ||

@@ -356,6 +356,8 @@ attn_status attn_kv_append_fp8(const void* K, long long k_stride, const void* V,
  *   O   [T, Hq, d] out_dtype (bf16 or fp32), LSE [T, Hq] fp32
  *   workspace: attn_fwd_paged_workspace_size(R, T, Hq, Hkv, d) bytes, 256-byte
  *       aligned, owned by the caller, not shared with a concurrent call.
+ * O, LSE and the workspace may overlap neither one another nor an input
+ * (ATTN_ERR_INVALID_ARG).
  * Lengths past the table and page ids outside [0, num_pages) in it are
  * reported as ATTN_ERR_DEVICE by attn_last_device_status; such keys take no
  * part.  cu_q is clipped to [0, T].  R <= 16384 and T * Hq < 2^31 - 256, else
