@@ -318,7 +318,9 @@ __device__ __forceinline__ void append_run(const Run<D>& r, int id, int count, F
       *q = c;
     }
   }
-  // Every lane has read the scale: fold() was a meeting of all of them.
+  // Every lane's read of the scale comes before this: of a warp's by the barrier, of a
+  // CTA's by those of fold() (a shuffle or a vote orders no memory).
+  __syncwarp();
   if (id == 0 && r.n > 0) *r.scale = s;
 }
 
