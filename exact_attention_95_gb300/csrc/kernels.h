@@ -156,6 +156,7 @@ struct KvTablesParams {
   long long* slots;       // [T]
   int* positions;         // [T]
   int* taken;             // [2]
+  int* status;            // (debug builds' checks)
   int R, n_free, max_pages, page_log2, T;
 };
 cudaError_t launch_kv_tables(const KvTablesParams& p, int sms, cudaStream_t stream);
@@ -170,6 +171,7 @@ struct KvAppendParams {
   uint8_t* v_pages;
   float* k_scale;          // [num_pages, Hkv]
   float* v_scale;
+  int* status;             // (debug builds' checks)
   long long T;
   int Hkv, num_pages, page_log2;
 };

@@ -345,6 +345,18 @@ __device__ __forceinline__ size_t output_row(const PagedFwdParams& p, int start,
   return (size_t)(start + tok) * p.Hq + h * p.G + (rho - tok * p.G);
 }
 
+// Debug builds' checks of a copy's coordinate, of a row of the outputs and of a row
+// of a worker's partial sums (tiles of `rows` rows).
+__device__ __forceinline__ bool plane_ok(const PagedFwdParams& p, int plane) {
+  return dcheck(plane >= 0 && plane < p.num_pages * p.Hkv, p.status);
+}
+__device__ __forceinline__ bool output_ok(const PagedFwdParams& p, size_t orow) {
+  return dcheck(orow < (size_t)p.T * p.Hq, p.status);
+}
+__device__ __forceinline__ bool part_ok(const PagedFwdParams& p, size_t prow, int rows) {
+  return dcheck(prow < (size_t)gridDim.x * 2 * rows, p.status);
+}
+
 // 1 / l for the output: 0 for a row without keys, NaN stays.
 __device__ __forceinline__ float output_factor(float l) { return l > 0.f ? __fdiv_rn(1.f, l) : l == 0.f ? 0.f : l; }
 // ln of the sum of a row with maximum m (log2 units).

@@ -154,6 +154,7 @@ attn_status attn_kv_tables(const int32_t* cached, const int32_t* added, const in
   p.slots = reinterpret_cast<long long*>(slots);
   p.positions = positions;
   p.taken = taken;
+  if (attn::kDebugChecks && !(p.status = attn::device_status_word())) return ATTN_ERR_CUDA;
   p.R = R;
   p.n_free = n_free;
   p.max_pages = max_pages;
@@ -189,6 +190,7 @@ attn_status attn_kv_append_fp8(const void* K, long long k_stride, const void* V,
   p.v_pages = static_cast<uint8_t*>(v_pages);
   p.k_scale = k_scale;
   p.v_scale = v_scale;
+  if (attn::kDebugChecks && !(p.status = attn::device_status_word())) return ATTN_ERR_CUDA;
   p.T = T;
   p.Hkv = Hkv;
   p.num_pages = num_pages;

@@ -130,10 +130,12 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const KvTablesPa
         const int pg = pos >> p.page_log2;
         const int held = (int)(((long long)ci + P - 1) >> p.page_log2);
         const unsigned f0 = i ? s_need[i - 1] : need0;
+        if (!dcheck(base + i < p.R && pg < p.max_pages && (pg < held || f0 + (pg - held) < F), p.status)) continue;
         const int id = pg >= held ? p.free_pages[f0 + (pg - held)]
                                   : p.block_table[(size_t)(base + i) * p.max_pages + pg];
         slot = (long long)id * P + (pos & (P - 1));
       }
+      if (!dcheck(t < T, p.status)) continue;
       p.slots[t] = slot;
       p.positions[t] = pos;
     }
@@ -142,7 +144,9 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const KvTablesPa
       if (!s_served[i]) continue;
       const int held = (int)(((long long)s_cached[i] + P - 1) >> p.page_log2);
       const unsigned f0 = i ? s_need[i - 1] : need0;
-      p.block_table[(size_t)(base + i) * p.max_pages + held + ((unsigned)x - f0)] = p.free_pages[x];
+      const unsigned col = held + ((unsigned)x - f0);
+      if (!dcheck(base + i < p.R && col < (unsigned)p.max_pages && x < F, p.status)) continue;
+      p.block_table[(size_t)(base + i) * p.max_pages + col] = p.free_pages[x];
     }
     tok0 = tok1;
     need0 = need1;
@@ -267,7 +271,12 @@ __device__ __forceinline__ Run<D> run_of(const KvAppendParams& p, long long t, l
   r.dst = (is_v ? p.v_pages : p.k_pages) + (place << p.page_log2) * D;
   r.scale = (is_v ? p.v_scale : p.k_scale) + place;
   r.off = (int)(slot & ((1 << p.page_log2) - 1));
-  r.n = n;
+  // The rows [t, t + n) and [off, off + n) are within the call's tokens and the page.
+  r.n = n == 0 || dcheck(pair < 2 * p.Hkv && t >= 0 && t + n <= p.T && slot >= 0 && (slot >> p.page_log2) < p.num_pages &&
+                             r.off + n <= 1 << p.page_log2,
+                         p.status)
+            ? n
+            : 0;
   return r;
 }
 

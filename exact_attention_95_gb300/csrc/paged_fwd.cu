@@ -128,6 +128,7 @@ __device__ __forceinline__ uint32_t piece(uint32_t base, int row, int c) {
 template <int D>
 __device__ __forceinline__ void put_piece(const PagedFwdParams& p, size_t orow, int q4, float4 sum, float M, float L) {
   const float inv = output_factor(L);
+  if (!output_ok(p, orow)) return;
   if (p.out_f32)
     *reinterpret_cast<float4*>(static_cast<float*>(p.O) + orow * D + q4 * 4) =
         make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
@@ -245,8 +246,10 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
           if (load) {
             const uint32_t dst = sb + C::OFF_RING + s * C::SBYTES + lane * page_bytes;
             const int plane = my * p.Hkv + h;
-            tma_load_3d(dst, &tmK, bar(C::B_FULL + s), 0, 0, plane);
-            tma_load_3d(dst + C::KBYTES, &tmV, bar(C::B_FULL + s), 0, 0, plane);
+            if (plane_ok(p, plane)) {
+              tma_load_3d(dst, &tmK, bar(C::B_FULL + s), 0, 0, plane);
+              tma_load_3d(dst + C::KBYTES, &tmV, bar(C::B_FULL + s), 0, 0, plane);
+            }
           }
           UnitMeta* m = metas + s;
           const float mk = __shfl_sync(0xffffffffu, ks, in_batch + (lane & 7));
@@ -633,6 +636,7 @@ __global__ void __launch_bounds__(PC<D, NB>::THREADS, PC<D, NB>::CTAS)
           if (q4 == 0) ml[row - kHalf * kRows] = make_float2(M, L);
         } else if (slot >= 0) {
           const size_t base = (size_t)(blockIdx.x * 2 + slot) * kRows + row;
+          if (!part_ok(p, base, kRows)) continue;
           *reinterpret_cast<float4*>(p.part_o + base * D + q4 * 4) = sum;
           if (q4 == 0) *reinterpret_cast<float2*>(p.part_ml + base * 2) = make_float2(M, L);
         } else {

@@ -98,8 +98,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Mer
       M = mn;
     }
     const size_t orow = output_row(p, start, h, tile * t.rows + row);
+    const bool in = output_ok(p, orow);
     // Columns c, c + 1 of the row.
     auto put = [&](int c, float x, float y, float inv) {
+      if (!in) return;
       if (p.out_f32)
         *reinterpret_cast<float2*>(static_cast<float*>(p.O) + orow * D + c) = make_float2(x * inv, y * inv);
       else
@@ -108,7 +110,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Mer
     if (team == 1) {
 #pragma unroll
       for (int v = 0; v < V; v += 2) put(lane * V + v, acc[v], acc[v + 1], output_factor(L));
-      if (lane == 0) p.LSE[orow] = output_lse(M, L);
+      if (lane == 0 && in) p.LSE[orow] = output_lse(M, L);
       continue;
     }
 #pragma unroll
@@ -134,7 +136,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Mer
         L += wgt * s_l[j];
       }
       put(c, x, y, output_factor(L));
-      if (c == 0) p.LSE[orow] = output_lse(M, L);
+      if (c == 0 && in) p.LSE[orow] = output_lse(M, L);
     }
     __syncthreads();
   }

@@ -249,7 +249,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int plane = my * p.Hkv + h;
             if (!reuse(C::B_KEMPTY, u, C::KS)) return false;
             const int sk = u % C::KS;
-            if (load) tma_load_3d(sb + C::OFF_K + sk * C::T8 + lane * page_bytes, &tmK, bar(C::B_KFULL + sk), 0, 0, plane);
+            if (load && plane_ok(p, plane))
+              tma_load_3d(sb + C::OFF_K + sk * C::T8 + lane * page_bytes, &tmK, bar(C::B_KFULL + sk), 0, 0, plane);
             if (lane == 0) mbar_arrive_expect_tx(bar(C::B_KFULL + sk), bytes);
             if (!reuse(C::B_MEMPTY, u, kMetas)) return false;
             UnitMeta* m = metas + u % kMetas;
@@ -264,7 +265,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             release(C::B_MFULL + u % kMetas);
             if (!reuse(C::B_VEMPTY, u, C::VS)) return false;
             const int sv = u % C::VS;
-            if (load) tma_load_3d(sb + C::OFF_V + sv * C::T8 + lane * page_bytes, &tmV, bar(C::B_VFULL + sv), 0, 0, plane);
+            if (load && plane_ok(p, plane))
+              tma_load_3d(sb + C::OFF_V + sv * C::T8 + lane * page_bytes, &tmV, bar(C::B_VFULL + sv), 0, 0, plane);
             if (lane == 0) mbar_arrive_expect_tx(bar(C::B_VFULL + sv), bytes);
             ++u;
             return true;
@@ -654,13 +656,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       if (live) {
-        const bool valid = rho <= last;
         // O = sums * part * mul.  (In one factor the smallest V scales would be lost:
         // 2^-126 * 2^-9 / l is subnormal.)
         const size_t orow = output_row(p, im->start, im->h, min(rho, last));
         const float part = (im->slot < 0 ? output_factor(l) : 1.f) * (1.f / (1 << (int)kShift));
         const float mul = n > 0 ? ex2(lvref) : 0.f;
         const size_t prow = (size_t)(blockIdx.x * 2 + max(im->slot, 0)) * kPagedWideRows + t * kBM + row;
+        const bool valid = rho <= last && output_ok(p, orow) && part_ok(p, prow, kPagedWideRows);
         // bf16 rows go through the warp's quarter of the Q tile (whose products have completed).
         const uint32_t stage = q_hi + quad * 32 * D;
 #pragma unroll 1
@@ -693,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int r = 4 * x + (lane >> 3), k = lane & 7;
                 const uint4 v = lds_u4(stage + r * 128 + ((k ^ (r & 7)) << 4));
                 const size_t to = __shfl_sync(0xffffffffu, (unsigned long long)orow, r);
-                if (rho - lane + r <= last)
+                if (rho - lane + r <= last && output_ok(p, to))
                   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.O) + to * D + (c >> 1) * 64 + k * 8) = v;
               }
               __syncwarp();
