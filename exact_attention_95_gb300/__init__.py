@@ -550,6 +550,9 @@ def attn_kv_append_fp8(K, V, slots, k_pages, k_scale, v_pages, v_scale, stream=N
 
 
 def attn_fwd_paged_workspace_size(R: int, T: int, Hq: int, Hkv: int, d: int) -> int:
+    """Bytes of attn_fwd_paged_fp8's workspace.  A workspace for several steps has the largest
+    of their sizes: a decoding step (T <= R, Hq / Hkv <= 8) needs less than one of fewer
+    requests with more tokens."""
     return int(load_library().attn_fwd_paged_workspace_size(R, T, Hq, Hkv, d))
 
 

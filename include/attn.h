@@ -369,7 +369,10 @@ attn_status attn_fwd_paged_fp8(const void* Q, long long q_stride, const void* k_
                                int Hkv, int d, int num_pages, int page_size, int max_pages, float scale, int causal,
                                attn_dtype out_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Bytes of workspace attn_fwd_paged_fp8 needs on the current device; 0 on bad sizes. */
+/* Bytes of workspace attn_fwd_paged_fp8 needs on the current device; 0 on bad sizes.
+ * The size falls where a step becomes a decoding step (T <= R and Hq / Hkv <= 8 need
+ * room for small tiles only): a workspace for several steps has the largest of their
+ * sizes, not that of the largest R and T. */
 size_t attn_fwd_paged_workspace_size(int R, int T, int Hq, int Hkv, int d);
 
 /* Static string naming a status code. */

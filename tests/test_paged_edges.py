@@ -121,6 +121,29 @@ def test_a_tall_chunk_among_idle_requests(R, tall, Hq, Hkv, d, ones):
     _check_attention(rng, lens, news, Hq, Hkv, d, 16, True, torch.float32)
 
 
+# ------------------------------------------------------------------ one workspace for several steps
+def test_the_largest_of_the_steps_sizes_is_enough_for_each():
+    """By the rule alone: sizes take two values for given heads and d, so that of one token
+    more than requests is the largest for any R and T."""
+    size = pkg.attn_fwd_paged_workspace_size
+    for Hq, Hkv, d in ((8, 2, 128), (32, 2, 128), (4, 4, 64)):
+        most = size(1, 2, Hq, Hkv, d)
+        assert all(0 < size(R, T, Hq, Hkv, d) <= most for R in (1, 3, 256, 16384) for T in (1, 2, 4, 300, 20000))
+
+
+@gpu
+def test_one_workspace_through_steps_of_every_kind():
+    """Many requests decode, then few take many tokens, then few decode: each in the same
+    workspace, of the largest of the sizes, which holds what the step before left."""
+    Hq, Hkv, d = 8, 2, 128
+    steps = [([1] * 90, 90), ([5, 70], 2), ([1, 1], 2), ([4, 3, 2], 3), ([1] * 40, 40)]
+    size = max(pkg.attn_fwd_paged_workspace_size(R, sum(n), Hq, Hkv, d) for n, R in steps)
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    rng = np.random.default_rng(71)
+    for news, R in steps:
+        _check_attention(rng, [n + int(rng.integers(0, 900)) for n in news], news, Hq, Hkv, d, 32, True, workspace=ws)
+
+
 # ------------------------------------------------------------------ waits
 def test_the_waits_self_test_refuses_limits_out_of_range():
     for limit in (0, 10 ** 9 + 1, 2 ** 32):
