@@ -49,14 +49,12 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Wa
 constexpr int kMaxGroups = 512;  // 32 requests each
 
 // An item, or the part of it that a worker has.
-struct Item {
+struct alignas(16) Item {
   int start, n, len;  // the request's query rows, tokens [start, start + n), and its keys
   int req;            // the request
   int tile, h;        // row tile, kv head
-  int k0;             // first unit's number in the item
-  int first, count;   // the units' numbers in the worker's line of units; count < 0: no more items
+  int k0, count;      // the units' numbers in the item: first and how many; count < 0: no more items
   int slot;           // where the result goes: -1 output, else partial slot of this worker
-  int pad[2];
 };
 
 // The request's query rows and keys, clipped to the arrays, and its units
@@ -133,7 +131,7 @@ struct Walker {
   Item im;                 // current item
   int seen, ke;            // keys its rows see, end of its units
   int kt, tiles, item;     // units of an item, tiles of the request, next item
-  int k, line;             // next unit of the item; units walked
+  int k;                   // next unit of the item
   bool opened;             // the current item's first batch has been given
   int merge_parts = 0, merge_start = 0, merge_n = 0, merge_tile = 0, merge_h = 0;
 
@@ -151,7 +149,7 @@ struct Walker {
     per = SPLIT ? 1 : divide(total + gridDim.x - 1, gridDim.x);
     pos = min(total, per * blockIdx.x);
     end = min(total, pos + per);
-    g = l = line = k = ke = 0;
+    g = l = k = ke = 0;
     off = units = 0;
     opened = true;
     if (pos >= end) return;
@@ -212,9 +210,7 @@ struct Walker {
     }
     seen = key_limit(p, im.len, im.n, (min(im.n * p.G, (im.tile + 1) * ROWS) - 1) / p.G);
     ke = max(k0, min(k1, (seen + kUnit - 1) / kUnit));
-    im.first = line;
     im.count = ke - k0;
-    line += im.count;
     k = k0;
     opened = false;
   }
@@ -323,6 +319,23 @@ __device__ __forceinline__ bool walk_range(const PagedFwdParams& p, const long l
   }
   if (SPLIT == 0) w.write_descriptor();
   return ok;
+}
+
+// Two e4m3 codes as two f16 numbers (exact).
+__device__ __forceinline__ uint32_t widen(uint32_t two) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
+  return h;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Address of 16-byte piece `c` of row `row` of a code tile (rows of D bytes, swizzled).
+template <int D>
+__device__ __forceinline__ uint32_t piece(uint32_t base, int row, int c) {
+  return D == 128 ? base + row * 128 + ((c ^ (row & 7)) << 4) : base + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
 }
 
 // Bytes 0xff where four codes hold a NaN.

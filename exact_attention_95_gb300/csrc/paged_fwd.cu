@@ -83,16 +83,6 @@ struct PC {
   static_assert(kMaxGroups * 8 <= HALF * ROWS * D * 4, "the sums fit the exchange buffer");
 };
 
-__device__ __forceinline__ uint32_t widen(uint32_t two) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
-  return h;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -118,12 +108,6 @@ template <int D>
 __device__ __forceinline__ int key_of(int n) {
   return D == 128 ? (n >> 1) | ((n & 1) << 2) : n ^ ((n >> 1) & 1);
 }
-// Address of 16-byte piece `c` of row `row` in a swizzled page tile.
-template <int D>
-__device__ __forceinline__ uint32_t piece(uint32_t base, int row, int c) {
-  return D == 128 ? base + row * 128 + ((c ^ (row & 7)) << 4) : base + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
-}
-
 // Piece q4 (four columns) of an output row: its sum, maximum and weights' sum.
 template <int D>
 __device__ __forceinline__ void put_piece(const PagedFwdParams& p, size_t orow, int q4, float4 sum, float M, float L) {

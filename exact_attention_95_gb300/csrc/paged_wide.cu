@@ -105,27 +105,12 @@ struct WC {
 static_assert(WC<128>::SMEM <= 232448 && WC<64>::SMEM <= 232448, "shared memory");
 static_assert(kMaxGroups * 8 <= WC<64>::WS * WC<64>::T16, "the sums fit the widened tiles");
 
-// 16-byte piece c of row `row` of a code tile (rows of D bytes, swizzled).
-template <int D>
-__device__ __forceinline__ uint32_t piece(uint32_t base, int row, int c) {
-  return D == 128 ? base + row * 128 + ((c ^ (row & 7)) << 4) : base + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
-}
 // Descriptor of a K-major tile of D-byte rows: 128-byte or 64-byte swizzle, groups of eight rows 8 * D bytes apart.
 template <int D>
 __device__ __forceinline__ uint64_t code_desc(uint32_t addr) {
   if constexpr (D == 128) return sdesc_sw128(addr, 16, 1024);
   // Layout code 4: 64-byte swizzle.
   return (sdesc_sw128(addr, 16, 512) & ~(uint64_t(7) << 61)) | (uint64_t(4) << 61);
-}
-__device__ __forceinline__ uint32_t widen(uint32_t two) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
-  return h;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 // The four e4m3 values of packed codes.
 __device__ __forceinline__ void values4(uint32_t c, float (&x)[4]) {
