@@ -41,10 +41,15 @@ attn_status check_cache(const void* kp, const float* ks, const void* vp, const f
 // Tokens of `heads` rows of d elements, `stride` elements apart.
 bool token_stride_ok(long long stride, long long heads, int d) { return stride >= heads * d && stride % 8 == 0; }
 
-// Which kernels a call runs.  A decoding step (T <= R: on average a token a
-// request at most) with groups of up to eight heads runs the eight-row kernel
-// alone, whatever the requests' rows are: a launch for wider ones would find
-// nothing to do.  Any other call runs the 16-row kernel for the requests with
+// Which kernels a call runs, by T, R and G: the host does not know the requests'
+// rows.  A decoding step (T <= R: on average a token a request at most) with
+// groups of up to eight heads runs the eight-row kernel alone, whatever the
+// requests' rows are: mostly a launch for wider ones would find nothing to do.
+// Where it would, a tall request among idle ones is slow: 128 tokens against
+// 4000 keys, 32/8 heads, d = 128, 60.5 us in 256 slots and 35.0 in 101 (500 keys:
+// 21.7 and 27.1).  Groups above eight heads always take the other way: 64
+// requests of 4096 keys with 16 heads a kv head 115 us (81 by their bytes), four
+// of 700 keys 14.8.  Any other call runs the 16-row kernel for the requests with
 // up to kNarrowMost query rows of a kv head and the 256-row kernel for the
 // rest.  Measured with 16 requests of 4096 keys, 8 kv heads, d = 128: 32 rows
 // 66 us by two tiles of 16 and 69 us by a tile of 256, 48 rows 94 and 70 us.
@@ -57,7 +62,8 @@ bool runs_wide(int R, int T, int G) { return T > R || G > 8; }
 // of eight rows, and no more than T * Hkv of them as G <= 8.  Clusters where all
 // are resident at once (from 7/8 of the workers on they are not: GPCs leave
 // holes) and where the table is too narrow for a CTA to get more than eight
-// units.  Measured against the ranges, us, 8 kv heads, d = 128, requests of 700 /
+// units (its width is all that the host knows of the lengths: four requests of
+// 700 keys 7.4 us, with a table of 32768 keys a request 10.1).  Measured against the ranges, us, 8 kv heads, d = 128, requests of 700 /
 // 4096 / 8192 keys each: clusters of 8, two requests 7.1 / 9.7 / 13.8 against
 // 9.8 / 13.2 / 15.0, six 7.8 / 12.1 / 20.0 against 10.3 / 14.8 / 23.9, one of
 // 16384 keys (beyond the rule) 19.0 against 15.8; clusters of 4, twelve 9.5 / 19.8 / - against

@@ -181,8 +181,9 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const KvTablesPa
 // runs or two to a warp), the warp for up to kWarpRun, else the CTA.  A CTA
 // looks at `chunk` tokens and `pairs` of the 2 * Hkv (K or V, head) pairs.
 // Measured: 64 requests of one token, 8 kv heads, d = 128: 2.5 us, 500 requests,
-// 16 kv heads, d = 64: 3.7 us (launch and three dependent reads: slot, row and
-// scale, page); nine prompts of up to 4096 tokens 34 us, 4.5 TB/s, where the
+// 16 kv heads, d = 64: 3.7 us (launch, then the slots, then rows and scales,
+// which this code asks for behind the slots though a row's place does not depend
+// on its slot, then the page where its scale grows); nine prompts of up to 4096 tokens 34 us, 4.5 TB/s, where the
 // integer pipe is 54 % busy (maxima, packing) and each CTA's first reads are
 // waited for.  Reading the next run while this one is written, prefetching the
 // chunk's rows to L2 while its slots are read, and neighbouring CTAs for the

@@ -8,7 +8,7 @@
 // HBM bound: two bytes per key, kv head and column against 4 * G products.
 // All products run in f16 with fp32 sums: an e4m3 code is an f16 number
 // exactly, and so is a bf16 query times a power of two of its row (elements
-// below 2^-29 of the row's largest lose bits).  The weights are rounded to
+// below 2^-31 of the row's largest lose bits).  The weights are rounded to
 // f16, relative to the largest V scale seen, times 2^14: 2^-11 relative for
 // every weight down to 2^-28 of the row's largest, which a long tail behind
 // one dominant key needs (an 8-bit weight, even as a sum of two, would lose
@@ -27,9 +27,9 @@
 //
 // Measured (whole calls, 8 kv heads, d = 128, a token a request): 64 requests of
 // up to 8192 keys 121 us, 6.2 TB/s; one of 131072 keys 51 us, 5.3 TB/s; four of
-// up to 700 keys 7.5 us in clusters (start, lengths, page ids, codes, the meeting:
+// up to 700 keys 7.4 us in clusters (start, lengths, page ids, codes, the meeting:
 // each waits for the one before; 9.4 us with the merge's launch).  33 requests of
-// up to 3001 keys, 16 kv heads, d = 64: 34 us, 4.2 TB/s.  16 requests of up to
+// up to 3001 keys, 16 kv heads, d = 64: 33 us, 4.3 TB/s.  16 requests of up to
 // 5000 keys with six tokens of four heads each, two tiles of 16 rows: 54 us, bound
 // by the latencies of a tile's own instructions.  Dropped: a tile of 24 rows, whose sums leave no
 // registers for the queries (16 requests of 4096 keys, 24 rows: 71 us against

@@ -9,8 +9,9 @@
 //      two e4m3 numbers, hi = e4m3(q / s), lo = e4m3(q / s - hi) with s a power
 //      of two of the row (kind::f8f6f4, twice the rate, two products: the
 //      time of one 16-bit product and no widening of K).  bf16 has 8
-//      significant bits, hi and lo four each: the sum is exact down to
-//      2^-10.8 of the row's largest element and off by at most 2^-19 of it below.
+//      significant bits, hi and lo four each.  With the row's largest element
+//      scaled to (224, 448] the sum is exact for elements from 2^-2 on, 2^-9.8 of
+//      the largest, and off by at most 2^-10 below, 2^-17.8 of it.
 //   P V: P in f16 from TMEM, V's codes widened to f16 in shared memory (kind::f16).
 //      P is not split into 8-bit terms: below 2^-18 of the row's largest
 //      weight they hold nothing, and the tail behind one dominant key is lost.
@@ -26,7 +27,7 @@
 // and skips the work.
 //
 // Measured: three requests with chunks of up to 1000 tokens against up to 16384
-// keys, 32 query and 8 kv heads, d = 128: 434 us, 1220 TFLOPS (64 % of a plain
+// keys, 32 query and 8 kv heads, d = 128: 440 us, 1200 TFLOPS (63 % of a plain
 // bf16 product's rate); the tensor pipe is busy 56 % of the time, the softmax
 // warps issue the rest.  Dropped: the tiles with an S buffer each, or a unit to
 // each tile in turn where an item has up to 128 rows (477 to 635 us).

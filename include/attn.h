@@ -302,6 +302,9 @@ size_t attn_bwd_workspace_size(int B, int Hq, int Hkv, int N, int d);
  * 4-byte.  Page ids are copied as they are.  A refused request keeps its
  * places in the step's arrays: its tokens are appended nowhere, and attention
  * over its rows takes them for the last ones of the cached tokens.
+ * free_pages and n_free are this call's: the list does not move on by itself.  A
+ * captured step that is replayed takes from the same head again, unless what is
+ * replayed with it moves the list's entries by taken[0] places.
  */
 attn_status attn_kv_tables(const int32_t* cached, const int32_t* added, const int32_t* free_pages, int n_free,
                            int32_t* block_table, int max_pages, int page_size, int32_t* kv_lens,
@@ -345,7 +348,7 @@ attn_status attn_kv_append_fp8(const void* K, long long k_stride, const void* V,
  * O = 0 and LSE = -inf.  Rows t >= cu_q[R] are left as they were.  A NaN or
  * infinity in a row of Q makes that row NaN if it has a kept key, one in K or V
  * the rows that see it.  The codes enter the products exactly and sums are fp32.  Queries enter
- * exactly down to 2^-10 of their row's largest element, and off by at most
+ * exactly down to 2^-9 of their row's largest element, and off by at most
  * 2^-17 of it below.  The weights are rounded to f16 (2^-11 relative, for
  * weights down to 2^-23 of the row's largest and V scales of like size: the
  * product of a weight and its page's V scale relative to the largest V scale
