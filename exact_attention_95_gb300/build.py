@@ -10,6 +10,7 @@ PyTorch: its file's name has both.  The library does not need it.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import contextlib
 import glob
 import os
 import subprocess
@@ -92,10 +93,13 @@ def build_binding(force: bool = False) -> str:
 
 def _try_binding(force: bool = False) -> None:
     """The module where the host can build it; a warning where it cannot (no headers
-    of Python's or PyTorch's, say): the paged calls then make their checks in Python."""
+    of Python's or PyTorch's, say): the paged calls then make their checks in Python.
+    A module of older sources goes: it would call the new library by the old header."""
     try:
         build_binding(force)
     except Exception as e:
+        with contextlib.suppress(ImportError, FileNotFoundError):
+            os.remove(binding_path())
         warnings.warn(f"the extension module of the paged calls was not built: {e}", RuntimeWarning, stacklevel=3)
 
 

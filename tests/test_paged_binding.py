@@ -56,14 +56,20 @@ def test_the_modules_name_has_the_versions_it_is_built_for(monkeypatch):
     assert libbuild.binding_path() != path and not os.path.exists(libbuild.binding_path())
 
 
-def test_the_library_is_built_where_the_module_cannot_be(monkeypatch):
+def test_the_library_is_built_where_the_module_cannot_be(monkeypatch, tmp_path):
+    """And a module of older sources is not left for it to be called by."""
     def fail(force=False):
         raise RuntimeError("Python.h: no such file")
 
     libbuild.build()
+    old = tmp_path / "old.so"
+    old.write_bytes(b"a module of older sources")
     monkeypatch.setattr(libbuild, "build_binding", fail)
-    with pytest.warns(RuntimeWarning, match="Python.h"):
-        assert os.path.exists(libbuild.build())
+    monkeypatch.setattr(libbuild, "binding_path", lambda: str(old))
+    for _ in range(2):
+        with pytest.warns(RuntimeWarning, match="Python.h"):
+            assert os.path.exists(libbuild.build())
+        assert not old.exists()
 
 
 def test_the_module_is_the_one_that_is_used():
