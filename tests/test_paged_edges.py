@@ -155,7 +155,8 @@ def test_the_waits_self_test_refuses_limits_out_of_range():
 def test_a_wait_ends_at_its_limit_and_is_reported(ms):
     """The kernels' bounded wait on a barrier that nothing completes: a time, not a number of
     tries, so it is neither early nor late."""
-    ok()
+    assert pkg.attn_selftest_paged_wait_timeout(10 ** 5) == pkg.ATTN_OK  # (the kernel's first launch loads it)
+    assert pkg.attn_last_device_status() == pkg.ATTN_ERR_TIMEOUT
     a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
     a.record()
     assert pkg.attn_selftest_paged_wait_timeout(ms * 10 ** 6) == pkg.ATTN_OK
