@@ -121,6 +121,35 @@ def test_a_tall_chunk_among_idle_requests(R, tall, Hq, Hkv, d, ones):
     _check_attention(rng, lens, news, Hq, Hkv, d, 16, True, torch.float32)
 
 
+@gpu
+@pytest.mark.parametrize("tall", [0, 50])
+def test_the_largest_number_of_requests(tall):
+    """16384 requests of up to 60 keys: a decoding step with some idle, and one with a tall chunk too."""
+    R = 16384
+    rng = np.random.default_rng(R + tall)
+    news = (rng.random(R) < 0.9).astype(int)
+    lens = rng.integers(0, 60, R)
+    if tall:
+        news[:] = 1
+        news[R - 3], lens[R - 3] = tall, 300
+    _check_attention(rng, lens, news, 2, 1, 64, 16, True, torch.float32)
+
+
+@gpu
+@pytest.mark.parametrize("R,pad,G,width", [(4, 2, 2, 0), (4, 2, 2, 700), (4, 9, 2, 0), (1, 90, 1, 0), (3, 2, 16, 0), (70, 70, 4, 0)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_step_in_which_every_request_is_idle(R, pad, G, width, d):
+    """Nothing is written, whichever kernels run."""
+    rng = np.random.default_rng(R + pad)
+    kc, ks, vc, vs, table = _cache(rng, [100] * R, 16, 2, d, width_extra=1 + width)
+    g = [dev(a) for a in (kc, ks, vc, vs, table, np.zeros(R + 1, I32), np.full(R, 100, I32))]
+    q = dev_bf16(paged.bf16_bits(rng.standard_normal((pad, 2 * G, d)).astype(np.float32)))
+    O, L = torch.full_like(q, 7.0), torch.full((pad, 2 * G), 7.0, device="cuda")
+    pkg.attn_fwd_paged_fp8(q, *g, None, True, O=O, LSE=L)
+    ok()
+    assert (O == 7).all() and (L == 7).all()
+
+
 # ------------------------------------------------------------------ one workspace for several steps
 def test_the_largest_of_the_steps_sizes_is_enough_for_each():
     """By the rule alone: sizes take two values for given heads and d, so that of one token
