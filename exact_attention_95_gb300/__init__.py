@@ -28,6 +28,12 @@ Functions carry the C names:
   a paged e4m3 key/value cache -- its block table and slot map from the requests'
   lengths, the quantizing append, and ragged attention over it;
   ``attn_fwd_paged_workspace_size(R, T, Hq, Hkv, d)``
+* ``attn_rope_freqs(rot, base=10000.0, scaling="none", ...) -> (freqs, amplitude)``,
+  ``attn_rope(Q, K, freqs, positions=None, ...) -> (Q_out, K_out)`` and
+  ``attn_rope_bwd(dQ, dK, freqs, positions=None, ...)``: rotary positions and their
+  gradient, for ``[B, H, N, d]`` and ``[T, H, d]`` tensors of any strides;
+  ``attn_kv_append_rope_fp8(Q, K, V, positions, slots, freqs, k_pages, ...) -> Q_out``:
+  the paged append with them applied on the way
 * ``attn_bwd(Q, K, V, O, dO, LSE, scale, causal) -> (dQ, dK, dV)``
 * ``attn_bwd_workspace_size(B, Hq, Hkv, N, d)``
 * ``attn_last_device_status(stream=None)``, ``attn_status_string(code)``
@@ -64,6 +70,7 @@ EXPORTED = ("attn_fwd", "attn_fwd_split", "attn_fwd_split_workspace_size", "attn
             "attn_bwd_masked", "attn_quantize_fp8", "attn_fp8_vt_stride", "attn_fwd_fp8", "attn_bwd",
             "attn_bwd_preprocess", "attn_bwd_main", "attn_bwd_convert", "attn_bwd_workspace_size",
             "attn_kv_tables", "attn_kv_append_fp8", "attn_fwd_paged_fp8", "attn_fwd_paged_workspace_size",
+            "attn_rope_freqs", "attn_rope", "attn_rope_bwd", "attn_kv_append_rope_fp8",
             "attn_status_string", "attn_last_device_status", "attn_selftest_wait_timeout",
             "attn_selftest_paged_wait_timeout")
 _BWD_STAGES = {"all": "attn_bwd", "preprocess": "attn_bwd_preprocess", "main": "attn_bwd_main",
@@ -72,6 +79,13 @@ _BWD_STAGES = {"all": "attn_bwd", "preprocess": "attn_bwd_preprocess", "main": "
 _lock = threading.Lock()
 _lib = None
 _fast = None  # the extension module, bound to the loaded library; False where there is none
+
+
+class _Rows(ctypes.Structure):
+    """attn_rows: rows of d elements and the elements between them."""
+
+    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_longlong), ("head", ctypes.c_longlong),
+                ("token", ctypes.c_longlong)]
 
 
 class AttnError(RuntimeError):
@@ -115,7 +129,7 @@ def load_library(path: str = LIB_PATH):
         lib.attn_quantize_fp8.restype = i32
         lib.attn_fwd_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, i32, i32, vp]
         lib.attn_fwd_fp8.restype = i32
-        i64 = ctypes.c_longlong
+        i64, f64 = ctypes.c_longlong, ctypes.c_double
         lib.attn_kv_tables.argtypes = [vp, vp, vp, i32, vp, i32, i32, vp, vp, vp, vp, vp, i32, i32, vp]
         lib.attn_kv_tables.restype = i32
         lib.attn_kv_append_fp8.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp]
@@ -125,6 +139,15 @@ def load_library(path: str = LIB_PATH):
         lib.attn_fwd_paged_fp8.restype = i32
         lib.attn_fwd_paged_workspace_size.argtypes = [i32, i32, i32, i32, i32]
         lib.attn_fwd_paged_workspace_size.restype = sz
+        rows = ctypes.POINTER(_Rows)
+        for fn in (lib.attn_rope, lib.attn_rope_bwd):
+            fn.argtypes = [rows, rows, rows, rows, vp, i64, vp, i32, i32, f32, i32, i32, i32, i32, i32, i32, vp]
+            fn.restype = i32
+        lib.attn_rope_freqs.argtypes = [vp, vp, i32, f64, i32, f64, f64, f64, f64]
+        lib.attn_rope_freqs.restype = i32
+        lib.attn_kv_append_rope_fp8.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, vp, i32, i32, f32, vp, i64, vp, vp,
+                                                vp, vp, i32, i32, i32, i32, i32, i32, vp]
+        lib.attn_kv_append_rope_fp8.restype = i32
         lib.attn_bwd_workspace_size.argtypes = [i32, i32, i32, i32, i32]
         lib.attn_bwd_workspace_size.restype = sz
         lib.attn_status_string.argtypes = [i32]
@@ -140,8 +163,8 @@ def load_library(path: str = LIB_PATH):
 
 
 def _bound():
-    """The extension module (csrc/binding.cpp) with the library loaded, at the first paged
-    call; False, after a warning, where it cannot be loaded."""
+    """The extension module (csrc/binding.cpp) with the library loaded, at the first call that
+    uses it; False, after a warning, where it cannot be loaded."""
     global _fast
     if _fast is not None:
         return _fast
@@ -155,7 +178,8 @@ def _bound():
                 spec.loader.exec_module(module)
                 module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
                     lib.attn_kv_tables, lib.attn_kv_append_fp8, lib.attn_fwd_paged_fp8,
-                    lib.attn_fwd_paged_workspace_size)))
+                    lib.attn_fwd_paged_workspace_size, lib.attn_rope, lib.attn_rope_bwd,
+                    lib.attn_kv_append_rope_fp8)))
                 _fast = module
             except ImportError as e:
                 _fast = False
@@ -601,6 +625,159 @@ def attn_fwd_paged_fp8(Q, k_pages, k_scale, v_pages, v_scale, block_table, cu_q,
               O.data_ptr(), LSE.data_ptr(), R, T, Hq, Hkv, d, num_pages, page_size, max_pages, float(scale),
               int(bool(causal)), out_dt, workspace.data_ptr(), workspace.numel())
     return O, LSE
+
+
+# ---------------------------------------------------------------- rotary positions
+_SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
+
+
+def attn_rope_freqs(rot, base=10000.0, scaling="none", factor=1.0, original_len=0.0, low=1.0, high=32.0, device="cuda"):
+    """(freqs, amplitude) for attn_rope: turns a position of each of rot / 2 pairs, as int64
+    in units of 2^-64 turn, and what the rotated elements are multiplied with.
+
+    scaling: "none"; for contexts `factor` times longer "linear" (positions divided),
+    "base" (the base raised), or "parts" (pairs that turn at most `low` times over
+    original_len positions divided, those that turn `high` times left, a ramp between)."""
+    lib = load_library()
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling must be one of {', '.join(_SCALINGS)}, got {scaling!r}")
+    rot = int(rot)
+    host = torch.empty(max(rot, 0) // 2, dtype=torch.int64)
+    amplitude = ctypes.c_double()
+    rc = lib.attn_rope_freqs(host.data_ptr(), ctypes.addressof(amplitude), rot, float(base), _SCALINGS[scaling],
+                             float(factor), float(original_len), float(low), float(high))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_rope_freqs")
+    return host.to(device), amplitude.value
+
+
+def _rope_rows(name, t, shape, dtype, device):
+    """attn_rows of a [T, H, d] or [B, H, N, d] tensor whose rows may be anywhere."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    st = t.stride()
+    return _Rows(t.data_ptr(), *((0, st[1], st[0]) if t.dim() == 3 else st[:3]))
+
+
+def _check_freqs(freqs, d, device):
+    if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
+        raise TypeError("freqs must be a CUDA tensor [rot / 2] (attn_rope_freqs makes it)")
+    _check_tensor("freqs", freqs, torch.int64, freqs.shape, device)
+    rot = 2 * freqs.shape[0]
+    if rot < 1 or rot > d:
+        raise ValueError(f"freqs turns {rot} elements of {d}")
+    return rot
+
+
+def _rope(fname, q_name, k_name, Q, K, freqs, positions, interleaved, amplitude, Q_out, K_out, stream):
+    fast = stream is None and _bound()
+    if fast:
+        r = fast.rope(fname == "attn_rope_bwd", Q, K, freqs, positions, interleaved, amplitude, Q_out, K_out)
+        if r is not None:
+            return _result(r, fname)
+    lib = load_library()
+    dev = _cuda_device(q_name, Q)
+    dtype = {torch.bfloat16: ATTN_BF16, torch.float32: ATTN_F32}.get(Q.dtype)
+    if dtype is None:
+        raise TypeError(f"{q_name} must be bf16 or fp32")
+    if Q.dim() not in (3, 4):
+        raise ValueError(f"{q_name} must have shape (T, Hq, d) or (B, Hq, N, d), got {tuple(Q.shape)}")
+    tokens = Q.dim() == 3
+    B, Hq, N, d = (1, Q.shape[1], Q.shape[0], Q.shape[2]) if tokens else Q.shape
+    q_shape = tuple(Q.shape)
+    q = _rope_rows(q_name, Q, q_shape, Q.dtype, dev)
+    k, k_shape, Hkv = None, None, 0
+    if K is not None:
+        if not isinstance(K, torch.Tensor) or K.dim() != Q.dim():
+            raise TypeError(f"{k_name} must be a {Q.dim()}-dimensional CUDA tensor or None")
+        Hkv = K.shape[1]
+        k_shape = (N, Hkv, d) if tokens else (B, Hkv, N, d)
+        k = _rope_rows(k_name, K, k_shape, Q.dtype, dev)
+    elif K_out is not None:
+        raise ValueError(f"{k_name}_out without {k_name}")
+    rot = _check_freqs(freqs, d, dev)
+    pos_batch = 0
+    if positions is not None:
+        if not isinstance(positions, torch.Tensor) or not positions.is_cuda:
+            raise TypeError("positions must be a CUDA tensor")
+        batched = not tokens and positions.dim() == 2
+        _check_tensor("positions", positions, torch.int32, (B, N) if batched else (N,), dev)
+        pos_batch = N if batched else 0
+    with _on(dev, stream):
+        Q_out = torch.empty(q_shape, dtype=Q.dtype, device=dev) if Q_out is None else Q_out
+        qo = _rope_rows(q_name + "_out", Q_out, q_shape, Q.dtype, dev)
+        ko = None
+        if K is not None:
+            K_out = torch.empty(k_shape, dtype=Q.dtype, device=dev) if K_out is None else K_out
+            ko = _rope_rows(k_name + "_out", K_out, k_shape, Q.dtype, dev)
+        if Q.numel() or (K is not None and K.numel()):
+            _call(getattr(lib, fname), q, k, qo, ko, positions.data_ptr() if positions is not None else None, pos_batch,
+                  freqs.data_ptr(), rot, int(bool(interleaved)), float(amplitude), B, Hq, Hkv, N, d, dtype)
+    return Q_out, K_out
+
+
+def attn_rope(Q, K, freqs, positions=None, interleaved=False, amplitude=1.0, Q_out=None, K_out=None, stream=None):
+    """Rotary positions: Q [B, Hq, N, d] and K [B, Hkv, N, d], or [T, H, d] both (bf16 or
+    fp32, of any strides between rows; K may be None), rotated into Q_out and K_out.
+
+    freqs, amplitude: from attn_rope_freqs.  positions int32 [N] ([T]) or [B, N]; None:
+    0 .. N - 1.  A token with a negative position is copied.  New outputs are contiguous;
+    Q_out may be Q and K_out K."""
+    return _rope("attn_rope", "Q", "K", Q, K, freqs, positions, interleaved, amplitude, Q_out, K_out, stream)
+
+
+def attn_rope_bwd(dQ, dK, freqs, positions=None, interleaved=False, amplitude=1.0, dQ_out=None, dK_out=None,
+                  stream=None):
+    """The gradient of attn_rope: from those of its outputs to those of its inputs."""
+    return _rope("attn_rope_bwd", "dQ", "dK", dQ, dK, freqs, positions, interleaved, amplitude, dQ_out, dK_out, stream)
+
+
+def attn_kv_append_rope_fp8(Q, K, V, positions, slots, freqs, k_pages, k_scale, v_pages, v_scale, interleaved=False,
+                            amplitude=1.0, Q_out=None, stream=None):
+    """attn_kv_append_fp8 with the keys rotated before they are quantized; returns the
+    queries [T, Hq, d] of the same tokens, rotated too (in Q_out; new: contiguous).
+
+    positions int32 [T] as attn_kv_tables writes them (negative: not rotated); freqs,
+    interleaved and amplitude as for attn_rope."""
+    fast = stream is None and _bound()
+    if fast:
+        r = fast.kv_append_rope_fp8(Q, K, V, positions, slots, freqs, k_pages, k_scale, v_pages, v_scale, interleaved,
+                                    amplitude, Q_out)
+        if r is not None:
+            return _result(r, "attn_kv_append_rope_fp8")
+    lib = load_library()
+    dev = _cuda_device("K", K)
+    num_pages, Hkv, page_size, d = _check_cache(k_pages, k_scale, v_pages, v_scale, dev)
+    k_stride = _check_tokens("K", K, Hkv, d, dev)
+    v_stride = _check_tokens("V", V, Hkv, d, dev)
+    if not isinstance(Q, torch.Tensor) or Q.dim() != 3:
+        raise TypeError("Q must be a CUDA tensor (T, Hq, d)")
+    T, Hq = K.shape[0], Q.shape[1]
+    q_stride = _check_tokens("Q", Q, Hq, d, dev)
+    for name, t in (("Q", Q), ("V", V)):
+        if t.shape[0] != T:
+            raise ValueError(f"{name} has {t.shape[0]} tokens, K has {T}")
+    _check_tensor("positions", positions, torch.int32, (T,), dev)
+    _check_tensor("slots", slots, torch.int64, (T,), dev)
+    rot = _check_freqs(freqs, d, dev)
+    with _on(dev, stream):
+        Q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev) if Q_out is None else Q_out
+        qo_stride = _check_tokens("Q_out", Q_out, Hq, d, dev)
+        if Q_out.shape[0] != T:
+            raise ValueError(f"Q_out has {Q_out.shape[0]} tokens, K has {T}")
+        _call(lib.attn_kv_append_rope_fp8, Q.data_ptr(), q_stride, K.data_ptr(), k_stride, V.data_ptr(), v_stride,
+              positions.data_ptr(), slots.data_ptr(), freqs.data_ptr(), rot, int(bool(interleaved)), float(amplitude),
+              Q_out.data_ptr(), qo_stride, k_pages.data_ptr(), k_scale.data_ptr(), v_pages.data_ptr(),
+              v_scale.data_ptr(), T, Hq, Hkv, d, num_pages, page_size)
+    return Q_out
 
 
 def _bwd_inputs(Q, K, V, O, dO, LSE):

@@ -1,5 +1,5 @@
-// binding.cpp -- the Python calls of the paged 8-bit cache without Python's
-// share of the work.
+// binding.cpp -- the Python calls of the paged 8-bit cache and of rotary positions
+// without Python's share of the work.
 //
 // A decoding step makes these calls once a layer around kernels of a few
 // microseconds; checks, allocations and pointer passing in Python take three
@@ -31,6 +31,8 @@ decltype(&attn_kv_tables) g_tables = nullptr;
 decltype(&attn_kv_append_fp8) g_append = nullptr;
 decltype(&attn_fwd_paged_fp8) g_fwd = nullptr;
 decltype(&attn_fwd_paged_workspace_size) g_workspace = nullptr;
+decltype(&attn_rope) g_rope[2] = {nullptr, nullptr};  // forward, gradient
+decltype(&attn_kv_append_rope_fp8) g_append_rope = nullptr;
 
 // The tensor of an argument, or null.
 const at::Tensor* tensor(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
@@ -264,14 +266,128 @@ PyObject* fwd_paged_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return tuple(wrap(a[11], O), wrap(a[12], LSE));)
 }
 
-// bind(addresses of attn_kv_tables, attn_kv_append_fp8, attn_fwd_paged_fp8, attn_fwd_paged_workspace_size)
+// Rows of a [T, H, d] or [B, H, N, d] tensor.
+bool rows_of(const at::Tensor* t, at::ScalarType type, at::IntArrayRef shape, at::Device device, attn_rows& r) {
+  if (!t || t->scalar_type() != type || t->device() != device || t->sizes() != shape) return false;
+  const int64_t k = t->dim();
+  if (t->size(k - 1) > 1 && t->stride(k - 1) != 1) return false;
+  r.data = t->data_ptr();
+  r.batch = k == 4 ? t->stride(0) : 0;
+  r.head = t->stride(1);
+  r.token = k == 4 ? t->stride(2) : t->stride(0);
+  return true;
+}
+// An output of such rows: the caller's, or a new contiguous one for None.
+bool rows_out(PyObject* o, at::Tensor& t, at::ScalarType type, at::IntArrayRef shape, at::Device device, attn_rows& r) {
+  if (o == Py_None)
+    t = fresh(type, shape);
+  else if (const at::Tensor* given = tensor(o))
+    t = *given;
+  else
+    return false;
+  return rows_of(&t, type, shape, device, r);
+}
+bool amplitude_of(PyObject* o, float& v) {
+  if (!PyFloat_Check(o)) return false;
+  v = (float)PyFloat_AS_DOUBLE(o);
+  return true;
+}
+
+// gradient, Q, K, freqs, positions, interleaved, amplitude, Q_out, K_out
+PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  ATTN_GUARD(
+    if (n != 9) Py_RETURN_NONE;
+    const at::Tensor *Q = tensor(a[1]), *K = tensor(a[2]), *freqs = tensor(a[3]), *pos = tensor(a[4]);
+    if (!Q || !Q->is_cuda() || (Q->dim() != 3 && Q->dim() != 4) || Q->numel() == 0 || (!K && (a[2] != Py_None || a[8] != Py_None)) ||
+        (K && K->dim() != Q->dim()) || (!pos && a[4] != Py_None))
+      Py_RETURN_NONE;
+    const at::Device dev = Q->device();
+    const at::ScalarType type = Q->scalar_type();
+    if (type != at::kBFloat16 && type != at::kFloat) Py_RETURN_NONE;
+    const bool tokens = Q->dim() == 3;
+    const int64_t B = tokens ? 1 : Q->size(0), N = Q->size(tokens ? 0 : 2), Hq = Q->size(1), d = Q->size(tokens ? 2 : 3);
+    const int64_t Hkv = K ? K->size(1) : 0;
+    float amplitude = 1;
+    attn_rows q, k{}, qo, ko{};
+    const int64_t three[3] = {N, Hkv, d}, four[4] = {B, Hkv, N, d};
+    const at::IntArrayRef k_shape = tokens ? at::IntArrayRef(three, 3) : at::IntArrayRef(four, 4);
+    if (!fits(B) || !fits(N) || !fits(Hq) || !fits(Hkv) || !fits(d) || (K && Hkv == 0) || !amplitude_of(a[6], amplitude) ||
+        !rows_of(Q, type, Q->sizes(), dev, q) || (K && !rows_of(K, type, k_shape, dev, k)) || !freqs ||
+        freqs->dim() != 1 || freqs->size(0) < 1 || 2 * freqs->size(0) > d || !is(freqs, at::kLong, freqs->sizes(), dev))
+      Py_RETURN_NONE;
+    long long pos_batch = 0;
+    if (pos) {
+      if (!tokens && pos->dim() == 2 ? !is(pos, at::kInt, {B, N}, dev) : !is(pos, at::kInt, {N}, dev)) Py_RETURN_NONE;
+      pos_batch = pos->dim() == 2 ? N : 0;
+    }
+    const int gradient = PyObject_IsTrue(a[0]), pairs = PyObject_IsTrue(a[5]);
+    if (gradient < 0 || pairs < 0) return nullptr;
+    const OnDevice on(dev);
+    at::Tensor Qo, Ko;
+    if (!rows_out(a[7], Qo, type, Q->sizes(), dev, qo) || (K && !rows_out(a[8], Ko, type, k_shape, dev, ko))) Py_RETURN_NONE;
+    const int rc = without_lock(dev, [&](void* stream) {
+      return g_rope[gradient](&q, K ? &k : nullptr, &qo, K ? &ko : nullptr, pos ? (const int32_t*)pos->data_ptr() : nullptr,
+                              pos_batch, (const uint64_t*)freqs->data_ptr(), (int)(2 * freqs->size(0)), pairs, amplitude,
+                              (int)B, (int)Hq, (int)Hkv, (int)N, (int)d, type == at::kFloat ? ATTN_F32 : ATTN_BF16, stream);
+    });
+    if (rc != ATTN_OK) return PyLong_FromLong(rc);
+    if (!K) {
+      Py_INCREF(Py_None);
+      return tuple(wrap(a[7], Qo), Py_None);
+    }
+    return tuple(wrap(a[7], Qo), wrap(a[8], Ko));)
+}
+
+// Q, K, V, positions, slots, freqs, k_pages, k_scale, v_pages, v_scale, interleaved, amplitude, Q_out
+PyObject* kv_append_rope_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  ATTN_GUARD(
+    if (n != 13) Py_RETURN_NONE;
+    const at::Tensor *Q = tensor(a[0]), *K = tensor(a[1]), *V = tensor(a[2]), *pos = tensor(a[3]), *slots = tensor(a[4]);
+    const at::Tensor* freqs = tensor(a[5]);
+    Cache c;
+    float amplitude = 1;
+    if (!Q || Q->dim() != 3 || !K || !K->is_cuda() || !c.read(a + 6, K->device()) || !amplitude_of(a[11], amplitude))
+      Py_RETURN_NONE;
+    const at::Device dev = K->device();
+    const int64_t T = K->size(0), Hq = Q->size(1);
+    const long long qs = token_stride(Q, Hq, c.d, dev), ks = token_stride(K, c.Hkv, c.d, dev), vs = token_stride(V, c.Hkv, c.d, dev);
+    if (qs < 0 || ks < 0 || vs < 0 || Q->size(0) != T || V->size(0) != T || !fits(T) || !fits(Hq) ||
+        !is(slots, at::kLong, {T}, dev) || !is(pos, at::kInt, {T}, dev) || !freqs || freqs->dim() != 1 ||
+        freqs->size(0) < 1 || 2 * freqs->size(0) > c.d || !is(freqs, at::kLong, freqs->sizes(), dev))
+      Py_RETURN_NONE;
+    const int pairs = PyObject_IsTrue(a[10]);
+    if (pairs < 0) return nullptr;
+    const OnDevice on(dev);
+    at::Tensor Qo;
+    if (a[12] == Py_None)
+      Qo = fresh(at::kBFloat16, {T, Hq, c.d});
+    else if (const at::Tensor* given = tensor(a[12]))
+      Qo = *given;
+    else
+      Py_RETURN_NONE;
+    const long long qos = token_stride(&Qo, Hq, c.d, dev);
+    if (qos < 0 || Qo.size(0) != T) Py_RETURN_NONE;
+    const int rc = without_lock(dev, [&](void* stream) {
+      return g_append_rope(Q->data_ptr(), qs, K->data_ptr(), ks, V->data_ptr(), vs, (const int32_t*)pos->data_ptr(),
+                           (const int64_t*)slots->data_ptr(), (const uint64_t*)freqs->data_ptr(),
+                           (int)(2 * freqs->size(0)), pairs, amplitude, Qo.data_ptr(), qos, c.kp->data_ptr(),
+                           (float*)c.ks->data_ptr(), c.vp->data_ptr(), (float*)c.vs->data_ptr(), (int)T, (int)Hq,
+                           (int)c.Hkv, (int)c.d, (int)c.num_pages, (int)c.page, stream);
+    });
+    if (rc != ATTN_OK) return PyLong_FromLong(rc);
+    return wrap(a[12], Qo);)
+}
+
+// bind(addresses of attn_kv_tables, attn_kv_append_fp8, attn_fwd_paged_fp8, attn_fwd_paged_workspace_size, attn_rope,
+// attn_rope_bwd, attn_kv_append_rope_fp8)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 4) {
-    PyErr_SetString(PyExc_TypeError, "bind takes four addresses");
+  constexpr int kAddresses = 7;
+  if (n != kAddresses) {
+    PyErr_SetString(PyExc_TypeError, "bind takes seven addresses");
     return nullptr;
   }
-  void* p[4];
-  for (int i = 0; i < 4; ++i) {
+  void* p[kAddresses];
+  for (int i = 0; i < kAddresses; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred()) return nullptr;
   }
@@ -279,6 +395,9 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_append = reinterpret_cast<decltype(g_append)>(p[1]);
   g_fwd = reinterpret_cast<decltype(g_fwd)>(p[2]);
   g_workspace = reinterpret_cast<decltype(g_workspace)>(p[3]);
+  g_rope[0] = reinterpret_cast<decltype(&attn_rope)>(p[4]);
+  g_rope[1] = reinterpret_cast<decltype(&attn_rope)>(p[5]);
+  g_append_rope = reinterpret_cast<decltype(g_append_rope)>(p[6]);
   Py_RETURN_NONE;
 }
 
@@ -287,7 +406,8 @@ PyMethodDef method(const char* name) {
   return {name, (PyCFunction)(void*)F, METH_FASTCALL, ""};
 }
 PyMethodDef g_methods[] = {method<kv_tables>("kv_tables"), method<kv_append_fp8>("kv_append_fp8"),
-                           method<fwd_paged_fp8>("fwd_paged_fp8"), method<bind>("bind"),
+                           method<fwd_paged_fp8>("fwd_paged_fp8"), method<rope>("rope"),
+                           method<kv_append_rope_fp8>("kv_append_rope_fp8"), method<bind>("bind"),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods};
 

@@ -177,6 +177,30 @@ struct KvAppendParams {
 };
 cudaError_t launch_kv_append(int d, const KvAppendParams& p, int sms, cudaStream_t stream);
 
+// Rotary positions (rope.cu); see attn_rope.  Rows of d elements, strides in elements.
+struct RopeRows {
+  const void* in;
+  long long in_batch, in_head, in_token;
+  void* out;
+  long long out_batch, out_head, out_token;
+};
+struct RopeParams {
+  RopeRows q, k;
+  const int* positions;  // [B, N], pos_batch elements between batches; NULL: 0 .. N - 1
+  long long pos_batch;
+  const uint64_t* freqs;  // [rot / 2] turns a position, times 2^64
+  float amplitude, sine;  // what cos and sin are multiplied with (the gradient: sine = -amplitude)
+  int rot, B, N, Hq, Hkv;
+  int* status;  // (debug builds' checks)
+};
+cudaError_t launch_rope(int d, int f32, const RopeParams& p, int interleaved, int sms, cudaStream_t stream);
+int rope_heads(long long groups, int all, int sms);
+
+// Append with the keys rotated, and the queries of the same tokens (p.q in, p.q
+// out; no other rows of `r`); see attn_kv_append_rope_fp8.
+cudaError_t launch_kv_append_rope(int d, const KvAppendParams& p, const RopeParams& r, int interleaved, int sms,
+                                  cudaStream_t stream);
+
 // Attention over a paged 8-bit cache (paged_fwd.cu); see attn_fwd_paged_fp8.
 struct PagedFwdParams {
   const uint16_t* Q;     // [T, Hq, d] bf16, q_stride elements between tokens

@@ -5,12 +5,15 @@
 #include <cstdint>
 
 #include "../../include/attn.h"
+#include "checks.h"
 #include "kernels.h"
 #include "paged.cuh"
 
 namespace {
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+using attn::aligned;
+using attn::any_overlap;
+using attn::Span;
 
 // log2 of a supported page size, else -1.
 int page_log2(int page_size) {
@@ -92,20 +95,6 @@ void place(attn::PagedFwdParams& p, uint8_t* ws, int rows, int d, int sms) {
   p.desc = reinterpret_cast<int*>(ws + part_o_bytes(rows, d, sms) + part_ml_bytes(rows, sms));
 }
 
-// Whether one of the first `written` of `count` arrays shares a byte with another.
-struct Span {
-  const void* p;
-  size_t n;  // bytes
-};
-bool any_overlap(const Span* a, int written, int count) {
-  for (int i = 0; i < written; ++i)
-    for (int j = i + 1; j < count; ++j) {
-      const uintptr_t x = reinterpret_cast<uintptr_t>(a[i].p), y = reinterpret_cast<uintptr_t>(a[j].p);
-      if (a[i].n > 0 && a[j].n > 0 && x < y + a[j].n && y < x + a[i].n) return true;
-    }
-  return false;
-}
-
 // Diagnostic: one warp waits, as the paged kernels do, on an mbarrier that is never completed.
 __global__ void selftest_paged_wait_kernel(int* status, uint32_t limit_ns) {
   __shared__ __align__(8) uint64_t bar;
@@ -124,6 +113,40 @@ __global__ void selftest_paged_wait_kernel(int* status, uint32_t limit_ns) {
 int sms_or_default() {
   const int n = attn::device_sms();
   return n > 0 ? n : 152;
+}
+
+// Checks of an append and its parameters (T may be 0: K, V and slots are then not read).
+attn_status append_params(const void* K, long long k_stride, const void* V, long long v_stride, const int64_t* slots,
+                          void* k_pages, float* k_scale, void* v_pages, float* v_scale, int T, int Hkv, int d,
+                          int num_pages, int page_size, attn::KvAppendParams& p) {
+  attn_status st = check_cache(k_pages, k_scale, v_pages, v_scale, Hkv, d, num_pages, page_size);
+  if (st != ATTN_OK) return st;
+  if (T < 0) return ATTN_ERR_INVALID_ARG;
+  if (T == 0) return ATTN_OK;
+  if (!K || !V || !slots) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(K, 16) || !aligned(V, 16) || !aligned(slots, 8)) return ATTN_ERR_INVALID_ARG;
+  if (!token_stride_ok(k_stride, Hkv, d) || !token_stride_ok(v_stride, Hkv, d)) return ATTN_ERR_INVALID_ARG;
+  // No updated array may be another array of the call.
+  const size_t codes = (size_t)num_pages * Hkv * page_size * d, scales = (size_t)num_pages * Hkv * 4;
+  const Span all[] = {{k_pages, codes}, {v_pages, codes}, {k_scale, scales}, {v_scale, scales}, {slots, (size_t)T * 8},
+                      {K, ((size_t)(T - 1) * k_stride + (size_t)Hkv * d) * 2},
+                      {V, ((size_t)(T - 1) * v_stride + (size_t)Hkv * d) * 2}};
+  if (any_overlap(all, 4, 7)) return ATTN_ERR_INVALID_ARG;
+  p.K = static_cast<const uint16_t*>(K);
+  p.V = static_cast<const uint16_t*>(V);
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.slots = reinterpret_cast<const long long*>(slots);
+  p.k_pages = static_cast<uint8_t*>(k_pages);
+  p.v_pages = static_cast<uint8_t*>(v_pages);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  if (attn::kDebugChecks && !(p.status = attn::device_status_word())) return ATTN_ERR_CUDA;
+  p.T = T;
+  p.Hkv = Hkv;
+  p.num_pages = num_pages;
+  p.page_log2 = page_log2(page_size);
+  return ATTN_OK;
 }
 
 }  // namespace
@@ -173,35 +196,55 @@ attn_status attn_kv_tables(const int32_t* cached, const int32_t* added, const in
 attn_status attn_kv_append_fp8(const void* K, long long k_stride, const void* V, long long v_stride,
                                const int64_t* slots, void* k_pages, float* k_scale, void* v_pages, float* v_scale,
                                int T, int Hkv, int d, int num_pages, int page_size, void* stream) {
-  attn_status st = check_cache(k_pages, k_scale, v_pages, v_scale, Hkv, d, num_pages, page_size);
-  if (st != ATTN_OK) return st;
-  if (T < 0) return ATTN_ERR_INVALID_ARG;
-  if (T == 0) return ATTN_OK;
-  if (!K || !V || !slots) return ATTN_ERR_INVALID_ARG;
-  if (!aligned(K, 16) || !aligned(V, 16) || !aligned(slots, 8)) return ATTN_ERR_INVALID_ARG;
-  if (!token_stride_ok(k_stride, Hkv, d) || !token_stride_ok(v_stride, Hkv, d)) return ATTN_ERR_INVALID_ARG;
-  // No updated array may be another array of the call.
-  const size_t codes = (size_t)num_pages * Hkv * page_size * d, scales = (size_t)num_pages * Hkv * 4;
-  const Span all[] = {{k_pages, codes}, {v_pages, codes}, {k_scale, scales}, {v_scale, scales}, {slots, (size_t)T * 8},
-                      {K, ((size_t)(T - 1) * k_stride + (size_t)Hkv * d) * 2},
-                      {V, ((size_t)(T - 1) * v_stride + (size_t)Hkv * d) * 2}};
-  if (any_overlap(all, 4, 7)) return ATTN_ERR_INVALID_ARG;
   attn::KvAppendParams p{};
-  p.K = static_cast<const uint16_t*>(K);
-  p.V = static_cast<const uint16_t*>(V);
-  p.k_stride = k_stride;
-  p.v_stride = v_stride;
-  p.slots = reinterpret_cast<const long long*>(slots);
-  p.k_pages = static_cast<uint8_t*>(k_pages);
-  p.v_pages = static_cast<uint8_t*>(v_pages);
-  p.k_scale = k_scale;
-  p.v_scale = v_scale;
-  if (attn::kDebugChecks && !(p.status = attn::device_status_word())) return ATTN_ERR_CUDA;
-  p.T = T;
-  p.Hkv = Hkv;
-  p.num_pages = num_pages;
-  p.page_log2 = page_log2(page_size);
+  attn_status st = append_params(K, k_stride, V, v_stride, slots, k_pages, k_scale, v_pages, v_scale, T, Hkv, d, num_pages,
+                                 page_size, p);
+  if (st != ATTN_OK || T == 0) return st;
   cudaError_t e = attn::launch_kv_append(d, p, sms_or_default(), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+attn_status attn_kv_append_rope_fp8(const void* Q, long long q_stride, const void* K, long long k_stride, const void* V,
+                                    long long v_stride, const int32_t* positions, const int64_t* slots,
+                                    const uint64_t* freqs, int rot, int interleaved, float amplitude, void* Q_out,
+                                    long long q_out_stride, void* k_pages, float* k_scale, void* v_pages, float* v_scale,
+                                    int T, int Hq, int Hkv, int d, int num_pages, int page_size, void* stream) {
+  attn::KvAppendParams p{};
+  attn_status st = append_params(K, k_stride, V, v_stride, slots, k_pages, k_scale, v_pages, v_scale, T, Hkv, d, num_pages,
+                                 page_size, p);
+  if (st != ATTN_OK) return st;
+  if (Hq < 1 || rot < 1 || rot > d || (interleaved != 0 && interleaved != 1) || !std::isfinite(amplitude) || !(amplitude > 0.f))
+    return ATTN_ERR_INVALID_ARG;
+  if (rot % 16 != 0 || Hq > 65535) return ATTN_ERR_UNSUPPORTED;
+  if (T == 0) return ATTN_OK;
+  if (!Q || !Q_out || !positions || !freqs) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(Q, 16) || !aligned(Q_out, 16) || !aligned(positions, 4) || !aligned(freqs, 8)) return ATTN_ERR_INVALID_ARG;
+  if (!token_stride_ok(q_stride, Hq, d) || !token_stride_ok(q_out_stride, Hq, d)) return ATTN_ERR_INVALID_ARG;
+  // Q_out may be Q, or lie between K's and V's rows in a packed projection; what is
+  // written may be no other array of the call.
+  const attn::Rows q(Q, 1, Hq, T, 0, d, q_stride, d, 2), qo(Q_out, 1, Hq, T, 0, d, q_out_stride, d, 2);
+  const attn::Rows k(K, 1, Hkv, T, 0, d, k_stride, d, 2), v(V, 1, Hkv, T, 0, d, v_stride, d, 2);
+  if (!(qo.same(q) || apart(qo, q)) || !apart(qo, k) || !apart(qo, v)) return ATTN_ERR_INVALID_ARG;
+  const size_t codes = (size_t)num_pages * Hkv * page_size * d, scales = (size_t)num_pages * Hkv * 4;
+  const Span written[] = {qo.span(), {k_pages, codes}, {v_pages, codes}, {k_scale, scales}, {v_scale, scales}};
+  const Span read[] = {{positions, (size_t)T * 4}, {freqs, (size_t)rot * 4}};
+  for (int i = 0; i < 5; ++i) {
+    if (overlap(written[i], read[0]) || overlap(written[i], read[1])) return ATTN_ERR_INVALID_ARG;
+    if (i > 0 && (overlap(written[i], qo.span()) || overlap(written[i], q.span()))) return ATTN_ERR_INVALID_ARG;
+  }
+  if (overlap({slots, (size_t)T * 8}, qo.span())) return ATTN_ERR_INVALID_ARG;
+  attn::RopeParams r{};
+  r.q = {Q, 0, d, q_stride, Q_out, 0, d, q_out_stride};
+  r.positions = positions;
+  r.freqs = freqs;
+  r.amplitude = r.sine = amplitude;
+  r.rot = rot;
+  r.B = 1;
+  r.N = T;
+  r.Hq = Hq;
+  r.status = p.status;
+  cudaError_t e = attn::launch_kv_append_rope(d, p, r, interleaved, sms_or_default(), static_cast<cudaStream_t>(stream));
+  if (e == cudaErrorNotSupported) return ATTN_ERR_UNSUPPORTED;
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

@@ -339,6 +339,26 @@ attn_status attn_kv_append_fp8(const void* K, long long k_stride, const void* V,
                                int T, int Hkv, int d, int num_pages, int page_size, void* stream);
 
 /*
+ * attn_kv_append_fp8 with rotary positions applied on the way: the keys are rotated
+ * before they are quantized (in fp32; the scale and the codes are those of the rotated
+ * numbers, rounded once), and the queries of the same tokens are rotated into Q_out,
+ * as attn_rope rotates them.  V is appended as it is.
+ *   Q [T, Hq, d] bf16, q_stride elements between tokens (>= Hq * d, a multiple of 8);
+ *   Q_out likewise, and may be Q (same stride) or lie between the rows of Q, K and V in a
+ *         packed projection; beyond that it may overlap no array of the call
+ *   positions [T] int32 (as attn_kv_tables writes them); negative: not rotated
+ *   freqs [rot / 2] in device memory, rot, interleaved, amplitude as for attn_rope
+ * Every token's query is rotated, also where its slot is skipped.  Hq <= 65535, else
+ * ATTN_ERR_UNSUPPORTED.  An infinity or NaN in K is one in its pair.  The other arguments
+ * and rules are attn_kv_append_fp8's.
+ */
+attn_status attn_kv_append_rope_fp8(const void* Q, long long q_stride, const void* K, long long k_stride, const void* V,
+                                    long long v_stride, const int32_t* positions, const int64_t* slots,
+                                    const uint64_t* freqs, int rot, int interleaved, float amplitude, void* Q_out,
+                                    long long q_out_stride, void* k_pages, float* k_scale, void* v_pages, float* v_scale,
+                                    int T, int Hq, int Hkv, int d, int num_pages, int page_size, void* stream);
+
+/*
  * Attention of ragged queries over the paged cache.  Request r has the query
  * tokens cu_q[r] <= t < cu_q[r+1] and the keys 0 .. kv_lens[r]-1; with causal
  * the mask is aligned to the bottom-right corner (its last query sees all its
@@ -377,6 +397,69 @@ attn_status attn_fwd_paged_fp8(const void* Q, long long q_stride, const void* k_
  * room for small tiles only): a workspace for several steps has the largest of their
  * sizes, not that of the largest R and T. */
 size_t attn_fwd_paged_workspace_size(int R, int T, int Hq, int Hkv, int d);
+
+/*
+ * Rotary positions.  Pair i of the first `rot` elements (x1, x2) of a row at position
+ * pos turns by the angle a = 2 pi * pos * f_i:
+ *   y1 = amplitude * (x1 cos a - x2 sin a),   y2 = amplitude * (x2 cos a + x1 sin a);
+ * the other elements stay.  Pairs are elements (i, i + rot / 2), or (2 i, 2 i + 1) where
+ * interleaved is 1.  Frequencies are held as freqs[i] = f_i * 2^64, f_i in turns a
+ * position, so that pos * f_i loses no fraction of a turn at any 32-bit position.
+ * Products and sums are fp32, cos and sin within 2^-22, the result is rounded once.
+ * (The notes this library follows do not treat positions; the interface is its own.)
+ */
+
+/*
+ * The frequencies, in host memory: f_i = base^(-2 i / rot) / (2 pi), base > 1, and for
+ * contexts `factor` (>= 1) times longer than the original ones
+ *   ATTN_ROPE_LINEAR  f_i / factor ("Extending Context Window of Large Language Models
+ *                     via Positional Interpolation");
+ *   ATTN_ROPE_BASE    base * factor^(rot / (rot - 2)): the slowest pair slows down by the
+ *                     factor, the fastest not at all (rot > 2);
+ *   ATTN_ROPE_PARTS   f_i / factor for pairs that turn at most `low` times over
+ *                     original_len positions, f_i for those that turn at least `high`
+ *                     times, linear between, and amplitude 0.1 ln(factor) + 1 ("YaRN:
+ *                     Efficient Context Window Extension of Large Language Models",
+ *                     3.2 and 3.4; low 1, high 32 there).
+ * factor is not read with ATTN_ROPE_NONE, the last three only with ATTN_ROPE_PARTS.
+ *   freqs [rot / 2], rot even, 2 .. 1024; *amplitude: 1 but for ATTN_ROPE_PARTS.
+ */
+typedef enum { ATTN_ROPE_NONE = 0, ATTN_ROPE_LINEAR = 1, ATTN_ROPE_BASE = 2, ATTN_ROPE_PARTS = 3 } attn_rope_scaling;
+attn_status attn_rope_freqs(uint64_t* freqs, double* amplitude, int rot, double base, attn_rope_scaling scaling,
+                            double factor, double original_len, double low, double high);
+
+/* Rows of d contiguous elements, `batch`, `head` and `token` elements apart (not looked
+ * at where there is only one).  data 16-byte aligned, strides whole 16 bytes. */
+typedef struct {
+  void* data;
+  long long batch, head, token;
+} attn_rows;
+
+/*
+ * Rotates the rows of Q [B, Hq, N, d] and K [B, Hkv, N, d], whatever their order in
+ * memory: out of a packed projection into the attention's layout, for one.
+ *   K and K_out may both be NULL (Hkv is then not read).
+ *   Q_out may be Q and K_out may be K (same rows, same strides); an output may lie
+ *   between other rows of one packed array [.., tokens, heads, d]; beyond that no output may
+ *   overlap an array of the call (ATTN_ERR_INVALID_ARG), nor two rows of an output each other.
+ *   positions [B, N] int32, positions_batch elements between batches (0: one
+ *   [N] for all); NULL: 0 .. N - 1.  A row with a negative position has none and is
+ *   copied as it is.
+ *   freqs [rot / 2] in device memory, 8-byte aligned; rot a multiple of 16, at most d
+ *   (other multiples: ATTN_ERR_UNSUPPORTED); d in {64, 128}; dtype bf16 or fp32 of all
+ *   rows; amplitude finite and positive; N may be 0 (nothing is done).
+ */
+attn_status attn_rope(const attn_rows* Q, const attn_rows* K, const attn_rows* Q_out, const attn_rows* K_out,
+                      const int32_t* positions, long long positions_batch, const uint64_t* freqs, int rot,
+                      int interleaved, float amplitude, int B, int Hq, int Hkv, int N, int d, attn_dtype dtype,
+                      void* stream);
+
+/* The gradient: with dQ, dK those of attn_rope's outputs, writes those of its inputs
+ * (the rotation by -a, times the amplitude).  Arguments as attn_rope. */
+attn_status attn_rope_bwd(const attn_rows* dQ, const attn_rows* dK, const attn_rows* dQ_out, const attn_rows* dK_out,
+                          const int32_t* positions, long long positions_batch, const uint64_t* freqs, int rot,
+                          int interleaved, float amplitude, int B, int Hq, int Hkv, int N, int d, attn_dtype dtype,
+                          void* stream);
 
 /* Static string naming a status code. */
 const char* attn_status_string(attn_status s);
