@@ -36,6 +36,9 @@ Functions carry the C names:
   the paged append with them applied on the way
 * ``attn_bwd(Q, K, V, O, dO, LSE, scale, causal) -> (dQ, dK, dV)``
 * ``attn_bwd_workspace_size(B, Hq, Hkv, N, d)``
+* ``attn_fwd_dropout(Q, K, V, p, rng, scale, causal) -> (O, LSE)`` and
+  ``attn_bwd_dropout(Q, K, V, O, dO, LSE, p, rng, scale, causal) -> (dQ, dK, dV)``: with
+  dropout on the softmax, from a counter-based generator (seed and offset in ``rng``)
 * ``attn_last_device_status(stream=None)``, ``attn_status_string(code)``
 * ``attn_selftest_wait_timeout(limit_ns)``, ``attn_selftest_paged_wait_timeout(limit_ns)``
 
@@ -70,7 +73,7 @@ EXPORTED = ("attn_fwd", "attn_fwd_split", "attn_fwd_split_workspace_size", "attn
             "attn_bwd_masked", "attn_quantize_fp8", "attn_fp8_vt_stride", "attn_fwd_fp8", "attn_bwd",
             "attn_bwd_preprocess", "attn_bwd_main", "attn_bwd_convert", "attn_bwd_workspace_size",
             "attn_kv_tables", "attn_kv_append_fp8", "attn_fwd_paged_fp8", "attn_fwd_paged_workspace_size",
-            "attn_rope_freqs", "attn_rope", "attn_rope_bwd", "attn_kv_append_rope_fp8",
+            "attn_fwd_dropout", "attn_bwd_dropout", "attn_rope_freqs", "attn_rope", "attn_rope_bwd", "attn_kv_append_rope_fp8",
             "attn_status_string", "attn_last_device_status", "attn_selftest_wait_timeout",
             "attn_selftest_paged_wait_timeout")
 _BWD_STAGES = {"all": "attn_bwd", "preprocess": "attn_bwd_preprocess", "main": "attn_bwd_main",
@@ -139,6 +142,11 @@ def load_library(path: str = LIB_PATH):
         lib.attn_fwd_paged_fp8.restype = i32
         lib.attn_fwd_paged_workspace_size.argtypes = [i32, i32, i32, i32, i32]
         lib.attn_fwd_paged_workspace_size.restype = sz
+        lib.attn_fwd_dropout.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, i32, f32, vp, i32, vp]
+        lib.attn_fwd_dropout.restype = i32
+        lib.attn_bwd_dropout.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, i32, f32, vp,
+                                         vp, sz, vp]
+        lib.attn_bwd_dropout.restype = i32
         rows = ctypes.POINTER(_Rows)
         for fn in (lib.attn_rope, lib.attn_rope_bwd):
             fn.argtypes = [rows, rows, rows, rows, vp, i64, vp, i32, i32, f32, i32, i32, i32, i32, i32, i32, vp]
@@ -845,6 +853,66 @@ def attn_bwd(Q, K, V, O, dO, LSE, scale=None, causal=False, dQ=None, dK=None, dV
                                  _stream(stream))
     if rc != ATTN_OK:
         raise AttnError(rc, fname)
+    return dQ, dK, dV
+
+
+# ---------------------------------------------------------------- dropout
+def _check_rng(rng, device):
+    if not isinstance(rng, torch.Tensor):
+        raise TypeError("rng must be a CUDA tensor [2] (seed, offset)")
+    _check_tensor("rng", rng, torch.int64, (2,), device)
+
+
+def attn_fwd_dropout(Q, K, V, p, rng, scale=None, causal=False, out_dtype=None, O=None, LSE=None, stream=None):
+    """attn_fwd (bf16) with elements of the softmax dropped with probability p, rounded to a
+    multiple of 1/256.
+
+    rng int64 [2] on the device: seed, and an offset (its low 32 bits count) that tells calls of
+    one seed apart; read when the kernels run.  The mask follows from them and is
+    never stored; LSE is that without dropout."""
+    lib = load_library()
+    B, Hq, N, d = Q.shape
+    Hkv = K.shape[1]
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    bf = torch.bfloat16
+    out_dtype = bf if out_dtype is None else out_dtype
+    out_dt = {torch.bfloat16: ATTN_BF16, torch.float32: ATTN_F32}[out_dtype]
+    _check_tensor("Q", Q, bf, (B, Hq, N, d))
+    dev = Q.device
+    _check_tensor("K", K, bf, (B, Hkv, N, d), dev)
+    _check_tensor("V", V, bf, (B, Hkv, N, d), dev)
+    _check_rng(rng, dev)
+    with _on(dev, stream):
+        O = torch.empty((B, Hq, N, d), dtype=out_dtype, device=dev) if O is None else O
+        LSE = torch.empty((B, Hq, N), dtype=torch.float32, device=dev) if LSE is None else LSE
+        _check_tensor("O", O, out_dtype, (B, Hq, N, d), dev)
+        _check_tensor("LSE", LSE, torch.float32, (B, Hq, N), dev)
+        _call(lib.attn_fwd_dropout, Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), LSE.data_ptr(), B, Hq, Hkv, N,
+              d, float(scale), int(bool(causal)), float(p), rng.data_ptr(), out_dt)
+    return O, LSE
+
+
+def attn_bwd_dropout(Q, K, V, O, dO, LSE, p, rng, scale=None, causal=False, dQ=None, dK=None, dV=None, workspace=None,
+                     stream=None):
+    """dQ, dK, dV of attn_fwd_dropout's O, given dO and the forward's O, LSE, p and numbers in rng."""
+    lib = load_library()
+    B, Hq, Hkv, N, d, dev = _bwd_inputs(Q, K, V, O, dO, LSE)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    _check_rng(rng, dev)
+    with _on(dev, stream):
+        dQ = torch.empty_like(Q) if dQ is None else dQ
+        dK = torch.empty_like(K) if dK is None else dK
+        dV = torch.empty_like(V) if dV is None else dV
+        _check_bwd_outputs(dQ, dK, dV, B, Hq, Hkv, N, d, dev)
+        ws_bytes = attn_bwd_workspace_size(B, Hq, Hkv, N, d)
+        if workspace is None:
+            workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
+        _check_workspace(workspace, ws_bytes, dev)
+        _call(lib.attn_bwd_dropout, Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), dO.data_ptr(), LSE.data_ptr(),
+              dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), B, Hq, Hkv, N, d, float(scale), int(bool(causal)), float(p),
+              rng.data_ptr(), workspace.data_ptr(), workspace.numel())
     return dQ, dK, dV
 
 

@@ -313,7 +313,7 @@ size_t fwd_split_workspace_bytes(int B, int Hq, int Nq, int d, int splits) {
 attn_status fwd_bf16_run(const void* Q, const void* K, const void* V, void* O, float* LSE, int B, int Hq,
                          int Hkv, int Nq, int Nk, int d, float sl2, int causal, int out_f32, int splits,
                          long long o_stride, long long lse_stride, cudaStream_t s,
-                         const uint8_t* bmask = nullptr, int bmask_heads = 1) {
+                         const uint8_t* bmask = nullptr, int bmask_heads = 1, const DropParams* drop = nullptr) {
   int* status = status_ptr();
   if (!status) return ATTN_ERR_CUDA;
   // GQA packing when the whole group fits one 128-row tile (decoding).
@@ -354,7 +354,11 @@ attn_status fwd_bf16_run(const void* Q, const void* K, const void* V, void* O, f
   p.out_f32 = out_f32;
   p.wait_limit_ns = wait_limit();
   cudaError_t e;
-  if (rows > 128 && !bmask) {
+  if (drop) {
+    p.drop = *drop;
+    p.n_items = (int)(heads * p.n_pairs * splits);
+    e = rows > 128 ? launch_fwd_persist_drop(d, tq, tk, tv, p, s) : launch_fwd_drop(d, tq, tk, tv, p, s);
+  } else if (rows > 128 && !bmask) {
     // Dense two-tile forward: persistent, one CTA per SM (its shared memory
     // and TMEM allow one) over the items.
     const int sms = sm_count();
@@ -366,6 +370,17 @@ attn_status fwd_bf16_run(const void* Q, const void* K, const void* V, void* O, f
     e = launch_fwd_bf16(d, tq, tk, tv, p, s);
   }
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// The dropout's parameters; false for a probability outside [0, 1) or that rounds to 1.
+bool drop_params(float p, const void* rng, DropParams& out, int& T) {
+  if (!(p >= 0.f) || !(p < 1.f)) return false;
+  T = (int)std::floor(256.0 * (double)p + 0.5);
+  if (T > 255) return false;
+  out.rng = static_cast<const unsigned long long*>(rng);
+  for (int k = 0; k < 8; ++k) out.not_t[k] = (T >> k) & 1 ? 0u : 0xffffffffu;
+  out.mul = 256.f / (float)(256 - T);
+  return true;
 }
 
 }  // namespace
@@ -454,6 +469,23 @@ attn_status attn_fwd_masked(const void* Q, const void* K, const void* V, void* O
                       out_dtype == ATTN_F32, 1, 0, 0, static_cast<cudaStream_t>(stream), block_mask, mask_heads);
 }
 
+attn_status attn_fwd_dropout(const void* Q, const void* K, const void* V, void* O, float* LSE, int B, int Hq, int Hkv,
+                             int N, int d, float scale, int causal, float p_drop, const uint64_t* rng,
+                             attn_dtype out_dtype, void* stream) {
+  if (!Q || !K || !V || !O || !LSE || !rng) return ATTN_ERR_INVALID_ARG;
+  if (out_dtype != ATTN_BF16 && out_dtype != ATTN_F32) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(Q, 16) || !aligned(K, 16) || !aligned(V, 16) || !aligned(O, 16) || !aligned(LSE, 4) || !aligned(rng, 8))
+    return ATTN_ERR_INVALID_ARG;
+  attn_status st = check_shape(B, Hq, Hkv, N, d, scale, causal);
+  if (st != ATTN_OK) return st;
+  DropParams drop{};
+  int T = 0;
+  if (!drop_params(p_drop, rng, drop, T)) return ATTN_ERR_INVALID_ARG;
+  // T = 0 keeps everything: the forward without dropout.
+  return fwd_bf16_run(Q, K, V, O, LSE, B, Hq, Hkv, N, N, d, scale * 1.4426950408889634f, causal, out_dtype == ATTN_F32, 1,
+                      0, 0, static_cast<cudaStream_t>(stream), nullptr, 1, T ? &drop : nullptr);
+}
+
 int attn_fp8_vt_stride(int N) { return N < 1 ? 0 : (N + 15) / 16 * 16; }
 
 attn_status attn_quantize_fp8(const void* X, void* codes, float* scales, long long BH, int N, int d,
@@ -530,7 +562,7 @@ attn_status bwd_stages(unsigned stages, const void* Q, const void* K, const void
                        const void* O, const void* dO, const float* LSE, void* dQ, void* dK,
                        void* dV, int B, int Hq, int Hkv, int N, int d, float scale, int causal,
                        attn_dtype dtype, void* workspace, size_t workspace_bytes, void* stream,
-                       const uint8_t* bmask = nullptr, int bmask_heads = 1) {
+                       const uint8_t* bmask = nullptr, int bmask_heads = 1, const DropParams* drop = nullptr) {
   if (!Q || !K || !V || !O || !dO || !LSE || !dQ || !dK || !dV || !workspace)
     return ATTN_ERR_INVALID_ARG;
   if (dtype != ATTN_BF16 && dtype != ATTN_F32) return ATTN_ERR_INVALID_ARG;
@@ -575,6 +607,7 @@ attn_status bwd_stages(unsigned stages, const void* Q, const void* K, const void
   p.Npad = Npad;
   p.bmask = bmask;
   p.bmask_heads = bmask_heads;
+  if (drop) p.drop = *drop;
   p.scale = scale;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.causal = causal;
@@ -605,6 +638,17 @@ attn_status attn_bwd_masked(const void* Q, const void* K, const void* V, const v
     return ATTN_ERR_UNSUPPORTED;
   return bwd_stages(kBwdAll, Q, K, V, O, dO, LSE, dQ, dK, dV, B, Hq, Hkv, N, d, scale, causal, ATTN_BF16,
                     workspace, workspace_bytes, stream, block_mask, mask_heads);
+}
+
+attn_status attn_bwd_dropout(const void* Q, const void* K, const void* V, const void* O, const void* dO,
+                             const float* LSE, void* dQ, void* dK, void* dV, int B, int Hq, int Hkv, int N, int d,
+                             float scale, int causal, float p_drop, const uint64_t* rng, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  DropParams drop{};
+  int T = 0;
+  if (!rng || !aligned(rng, 8) || !drop_params(p_drop, rng, drop, T)) return ATTN_ERR_INVALID_ARG;
+  return bwd_stages(kBwdAll, Q, K, V, O, dO, LSE, dQ, dK, dV, B, Hq, Hkv, N, d, scale, causal, ATTN_BF16, workspace,
+                    workspace_bytes, stream, nullptr, 1, T ? &drop : nullptr);
 }
 
 attn_status attn_bwd(const void* Q, const void* K, const void* V, const void* O,

@@ -39,10 +39,18 @@
 // Shared memory: K and V tiles, two stages of (Q tile, dO tile, LSE, D).  dS
 // for the dQ product is written over the stage's dO tile once dV (the last
 // reader of dO) has completed.
+//
+// With dropout (DROP; dropout.cuh), r_ij = 1 / (1 - T / 256) where (i, j) is kept, else 0:
+//   dV_j += p_ij r_ij dO_i,  dS_ij = p_ij (r_ij dP_ij - D_i),
+// with D_i = <dO_i, O_i> as before.  Lane l of a math warp makes the keep words of query
+// rows l and 32 + l of its warpgroup's 64 against the warp's 32 keys, and two
+// transposes of 32 x 32 bits give every key's thread its 64 bits.  dV gets the
+// factor in its epilogue.
 #include <algorithm>
 
 #include <type_traits>
 
+#include "dropout.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -221,10 +229,11 @@ __global__ void __launch_bounds__(256) bwd_dq_kernel(const BwdParams p) {
 // warpgroup, two columns per packed FMA (the workspace holds -LSE2): fp32 pairs
 // into pv2 (for dS) and bf16 pairs into pk (the dV operand).  With MASK,
 // columns c < cmin are zero (keys after the query on a diagonal tile, or a key
-// row past N); other tiles skip the per-element test.
-template <bool MASK>
+// row past N); other tiles skip the per-element test.  With DROP, bits that are clear in
+// keep clear the dV operand.
+template <bool MASK, bool DROP>
 __device__ __forceinline__ void bwd_probs(const uint32_t (&sr)[2][32], uint32_t lse_addr, float sl2, int cmin,
-                                          uint64_t (&pv2)[32], uint32_t (&pk)[32]) {
+                                          const uint32_t (&keep)[2], uint64_t (&pv2)[32], uint32_t (&pk)[32]) {
   const uint64_t sl2x2 = f2pack(sl2, sl2);
 #pragma unroll
   for (int c4 = 0; c4 < 16; ++c4) {
@@ -242,13 +251,14 @@ __device__ __forceinline__ void bwd_probs(const uint32_t (&sr)[2][32], uint32_t 
       }
       pv2[c / 2] = f2pack(p0, p1);
       pk[c / 2] = pack_bf16(p0, p1);
+      if (DROP) pk[c / 2] &= pair_mask(keep[c >> 5], c & 31);
     }
   }
 }
 
 constexpr int kDevSmemAlign = 2;  // status: dynamic shared memory not 1024-byte aligned
 
-template <int D, bool MASKED>
+template <int D, bool MASKED, bool DROP>
 __global__ void __launch_bounds__(kMainThreads, 1)
     bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
@@ -532,14 +542,23 @@ __global__ void __launch_bounds__(kMainThreads, 1)
     const uint32_t tS = tmem + lane_off + C::TM_S + 64 * h;
     const uint32_t tDP = tmem + lane_off + C::TM_DP + 64 * h;
     const float sl2 = p.scale_log2;
+    const DropKey drop_key(p.drop, DROP);
     bool ok = true;
     for (int t = 0; t < T; ++t) {
       const int s = t % C::STAGES;
       int g, it;
       tile_of(t, g, it);
       const int qh0 = it * kBQ + 64 * h;  // first query column of this half
-      const int bhq = b * p.Hq + hk * G + g;
       const uint32_t st = stage(s);
+      uint32_t keep[2];  // bit c of word w: (query column 32 w + c, this thread's key) is kept
+      if (DROP) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          uint32_t word[1];
+          keep_words(word, qh0 + 32 * w + lane, b * p.Hq + hk * G + g, k0 / 32 + quad, drop_key, p.drop);
+          keep[w] = transpose_bits(word[0], lane);
+        }
+      }
       if (!mbar_wait(bar(C::B_STFULL + s), (t / C::STAGES) & 1, wc) ||
           !mbar_wait(bar(C::B_SFULL), t & 1, wc)) {
         ok = false;
@@ -558,9 +577,9 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       // Tile-uniform test: a ragged key tile, or a causal tile that crosses the diagonal.
       if (k0 + kBK > p.N || (p.causal && qh0 < k0 + kBK - 1)) {
         const int cmin = !key_ok ? 64 : (p.causal ? max(0, key - qh0) : 0);
-        bwd_probs<true>(sr, lse_addr, sl2, cmin, pv2, pk);
+        bwd_probs<true, DROP>(sr, lse_addr, sl2, cmin, keep, pv2, pk);
       } else {
-        bwd_probs<false>(sr, lse_addr, sl2, 0, pv2, pk);
+        bwd_probs<false, DROP>(sr, lse_addr, sl2, 0, keep, pv2, pk);
       }
       tmem_st32(tS, pk);
       tmem_st_wait();
@@ -583,8 +602,17 @@ __global__ void __launch_bounds__(kMainThreads, 1)
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const int cp = 16 * half + 2 * c4 + u;  // column pair index
-            const uint64_t dp2 = f2pack(__uint_as_float(dr[4 * c4 + 2 * u]), __uint_as_float(dr[4 * c4 + 2 * u + 1]));
-            const uint64_t ds2 = fmul2(pv2[cp], fadd2(dp2, u == 0 ? f2pack(nd.x, nd.y) : f2pack(nd.z, nd.w)));
+            const int c = 4 * c4 + 2 * u;  // column of dr
+            const uint64_t nd2 = u == 0 ? f2pack(nd.x, nd.y) : f2pack(nd.z, nd.w);
+            uint64_t t2;
+            if (DROP) {
+              const float d0 = (keep[half] >> c) & 1 ? __uint_as_float(dr[c]) : 0.f;
+              const float d1 = (keep[half] >> (c + 1)) & 1 ? __uint_as_float(dr[c + 1]) : 0.f;
+              t2 = ffma2(f2pack(d0, d1), f2pack(p.drop.mul, p.drop.mul), nd2);
+            } else {
+              t2 = fadd2(f2pack(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])), nd2);
+            }
+            const uint64_t ds2 = fmul2(pv2[cp], t2);
             float d0, d1;
             f2unpack(ds2, d0, d1);
             pk[cp] = pack_bf16(d0, d1);
@@ -648,7 +676,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
         uint16_t* dst = (which == 0 ? p.dV : p.dK) + row * D;
-        const float mul = which == 0 ? 1.f : p.scale;
+        const float mul = which == 0 ? (DROP ? p.drop.mul : 1.f) : p.scale;
         const uint32_t base = tmem + lane_off + (which == 0 ? C::TM_DV : C::TM_DK);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
@@ -686,12 +714,12 @@ __global__ void __launch_bounds__(kMainThreads, 1)
   }
 }
 
-template <int D, bool MASKED>
+template <int D, bool MASKED, bool DROP>
 cudaError_t launch_main(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                         const CUtensorMap& tmdO, const CUtensorMap& tmDQ, const BwdParams& p,
                         cudaStream_t stream) {
   using C = Bwd<D, MASKED>;
-  auto kern = bwd_main_kernel<D, MASKED>;
+  auto kern = bwd_main_kernel<D, MASKED, DROP>;
   // setmaxnreg moves registers inside the launch allocation; refuse to launch
   // if the compiler gave the kernel a different per-thread count than assumed.
   static int regs = -1;  // one per instantiation
@@ -724,8 +752,9 @@ cudaError_t launch(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtenso
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if (stages & kBwdMain) {
-    e = p.bmask ? launch_main<D, true>(tmQ, tmK, tmV, tmdO, tmDQ, p, stream)
-                : launch_main<D, false>(tmQ, tmK, tmV, tmdO, tmDQ, p, stream);
+    e = p.bmask      ? launch_main<D, true, false>(tmQ, tmK, tmV, tmdO, tmDQ, p, stream)
+        : p.drop.rng ? launch_main<D, false, true>(tmQ, tmK, tmV, tmdO, tmDQ, p, stream)
+                     : launch_main<D, false, false>(tmQ, tmK, tmV, tmdO, tmDQ, p, stream);
     if (e != cudaSuccess) return e;
   }
   if (stages & kBwdConvert) {

@@ -31,6 +31,13 @@
 // Every phase counter (ring slots, S buffer, P and O hand-offs) runs on
 // across items.  The counter pair of the launch is reset by the last CTA to
 // finish, so the next launch on the same counter starts at zero.
+//
+// With dropout (DROP; dropout.cuh) a softmax warp makes its rows' keep words of a tile
+// before it waits for the tile's scores, sums the row as without, and clears
+// the dropped elements in P as it is packed; 1 / (1 - T / 256) goes into 1 / l.  Items are
+// handed out by cluster launch control instead of the counters: a launch that shares
+// no memory with another, so that captured graphs may run side by side.
+#include "dropout.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -69,14 +76,16 @@ struct FwdP {
   static constexpr int B_ITFULL = B_ODONE + 2;        // IR: ring entry written
   static constexpr int B_ITEMPTY = B_ITFULL + IR;     // IR: ring entry read by every consumer warp
   static constexpr int B_DRAIN = B_ITEMPTY + IR;     // 2: one per issuing warp
-  static constexpr int NBARS = B_DRAIN + 2;
+  static constexpr int B_CLC = B_DRAIN + 2;          // dropout: the answer to a request for an item
+  static constexpr int NBARS = B_CLC + 1;
   static constexpr int OFF_TMEMSLOT = OFF_BAR + NBARS * 8;
   static constexpr int OFF_ABORT = OFF_TMEMSLOT + 4;
   static constexpr int OFF_RING = OFF_ABORT + 4;
   static constexpr int RING_INTS = 8;                  // one decoded item per entry
   // Epilogue staging: per softmax warp, its 32 rows x 64 columns of bf16 O.
   static constexpr int EPI_WARP_BYTES = 32 * 128;
-  static constexpr int OFF_EPI = (OFF_RING + 4 * RING_INTS * IR + 127) / 128 * 128;
+  static constexpr int OFF_CLC = (OFF_RING + 4 * RING_INTS * IR + 15) / 16 * 16;  // 16 bytes
+  static constexpr int OFF_EPI = (OFF_CLC + 16 + 127) / 128 * 128;
   static constexpr int SMEM_BYTES = OFF_EPI + 8 * EPI_WARP_BYTES + 1024;  // + alignment slack
   static_assert(SMEM_BYTES <= 232448, "exceeds the 227 KB of shared memory per block");
   static constexpr int CONSUMER_WARPS = 2 + 8;  // the two MMA warps and the softmax warps
@@ -118,7 +127,7 @@ __device__ __forceinline__ FwdItem fwd_item(int k, const FwdParams& p) {
   return w;
 }
 
-template <int D>
+template <int D, bool DROP>
 __global__ void __launch_bounds__(kThreads, 1)
     fwd_persist_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const FwdParams p) {
@@ -156,6 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(C::B_SREAD + t), 4);  // one arrival per softmax warp of tile t
       mbar_init(bar(C::B_DRAIN + t), 1);
     }
+    if (DROP) mbar_init(bar(C::B_CLC), 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -222,8 +232,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int it = 0; ok; ++it) {
         const int r = it % C::IR;
         if (it >= C::IR && !mbar_wait(bar(C::B_ITEMPTY + r), ((it / C::IR) - 1) & 1, wc)) break;
-        int k = (int)atomicAdd(p.sched, 1u);
-        if (k >= p.n_items) k = -1;
+        int k;
+        if constexpr (DROP) {
+          k = blockIdx.x;
+          if (it > 0) {
+            // (The fence orders the last answer's read before this one's write.)
+            fence_async_smem();
+            mbar_arrive_expect_tx(bar(C::B_CLC), 16);
+            clc_request(sb + C::OFF_CLC, bar(C::B_CLC));
+            if (!mbar_wait(bar(C::B_CLC), (it - 1) & 1, wc)) {
+              mbar_wait_drain(bar(C::B_CLC), (it - 1) & 1, wc);  // the answer must land before the CTA may exit
+              break;
+            }
+            k = clc_answer(sb + C::OFF_CLC);
+          }
+        } else {
+          k = (int)atomicAdd(p.sched, 1u);
+          if (k >= p.n_items) k = -1;
+        }
         volatile int* e = entry(it);
         const FwdItem w = fwd_item(k < 0 ? 0 : k, p);
         e[R_K] = k;
@@ -382,6 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // sg - 2 (after the increment below), in the epilogue sg - 1.
     int sg = 0;
     bool ok = true;
+    DropKey drop_key(p.drop, DROP);
     for (int it = 0; ok; ++it) {
       if (!wait_item(it)) break;
       volatile int* e = entry(it);
@@ -399,6 +426,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float corr = 0.f;
       for (int j = 0; j < n; ++j) {
         const int k0 = (e[R_KT0] + j) * kBN;
+        uint32_t keep[4];
+        if (DROP) keep_words(keep, q, e[R_BH], k0 / 32, drop_key, p.drop);
         if (!mbar_wait_warp(bar(C::B_SFULL + t), sg & 1, wc)) {
           ok = false;
           break;
@@ -462,6 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float p1 = ex2(x1);
             rs2[i & 3] = fadd2(rs2[i & 3], f2pack(p0, p1));
             wv[c >> 1][(c & 1) * 16 + i] = pack_bf16(p0, p1);
+            if (DROP) wv[c >> 1][(c & 1) * 16 + i] &= pair_mask(keep[c], 2 * i);
           }
         {
           float a0, a1;
@@ -509,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* const o_out = p.out_f32 ? static_cast<float*>(p.O) + split * p.o_split_stride : nullptr;
       uint16_t* const o_out16 = p.out_f32 ? nullptr : static_cast<uint16_t*>(p.O);
       const float lo = l - corr;
-      const float inv_l = lo > 0.f ? 1.f / lo : 0.f;
+      const float inv_l = lo > 0.f ? (DROP ? p.drop.mul : 1.f) / lo : 0.f;
       const int bh = e[R_BH];
       const bool bh_ok = dcheck(bh >= 0 && bh < p.heads && split >= 0 && split < p.n_splits, p.status);
       const bool valid = q < p.rows && bh_ok;
@@ -556,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
-  if (threadIdx.x == 0) {
+  if (!DROP && threadIdx.x == 0) {
     // Every item grab of this CTA happened before the barrier above.  The
     // last CTA to get here resets the counter pair for the next launch.
     __threadfence();
@@ -567,11 +597,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D>
+template <int D, bool DROP>
 cudaError_t launch_persist(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                            const FwdParams& p, int ctas, cudaStream_t stream) {
   using C = FwdP<D>;
-  auto kern = fwd_persist_kernel<D>;
+  auto kern = fwd_persist_kernel<D, DROP>;
   static int regs = -1;  // one per instantiation
   if (regs < 0) {
     cudaFuncAttributes fa;
@@ -590,8 +620,15 @@ cudaError_t launch_persist(const CUtensorMap& tmQ, const CUtensorMap& tmK, const
 
 cudaError_t launch_fwd_persist(int d, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                const FwdParams& p, int ctas, cudaStream_t stream) {
-  if (d == 128) return launch_persist<128>(tmQ, tmK, tmV, p, ctas, stream);
-  if (d == 64) return launch_persist<64>(tmQ, tmK, tmV, p, ctas, stream);
+  if (d == 128) return launch_persist<128, false>(tmQ, tmK, tmV, p, ctas, stream);
+  if (d == 64) return launch_persist<64, false>(tmQ, tmK, tmV, p, ctas, stream);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_fwd_persist_drop(int d, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                    const FwdParams& p, cudaStream_t stream) {
+  if (d == 128) return launch_persist<128, true>(tmQ, tmK, tmV, p, p.n_items, stream);
+  if (d == 64) return launch_persist<64, true>(tmQ, tmK, tmV, p, p.n_items, stream);
   return cudaErrorInvalidValue;
 }
 

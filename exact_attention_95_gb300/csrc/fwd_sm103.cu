@@ -36,6 +36,7 @@
 // TMEM columns: [0,128) S, [128,192) P_0, [192,256) P_1, then O_0, O_1.
 // Registers: warpgroup 0 gives registers to the two softmax warpgroups
 // (setmaxnreg), which hold a whole S row each.
+#include "dropout.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -89,8 +90,9 @@ struct Fwd {
 
 // ONE: every CTA computes query tile 0 only (N <= 128: decoding and short
 // sequences), with its own MMA schedule; otherwise both tiles (a last pair
-// whose second tile has no row below N still computes it, on zero rows).
-template <int D, bool ONE, bool MASKED>
+// whose second tile has no row below N still computes it, on zero rows).  DROP:
+// dropout, as in fwd_persist.cu.
+template <int D, bool ONE, bool MASKED, bool DROP>
 __global__ void __launch_bounds__(kThreads, 1)
     fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const FwdParams p) {
@@ -346,9 +348,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     float corr = 0.f;     // sum over tiles of (largest P - its bf16 rounding), same scale as l
     bool ok = true;
     const bool active = t == 0 || two;  // tile 1 of a one-tile CTA has no rows
+    const DropKey drop_key(p.drop, DROP);
+    const int drop_head = p.packed ? bh * (p.Hq / p.Hkv) + q / p.N : bh;  // b * Hq + the row's query head
     for (int j = 0; j < (active ? n_kv : 0); ++j) {
       const int k0 = ktile(j) * kBN;
       const bool on = !masked || ((tlist[j] >> (15 - t)) & 1);  // this tile keeps the block
+      uint32_t keep[4];
+      if (DROP) keep_words(keep, qc, drop_head, k0 / 32, drop_key, p.drop);
       if (!mbar_wait(bar(C::B_SFULL + t), j & 1, wc)) {
         ok = false;
         break;
@@ -418,6 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float p1 = ex2(x1);
           rs2[i & 3] = fadd2(rs2[i & 3], f2pack(p0, p1));
           w[c >> 1][(c & 1) * 16 + i] = pack_bf16(p0, p1);
+          if (DROP) w[c >> 1][(c & 1) * 16 + i] &= pair_mask(keep[c], 2 * i);
         }
       {
         float a0, a1;
@@ -467,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // P: when one key dominates a row, its bf16 rounding then cancels
       // between O and the divisor.  LSE uses the exact sum.
       const float lo = l - corr;
-      const float inv_l = lo > 0.f ? 1.f / lo : 0.f;
+      const float inv_l = lo > 0.f ? (DROP ? p.drop.mul : 1.f) / lo : 0.f;
       const bool split_ok = dcheck(split < p.n_splits, p.status);
       const bool valid = q < p.rows && split_ok;
       const size_t row_idx = (size_t)bh * p.rows + q;
@@ -513,11 +520,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool ONE, bool MASKED>
+template <int D, bool ONE, bool MASKED, bool DROP = false>
 cudaError_t launch_one(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                        const FwdParams& p, cudaStream_t stream) {
   using C = Fwd<D, ONE>;
-  auto kern = fwd_bf16_kernel<D, ONE, MASKED>;
+  auto kern = fwd_bf16_kernel<D, ONE, MASKED, DROP>;
   // setmaxnreg moves registers inside the launch allocation; refuse to launch
   // if the compiler gave the kernel a different per-thread count than assumed
   // (a larger split than the allocation would leave setmaxnreg.inc waiting).
@@ -556,6 +563,14 @@ cudaError_t launch_fwd_bf16(int d, const CUtensorMap& tmQ, const CUtensorMap& tm
     return one ? (m ? launch_one<64, true, true>(tmQ, tmK, tmV, p, stream)
                     : launch_one<64, true, false>(tmQ, tmK, tmV, p, stream))
                : launch_one<64, false, true>(tmQ, tmK, tmV, p, stream);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_fwd_drop(int d, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                            const FwdParams& p, cudaStream_t stream) {
+  if (p.rows > kBM || p.bmask) return cudaErrorInvalidValue;
+  if (d == 128) return launch_one<128, true, false, true>(tmQ, tmK, tmV, p, stream);
+  if (d == 64) return launch_one<64, true, false, true>(tmQ, tmK, tmV, p, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -8,6 +8,13 @@
 
 namespace attn {
 
+// Dropout on the softmax (dropout.cuh).
+struct DropParams {
+  const unsigned long long* rng;  // seed, offset; in device memory
+  uint32_t not_t[8];              // all ones where that bit of T = round(256 p) is clear
+  float mul;                      // 1 / (1 - T / 256)
+};
+
 struct FwdParams {
   void* O;          // [B, Hq, N, d] bf16 or fp32
   float* LSE;       // [B, Hq, N] natural-log units
@@ -41,6 +48,7 @@ struct FwdParams {
   // at launch and reset to 0 by the last CTA.
   unsigned* sched;
   int n_items;
+  DropParams drop;  // launches with dropout
 };
 
 // Counter pair for a persistent launch on `stream`: each stream has its own
@@ -53,11 +61,18 @@ unsigned* sched_counter_pair(cudaStream_t stream);
 // box and 128-byte swizzle.
 cudaError_t launch_fwd_bf16(int d, const CUtensorMap& tmQ, const CUtensorMap& tmK,
                             const CUtensorMap& tmV, const FwdParams& p, cudaStream_t stream);
+// The same with dropout (no block mask).
+cudaError_t launch_fwd_drop(int d, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                            const FwdParams& p, cudaStream_t stream);
 size_t fwd_bf16_smem_bytes(int d);
 // Persistent form of the dense two-tile forward (rows > 128, no block mask):
 // `ctas` CTAs (at most one per SM) walk the p.n_items work items.
 cudaError_t launch_fwd_persist(int d, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                const FwdParams& p, int ctas, cudaStream_t stream);
+// The same with dropout: a CTA an item, of which running CTAs take those not yet
+// started (no counters: p.sched is not used).
+cudaError_t launch_fwd_persist_drop(int d, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                    const FwdParams& p, cudaStream_t stream);
 constexpr int kMaxMaskTiles = 2048;  // key tiles a block-sparse forward may list per CTA
 
 // Merge of a split forward's partial results: Opart [n_splits][rows][d] fp32
@@ -120,6 +135,7 @@ struct BwdParams {
   // Block-sparse mask (NULL: dense), as FwdParams::bmask with Nk = N.
   const uint8_t* bmask;
   int bmask_heads;
+  DropParams drop;  // drop.rng NULL: no dropout (with a block mask there is none)
 };
 constexpr int kMaxMaskIters = 4096;  // (query head, query tile) pairs a masked backward CTA may list
 

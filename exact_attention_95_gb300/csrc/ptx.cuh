@@ -546,3 +546,31 @@ __device__ __forceinline__ void bulk_wait_read1() {
 }
 
 }  // namespace attn
+
+namespace attn {
+
+// Cluster launch control: a running CTA takes over the block index of one of the
+// same grid that has not been started.  The request writes 16 bytes to `dst`
+// and completes them on `bar`; after one that came back without an index
+// none may follow.
+__device__ __forceinline__ void clc_request(uint32_t dst, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+               "r"(bar)
+               : "memory");
+}
+// The block index (x) that a request got, or -1.
+__device__ __forceinline__ int clc_answer(uint32_t src) {
+  int x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 h, [%1];\n\t"
+      "mov.b32 %0, -1;\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n\t}\n"
+      : "=r"(x)
+      : "r"(src)
+      : "memory");
+  return x;
+}
+
+}  // namespace attn

@@ -258,6 +258,40 @@ attn_status attn_bwd_noalloc(const void* Q, const void* K, const void* V, const 
                              int B, int Hq, int Hkv, int N, int d, float scale, int causal,
                              attn_dtype dtype, void* stream);
 
+/*
+ * Attention with dropout on the softmax, for training; the mask is never stored.  With
+ * T = round(256 * p_drop) (halves up; p_drop in [0, 1), and below 1 - 2^-9, so that T <= 255),
+ * element (b, h, i, j) of the softmax is kept where u(b, h, i, j) >= T, else it is 0,
+ * and what is kept is multiplied by 1 / (1 - T / 256): the probability is p_drop rounded
+ * to a multiple of 1/256, and the mean is exact for the rounded one.
+ *   O_i = sum_j softmax_j(s_i) keep_ij / (1 - T / 256) v_j;   LSE is that without dropout.
+ * u is a number of eight bits.  For the keys 32 g .. 32 g + 31 of a row, bit k of u is bit j % 32 of
+ * word k of eight: four that Philox4x32 with seven rounds ("Parallel random numbers: as
+ * easy as 1, 2, 3") gives for the counter (i, 2 g, b * Hq + h, offset), four for (i, 2 g + 1,
+ * b * Hq + h, offset), the key being the seed's low and high 32 bits.
+ *   rng [2] in device memory, 8-byte aligned: seed, offset (its low 32 bits count).  Read when the
+ *       kernels run, so a captured step follows new numbers; the backward has to
+ *       be given the numbers of its forward, and calls that are to differ other offsets.
+ *   Q, K, V bf16; the other arguments and rules are attn_fwd's.  A row whose kept keys are all
+ *   dropped gets O = 0.  Captured calls may be replayed side by side: no launch shares
+ *   memory of the library with another.
+ * With T = 0 the calls are attn_fwd and attn_bwd (whose rules on captured graphs then hold).
+ */
+attn_status attn_fwd_dropout(const void* Q, const void* K, const void* V, void* O, float* LSE, int B, int Hq, int Hkv,
+                             int N, int d, float scale, int causal, float p_drop, const uint64_t* rng,
+                             attn_dtype out_dtype, void* stream);
+
+/*
+ * Its backward: attn_bwd's gradient with r_ij = keep_ij / (1 - T / 256):
+ *   dV_j = sum p_ij r_ij dO_i,  dS_ij = p_ij (r_ij <dO_i, v_j> - D_i),  D_i = <dO_i, O_i>,
+ * dQ and dK from dS as there.  O and LSE are attn_fwd_dropout's for the same numbers.
+ * Workspace (attn_bwd_workspace_size) and other arguments as attn_bwd.
+ */
+attn_status attn_bwd_dropout(const void* Q, const void* K, const void* V, const void* O, const void* dO,
+                             const float* LSE, void* dQ, void* dK, void* dV, int B, int Hq, int Hkv, int N, int d,
+                             float scale, int causal, float p_drop, const uint64_t* rng, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
 /* Bytes of workspace attn_bwd needs: an fp32 dQ accumulator and two fp32
  * per-row vectors (D = rowsum(dO * O) and LSE in log2 units).  0 on bad sizes. */
 size_t attn_bwd_workspace_size(int B, int Hq, int Hkv, int N, int d);
