@@ -187,7 +187,8 @@ def _bound():
                 module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
                     lib.attn_kv_tables, lib.attn_kv_append_fp8, lib.attn_fwd_paged_fp8,
                     lib.attn_fwd_paged_workspace_size, lib.attn_rope, lib.attn_rope_bwd,
-                    lib.attn_kv_append_rope_fp8)))
+                    lib.attn_kv_append_rope_fp8, lib.attn_fwd_dropout, lib.attn_bwd_dropout,
+                    lib.attn_bwd_workspace_size)))
                 _fast = module
             except ImportError as e:
                 _fast = False
@@ -870,14 +871,19 @@ def attn_fwd_dropout(Q, K, V, p, rng, scale=None, causal=False, out_dtype=None, 
     rng int64 [2] on the device: seed, and an offset (its low 32 bits count) that tells calls of
     one seed apart; read when the kernels run.  The mask follows from them and is
     never stored; LSE is that without dropout."""
+    bf = torch.bfloat16
+    out_dtype = bf if out_dtype is None else out_dtype
+    out_dt = {torch.bfloat16: ATTN_BF16, torch.float32: ATTN_F32}[out_dtype]
+    fast = stream is None and _bound()
+    if fast:
+        r = fast.fwd_dropout(Q, K, V, p, rng, scale, causal, out_dt, O, LSE)
+        if r is not None:
+            return _result(r, "attn_fwd_dropout")
     lib = load_library()
     B, Hq, N, d = Q.shape
     Hkv = K.shape[1]
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    bf = torch.bfloat16
-    out_dtype = bf if out_dtype is None else out_dtype
-    out_dt = {torch.bfloat16: ATTN_BF16, torch.float32: ATTN_F32}[out_dtype]
     _check_tensor("Q", Q, bf, (B, Hq, N, d))
     dev = Q.device
     _check_tensor("K", K, bf, (B, Hkv, N, d), dev)
@@ -896,6 +902,11 @@ def attn_fwd_dropout(Q, K, V, p, rng, scale=None, causal=False, out_dtype=None, 
 def attn_bwd_dropout(Q, K, V, O, dO, LSE, p, rng, scale=None, causal=False, dQ=None, dK=None, dV=None, workspace=None,
                      stream=None):
     """dQ, dK, dV of attn_fwd_dropout's O, given dO and the forward's O, LSE, p and numbers in rng."""
+    fast = stream is None and _bound()
+    if fast:
+        r = fast.bwd_dropout(Q, K, V, O, dO, LSE, p, rng, scale, causal, dQ, dK, dV, workspace)
+        if r is not None:
+            return _result(r, "attn_bwd_dropout")
     lib = load_library()
     B, Hq, Hkv, N, d, dev = _bwd_inputs(Q, K, V, O, dO, LSE)
     if scale is None:

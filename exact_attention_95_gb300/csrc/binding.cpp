@@ -1,5 +1,5 @@
-// binding.cpp -- the Python calls of the paged 8-bit cache and of rotary positions
-// without Python's share of the work.
+// binding.cpp -- the Python calls of the paged 8-bit cache, of rotary positions and of
+// attention with dropout without Python's share of the work.
 //
 // A decoding step makes these calls once a layer around kernels of a few
 // microseconds; checks, allocations and pointer passing in Python take three
@@ -33,6 +33,9 @@ decltype(&attn_fwd_paged_fp8) g_fwd = nullptr;
 decltype(&attn_fwd_paged_workspace_size) g_workspace = nullptr;
 decltype(&attn_rope) g_rope[2] = {nullptr, nullptr};  // forward, gradient
 decltype(&attn_kv_append_rope_fp8) g_append_rope = nullptr;
+decltype(&attn_fwd_dropout) g_fwd_dropout = nullptr;
+decltype(&attn_bwd_dropout) g_bwd_dropout = nullptr;
+decltype(&attn_bwd_workspace_size) g_bwd_workspace = nullptr;
 
 // The tensor of an argument, or null.
 const at::Tensor* tensor(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
@@ -216,6 +219,12 @@ PyObject* kv_append_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return PyTuple_Pack(4, a[3], a[4], a[5], a[6]);)
 }
 
+// The softmax scale: a number, or None for 1 / sqrt(d); false with Python's error set.
+bool scale_of(PyObject* o, int64_t d, double& scale) {
+  scale = o == Py_None ? 1.0 / std::sqrt((double)d) : PyFloat_AsDouble(o);
+  return o == Py_None || !PyErr_Occurred();
+}
+
 // Q, k_pages, k_scale, v_pages, v_scale, block_table, cu_q, kv_lens, scale, causal, fp32 output, O, LSE, workspace
 PyObject* fwd_paged_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   ATTN_GUARD(
@@ -231,12 +240,7 @@ PyObject* fwd_paged_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
         !is(cu, at::kInt, {R + 1}, dev) || !is(lens, at::kInt, {R}, dev))
       Py_RETURN_NONE;
     double scale = 0;
-    if (a[8] == Py_None) {
-      scale = 1.0 / std::sqrt((double)c.d);
-    } else {
-      scale = PyFloat_AsDouble(a[8]);
-      if (PyErr_Occurred()) return nullptr;
-    }
+    if (!scale_of(a[8], c.d, scale)) return nullptr;
     const int causal = PyObject_IsTrue(a[9]), f32 = PyObject_IsTrue(a[10]);
     if (causal < 0 || f32 < 0) return nullptr;
     const OnDevice on(dev);
@@ -287,7 +291,7 @@ bool rows_out(PyObject* o, at::Tensor& t, at::ScalarType type, at::IntArrayRef s
     return false;
   return rows_of(&t, type, shape, device, r);
 }
-bool amplitude_of(PyObject* o, float& v) {
+bool float_of(PyObject* o, float& v) {
   if (!PyFloat_Check(o)) return false;
   v = (float)PyFloat_AS_DOUBLE(o);
   return true;
@@ -311,7 +315,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     attn_rows q, k{}, qo, ko{};
     const int64_t three[3] = {N, Hkv, d}, four[4] = {B, Hkv, N, d};
     const at::IntArrayRef k_shape = tokens ? at::IntArrayRef(three, 3) : at::IntArrayRef(four, 4);
-    if (!fits(B) || !fits(N) || !fits(Hq) || !fits(Hkv) || !fits(d) || (K && Hkv == 0) || !amplitude_of(a[6], amplitude) ||
+    if (!fits(B) || !fits(N) || !fits(Hq) || !fits(Hkv) || !fits(d) || (K && Hkv == 0) || !float_of(a[6], amplitude) ||
         !rows_of(Q, type, Q->sizes(), dev, q) || (K && !rows_of(K, type, k_shape, dev, k)) || !freqs ||
         freqs->dim() != 1 || freqs->size(0) < 1 || 2 * freqs->size(0) > d || !is(freqs, at::kLong, freqs->sizes(), dev))
       Py_RETURN_NONE;
@@ -346,7 +350,7 @@ PyObject* kv_append_rope_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor* freqs = tensor(a[5]);
     Cache c;
     float amplitude = 1;
-    if (!Q || Q->dim() != 3 || !K || !K->is_cuda() || !c.read(a + 6, K->device()) || !amplitude_of(a[11], amplitude))
+    if (!Q || Q->dim() != 3 || !K || !K->is_cuda() || !c.read(a + 6, K->device()) || !float_of(a[11], amplitude))
       Py_RETURN_NONE;
     const at::Device dev = K->device();
     const int64_t T = K->size(0), Hq = Q->size(1);
@@ -378,12 +382,98 @@ PyObject* kv_append_rope_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return wrap(a[12], Qo);)
 }
 
+// Sizes of Q [B, Hq, N, d] and K [B, Hkv, N, d].
+struct Heads {
+  int64_t B, Hq, Hkv, N, d;
+  at::Device dev = at::kCPU;
+  // Q, K and V (bf16, contiguous) and the generator's state.
+  bool read(const at::Tensor* Q, const at::Tensor* K, const at::Tensor* V, const at::Tensor* rng) {
+    if (!Q || !Q->is_cuda() || Q->dim() != 4 || !K || K->dim() != 4) return false;
+    B = Q->size(0);
+    Hq = Q->size(1);
+    N = Q->size(2);
+    d = Q->size(3);
+    Hkv = K->size(1);
+    dev = Q->device();
+    return fits(B) && fits(Hq) && fits(Hkv) && fits(N) && fits(d) && q(Q) && kv(K) && kv(V) && is(rng, at::kLong, {2}, dev);
+  }
+  bool q(const at::Tensor* t) const { return is(t, at::kBFloat16, {B, Hq, N, d}, dev); }
+  bool kv(const at::Tensor* t) const { return is(t, at::kBFloat16, {B, Hkv, N, d}, dev); }
+};
+
+// Q, K, V, p, rng, scale, causal, fp32 output, O, LSE
+PyObject* fwd_dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  ATTN_GUARD(
+    if (n != 10) Py_RETURN_NONE;
+    const at::Tensor *Q = tensor(a[0]), *K = tensor(a[1]), *V = tensor(a[2]), *rng = tensor(a[4]);
+    Heads s;
+    float p = 0;
+    double scale = 0;
+    if (!s.read(Q, K, V, rng) || !float_of(a[3], p)) Py_RETURN_NONE;
+    if (!scale_of(a[5], s.d, scale)) return nullptr;
+    const int causal = PyObject_IsTrue(a[6]), f32 = PyObject_IsTrue(a[7]);
+    if (causal < 0 || f32 < 0) return nullptr;
+    const OnDevice on(s.dev);
+    at::Tensor O, LSE;
+    if (!output(a[8], O, f32 ? at::kFloat : at::kBFloat16, Q->sizes(), s.dev) ||
+        !output(a[9], LSE, at::kFloat, {s.B, s.Hq, s.N}, s.dev))
+      Py_RETURN_NONE;
+    const int rc = without_lock(s.dev, [&](void* stream) {
+      return g_fwd_dropout(Q->data_ptr(), K->data_ptr(), V->data_ptr(), O.data_ptr(), (float*)LSE.data_ptr(), (int)s.B,
+                           (int)s.Hq, (int)s.Hkv, (int)s.N, (int)s.d, (float)scale, causal, p,
+                           (const uint64_t*)rng->data_ptr(), f32 ? ATTN_F32 : ATTN_BF16, stream);
+    });
+    if (rc != ATTN_OK) return PyLong_FromLong(rc);
+    return tuple(wrap(a[8], O), wrap(a[9], LSE));)
+}
+
+// Q, K, V, O, dO, LSE, p, rng, scale, causal, dQ, dK, dV, workspace
+PyObject* bwd_dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  ATTN_GUARD(
+    if (n != 14) Py_RETURN_NONE;
+    const at::Tensor *Q = tensor(a[0]), *K = tensor(a[1]), *V = tensor(a[2]), *O = tensor(a[3]), *dO = tensor(a[4]);
+    const at::Tensor *LSE = tensor(a[5]), *rng = tensor(a[7]);
+    Heads s;
+    float p = 0;
+    double scale = 0;
+    if (!s.read(Q, K, V, rng) || !s.q(O) || !s.q(dO) || !is(LSE, at::kFloat, {s.B, s.Hq, s.N}, s.dev) ||
+        !float_of(a[6], p))
+      Py_RETURN_NONE;
+    if (!scale_of(a[8], s.d, scale)) return nullptr;
+    const int causal = PyObject_IsTrue(a[9]);
+    if (causal < 0) return nullptr;
+    const OnDevice on(s.dev);
+    at::Tensor dQ, dK, dV;
+    if (!output(a[10], dQ, at::kBFloat16, Q->sizes(), s.dev) || !output(a[11], dK, at::kBFloat16, K->sizes(), s.dev) ||
+        !output(a[12], dV, at::kBFloat16, K->sizes(), s.dev))
+      Py_RETURN_NONE;
+    size_t bytes = g_bwd_workspace((int)s.B, (int)s.Hq, (int)s.Hkv, (int)s.N, (int)s.d);
+    c10::DataPtr own;  // freed at the end of this call, for later work of the same stream
+    void* ws = nullptr;
+    if (a[13] == Py_None) {
+      own = c10::cuda::CUDACachingAllocator::get()->allocate(bytes);
+      ws = own.get();
+    } else {
+      const at::Tensor* given = tensor(a[13]);
+      if (!given || !is(given, at::kByte, given->sizes(), s.dev) || (size_t)given->numel() < bytes) Py_RETURN_NONE;
+      ws = given->data_ptr();
+    }
+    const int rc = without_lock(s.dev, [&](void* stream) {
+      return g_bwd_dropout(Q->data_ptr(), K->data_ptr(), V->data_ptr(), O->data_ptr(), dO->data_ptr(),
+                           (const float*)LSE->data_ptr(), dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), (int)s.B, (int)s.Hq,
+                           (int)s.Hkv, (int)s.N, (int)s.d, (float)scale, causal, p, (const uint64_t*)rng->data_ptr(), ws,
+                           bytes, stream);
+    });
+    if (rc != ATTN_OK) return PyLong_FromLong(rc);
+    return tuple(wrap(a[10], dQ), wrap(a[11], dK), wrap(a[12], dV));)
+}
+
 // bind(addresses of attn_kv_tables, attn_kv_append_fp8, attn_fwd_paged_fp8, attn_fwd_paged_workspace_size, attn_rope,
-// attn_rope_bwd, attn_kv_append_rope_fp8)
+// attn_rope_bwd, attn_kv_append_rope_fp8, attn_fwd_dropout, attn_bwd_dropout, attn_bwd_workspace_size)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  constexpr int kAddresses = 7;
+  constexpr int kAddresses = 10;
   if (n != kAddresses) {
-    PyErr_SetString(PyExc_TypeError, "bind takes seven addresses");
+    PyErr_SetString(PyExc_TypeError, "bind takes ten addresses");
     return nullptr;
   }
   void* p[kAddresses];
@@ -398,6 +488,9 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_rope[0] = reinterpret_cast<decltype(&attn_rope)>(p[4]);
   g_rope[1] = reinterpret_cast<decltype(&attn_rope)>(p[5]);
   g_append_rope = reinterpret_cast<decltype(g_append_rope)>(p[6]);
+  g_fwd_dropout = reinterpret_cast<decltype(g_fwd_dropout)>(p[7]);
+  g_bwd_dropout = reinterpret_cast<decltype(g_bwd_dropout)>(p[8]);
+  g_bwd_workspace = reinterpret_cast<decltype(g_bwd_workspace)>(p[9]);
   Py_RETURN_NONE;
 }
 
@@ -407,7 +500,8 @@ PyMethodDef method(const char* name) {
 }
 PyMethodDef g_methods[] = {method<kv_tables>("kv_tables"), method<kv_append_fp8>("kv_append_fp8"),
                            method<fwd_paged_fp8>("fwd_paged_fp8"), method<rope>("rope"),
-                           method<kv_append_rope_fp8>("kv_append_rope_fp8"), method<bind>("bind"),
+                           method<kv_append_rope_fp8>("kv_append_rope_fp8"), method<fwd_dropout>("fwd_dropout"),
+                           method<bwd_dropout>("bwd_dropout"), method<bind>("bind"),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods};
 

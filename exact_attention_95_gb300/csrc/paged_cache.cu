@@ -590,18 +590,19 @@ __global__ void __launch_bounds__(kAppThreads, 4) kv_append_kernel(const KvAppen
   append_chunk<D, Turn::kNone>(p, Turning{}, chunk, pairs, blockIdx.x, blockIdx.y);
 }
 
-// The first `appends` CTAs append, the others rotate the queries.
+// `appends` CTAs append, the others rotate the queries; the two kinds are spread evenly
+// over the grid, as the one is held by its arithmetic and the other by memory.
 template <int D, Turn TURN>
 __global__ void __launch_bounds__(kAppThreads, 2)
     kv_append_rope_kernel(const KvAppendParams p, const RopeParams q, int chunk, int pairs, int chunks, int appends,
                           int groups, int heads) {
   static_assert(kAppThreads == kRopeThreads, "one block size for both kinds of CTA");
   griddep_wait();
-  const int i = blockIdx.x;
-  if (i < appends) {
+  const unsigned i = (unsigned)((uint64_t)blockIdx.x * appends / gridDim.x);  // appends among the CTAs before this one
+  if (i != (unsigned)((uint64_t)(blockIdx.x + 1) * appends / gridDim.x)) {
     append_chunk<D, TURN>(p, Turning{q.positions, q.freqs, q.amplitude, q.rot}, chunk, pairs, i % chunks, i / chunks);
   } else {
-    const int k = i - appends;
+    const int k = blockIdx.x - i;
     rope_block<uint16_t, D, TURN == Turn::kPairs>(q, k % groups, k / groups * heads, heads);
   }
 }

@@ -304,7 +304,10 @@ def test_graphs_replayed_side_by_side_follow_their_numbers():
 
 
 @gpu
-def test_what_python_refuses():
+@pytest.mark.parametrize("module", [True, False])
+def test_what_python_refuses(module, monkeypatch):
+    if not module:
+        monkeypatch.setattr(pkg, "_fast", False)
     Q, K, V, dO = _make(1, 1, 2, 2, 8, 64)
     L = torch.zeros(1, 2, 8, device="cuda")
     for exc, rng, p, kw in [
@@ -324,6 +327,25 @@ def test_what_python_refuses():
     with pytest.raises(ValueError):
         pkg.attn_bwd_dropout(Q, K, V, Q, dO, L, 0.1, _rng(), workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     ok()
+
+
+@gpu
+@pytest.mark.parametrize("N", [40, 300])
+def test_the_calls_give_the_same_without_the_module(N, monkeypatch):
+    Q, K, V, dO = _make(N, 2, 6, 2, N, 64)
+    ws = torch.empty(pkg.attn_bwd_workspace_size(2, 6, 2, N, 64), dtype=torch.uint8, device="cuda")
+    got = []
+    for module in (True, False):
+        if not module:
+            monkeypatch.setattr(pkg, "_fast", False)
+        given = torch.empty_like(Q)
+        O, L = pkg.attn_fwd_dropout(Q, K, V, 0.3, _rng(), 0.2, True, O=given)
+        O32, _ = pkg.attn_fwd_dropout(Q, K, V, 0.3, _rng(), None, False, torch.float32)
+        _, dK, dV = pkg.attn_bwd_dropout(Q, K, V, O, dO, L, 0.3, _rng(), 0.2, True, workspace=ws)
+        assert O is given
+        got.append((O, L, O32, dK, dV))
+    ok()
+    assert all(torch.equal(a, b) for a, b in zip(*got))
 
 
 # ------------------------------------------------------------------ a layer's step
