@@ -210,7 +210,7 @@ struct RopeParams {
   int* status;  // (debug builds' checks)
 };
 cudaError_t launch_rope(int d, int f32, const RopeParams& p, int interleaved, int sms, cudaStream_t stream);
-int rope_heads(long long groups, int all, int sms);
+int rope_heads(long long groups, int all, long long ctas);
 
 // Append with the keys rotated, and the queries of the same tokens (p.q in, p.q
 // out; no other rows of `r`); see attn_kv_append_rope_fp8.

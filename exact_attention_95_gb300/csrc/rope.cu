@@ -17,7 +17,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, 
 template <class T, int D>
 cudaError_t launch(const RopeParams& p, int interleaved, int sms, cudaStream_t stream) {
   const long long groups = ((long long)p.B * p.N + rope_tokens(D) - 1) / rope_tokens(D);
-  const int heads = rope_heads(groups, p.Hq + p.Hkv, sms);
+  const int heads = rope_heads(groups, p.Hq + p.Hkv, 16LL * sms);
   const dim3 grid((unsigned)groups, (unsigned)((p.Hq + p.Hkv + heads - 1) / heads));
   return interleaved ? launch_behind(rope_kernel<T, D, true>, grid, kRopeThreads, stream, p, heads)
                      : launch_behind(rope_kernel<T, D, false>, grid, kRopeThreads, stream, p, heads);
@@ -25,10 +25,11 @@ cudaError_t launch(const RopeParams& p, int interleaved, int sms, cudaStream_t s
 
 }  // namespace
 
-// Heads of a CTA: as many as leave eight CTAs for every SM, in fours.
-int rope_heads(long long groups, int all, int sms) {
-  const long long want = groups * all / (8LL * sms);
-  return want < 2 ? 1 : (int)std::min<long long>(all, want < 4 ? want : want / 4 * 4);
+// Heads of a CTA: as many as leave `ctas` CTAs for every SM, spread evenly.
+int rope_heads(long long groups, int all, long long ctas) {
+  const long long want = std::min<long long>(all, std::max(1LL, groups * all / ctas));
+  const long long parts = (all + want - 1) / want;
+  return (int)((all + parts - 1) / parts);
 }
 
 cudaError_t launch_rope(int d, int f32, const RopeParams& p, int interleaved, int sms, cudaStream_t stream) {

@@ -75,23 +75,39 @@ struct Eight<float> {
 
 constexpr int kRopeThreads = 256;
 // Tokens of a CTA: a thread has 16 elements of a row (eight pairs).
-constexpr int rope_tokens(int d) { return kRopeThreads / (d / 16); }
+constexpr int rope_tokens(int d, int threads = kRopeThreads) { return threads / (d / 16); }
 
-// Rotates `heads` heads from head `h0` on of a group of rope_tokens(D) tokens.
+// Rotates `heads` heads from head `h0` on of a group of rope_tokens(D, THREADS) tokens.
 //
 // HBM bound: every element is read and written once.  A thread computes the
 // eight angles of its pairs of one token once and takes all the CTA's heads
 // through them, a batch of heads' loads ahead of their use.  The 16 elements are
 // two pieces of eight: i.. and rot / 2 + i.. where halves pair, 16 adjacent
 // ones otherwise, so both are 16-byte accesses (32 in fp32) and pairs never leave a thread.
-template <class T, int D, bool INTER>
+template <class T, int D, bool INTER, int THREADS = kRopeThreads>
 __device__ __forceinline__ void rope_block(const RopeParams& p, long long group, int h0, int heads) {
   constexpr int UNITS = D / 16;
   constexpr int BATCH = sizeof(T) == 2 ? 4 : 2;  // heads in flight
   const int unit = threadIdx.x % UNITS;
-  const long long row = group * rope_tokens(D) + threadIdx.x / UNITS;
+  const long long row = group * rope_tokens(D, THREADS) + threadIdx.x / UNITS;
   if (row >= (long long)p.B * p.N) return;
   const long long b = row / p.N, n = row - b * p.N;
+  const bool halves = !INTER && unit < p.rot / 16;
+  const int at = halves ? 8 * unit : 16 * unit, to = halves ? p.rot / 2 + 8 * unit : 16 * unit + 8;
+  const int end = min(h0 + heads, p.Hq + p.Hkv);
+  Eight<T> x[BATCH][2];
+  auto read = [&](int h) {
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k)
+      if (h + k < end) {
+        const bool is_q = h + k < p.Hq;
+        const RopeRows& r = is_q ? p.q : p.k;
+        const T* src = static_cast<const T*>(r.in) + b * r.in_batch + (is_q ? h + k : h + k - p.Hq) * r.in_head + n * r.in_token;
+        x[k][0].load(src + at);
+        x[k][1].load(src + to);
+      }
+  };
+  read(h0);  // (on their way while the angles are computed)
   const int pos = p.positions ? p.positions[b * p.pos_batch + n] : (int)n;
   // A token with a negative position has none: it is copied.
   const bool turns = unit < p.rot / 16 && pos >= 0;
@@ -104,26 +120,7 @@ __device__ __forceinline__ void rope_block(const RopeParams& p, long long group,
       s[k] *= p.sine;
     }
   }
-  const bool halves = !INTER && unit < p.rot / 16;
-  const int at = halves ? 8 * unit : 16 * unit, to = halves ? p.rot / 2 + 8 * unit : 16 * unit + 8;
-  auto in = [&](int h) -> const T* {
-    const RopeRows& r = h < p.Hq ? p.q : p.k;
-    return static_cast<const T*>(r.in) + b * r.in_batch + (h < p.Hq ? h : h - p.Hq) * r.in_head + n * r.in_token;
-  };
-  auto out = [&](int h) -> T* {
-    const RopeRows& r = h < p.Hq ? p.q : p.k;
-    return static_cast<T*>(r.out) + b * r.out_batch + (h < p.Hq ? h : h - p.Hq) * r.out_head + n * r.out_token;
-  };
-  const int end = min(h0 + heads, p.Hq + p.Hkv);
   for (int h = h0; h < end; h += BATCH) {
-    Eight<T> x[BATCH][2];
-#pragma unroll
-    for (int k = 0; k < BATCH; ++k)
-      if (h + k < end) {
-        const T* src = in(h + k);
-        x[k][0].load(src + at);
-        x[k][1].load(src + to);
-      }
 #pragma unroll
     for (int k = 0; k < BATCH; ++k)
       if (h + k < end) {
@@ -146,12 +143,15 @@ __device__ __forceinline__ void rope_block(const RopeParams& p, long long group,
           x[k][0].set(y);
           x[k][1].set(z);
         }
-        T* dst = out(h + k);
+        const bool is_q = h + k < p.Hq;
+        const RopeRows& r = is_q ? p.q : p.k;
+        T* dst = static_cast<T*>(r.out) + b * r.out_batch + (is_q ? h + k : h + k - p.Hq) * r.out_head + n * r.out_token;
         if (dcheck(h + k < p.Hq + p.Hkv && to + 8 <= D && n < p.N, p.status)) {
           x[k][0].store(dst + at);
           x[k][1].store(dst + to);
         }
       }
+    read(h + BATCH);
   }
 }
 
