@@ -37,20 +37,17 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t c, float r) {
 template <int D>
 struct Run {
   const uint16_t* src;  // the first row's element 0
-  const int* pos;       // of K's rows to be rotated, their positions, else null
   long long ld;
   uint8_t* dst;  // the page's row 0
   float* scale;
   int off, n;
 };
 template <int D>
-__device__ __forceinline__ Run<D> run_of(const KvAppendParams& p, const int* positions, long long t, long long slot, int n,
-                                         int pair) {
+__device__ __forceinline__ Run<D> run_of(const KvAppendParams& p, long long t, long long slot, int n, int pair) {
   const bool is_v = pair >= p.Hkv;
   const int h = is_v ? pair - p.Hkv : pair;
   const long long place = (slot >> p.page_log2) * p.Hkv + h;
   Run<D> r;
-  r.pos = is_v || !positions ? nullptr : positions + t;
   r.ld = is_v ? p.v_stride : p.k_stride;
   r.src = (is_v ? p.V : p.K) + t * r.ld + h * D;
   r.dst = (is_v ? p.v_pages : p.k_pages) + (place << p.page_log2) * D;
@@ -150,27 +147,6 @@ __device__ __forceinline__ int find_runs(const KvAppendParams& p, int chunk, int
   any_warp = __syncthreads_or(len > kGroupRun && len <= kWarpRun);
   any_cta = __syncthreads_or(len > kWarpRun);
   return nruns;
-}
-
-// How an append is cut: tokens and pairs of a CTA.
-//
-// Up to kFewTokens tokens: eight, and as many pairs as give every group of
-// lanes a run of one token; more: 64 and two pairs.  Measured on both sides
-// of the border, 16 pairs, d = 128, us, the few tokens' way first: 500 tokens
-// of a prompt 6.0 / 4.2, of 500 requests (32 pairs, d = 64) 4.0 / 5.1; 2000
-// tokens 10.4 / 6.8 and 10.5 / 10.0.  128 tokens and one pair against 64 and
-// two: 25000 tokens of five prompts 32.9 / 32.3, 8000 requests 25.8 / 24.3.
-struct AppendCut {
-  int chunk, pairs;
-  long long chunks, groups;  // CTAs along the tokens and the pairs
-};
-inline AppendCut append_cut(int d, const KvAppendParams& p) {
-  AppendCut c;
-  c.chunk = p.T <= kFewTokens ? 8 : kMaxChunk;
-  c.pairs = p.T <= kFewTokens ? kAppThreads / (d / 8) / 8 : 2;
-  c.chunks = (p.T + c.chunk - 1) / c.chunk;
-  c.groups = (2 * p.Hkv + c.pairs - 1) / c.pairs;
-  return c;
 }
 
 }  // namespace attn

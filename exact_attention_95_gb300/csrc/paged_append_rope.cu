@@ -32,9 +32,12 @@ __device__ __noinline__ uint2 encode8_div(float4 a, float4 b, float s) {
                     pack_e4m3x4(__fdiv_rn(b.x, s), __fdiv_rn(b.y, s), __fdiv_rn(b.z, s), __fdiv_rn(b.w, s)));
 }
 __device__ __forceinline__ uint2 encode8(const float* y, float inv, float s) {
-  if (inv > 0.f)
-    return make_uint2(pack_e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
-                      pack_e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+  if (inv > 0.f) {
+    float q[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f2unpack(fmul2(f2pack(y[2 * k], y[2 * k + 1]), f2pack(inv, inv)), q[2 * k], q[2 * k + 1]);
+    return make_uint2(pack_e4m3x4(q[0], q[1], q[2], q[3]), pack_e4m3x4(q[4], q[5], q[6], q[7]));
+  }
   return encode8_div(make_float4(y[0], y[1], y[2], y[3]), make_float4(y[4], y[5], y[6], y[7]), s);
 }
 
@@ -60,19 +63,21 @@ struct Unit {
     amplitude = q.amplitude;
   }
   // Reads rows row0, row0 + step, .. of a run.
-  __device__ __forceinline__ void read(const Run<D>& r, int row0, int step, Held& x) const {
+  __device__ __forceinline__ void read(const Run<D>& r, const int* pos, int row0, int step, Held& x) const {
     x.old = *r.scale;
+    const uint16_t* src = r.src + row0 * r.ld;
+    const long long far = step * r.ld;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int row = row0 + step * j;
       x.a[j].v = x.b[j].v = make_uint4(0, 0, 0, 0);
       x.pos[j] = -1;
       if (row < r.n) {
-        const uint16_t* src = r.src + row * r.ld;
         x.a[j].v = __ldg(reinterpret_cast<const uint4*>(src + at));
         x.b[j].v = __ldg(reinterpret_cast<const uint4*>(src + to));
-        if (r.pos && turns) x.pos[j] = __ldg(r.pos + row);
+        if (pos && turns) x.pos[j] = __ldg(pos + row);
       }
+      src += far;
     }
   }
   // Rotates and quantizes what was read; fold(v, keep) is the largest v of the run's threads
@@ -94,7 +99,7 @@ struct Unit {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           float c, s;
-          cos_sin((uint64_t)x.pos[j] * freqs[k], c, s);
+          cos_sin(x.pos[j], freqs[k], c, s);
           c *= amplitude;
           s *= amplitude;
           float &x1 = y[j][INTER ? 2 * k : k], &x2 = y[j][INTER ? 2 * k + 1 : 8 + k];
@@ -122,14 +127,14 @@ struct Unit {
     const float want = power_scale(amax);
     const float s = r.off > 0 ? fmaxf(x.old, want) : want;
     const float inv = exact_inverse(s);
+    uint8_t* dst = r.dst + (r.off + row0) * D;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const int row = row0 + step * j;
-      if (row < r.n) {
-        uint8_t* dst = r.dst + (r.off + row) * D;
+      if (row0 + step * j < r.n) {
         *reinterpret_cast<uint2*>(dst + at) = encode8(&y[j][0], inv, s);
         *reinterpret_cast<uint2*>(dst + to) = encode8(&y[j][8], inv, s);
       }
+      dst += step * D;
     }
     finish_run<D>(r, id, count, x.old, s);
   }
@@ -152,10 +157,11 @@ __device__ __forceinline__ void append_chunk(const KvAppendParams& p, const Rope
   const int nruns = find_runs(p, chunk, bx, runs, any_group, any_warp, any_cta);
   const int tasks = nruns * npairs;
   const Unit<D, INTER> unit(q, s_freqs, tid % UNITS);
-  auto task_run = [&](int task, int lo, int hi) -> Run<D> {  // n = 0 unless lo < tokens <= hi
+  auto task_run = [&](int task, int lo, int hi, const int*& pos) -> Run<D> {  // n = 0 unless lo < tokens <= hi
     const int k = min(task, tasks - 1) / npairs, pair = min(task, tasks - 1) - k * npairs;
     const int n = runs.len[k];
-    return run_of<D>(p, q.positions, t0 + runs.first[k], runs.slot[k], task < tasks && n > lo && n <= hi ? n : 0, pair0 + pair);
+    pos = pair0 + pair < p.Hkv ? q.positions + t0 + runs.first[k] : nullptr;
+    return run_of<D>(p, t0 + runs.first[k], runs.slot[k], task < tasks && n > lo && n <= hi ? n : 0, pair0 + pair);
   };
   // Short, middling and long runs, one after the other in the same code (three copies of
   // it are fetched for longer than a decoding step takes): held by UNITS threads, a
@@ -169,10 +175,11 @@ __device__ __forceinline__ void append_chunk(const KvAppendParams& p, const Rope
     const int id = tid & (count - 1), row0 = id / UNITS, step = count / UNITS;
 #pragma unroll 1
     for (int base = 0; base < tasks; base += kAppThreads / count) {
-      const Run<D> r = task_run(base + tid / count, lo, hi);
+      const int* pos;  // of K's rows
+      const Run<D> r = task_run(base + tid / count, lo, hi, pos);
       if (kind == 2 ? r.n == 0 : __all_sync(0xffffffffu, r.n == 0)) continue;  // (the whole warp or CTA)
       Held x;
-      unit.read(r, row0, step, x);
+      unit.read(r, pos, row0, step, x);
       unit.write(r, row0, step, id, count, x, [&](uint32_t v, uint32_t keep) {
         // A kind's threads all come here, with the same `keep` in a run.
         uint32_t most = v;
@@ -217,18 +224,19 @@ __global__ void __launch_bounds__(kAppThreads, 3)
 
 template <int D, bool INTER>
 cudaError_t launch(const KvAppendParams& p, const RopeParams& q, int sms, cudaStream_t stream) {
-  AppendCut c = append_cut(D, p);
+  const bool few = p.T <= kFewTokens;
   const long long q_groups = (p.T + rope_tokens(D) - 1) / rope_tokens(D);
   Grid g;
+  g.chunk = few ? 8 : kMaxChunk;
+  g.pairs = few ? kAppThreads / (D / 16) / 8 : 2;
   g.q_heads = rope_heads(q_groups, q.Hq, 8LL * sms);
-  const long long appends = c.chunks * c.groups, all = appends + q_groups * ((q.Hq + g.q_heads - 1) / g.q_heads);
+  const long long chunks = (p.T + g.chunk - 1) / g.chunk, appends = chunks * ((2 * p.Hkv + g.pairs - 1) / g.pairs);
+  const long long all = appends + q_groups * ((q.Hq + g.q_heads - 1) / g.q_heads);
   if (all >= 0x7fffffffLL) return cudaErrorNotSupported;
-  g.chunk = c.chunk;
-  g.pairs = c.pairs;
-  g.chunks = (int)c.chunks;
+  g.chunks = (int)chunks;
   g.q_groups = (int)q_groups;
   g.appends = (int)appends;
-  return launch_behind(kv_append_rope_kernel<D, INTER>, dim3((unsigned)all), kAppThreads, stream, p, q, g);
+  return launch_behind(kv_append_rope_kernel<D, INTER>, dim3((unsigned)all), kAppThreads, stream, 0, p, q, g);
 }
 
 }  // namespace

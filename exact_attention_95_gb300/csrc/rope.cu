@@ -9,7 +9,7 @@ namespace attn {
 namespace {
 
 template <class T, int D, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, int heads) {
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams p, int heads) {
   griddep_wait();
   rope_block<T, D, INTER>(p, blockIdx.x, blockIdx.y * heads, heads);
 }
@@ -19,8 +19,8 @@ cudaError_t launch(const RopeParams& p, int interleaved, int sms, cudaStream_t s
   const long long groups = ((long long)p.B * p.N + rope_tokens(D) - 1) / rope_tokens(D);
   const int heads = rope_heads(groups, p.Hq + p.Hkv, 16LL * sms);
   const dim3 grid((unsigned)groups, (unsigned)((p.Hq + p.Hkv + heads - 1) / heads));
-  return interleaved ? launch_behind(rope_kernel<T, D, true>, grid, kRopeThreads, stream, p, heads)
-                     : launch_behind(rope_kernel<T, D, false>, grid, kRopeThreads, stream, p, heads);
+  return interleaved ? launch_behind(rope_kernel<T, D, true>, grid, kRopeThreads, stream, 0, p, heads)
+                     : launch_behind(rope_kernel<T, D, false>, grid, kRopeThreads, stream, 0, p, heads);
 }
 
 }  // namespace

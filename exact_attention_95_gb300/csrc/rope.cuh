@@ -12,16 +12,16 @@
 
 namespace attn {
 
-// cos and sin of 2 pi * phase / 2^64.  Frequencies are fractions of a turn in
-// units of 2^-64, so phase = pos * freq keeps the fraction of a turn exactly
+// cos and sin of 2 pi * pos * freq / 2^64.  Frequencies are fractions of a turn in
+// units of 2^-64, so the product keeps the fraction of a turn exactly
 // for every 32-bit position (a 32-bit float angle is off by 0.01 rad at 131072).
 // The nearest quarter turn is taken off in whole numbers; the rest, within
 // pi / 4, goes through Taylor's series up to x^9 and x^8 (cut off below 3e-8).
 // About 20 instructions.  Off by at most 2^-22: 2^-24 relative each from the
 // conversion and the constant, together 0.8 * 2^-23 of an angle of pi / 4, the
 // sums' roundings, and the rest of the series.
-__device__ __forceinline__ void cos_sin(uint64_t phase, float& c, float& s) {
-  const uint32_t t = (uint32_t)(phase >> 32);
+__device__ __forceinline__ void cos_sin(uint32_t pos, uint64_t freq, float& c, float& s) {
+  const uint32_t t = __umulhi(pos, (uint32_t)freq) + pos * (uint32_t)(freq >> 32);  // of pos * freq, the upper half
   const uint32_t q = (t + 0x20000000u) >> 30;
   const float x = (float)(int)(t - (q << 30)) * 1.46291807926715968e-9f;  // 2 pi / 2^32
   const float z = x * x;
@@ -95,16 +95,27 @@ __device__ __forceinline__ void rope_block(const RopeParams& p, long long group,
   const bool halves = !INTER && unit < p.rot / 16;
   const int at = halves ? 8 * unit : 16 * unit, to = halves ? p.rot / 2 + 8 * unit : 16 * unit + 8;
   const int end = min(h0 + heads, p.Hq + p.Hkv);
+  // Queries' heads come before the keys'; both sides' pointers step from head to head.
+  auto in = [&](int h) -> const T* {
+    const bool is_q = h < p.Hq;
+    const RopeRows& r = is_q ? p.q : p.k;
+    return static_cast<const T*>(r.in) + b * r.in_batch + (is_q ? h : h - p.Hq) * r.in_head + n * r.in_token;
+  };
+  auto out = [&](int h) -> T* {
+    const bool is_q = h < p.Hq;
+    const RopeRows& r = is_q ? p.q : p.k;
+    return static_cast<T*>(r.out) + b * r.out_batch + (is_q ? h : h - p.Hq) * r.out_head + n * r.out_token;
+  };
+  const T* src = in(h0);
+  T* dst = out(h0);
   Eight<T> x[BATCH][2];
   auto read = [&](int h) {
 #pragma unroll
     for (int k = 0; k < BATCH; ++k)
       if (h + k < end) {
-        const bool is_q = h + k < p.Hq;
-        const RopeRows& r = is_q ? p.q : p.k;
-        const T* src = static_cast<const T*>(r.in) + b * r.in_batch + (is_q ? h + k : h + k - p.Hq) * r.in_head + n * r.in_token;
         x[k][0].load(src + at);
         x[k][1].load(src + to);
+        src = h + k + 1 == p.Hq ? in(p.Hq) : src + (h + k < p.Hq ? p.q.in_head : p.k.in_head);
       }
   };
   read(h0);  // (on their way while the angles are computed)
@@ -115,7 +126,7 @@ __device__ __forceinline__ void rope_block(const RopeParams& p, long long group,
   if (turns) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      cos_sin((uint64_t)pos * p.freqs[8 * unit + k], c[k], s[k]);
+      cos_sin(pos, p.freqs[8 * unit + k], c[k], s[k]);
       c[k] *= p.amplitude;
       s[k] *= p.sine;
     }
@@ -143,13 +154,11 @@ __device__ __forceinline__ void rope_block(const RopeParams& p, long long group,
           x[k][0].set(y);
           x[k][1].set(z);
         }
-        const bool is_q = h + k < p.Hq;
-        const RopeRows& r = is_q ? p.q : p.k;
-        T* dst = static_cast<T*>(r.out) + b * r.out_batch + (is_q ? h + k : h + k - p.Hq) * r.out_head + n * r.out_token;
         if (dcheck(h + k < p.Hq + p.Hkv && to + 8 <= D && n < p.N, p.status)) {
           x[k][0].store(dst + at);
           x[k][1].store(dst + to);
         }
+        dst = h + k + 1 == p.Hq ? out(p.Hq) : dst + (h + k < p.Hq ? p.q.out_head : p.k.out_head);
       }
     read(h + BATCH);
   }

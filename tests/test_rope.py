@@ -300,6 +300,24 @@ def test_append_at_scales_that_are_no_power_of_two_and_of_tokens_without_positio
     pos64.check_append(y, size + 2.0 ** -2 * np.abs(y), slots, codes[0], scales[0], cache[0].cpu().numpy(), cache[1].cpu().numpy())
 
 
+@pytest.mark.parametrize("new", [1, 9, 50])
+def test_tokens_without_positions_keep_infinities_apart(new):
+    """A key that is not rotated is appended as attn_kv_append_fp8 appends it, infinities and NaNs among its numbers."""
+    page, d, H = 64, 64, 2
+    freqs, _ = pkg.attn_rope_freqs(d)
+    rng = np.random.default_rng(new)
+    slots, positions, num_pages = _append_case(rng, [(2, new)], page, 0)
+    codes, scales = _cache_for(rng, num_pages, H, page, d)
+    K, V = _rand(1, new, H, d), _rand(2, new, H, d)
+    K[0, 1, 3], K[new - 1, 0, 40] = float("inf"), float("nan")
+    one, two = ([dev(codes[0]), dev(scales[0]), dev(codes[1]), dev(scales[1])] for _ in range(2))
+    Qo = pkg.attn_kv_append_rope_fp8(K, K, V, dev(np.full(new, -1, I32)), dev(slots), freqs, *one)
+    pkg.attn_kv_append_fp8(K, V, dev(slots), *two)
+    ok()
+    assert all(torch.equal(a, b) for a, b in zip(one, two))
+    assert torch.equal(Qo.view(torch.int16), K.view(torch.int16))
+
+
 @pytest.mark.parametrize("new", [1, 6, 40])
 def test_append_of_infinities_and_nans(new):
     """They reach no other pair's codes, and no scale."""
