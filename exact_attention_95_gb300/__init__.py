@@ -38,7 +38,8 @@ Functions carry the C names:
 * ``attn_bwd_workspace_size(B, Hq, Hkv, N, d)``
 * ``attn_fwd_dropout(Q, K, V, p, rng, scale, causal) -> (O, LSE)`` and
   ``attn_bwd_dropout(Q, K, V, O, dO, LSE, p, rng, scale, causal) -> (dQ, dK, dV)``: with
-  dropout on the softmax, from a counter-based generator (seed and offset in ``rng``)
+  dropout on the softmax, from a counter-based generator (seed and offset in ``rng``);
+  ``attn_bwd_dropout_workspace_size(B, Hq, Hkv, N, d, causal)``
 * ``attn_last_device_status(stream=None)``, ``attn_status_string(code)``
 * ``attn_selftest_wait_timeout(limit_ns)``, ``attn_selftest_paged_wait_timeout(limit_ns)``
 
@@ -73,7 +74,7 @@ EXPORTED = ("attn_fwd", "attn_fwd_split", "attn_fwd_split_workspace_size", "attn
             "attn_bwd_masked", "attn_quantize_fp8", "attn_fp8_vt_stride", "attn_fwd_fp8", "attn_bwd",
             "attn_bwd_preprocess", "attn_bwd_main", "attn_bwd_convert", "attn_bwd_workspace_size",
             "attn_kv_tables", "attn_kv_append_fp8", "attn_fwd_paged_fp8", "attn_fwd_paged_workspace_size",
-            "attn_fwd_dropout", "attn_bwd_dropout", "attn_rope_freqs", "attn_rope", "attn_rope_bwd", "attn_kv_append_rope_fp8",
+            "attn_fwd_dropout", "attn_bwd_dropout", "attn_bwd_dropout_workspace_size", "attn_rope_freqs", "attn_rope", "attn_rope_bwd", "attn_kv_append_rope_fp8",
             "attn_status_string", "attn_last_device_status", "attn_selftest_wait_timeout",
             "attn_selftest_paged_wait_timeout")
 _BWD_STAGES = {"all": "attn_bwd", "preprocess": "attn_bwd_preprocess", "main": "attn_bwd_main",
@@ -147,6 +148,8 @@ def load_library(path: str = LIB_PATH):
         lib.attn_bwd_dropout.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, i32, f32, vp,
                                          vp, sz, vp]
         lib.attn_bwd_dropout.restype = i32
+        lib.attn_bwd_dropout_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32]
+        lib.attn_bwd_dropout_workspace_size.restype = sz
         rows = ctypes.POINTER(_Rows)
         for fn in (lib.attn_rope, lib.attn_rope_bwd):
             fn.argtypes = [rows, rows, rows, rows, vp, i64, vp, i32, i32, f32, i32, i32, i32, i32, i32, i32, vp]
@@ -188,7 +191,7 @@ def _bound():
                     lib.attn_kv_tables, lib.attn_kv_append_fp8, lib.attn_fwd_paged_fp8,
                     lib.attn_fwd_paged_workspace_size, lib.attn_rope, lib.attn_rope_bwd,
                     lib.attn_kv_append_rope_fp8, lib.attn_fwd_dropout, lib.attn_bwd_dropout,
-                    lib.attn_bwd_workspace_size)))
+                    lib.attn_bwd_dropout_workspace_size)))
                 _fast = module
             except ImportError as e:
                 _fast = False
@@ -899,6 +902,10 @@ def attn_fwd_dropout(Q, K, V, p, rng, scale=None, causal=False, out_dtype=None, 
     return O, LSE
 
 
+def attn_bwd_dropout_workspace_size(B: int, Hq: int, Hkv: int, N: int, d: int, causal: bool = False) -> int:
+    return int(load_library().attn_bwd_dropout_workspace_size(B, Hq, Hkv, N, d, int(bool(causal))))
+
+
 def attn_bwd_dropout(Q, K, V, O, dO, LSE, p, rng, scale=None, causal=False, dQ=None, dK=None, dV=None, workspace=None,
                      stream=None):
     """dQ, dK, dV of attn_fwd_dropout's O, given dO and the forward's O, LSE, p and numbers in rng."""
@@ -917,7 +924,7 @@ def attn_bwd_dropout(Q, K, V, O, dO, LSE, p, rng, scale=None, causal=False, dQ=N
         dK = torch.empty_like(K) if dK is None else dK
         dV = torch.empty_like(V) if dV is None else dV
         _check_bwd_outputs(dQ, dK, dV, B, Hq, Hkv, N, d, dev)
-        ws_bytes = attn_bwd_workspace_size(B, Hq, Hkv, N, d)
+        ws_bytes = attn_bwd_dropout_workspace_size(B, Hq, Hkv, N, d, causal)
         if workspace is None:
             workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
         _check_workspace(workspace, ws_bytes, dev)

@@ -214,6 +214,11 @@ attn_status check_shape(int B, int Hq, int Hkv, int N, int d, float scale, int c
 
 unsigned long long wait_limit() { return kDefaultWaitLimitNs; }
 
+int sms_or_default() {
+  const int n = sm_count();
+  return n > 0 ? n : 152;
+}
+
 // Number of heads whose CTAs are scheduled together so that the operands they
 // share (about `bytes_per_head` each) stay resident in L2 (`budget` bytes of
 // the 126 MiB L2).  Fewer, larger groups shorten the tail: the heaviest CTAs of
@@ -554,6 +559,12 @@ size_t attn_bwd_workspace_size(int B, int Hq, int Hkv, int N, int d) {
   return bwd_workspace_bytes(B, Hq, N, d);
 }
 
+size_t attn_bwd_dropout_workspace_size(int B, int Hq, int Hkv, int N, int d, int causal) {
+  if (check_shape(B, Hq, Hkv, N, d, 1.0f, causal) != ATTN_OK) return 0;
+  return bwd_workspace_bytes(B, Hq, N, d) +
+         bwd_parts_bytes(B, Hkv, N, d, bwd_q_splits(B, Hq, Hkv, N, causal, sms_or_default()));
+}
+
 }  // extern "C"
 
 namespace {
@@ -573,7 +584,9 @@ attn_status bwd_stages(unsigned stages, const void* Q, const void* K, const void
   attn_status st = check_shape(B, Hq, Hkv, N, d, scale, causal);
   if (st != ATTN_OK) return st;
   if (dtype != ATTN_BF16) return ATTN_ERR_UNSUPPORTED;
-  if (workspace_bytes < bwd_workspace_bytes(B, Hq, N, d)) return ATTN_ERR_INVALID_ARG;
+  const int splits = drop ? bwd_q_splits(B, Hq, Hkv, N, causal, sms_or_default()) : 1;
+  const size_t base_bytes = bwd_workspace_bytes(B, Hq, N, d);
+  if (workspace_bytes < base_bytes + bwd_parts_bytes(B, Hkv, N, d, splits)) return ATTN_ERR_INVALID_ARG;
   int* status = status_ptr();
   if (!status) return ATTN_ERR_CUDA;
   CUtensorMap tq, tk, tv, tdo;
@@ -608,13 +621,15 @@ attn_status bwd_stages(unsigned stages, const void* Q, const void* K, const void
   p.bmask = bmask;
   p.bmask_heads = bmask_heads;
   if (drop) p.drop = *drop;
+  p.q_splits = splits;
+  p.parts = reinterpret_cast<float*>(ws + base_bytes);
   p.scale = scale;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.causal = causal;
   // Per kv head the CTAs share Q and dO (bf16) and the dQ accumulator (fp32) of its group.
   p.head_group = head_group_for((size_t)(Hq / Hkv) * N * d * (2 + 2 + 4), (long long)B * Hkv,
                                 size_t(32) << 20);
-  if ((long long)B * Hkv * ((N + 127) / 128) > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  if ((long long)B * Hkv * ((N + 127) / 128) > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;  // (split: below 16 times the SMs)
   p.wait_limit_ns = wait_limit();
   CUtensorMap tacc;
   if (!make_acc_map(&tacc, p.dQacc, (long long)rows, d)) return ATTN_ERR_CUDA;

@@ -35,7 +35,7 @@ decltype(&attn_rope) g_rope[2] = {nullptr, nullptr};  // forward, gradient
 decltype(&attn_kv_append_rope_fp8) g_append_rope = nullptr;
 decltype(&attn_fwd_dropout) g_fwd_dropout = nullptr;
 decltype(&attn_bwd_dropout) g_bwd_dropout = nullptr;
-decltype(&attn_bwd_workspace_size) g_bwd_workspace = nullptr;
+decltype(&attn_bwd_dropout_workspace_size) g_bwd_workspace = nullptr;
 
 // The tensor of an argument, or null.
 const at::Tensor* tensor(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
@@ -447,7 +447,7 @@ PyObject* bwd_dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!output(a[10], dQ, at::kBFloat16, Q->sizes(), s.dev) || !output(a[11], dK, at::kBFloat16, K->sizes(), s.dev) ||
         !output(a[12], dV, at::kBFloat16, K->sizes(), s.dev))
       Py_RETURN_NONE;
-    size_t bytes = g_bwd_workspace((int)s.B, (int)s.Hq, (int)s.Hkv, (int)s.N, (int)s.d);
+    size_t bytes = g_bwd_workspace((int)s.B, (int)s.Hq, (int)s.Hkv, (int)s.N, (int)s.d, causal);
     c10::DataPtr own;  // freed at the end of this call, for later work of the same stream
     void* ws = nullptr;
     if (a[13] == Py_None) {
@@ -469,7 +469,7 @@ PyObject* bwd_dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // bind(addresses of attn_kv_tables, attn_kv_append_fp8, attn_fwd_paged_fp8, attn_fwd_paged_workspace_size, attn_rope,
-// attn_rope_bwd, attn_kv_append_rope_fp8, attn_fwd_dropout, attn_bwd_dropout, attn_bwd_workspace_size)
+// attn_rope_bwd, attn_kv_append_rope_fp8, attn_fwd_dropout, attn_bwd_dropout, attn_bwd_dropout_workspace_size)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   constexpr int kAddresses = 10;
   if (n != kAddresses) {

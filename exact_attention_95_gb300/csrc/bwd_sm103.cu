@@ -46,6 +46,11 @@
 // rows l and 32 + l of its warpgroup's 64 against the warp's 32 keys, and two
 // transposes of 32 x 32 bits give every key's thread its 64 bits.  dV gets the
 // factor in its epilogue.
+//
+// Where there are fewer key tiles than SMs (few kv heads, short sequences), a tile's
+// (query head, query tile) pairs are cut into p.q_splits equal parts with a CTA
+// each, which write fp32 dK and dV of their own into the workspace; bwd_join, in place of
+// bwd_dq, adds them in the order of the parts.
 #include <algorithm>
 
 #include <type_traits>
@@ -196,12 +201,12 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(const BwdParams p) {
 // dQ = bf16(scale * accumulator): one warp per four consecutive padded rows of
 // one head, all four rows' loads issued first.
 template <int D>
-__global__ void __launch_bounds__(256) bwd_dq_kernel(const BwdParams p) {
+__device__ __forceinline__ void dq_rows(const BwdParams& p, int block, int blocks) {
   constexpr int V4 = D / 4;  // float4 per row
   const long long chunks = (long long)p.B * p.Hq * p.Npad / kRowsPerWarp;
   const int lane = threadIdx.x & 31;
-  for (long long c = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5; c < chunks;
-       c += ((long long)gridDim.x * blockDim.x) >> 5) {
+  for (long long c = ((long long)block * blockDim.x + threadIdx.x) >> 5; c < chunks;
+       c += ((long long)blocks * blockDim.x) >> 5) {
     const long long r0 = c * kRowsPerWarp;
     const long long bh = r0 / p.Npad;
     const int i0 = (int)(r0 - bh * p.Npad);
@@ -222,6 +227,49 @@ __global__ void __launch_bounds__(256) bwd_dq_kernel(const BwdParams p) {
       }
     }
   }
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) bwd_dq_kernel(const BwdParams p) {
+  dq_rows<D>(p, blockIdx.x, gridDim.x);
+}
+
+// Pairs (query head of the group, query tile) that a key tile meets, and those of a part.
+__device__ __forceinline__ int pairs_of(const BwdParams& p, int jt) {
+  return p.Hq / p.Hkv * ((p.N + kBQ - 1) / kBQ - (p.causal ? jt * kBK / kBQ : 0));
+}
+__device__ __forceinline__ int pairs_of_part(const BwdParams& p, int pairs) { return (pairs + p.q_splits - 1) / p.q_splits; }
+
+// dK, dV = bf16(sum of the parts' fp32 ones), 16 bytes of a row a thread at a time.
+template <int D>
+__device__ __forceinline__ void dkv_rows(const BwdParams& p, int block, int blocks) {
+  constexpr int V4 = D / 4;
+  const long long rows = (long long)p.B * p.Hkv * p.N, half = rows * V4;  // dV's, then dK's
+  const size_t part = (size_t)2 * p.B * p.Hkv * p.Npad * V4;              // float4 from part to part
+  for (long long i = (long long)block * blockDim.x + threadIdx.x; i < 2 * half; i += (long long)blocks * blockDim.x) {
+    const int which = i >= half;
+    const long long e = i - which * half, row = e / V4, bhk = row / p.N;
+    const int key = (int)(row - bhk * p.N), col = (int)(e - row * V4), pairs = pairs_of(p, key / kBK);
+    const int each = pairs_of_part(p, pairs), n = (pairs + each - 1) / each;
+    const float4* src = reinterpret_cast<const float4*>(p.parts) +
+                        ((size_t)which * p.B * p.Hkv * p.Npad + (size_t)bhk * p.Npad + key) * V4 + col;
+    float4 sum = src[0];
+    for (int k = 1; k < n; ++k) {
+      const float4 v = src[k * part];
+      sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+    }
+    *reinterpret_cast<uint2*>((which ? p.dK : p.dV) + row * D + 4 * col) =
+        make_uint2(pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w));
+  }
+}
+
+// The first `dq` blocks convert dQ, the others join the parts of dK and dV.
+template <int D>
+__global__ void __launch_bounds__(256) bwd_join_kernel(const BwdParams p, int dq) {
+  if ((int)blockIdx.x < dq)
+    dq_rows<D>(p, blockIdx.x, dq);
+  else
+    dkv_rows<D>(p, blockIdx.x - dq, gridDim.x - dq);
 }
 
 // ------------------------------------------------------------------ main
@@ -284,7 +332,8 @@ __global__ void __launch_bounds__(kMainThreads, 1)
   // so that their query-side operands and dQ accumulator stay in L2; within a
   // group, key tile 0 (the most query tiles when causal) comes first.
   int bhk, jt;
-  grouped_order(blockIdx.x, p.B * p.Hkv, (p.N + kBK - 1) / kBK, p.head_group, bhk, jt);
+  const int splits = DROP ? p.q_splits : 1, split = DROP ? blockIdx.x % splits : 0;
+  grouped_order(DROP ? blockIdx.x / splits : blockIdx.x, p.B * p.Hkv, (p.N + kBK - 1) / kBK, p.head_group, bhk, jt);
   const int k0 = jt * kBK;
   const int b = bhk / p.Hkv;
   const int hk = bhk - b * p.Hkv;
@@ -292,7 +341,13 @@ __global__ void __launch_bounds__(kMainThreads, 1)
   const int n_q = (p.N + kBQ - 1) / kBQ;
   const int i0 = p.causal ? (k0 / kBQ) : 0;  // first query tile that sees these keys
   const int per_head = n_q - i0;
-  int T = G * per_head;  // inner iterations (>= 1 since k0 < N; may be 0 when masked)
+  int T = G * per_head;  // inner iterations (>= 1 since k0 < N; may be 0 when masked, or for the last parts)
+  int t_first = 0;
+  if (DROP && splits > 1) {
+    const int each = pairs_of_part(p, T);
+    t_first = min(T, split * each);
+    T = min(T, t_first + each) - t_first;
+  }
   // Block-sparse: the (query head g, query tile) pairs whose block with this
   // key tile is kept, listed by the otherwise idle warp 3 (ballot compaction).
   constexpr bool masked = MASKED;  // p.bmask != NULL
@@ -321,6 +376,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       g = (int)(tlist[t] >> 16);
       it = (int)(tlist[t] & 0xffffu);
     } else {
+      if (DROP) t += t_first;
       g = t / per_head;
       it = i0 + (t - g * per_head);
     }
@@ -696,7 +752,17 @@ __global__ void __launch_bounds__(kMainThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = 0u;
           }
-          if (key_ok && dcheck(row < (size_t)p.B * p.Hkv * p.N, p.status)) {
+          if (DROP && splits > 1) {
+            // (A part without pairs is not read.)
+            if (have && key_ok && dcheck(split < splits && bhk < p.B * p.Hkv, p.status)) {
+              float4* f4 = reinterpret_cast<float4*>(
+                  p.parts + ((size_t)(2 * split + which) * p.B * p.Hkv * p.Npad + (size_t)bhk * p.Npad + key) * D + col);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                f4[i] = make_float4(__uint_as_float(o[4 * i]) * mul, __uint_as_float(o[4 * i + 1]) * mul,
+                                    __uint_as_float(o[4 * i + 2]) * mul, __uint_as_float(o[4 * i + 3]) * mul);
+            }
+          } else if (key_ok && dcheck(row < (size_t)p.B * p.Hkv * p.N, p.status)) {
             uint4* d4 = reinterpret_cast<uint4*>(dst + col);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -739,7 +805,7 @@ cudaError_t launch_main(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CU
   if (regs != kLaunchRegs) return cudaErrorInvalidKernelImage;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  dim3 grid(p.B * p.Hkv * ((p.N + kBK - 1) / kBK));
+  dim3 grid(p.B * p.Hkv * ((p.N + kBK - 1) / kBK) * (DROP ? p.q_splits : 1));
   kern<<<grid, kMainThreads, C::SMEM_BYTES, stream>>>(tmQ, tmK, tmV, tmdO, tmDQ, p);
   return cudaGetLastError();
 }
@@ -767,7 +833,13 @@ cudaError_t launch(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtenso
   if (stages & kBwdConvert) {
     const long long warps = (long long)p.B * p.Hq * p.Npad / kRowsPerWarp;
     const int cv_blocks = (int)std::min<long long>((warps + 7) / 8, (long long)sms * 8);
-    bwd_dq_kernel<D><<<cv_blocks, 256, 0, stream>>>(p);
+    if (p.q_splits > 1) {
+      const long long threads = (long long)p.B * p.Hkv * p.N * 2 * (D / 4);
+      const int join = (int)std::min<long long>((threads + 255) / 256, (long long)sms * 8);
+      bwd_join_kernel<D><<<cv_blocks + join, 256, 0, stream>>>(p, cv_blocks);
+    } else {
+      bwd_dq_kernel<D><<<cv_blocks, 256, 0, stream>>>(p);
+    }
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   return e;
@@ -781,6 +853,32 @@ size_t bwd_workspace_bytes(int B, int Hq, int N, int d) {
   const size_t Npad = (size_t)(N + kBQ - 1) / kBQ * kBQ;
   const size_t rows = (size_t)B * Hq * Npad;
   return (rows * d * 4 + 255) / 256 * 256 + 2 * ((rows * 4 + 255) / 256 * 256);
+}
+
+// Parts of a key tile's pairs: the number that ends first, by a count of rounds of CTAs, one an
+// SM, each as long as its pairs and two more (its start, and fp32 rows written and read again).
+// Causal tiles differ by up to all their pairs, heaviest first: the longest part, or the
+// average of all.  Only where an unsplit grid leaves SMs idle.
+int bwd_q_splits(int B, int Hq, int Hkv, int N, int causal, int sms) {
+  const long long tiles = (N + kBK - 1) / kBK, ctas = (long long)B * Hkv * tiles, most = (long long)(Hq / Hkv) * tiles;
+  if (ctas >= sms) return 1;
+  constexpr int kMostParts = 16;
+  double best = 0;
+  int parts = 1;
+  for (int s = 1; s <= std::min<long long>(kMostParts, most); ++s) {
+    const double longest = (double)((most + s - 1) / s) + (s > 1 ? 2 : 1);
+    const double all = (double)ctas * ((causal ? most * (tiles + 1) / (2.0 * tiles) : (double)most) + s * 2.0) / sms;
+    const double cost = causal ? std::max(longest, all) : longest * (double)((ctas * s + sms - 1) / sms);
+    if (s == 1 || cost < best * 0.95) {
+      best = cost;
+      parts = s;
+    }
+  }
+  return parts;
+}
+size_t bwd_parts_bytes(int B, int Hkv, int N, int d, int splits) {
+  const size_t Npad = (size_t)(N + kBK - 1) / kBK * kBK;
+  return splits > 1 ? (size_t)splits * 2 * B * Hkv * Npad * d * 4 : 0;
 }
 
 cudaError_t launch_bwd_bf16(int d, const CUtensorMap& tmQ, const CUtensorMap& tmK,

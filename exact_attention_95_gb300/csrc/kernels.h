@@ -136,6 +136,10 @@ struct BwdParams {
   const uint8_t* bmask;
   int bmask_heads;
   DropParams drop;  // drop.rng NULL: no dropout (with a block mask there is none)
+  // With dropout: parts of a key tile's (query head, query tile) pairs, a CTA each, and
+  // where they are more than one their fp32 [q_splits][dV, dK][B, Hkv, Npad, d].
+  int q_splits;
+  float* parts;
 };
 constexpr int kMaxMaskIters = 4096;  // (query head, query tile) pairs a masked backward CTA may list
 
@@ -143,6 +147,11 @@ constexpr int kMaxMaskIters = 4096;  // (query head, query tile) pairs a masked 
 int bwd_row_padding();
 // Workspace layout of the backward (bytes), all fp32: dQacc then D then LSE2.
 size_t bwd_workspace_bytes(int B, int Hq, int N, int d);
+
+// Parts that a backward with dropout cuts its key tiles' work into, and the bytes
+// of their sums behind the rest of the workspace.
+int bwd_q_splits(int B, int Hq, int Hkv, int N, int causal, int sms);
+size_t bwd_parts_bytes(int B, int Hkv, int N, int d, int splits);
 
 // Stages of the backward, launched in this order.
 enum : unsigned { kBwdPre = 1u, kBwdMain = 2u, kBwdConvert = 4u, kBwdAll = 7u };

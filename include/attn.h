@@ -285,12 +285,18 @@ attn_status attn_fwd_dropout(const void* Q, const void* K, const void* V, void* 
  * Its backward: attn_bwd's gradient with r_ij = keep_ij / (1 - T / 256):
  *   dV_j = sum p_ij r_ij dO_i,  dS_ij = p_ij (r_ij <dO_i, v_j> - D_i),  D_i = <dO_i, O_i>,
  * dQ and dK from dS as there.  O and LSE are attn_fwd_dropout's for the same numbers.
- * Workspace (attn_bwd_workspace_size) and other arguments as attn_bwd.
+ * Workspace (attn_bwd_dropout_workspace_size bytes) and other arguments as attn_bwd.  dK and
+ * dV are the same bits from call to call; dQ's fp32 sums have no fixed order.
  */
 attn_status attn_bwd_dropout(const void* Q, const void* K, const void* V, const void* O, const void* dO,
                              const float* LSE, void* dQ, void* dK, void* dV, int B, int Hq, int Hkv, int N, int d,
                              float scale, int causal, float p_drop, const uint64_t* rng, void* workspace,
                              size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace attn_bwd_dropout needs on the current device: attn_bwd's, and where
+ * there are fewer 128-key tiles (B * Hkv * ceil(N / 128)) than SMs, fp32 dK and dV of the parts
+ * that a tile's work is cut into.  0 on bad sizes. */
+size_t attn_bwd_dropout_workspace_size(int B, int Hq, int Hkv, int N, int d, int causal);
 
 /* Bytes of workspace attn_bwd needs: an fp32 dQ accumulator and two fp32
  * per-row vectors (D = rowsum(dO * O) and LSE in log2 units).  0 on bad sizes. */

@@ -169,7 +169,7 @@ SHAPES = [
     # B, Hq, Hkv, N, d
     (1, 1, 1, 1, 64), (2, 4, 2, 1, 128), (1, 8, 2, 31, 64), (1, 8, 2, 32, 128), (1, 8, 2, 33, 64),  # groups in one tile
     (2, 2, 2, 100, 128), (1, 4, 1, 100, 64), (1, 3, 3, 128, 64), (1, 2, 1, 129, 128), (1, 4, 2, 255, 64),
-    (2, 4, 2, 257, 128), (1, 6, 2, 513, 128), (1, 2, 2, 1000, 64), (2, 16, 4, 700, 128), (1, 2, 1, 2500, 128),
+    (2, 4, 2, 257, 128), (1, 6, 2, 513, 128), (1, 16, 1, 650, 64), (1, 2, 2, 1000, 64), (2, 16, 4, 700, 128), (1, 2, 1, 2500, 128),
 ]
 
 
@@ -333,7 +333,7 @@ def test_what_python_refuses(module, monkeypatch):
 @pytest.mark.parametrize("N", [40, 300])
 def test_the_calls_give_the_same_without_the_module(N, monkeypatch):
     Q, K, V, dO = _make(N, 2, 6, 2, N, 64)
-    ws = torch.empty(pkg.attn_bwd_workspace_size(2, 6, 2, N, 64), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(pkg.attn_bwd_dropout_workspace_size(2, 6, 2, N, 64, True), dtype=torch.uint8, device="cuda")
     got = []
     for module in (True, False):
         if not module:
