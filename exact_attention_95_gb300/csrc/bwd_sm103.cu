@@ -57,6 +57,7 @@
 
 #include "dropout.cuh"
 #include "kernels.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 
 namespace attn {
@@ -142,6 +143,7 @@ struct Bwd {
 constexpr int kRowsPerWarp = 4;
 template <int D>
 __global__ void __launch_bounds__(256) bwd_pre_kernel(const BwdParams p) {
+  griddep_wait();
   constexpr int EPL = D / 32;  // elements per lane
   using Vec = typename std::conditional<EPL == 4, uint2, uint32_t>::type;
   const long long chunks = (long long)p.B * p.Hq * p.Npad / kRowsPerWarp;
@@ -231,6 +233,7 @@ __device__ __forceinline__ void dq_rows(const BwdParams& p, int block, int block
 
 template <int D>
 __global__ void __launch_bounds__(256) bwd_dq_kernel(const BwdParams p) {
+  griddep_wait();
   dq_rows<D>(p, blockIdx.x, gridDim.x);
 }
 
@@ -266,6 +269,7 @@ __device__ __forceinline__ void dkv_rows(const BwdParams& p, int block, int bloc
 // The first `dq` blocks convert dQ, the others join the parts of dK and dV.
 template <int D>
 __global__ void __launch_bounds__(256) bwd_join_kernel(const BwdParams p, int dq) {
+  griddep_wait();
   if ((int)blockIdx.x < dq)
     dq_rows<D>(p, blockIdx.x, dq);
   else
@@ -416,6 +420,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const WaitCtx wc{abort_flag, p.status, p.wait_limit_ns};
   if (masked) T = *nlist;
+  if (DROP) griddep_wait();  // launched behind bwd_pre; nothing global has been read yet
 
   if (warp < 4) {
     regs_dec<kRegsLow>();
@@ -806,6 +811,7 @@ cudaError_t launch_main(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CU
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   dim3 grid(p.B * p.Hkv * ((p.N + kBK - 1) / kBK) * (DROP ? p.q_splits : 1));
+  if (DROP) return launch_behind(kern, grid, kMainThreads, stream, C::SMEM_BYTES, tmQ, tmK, tmV, tmdO, tmDQ, p);
   kern<<<grid, kMainThreads, C::SMEM_BYTES, stream>>>(tmQ, tmK, tmV, tmdO, tmDQ, p);
   return cudaGetLastError();
 }
@@ -817,16 +823,21 @@ cudaError_t launch(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtenso
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  // With dropout each kernel starts while the one before it in the stream ends.
+  const bool drop = p.drop.rng != nullptr;
   cudaError_t e = cudaSuccess;
   if (stages & kBwdPre) {
     const long long warps = (long long)p.B * p.Hq * p.Npad / kRowsPerWarp;
     const int pre_blocks = (int)std::min<long long>((warps + 7) / 8, (long long)sms * 8);
-    bwd_pre_kernel<D><<<pre_blocks, 256, 0, stream>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (drop)
+      e = launch_behind(bwd_pre_kernel<D>, pre_blocks, 256, stream, 0, p);
+    else
+      bwd_pre_kernel<D><<<pre_blocks, 256, 0, stream>>>(p);
+    if (e != cudaSuccess || (e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if (stages & kBwdMain) {
     e = p.bmask      ? launch_main<D, true, false>(tmQ, tmK, tmV, tmdO, tmDQ, p, stream)
-        : p.drop.rng ? launch_main<D, false, true>(tmQ, tmK, tmV, tmdO, tmDQ, p, stream)
+        : drop       ? launch_main<D, false, true>(tmQ, tmK, tmV, tmdO, tmDQ, p, stream)
                      : launch_main<D, false, false>(tmQ, tmK, tmV, tmdO, tmDQ, p, stream);
     if (e != cudaSuccess) return e;
   }
@@ -836,11 +847,13 @@ cudaError_t launch(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtenso
     if (p.q_splits > 1) {
       const long long threads = (long long)p.B * p.Hkv * p.N * 2 * (D / 4);
       const int join = (int)std::min<long long>((threads + 255) / 256, (long long)sms * 8);
-      bwd_join_kernel<D><<<cv_blocks + join, 256, 0, stream>>>(p, cv_blocks);
+      e = launch_behind(bwd_join_kernel<D>, cv_blocks + join, 256, stream, 0, p, cv_blocks);
+    } else if (drop) {
+      e = launch_behind(bwd_dq_kernel<D>, cv_blocks, 256, stream, 0, p);
     } else {
       bwd_dq_kernel<D><<<cv_blocks, 256, 0, stream>>>(p);
     }
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (e != cudaSuccess || (e = cudaGetLastError()) != cudaSuccess) return e;
   }
   return e;
 }

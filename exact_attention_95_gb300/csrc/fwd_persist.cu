@@ -39,6 +39,7 @@
 // no memory with another, so that captured graphs may run side by side.
 #include "dropout.cuh"
 #include "kernels.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 
 namespace attn {
@@ -177,6 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (DROP) griddep_wait();  // launched behind the kernel before; nothing global has been read yet
   const WaitCtx wc{abort_flag, p.status, p.wait_limit_ns};
 
   // Ring entry r: item index (-1: none left), then its decoded fields.  A
@@ -612,6 +614,7 @@ cudaError_t launch_persist(const CUtensorMap& tmQ, const CUtensorMap& tmK, const
   if (regs != kLaunchRegs) return cudaErrorInvalidKernelImage;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
+  if (DROP) return launch_behind(kern, ctas, kThreads, stream, C::SMEM_BYTES, tmQ, tmK, tmV, p);
   kern<<<ctas, kThreads, C::SMEM_BYTES, stream>>>(tmQ, tmK, tmV, p);
   return cudaGetLastError();
 }

@@ -38,6 +38,7 @@
 // (setmaxnreg), which hold a whole S row each.
 #include "dropout.cuh"
 #include "kernels.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 
 namespace attn {
@@ -191,6 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (DROP) griddep_wait();  // launched behind the kernel before; nothing global has been read yet
   if (masked) n_kv = *nlist;
   const WaitCtx wc{abort_flag, p.status, p.wait_limit_ns};
 
@@ -539,6 +541,7 @@ cudaError_t launch_one(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUt
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   dim3 grid(p.heads * p.n_pairs * p.n_splits);
+  if (DROP) return launch_behind(kern, grid, kThreads, stream, C::SMEM_BYTES, tmQ, tmK, tmV, p);
   kern<<<grid, kThreads, C::SMEM_BYTES, stream>>>(tmQ, tmK, tmV, p);
   return cudaGetLastError();
 }
