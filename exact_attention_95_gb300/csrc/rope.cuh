@@ -85,13 +85,13 @@ constexpr int rope_tokens(int d, int threads = kRopeThreads) { return threads / 
 // two pieces of eight: i.. and rot / 2 + i.. where halves pair, 16 adjacent
 // ones otherwise, so both are 16-byte accesses (32 in fp32) and pairs never leave a thread.
 template <class T, int D, bool INTER, int THREADS = kRopeThreads>
-__device__ __forceinline__ void rope_block(const RopeParams& p, long long group, int h0, int heads) {
+__device__ __forceinline__ void rope_block(const RopeParams& p, int group, int h0, int heads) {
   constexpr int UNITS = D / 16;
   constexpr int BATCH = sizeof(T) == 2 ? 4 : 2;  // heads in flight
   const int unit = threadIdx.x % UNITS;
-  const long long row = group * rope_tokens(D, THREADS) + threadIdx.x / UNITS;
-  if (row >= (long long)p.B * p.N) return;
-  const long long b = row / p.N, n = row - b * p.N;
+  const unsigned row = (unsigned)group * rope_tokens(D, THREADS) + threadIdx.x / UNITS;  // below 2^31 + 64
+  if (row >= (unsigned)p.B * (unsigned)p.N) return;
+  const long long b = p.B == 1 ? 0 : row / (unsigned)p.N, n = row - b * p.N;
   const bool halves = !INTER && unit < p.rot / 16;
   const int at = halves ? 8 * unit : 16 * unit, to = halves ? p.rot / 2 + 8 * unit : 16 * unit + 8;
   const int end = min(h0 + heads, p.Hq + p.Hkv);
