@@ -603,15 +603,21 @@ __global__ void __launch_bounds__(kMainThreads, 1)
     const uint32_t tS = tmem + lane_off + C::TM_S + 64 * h;
     const uint32_t tDP = tmem + lane_off + C::TM_DP + 64 * h;
     const float sl2 = p.scale_log2;
-    const DropKey drop_key(p.drop, DROP);
+    DropKey drop_key(p.drop, DROP);
+    uint32_t drop_group = 0;  // of 32 keys: the warp's
+    if (DROP) {
+      drop_key.uniform();
+      drop_group = warp_number(k0 / 32 + quad);
+    }
     uint32_t keep[2] = {0, 0};  // bit c of word w: (query column 32 w + c, this thread's key) is kept
     auto make_keep = [&](int t) {
       int g, it;
       tile_of(t, g, it);
+      const uint32_t bh = warp_number(b * p.Hq + hk * G + g);
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         uint32_t word[1];
-        keep_words(word, it * kBQ + 64 * h + 32 * w + lane, b * p.Hq + hk * G + g, k0 / 32 + quad, drop_key, p.drop);
+        keep_words(word, it * kBQ + 64 * h + 32 * w + lane, bh, drop_group, drop_key, p.drop);
         keep[w] = transpose_bits(word[0], lane);
       }
     };

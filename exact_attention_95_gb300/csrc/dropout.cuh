@@ -17,6 +17,9 @@
 
 namespace attn {
 
+// A number that is the same in all lanes, as the warp's (the reduction's result is one register a warp).
+__device__ __forceinline__ uint32_t warp_number(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
+
 struct DropKey {
   uint32_t seed0 = 0, seed1 = 0, offset = 0;
   __device__ __forceinline__ DropKey(const DropParams& p, bool on) {
@@ -25,6 +28,13 @@ struct DropKey {
     seed0 = (uint32_t)seed;
     seed1 = (uint32_t)(seed >> 32);
     offset = (uint32_t)p.rng[1];
+  }
+  // The same in what the compiler can tell to be one number a warp: round keys and the rounds that
+  // no lane's own numbers have entered are then kept and computed once a warp.
+  __device__ __forceinline__ void uniform() {
+    seed0 = warp_number(seed0);
+    seed1 = warp_number(seed1);
+    offset = warp_number(offset);
   }
 };
 
