@@ -304,6 +304,42 @@ def test_graphs_replayed_side_by_side_follow_their_numbers():
 
 
 @gpu
+@pytest.mark.parametrize("B,Hq,Hkv,N,d", [(1, 4, 2, 500, 128), (2, 2, 2, 100, 64), (4, 40, 40, 140, 64)])
+def test_steps_with_nothing_between_the_calls(B, Hq, Hkv, N, d):
+    """Each call overwrites what the call before it reads or writes (keys and values become the last step's
+    gradients, rotated; one workspace), and starts while that one ends: the bits are those of calls one at a time.
+    (dQ, whose sums have no fixed order, goes nowhere.)"""
+    Q, K0, V0, dO = _make(9, B, Hq, Hkv, N, d)
+    freqs, _ = pkg.attn_rope_freqs(d)
+    rng = _rng(4, 0)
+    ws = torch.empty(pkg.attn_bwd_dropout_workspace_size(B, Hq, Hkv, N, d, True), dtype=torch.uint8, device="cuda")
+
+    def run(wait):
+        K, V, dQ = K0.clone(), V0.clone(), torch.empty_like(Q)
+        dK, dV, O, L = torch.empty_like(K), torch.empty_like(K), torch.empty_like(Q), torch.empty(B, Hq, N, device="cuda")
+        seen = []
+        torch.cuda.synchronize()
+        calls = [lambda: pkg.attn_fwd_dropout(Q, K, V, 0.2, rng, None, True, O=O, LSE=L),
+                 lambda: pkg.attn_bwd_dropout(Q, K, V, O, dO, L, 0.2, rng, None, True, dQ, dK, dV, ws),
+                 lambda: pkg.attn_rope_bwd(dK, dV, freqs, dQ_out=K, dK_out=V, amplitude=4.0),
+                 lambda: pkg.attn_rope(K, None, freqs, Q_out=K)]
+        for _ in range(12):
+            for call in calls:
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+            seen += [O.clone(), L.clone()]
+        torch.cuda.synchronize()
+        return seen + [K, V, dK, dV]
+
+    want = run(True)
+    assert all(torch.isfinite(t).all() for t in want)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(run(False), want))
+    ok()
+
+
+@gpu
 @pytest.mark.parametrize("module", [True, False])
 def test_what_python_refuses(module, monkeypatch):
     if not module:

@@ -144,6 +144,21 @@ def test_strides_of_single_rows_and_repeated_inputs():
     assert pkg.attn_rope(x.new_empty(2, 4, 0, 64), None, freqs)[0].shape == (2, 4, 0, 64)
 
 
+def test_offsets_past_32_bits():
+    """Batches of a few tokens 2^32 elements and more apart (8 GB), in place."""
+    freqs, _ = pkg.attn_rope_freqs(128)
+    far = 2 ** 32 + 256
+    big = torch.empty(far + 8192, dtype=torch.bfloat16, device="cuda")
+    X = big.as_strided((2, 3, 5, 128), (far, 128, 768, 1))
+    X.copy_(_rand(8, 2, 3, 5, 128))
+    was = X.clone()
+    positions = torch.tensor([[1, 2, 3, 4, 5], [9, 8, 7, -1, 6]], dtype=torch.int32, device="cuda")
+    Y, _ = pkg.attn_rope(X, None, freqs, positions, Q_out=X)
+    ok()
+    assert Y is X
+    _check(X.contiguous(), was, positions.cpu().numpy().reshape(-1), freqs, False, 1.0)
+
+
 def test_gradient_against_differences():
     """The rotation is linear: differences of any size have no error of their own.  Per element in
     fp32, off by twice what each of the two rotations may be."""
