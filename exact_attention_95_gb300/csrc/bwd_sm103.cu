@@ -45,12 +45,15 @@
 // with D_i = <dO_i, O_i> as before.  Lane l of a math warp makes the keep words of query
 // rows l and 32 + l of its warpgroup's 64 against the warp's 32 keys, and two
 // transposes of 32 x 32 bits give every key's thread its 64 bits.  dV gets the
-// factor in its epilogue.
+// factor in its epilogue.  Measured, 32 heads of 4096 tokens twice, causal, d = 128: 742 us
+// for all three kernels (926 TFLOPS), without dropout 664; of the difference the words and
+// their transposes are two thirds, the masking of P and dP the rest.
 //
 // Where there are fewer key tiles than SMs (few kv heads, short sequences), a tile's
 // (query head, query tile) pairs are cut into p.q_splits equal parts with a CTA
 // each, which write fp32 dK and dV of their own into the workspace; bwd_join, in place of
-// bwd_dq, adds them in the order of the parts.
+// bwd_dq, adds them in the order of the parts (12 heads on 4, N = 777, twice: 45 us, in one
+// part 69; 16 heads on 1, N = 2000: 72 and 673).
 #include <algorithm>
 
 #include <type_traits>
@@ -622,8 +625,8 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       }
     };
     // The first tile's here, each further one's while the dQ product of the one before it runs: no
-    // other place of the step has as much time (before the scores: 778 us for 32 heads of
-    // 4096 tokens twice, here 769; before dV's end 785, behind the read-back 829).
+    // other place of the step has as much time (32 heads of 4096 tokens twice, when this was
+    // chosen: 769 us, before the scores 778, before dV's end 785, behind the read-back 829).
     if (DROP && T > 0) make_keep(0);
     bool ok = true;
     for (int t = 0; t < T; ++t) {

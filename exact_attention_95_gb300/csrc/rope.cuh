@@ -81,7 +81,11 @@ constexpr int rope_tokens(int d, int threads = kRopeThreads) { return threads / 
 //
 // HBM bound: every element is read and written once.  A thread computes the
 // eight angles of its pairs of one token once and takes all the CTA's heads
-// through them, a batch of heads' loads ahead of their use.  The 16 elements are
+// through them, a batch of heads' loads ahead of their use.  Measured (rope_kernel): 8192
+// tokens of 64 heads of 128, bf16, out of a packed projection 42.5 us, 6.3 TB/s, 94 % of the
+// measured copy rate; 64 tokens of 40 heads 2.4 us, a launch and two dependent
+// reads; 3003 tokens of 20 heads of 64 in fp32 7.5 to 8 us, which is mostly the start of a
+// grid of one round (30 MB).  The 16 elements are
 // two pieces of eight: i.. and rot / 2 + i.. where halves pair, 16 adjacent
 // ones otherwise, so both are 16-byte accesses (32 in fp32) and pairs never leave a thread.
 template <class T, int D, bool INTER, int THREADS = kRopeThreads>
