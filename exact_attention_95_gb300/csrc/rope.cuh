@@ -75,9 +75,9 @@ struct Eight<float> {
 
 constexpr int kRopeThreads = 256;
 // Tokens of a CTA: a thread has 16 elements of a row (eight pairs).
-constexpr int rope_tokens(int d, int threads = kRopeThreads) { return threads / (d / 16); }
+constexpr int rope_tokens(int d) { return kRopeThreads / (d / 16); }
 
-// Rotates `heads` heads from head `h0` on of a group of rope_tokens(D, THREADS) tokens.
+// Rotates `heads` heads from head `h0` on of a group of rope_tokens(D) tokens.
 //
 // HBM bound: every element is read and written once.  A thread computes the
 // eight angles of its pairs of one token once and takes all the CTA's heads
@@ -88,12 +88,12 @@ constexpr int rope_tokens(int d, int threads = kRopeThreads) { return threads / 
 // grid of one round (30 MB).  The 16 elements are
 // two pieces of eight: i.. and rot / 2 + i.. where halves pair, 16 adjacent
 // ones otherwise, so both are 16-byte accesses (32 in fp32) and pairs never leave a thread.
-template <class T, int D, bool INTER, int THREADS = kRopeThreads>
+template <class T, int D, bool INTER>
 __device__ __forceinline__ void rope_block(const RopeParams& p, int group, int h0, int heads) {
   constexpr int UNITS = D / 16;
   constexpr int BATCH = sizeof(T) == 2 ? 4 : 2;  // heads in flight
   const int unit = threadIdx.x % UNITS;
-  const unsigned row = (unsigned)group * rope_tokens(D, THREADS) + threadIdx.x / UNITS;  // below 2^31 + 64
+  const unsigned row = (unsigned)group * rope_tokens(D) + threadIdx.x / UNITS;  // below 2^31 + 64
   if (row >= (unsigned)p.B * (unsigned)p.N) return;
   const long long b = p.B == 1 ? 0 : row / (unsigned)p.N, n = row - b * p.N;
   const bool halves = !INTER && unit < p.rot / 16;

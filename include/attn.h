@@ -272,8 +272,8 @@ attn_status attn_bwd_noalloc(const void* Q, const void* K, const void* V, const 
  *   rng [2] in device memory, 8-byte aligned: seed, offset (its low 32 bits count).  Read when the
  *       kernels run, so a captured step follows new numbers; the backward has to
  *       be given the numbers of its forward, and calls that are to differ other offsets.
- *   Q, K, V bf16; the other arguments and rules are attn_fwd's.  A row whose kept keys are all
- *   dropped gets O = 0.  Captured calls may be replayed side by side: no launch shares
+ *   Q, K, V bf16; the other arguments and rules are attn_fwd's.  A row all of whose keys are
+ *   dropped gets O = 0 (an infinity or NaN in V times a weight of 0 is NaN, here as there).  Captured calls may be replayed side by side: no launch shares
  *   memory of the library with another.
  * With T = 0 the calls are attn_fwd and attn_bwd (whose rules on captured graphs then hold).
  */
@@ -488,6 +488,8 @@ typedef struct {
  *   freqs [rot / 2] in device memory, 8-byte aligned; rot a multiple of 16, at most d
  *   (other multiples: ATTN_ERR_UNSUPPORTED); d in {64, 128}; dtype bf16 or fp32 of all
  *   rows; amplitude finite and positive; N may be 0 (nothing is done).
+ * Hq + Hkv <= 65535 and B * N < 2^31, else ATTN_ERR_UNSUPPORTED.  An infinity or NaN is
+ * one in its pair.
  */
 attn_status attn_rope(const attn_rows* Q, const attn_rows* K, const attn_rows* Q_out, const attn_rows* K_out,
                       const int32_t* positions, long long positions_batch, const uint64_t* freqs, int rot,

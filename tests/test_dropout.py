@@ -4,6 +4,10 @@ bounds derived there."""
 
 import ctypes
 import math
+import os
+import subprocess
+import sys
+import threading
 
 import pytest
 import torch
@@ -169,7 +173,7 @@ SHAPES = [
     # B, Hq, Hkv, N, d
     (1, 1, 1, 1, 64), (2, 4, 2, 1, 128), (1, 8, 2, 31, 64), (1, 8, 2, 32, 128), (1, 8, 2, 33, 64),  # groups in one tile
     (2, 2, 2, 100, 128), (1, 4, 1, 100, 64), (1, 3, 3, 128, 64), (1, 2, 1, 129, 128), (1, 4, 2, 255, 64),
-    (2, 4, 2, 257, 128), (1, 6, 2, 513, 128), (1, 16, 1, 650, 64), (1, 2, 2, 1000, 64), (2, 16, 4, 700, 128), (1, 2, 1, 2500, 128),
+    (2, 4, 2, 257, 128), (1, 6, 2, 513, 128), (1, 16, 1, 650, 64), (1, 2, 2, 1000, 64), (2, 16, 4, 700, 128), (1, 2, 1, 2500, 128), (5, 40, 8, 520, 64),  # more key tiles than SMs
 ]
 
 
@@ -382,6 +386,75 @@ def test_the_calls_give_the_same_without_the_module(N, monkeypatch):
         got.append((O, L, O32, dK, dV))
     ok()
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+FIRST = """
+import torch
+import exact_attention_95_gb300 as pkg
+B, Hq, Hkv, N, d = 1, 4, 2, %d, %d
+g = torch.Generator(device="cuda").manual_seed(1)
+x = torch.randn(B, N, Hq + 2 * Hkv, d, generator=g, device="cuda").bfloat16()
+q, k = x[:, :, :Hq].transpose(1, 2), x[:, :, Hq:Hq + Hkv].transpose(1, 2)
+v = x[:, :, Hq + Hkv:].transpose(1, 2).contiguous()
+dO = torch.randn(B, Hq, N, d, generator=g, device="cuda").bfloat16()
+freqs, _ = pkg.attn_rope_freqs(d)
+rng = torch.tensor([3, 4], device="cuda")
+def step():
+    Q, K = pkg.attn_rope(q, k, freqs)
+    O, L = pkg.attn_fwd_dropout(Q, K, v, 0.1, rng, None, True)
+    dQ, dK, dV = pkg.attn_bwd_dropout(Q, K, v, O, dO, L, 0.1, rng, None, True)
+    gq, gk = pkg.attn_rope_bwd(dQ, dK, freqs)
+    return Q, K, O, L, dV, gk
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = step()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in out]
+want = step()
+torch.cuda.synchronize()
+assert pkg.attn_last_device_status() == pkg.ATTN_OK
+assert all(torch.equal(a, b) for a, b in zip(got, want)) and float(got[2].float().abs().max()) > 0
+print("captured first")
+"""
+
+
+@gpu
+@pytest.mark.parametrize("N,d", [(90, 64), (600, 128)])
+def test_the_first_calls_of_a_process_inside_a_capture(N, d):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST % (N, d)], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
+
+
+@gpu
+def test_threads_with_a_stream_each():
+    data = [_make(30 + i, 1, 4, 2, 300 + 100 * i, 64) for i in range(4)]
+    rng = _rng()
+
+    def one(Q, K, V, dO):
+        O, L = pkg.attn_fwd_dropout(Q, K, V, 0.4, rng, None, True)
+        _, dK, dV = pkg.attn_bwd_dropout(Q, K, V, O, dO, L, 0.4, rng, None, True)
+        return O, L, dK, dV
+
+    want = [one(*d) for d in data]
+    torch.cuda.synchronize()
+    got = [None] * len(data)
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(10):
+                got[i] = one(*data[i])
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(data))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    ok()
+    assert all(torch.equal(a, b) for g, w in zip(got, want) for a, b in zip(g, w))
 
 
 # ------------------------------------------------------------------ a layer's step
