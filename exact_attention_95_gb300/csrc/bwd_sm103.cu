@@ -52,8 +52,8 @@
 // Where there are fewer key tiles than SMs (few kv heads, short sequences), a tile's
 // (query head, query tile) pairs are cut into p.q_splits equal parts with a CTA
 // each, which write fp32 dK and dV of their own into the workspace; bwd_join, in place of
-// bwd_dq, adds them in the order of the parts (12 heads on 4, N = 777, twice: 45 us, in one
-// part 69; 16 heads on 1, N = 2000: 72 and 673).
+// bwd_dq, adds them in the order of the parts (12 heads on 4, N = 777, twice: 35 us, in one
+// part 66; 16 heads on 1, N = 2000: 78 and 648).
 #include <algorithm>
 
 #include <type_traits>
@@ -246,26 +246,51 @@ __device__ __forceinline__ int pairs_of(const BwdParams& p, int jt) {
 }
 __device__ __forceinline__ int pairs_of_part(const BwdParams& p, int pairs) { return (pairs + p.q_splits - 1) / p.q_splits; }
 
-// dK, dV = bf16(sum of the parts' fp32 ones), 16 bytes of a row a thread at a time.
+// A part's fp32 rows of a key tile lie as [four columns][row]: a warp's 32 rows are written and
+// read 512 bytes at a time (row by row, 16 of every 512, a step of 256 CTAs took 20 us longer).
+// float4 of (which: 0 dV, 1 dK; kv head; key; columns 4 c ..) in part 0, and from part to part.
+template <int D>
+__device__ __forceinline__ size_t part_at(const BwdParams& p, int which, long long bhk, int key, int c) {
+  return (((size_t)which * p.B * p.Hkv + bhk) * p.Npad + key / kBK * kBK) * (D / 4) + c * kBK + key % kBK;
+}
+template <int D>
+__device__ __forceinline__ size_t part_stride(const BwdParams& p) {
+  return (size_t)2 * p.B * p.Hkv * p.Npad * (D / 4);
+}
+
+// dK, dV = bf16(sum of the parts' fp32 ones): 16 columns of a key a thread, neighbours have neighbouring keys.
 template <int D>
 __device__ __forceinline__ void dkv_rows(const BwdParams& p, int block, int blocks) {
-  constexpr int V4 = D / 4;
-  const long long rows = (long long)p.B * p.Hkv * p.N, half = rows * V4;  // dV's, then dK's
-  const size_t part = (size_t)2 * p.B * p.Hkv * p.Npad * V4;              // float4 from part to part
-  for (long long i = (long long)block * blockDim.x + threadIdx.x; i < 2 * half; i += (long long)blocks * blockDim.x) {
-    const int which = i >= half;
-    const long long e = i - which * half, row = e / V4, bhk = row / p.N;
-    const int key = (int)(row - bhk * p.N), col = (int)(e - row * V4), pairs = pairs_of(p, key / kBK);
-    const int each = pairs_of_part(p, pairs), n = (pairs + each - 1) / each;
-    const float4* src = reinterpret_cast<const float4*>(p.parts) +
-                        ((size_t)which * p.B * p.Hkv * p.Npad + (size_t)bhk * p.Npad + key) * V4 + col;
-    float4 sum = src[0];
-    for (int k = 1; k < n; ++k) {
-      const float4 v = src[k * part];
-      sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
-    }
-    *reinterpret_cast<uint2*>((which ? p.dK : p.dV) + row * D + 4 * col) =
-        make_uint2(pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w));
+  constexpr int PIECES = D / 16;
+  const long long rows = (long long)p.B * p.Hkv * p.Npad, all = 2 * rows * PIECES;
+  const size_t stride = part_stride<D>(p);
+  for (long long i = (long long)block * blockDim.x + threadIdx.x; i < all; i += (long long)blocks * blockDim.x) {
+    // i: dV's then dK's heads' tiles' pieces' keys
+    const int in_tile = (int)(i % kBK);
+    long long rest = i / kBK;
+    const int piece = (int)(rest % PIECES);
+    rest /= PIECES;
+    const long long tiles = p.Npad / kBK, head = rest / tiles;
+    const int jt = (int)(rest - head * tiles), key = jt * kBK + in_tile;
+    if (key >= p.N) continue;
+    const int which = head >= (long long)p.B * p.Hkv;
+    const long long bhk = head - which * (long long)p.B * p.Hkv;
+    const int pairs = pairs_of(p, jt), each = pairs_of_part(p, pairs), n = (pairs + each - 1) / each;
+    const float4* src = reinterpret_cast<const float4*>(p.parts) + part_at<D>(p, which, bhk, key, 4 * piece);
+    float4 sum[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) sum[c] = src[c * kBK];
+    for (int k = 1; k < n; ++k)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float4 v = src[k * stride + c * kBK];
+        sum[c] = make_float4(sum[c].x + v.x, sum[c].y + v.y, sum[c].z + v.z, sum[c].w + v.w);
+      }
+    uint4* dst = reinterpret_cast<uint4*>((which ? p.dK : p.dV) + (bhk * p.N + key) * D + 16 * piece);
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      dst[c] = make_uint4(pack_bf16(sum[2 * c].x, sum[2 * c].y), pack_bf16(sum[2 * c].z, sum[2 * c].w),
+                          pack_bf16(sum[2 * c + 1].x, sum[2 * c + 1].y), pack_bf16(sum[2 * c + 1].z, sum[2 * c + 1].w));
   }
 }
 
@@ -769,12 +794,12 @@ __global__ void __launch_bounds__(kMainThreads, 1)
           if (DROP && splits > 1) {
             // (A part without pairs is not read.)
             if (have && key_ok && dcheck(split < splits && bhk < p.B * p.Hkv, p.status)) {
-              float4* f4 = reinterpret_cast<float4*>(
-                  p.parts + ((size_t)(2 * split + which) * p.B * p.Hkv * p.Npad + (size_t)bhk * p.Npad + key) * D + col);
+              float4* f4 = reinterpret_cast<float4*>(p.parts) + split * part_stride<D>(p) +
+                           part_at<D>(p, which, bhk, key, col / 4);
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                f4[i] = make_float4(__uint_as_float(o[4 * i]) * mul, __uint_as_float(o[4 * i + 1]) * mul,
-                                    __uint_as_float(o[4 * i + 2]) * mul, __uint_as_float(o[4 * i + 3]) * mul);
+                f4[i * kBK] = make_float4(__uint_as_float(o[4 * i]) * mul, __uint_as_float(o[4 * i + 1]) * mul,
+                                          __uint_as_float(o[4 * i + 2]) * mul, __uint_as_float(o[4 * i + 3]) * mul);
             }
           } else if (key_ok && dcheck(row < (size_t)p.B * p.Hkv * p.N, p.status)) {
             uint4* d4 = reinterpret_cast<uint4*>(dst + col);
@@ -854,7 +879,7 @@ cudaError_t launch(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtenso
     const long long warps = (long long)p.B * p.Hq * p.Npad / kRowsPerWarp;
     const int cv_blocks = (int)std::min<long long>((warps + 7) / 8, (long long)sms * 8);
     if (p.q_splits > 1) {
-      const long long threads = (long long)p.B * p.Hkv * p.N * 2 * (D / 4);
+      const long long threads = (long long)p.B * p.Hkv * p.Npad * 2 * (D / 16);
       const int join = (int)std::min<long long>((threads + 255) / 256, (long long)sms * 8);
       e = launch_behind(bwd_join_kernel<D>, cv_blocks + join, 256, stream, 0, p, cv_blocks);
     } else if (drop) {
@@ -877,21 +902,31 @@ size_t bwd_workspace_bytes(int B, int Hq, int N, int d) {
   return (rows * d * 4 + 255) / 256 * 256 + 2 * ((rows * 4 + 255) / 256 * 256);
 }
 
-// Parts of a key tile's pairs: the number that ends first, by a count of rounds of CTAs, one an
-// SM, each as long as its pairs and two more (its start, and fp32 rows written and read again).
-// Causal tiles differ by up to all their pairs, heaviest first: the longest part, or the
-// average of all.  Only where an unsplit grid leaves SMs idle.
+// Parts of a key tile's pairs: the number that ends first by a count in steps (a pair's time,
+// 2.1 us).  A CTA takes its pairs and three more (its start, its end), one to an SM at a time;
+// equal parts in rounds, causal tiles' (which differ by up to all their pairs, heaviest
+// first) until the longest is done or, where they are more than the SMs, for the average
+// load of an SM and half a CTA more; and a part's sums are written and read again,
+// an eightieth of a step each.  Only where an unsplit grid leaves SMs idle.
+// Measured by the number of parts, us: 12 heads on 4, N = 777, twice, causal 1 66, 2 43.6, 3 35.0 (taken),
+// 4 37.9, 8 46.6; not causal 1 67, 2 43.7 (taken), 3 57, 5 50.6; 32 on 8, N = 1000, causal 1 96, 2 59.7,
+// 3 49.8 (taken), 4 50.7; 8 on 2, N = 4096, causal 1 331, 3 129, 4 103 (taken), 5 107; 4 heads, N = 4096,
+// causal 1 93, 2 65 (taken), 3 74; 16 heads, N = 256, four times 1 18 (taken), 2 30.
 int bwd_q_splits(int B, int Hq, int Hkv, int N, int causal, int sms) {
   const long long tiles = (N + kBK - 1) / kBK, ctas = (long long)B * Hkv * tiles, most = (long long)(Hq / Hkv) * tiles;
   if (ctas >= sms) return 1;
   constexpr int kMostParts = 16;
+  constexpr double kOwn = 3.0, kJoin = 1.0 / 80;
+  const double average = causal ? most * (tiles + 1) / (2.0 * tiles) : (double)most;  // pairs of a tile
   double best = 0;
   int parts = 1;
   for (int s = 1; s <= std::min<long long>(kMostParts, most); ++s) {
-    const double longest = (double)((most + s - 1) / s) + (s > 1 ? 2 : 1);
-    const double all = (double)ctas * ((causal ? most * (tiles + 1) / (2.0 * tiles) : (double)most) + s * 2.0) / sms;
-    const double cost = causal ? std::max(longest, all) : longest * (double)((ctas * s + sms - 1) / sms);
-    if (s == 1 || cost < best * 0.95) {
+    const long long all = ctas * s;
+    const double longest = (double)((most + s - 1) / s) + kOwn;
+    const double load = (ctas * average + all * kOwn) / sms + (average / s + kOwn) / 2;
+    double cost = !causal ? longest * (double)((all + sms - 1) / sms) : all <= sms ? longest : std::max(longest, load);
+    if (s > 1) cost += kJoin * all;
+    if (s == 1 || cost < best * 0.97) {
       best = cost;
       parts = s;
     }

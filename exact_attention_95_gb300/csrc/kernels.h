@@ -137,7 +137,7 @@ struct BwdParams {
   int bmask_heads;
   DropParams drop;  // drop.rng NULL: no dropout (with a block mask there is none)
   // With dropout: parts of a key tile's (query head, query tile) pairs, a CTA each, and
-  // where they are more than one their fp32 [q_splits][dV, dK][B, Hkv, Npad, d].
+  // where they are more than one their fp32 dV and dK [q_splits][2][B, Hkv, Npad / 128][d / 4][128][4].
   int q_splits;
   float* parts;
 };
