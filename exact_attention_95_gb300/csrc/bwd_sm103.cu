@@ -45,8 +45,8 @@
 // with D_i = <dO_i, O_i> as before.  Lane l of a math warp makes the keep words of query
 // rows l and 32 + l of its warpgroup's 64 against the warp's 32 keys, and two
 // transposes of 32 x 32 bits give every key's thread its 64 bits.  dV gets the
-// factor in its epilogue.  Measured, 32 heads of 4096 tokens twice, causal, d = 128: 742 us
-// for all three kernels (926 TFLOPS), without dropout 664; of the difference the words and
+// factor in its epilogue.  Measured, 32 heads of 4096 tokens twice, causal, d = 128: 738 us
+// for all three kernels (931 TFLOPS), without dropout 663; of the difference the words and
 // their transposes are two thirds, the masking of P and dP the rest.
 //
 // Where there are fewer key tiles than SMs (few kv heads, short sequences), a tile's
@@ -638,21 +638,28 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       drop_group = warp_number(k0 / 32 + quad);
     }
     uint32_t keep[2] = {0, 0};  // bit c of word w: (query column 32 w + c, this thread's key) is kept
-    auto make_keep = [&](int t) {
-      int g, it;
-      tile_of(t, g, it);
-      const uint32_t bh = warp_number(b * p.Hq + hk * G + g);
+    int ahead_g = 0, ahead_it = 0;  // the tile that the words are next made for
+    if (DROP) tile_of(0, ahead_g, ahead_it);
+    auto make_keep = [&]() {
+      const uint32_t bh = warp_number(b * p.Hq + hk * G + ahead_g);
+      const int row = ahead_it * kBQ + 64 * h + lane;
+      if (++ahead_it == n_q) {
+        ahead_it = i0;
+        ++ahead_g;
+      }
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         uint32_t word[1];
-        keep_words(word, it * kBQ + 64 * h + 32 * w + lane, bh, drop_group, drop_key, p.drop);
+        keep_words(word, row + 32 * w, bh, drop_group, drop_key, p.drop);
         keep[w] = transpose_bits(word[0], lane);
       }
     };
     // The first tile's here, each further one's while the dQ product of the one before it runs: no
     // other place of the step has as much time (32 heads of 4096 tokens twice, when this was
-    // chosen: 769 us, before the scores 778, before dV's end 785, behind the read-back 829).
-    if (DROP && T > 0) make_keep(0);
+    // chosen: 769 us, before the scores 778, before dV's end 785, behind the read-back 829).  They
+    // take 1130 cycles, the wait there had 820; a word in each of two places, or a
+    // warpgroup in each, took as long a word as both here (763 to 830 us).
+    if (DROP && T > 0) make_keep();
     bool ok = true;
     for (int t = 0; t < T; ++t) {
       const int s = t % C::STAGES;
@@ -737,7 +744,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
         sts_u4(dsrow + ((c ^ (kr & 7)) << 4), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
       fence_async_smem();
       mbar_arrive(bar(C::B_DSSMEM));
-      if (DROP && t + 1 < T) make_keep(t + 1);
+      if (DROP && t + 1 < T) make_keep();
       // ---- dQ^T readback: 64 query columns of head-dim row dcol.
       if (!mbar_wait(bar(C::B_DQFULL), t & 1, wc)) {
         ok = false;
