@@ -273,8 +273,9 @@ attn_status attn_bwd_noalloc(const void* Q, const void* K, const void* V, const 
  *       kernels run, so a captured step follows new numbers; the backward has to
  *       be given the numbers of its forward, and calls that are to differ other offsets.
  *   Q, K, V bf16; the other arguments and rules are attn_fwd's.  A row all of whose keys are
- *   dropped gets O = 0 (an infinity or NaN in V times a weight of 0 is NaN, here as there).  Captured calls may be replayed side by side: no launch shares
- *   memory of the library with another.
+ *   dropped gets O = 0 (an infinity or NaN in V times a weight of 0 is NaN, here as there).
+ *   Captured calls may be replayed side by side: no launch shares memory of the library
+ *   with another.
  * With T = 0 the calls are attn_fwd and attn_bwd (whose rules on captured graphs then hold).
  */
 attn_status attn_fwd_dropout(const void* Q, const void* K, const void* V, void* O, float* LSE, int B, int Hq, int Hkv,
