@@ -660,8 +660,9 @@ __global__ void __launch_bounds__(kMainThreads, 1)
     // take 1130 cycles, the wait there had 820; a word in each of two places, or a
     // warpgroup in each, took as long a word as both here (763 to 830 us).
     if (DROP && T > 0) make_keep();
+    // (Each with one result for its warp: TMEM and the words are for whole warps.)
     auto wait = [&](uint32_t b, uint32_t parity) {
-      return DROP ? mbar_wait_warp(b, parity, wc) : mbar_wait(b, parity, wc);
+      return DROP ? mbar_wait_warp_short(b, parity, wc) : mbar_wait_warp(b, parity, wc);
     };
     bool ok = true;
     for (int t = 0; t < T; ++t) {
@@ -670,90 +671,86 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       tile_of(t, g, it);
       const int qh0 = it * kBQ + 64 * h;  // first query column of this half
       const uint32_t st = stage(s);
-      do {
-        if (!mbar_wait(bar(C::B_STFULL + s), (t / C::STAGES) & 1, wc) ||
-            !mbar_wait(bar(C::B_SFULL), t & 1, wc)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        // ---- P for this warpgroup's 64 query columns.
-        uint32_t sr[2][32];
-        tmem_ld32(tS, sr[0]);
-        tmem_ld32(tS + 32, sr[1]);
-        tmem_ld_wait(sr[0]);
-        reg_fence32(sr[1]);
-        uint64_t pv2[32];  // P, column pairs
-        uint32_t pk[32];
-        const uint32_t lse_addr = st + C::ST_LSE + 4 * 64 * h;
-        // Tile-uniform test: a ragged key tile, or a causal tile that crosses the diagonal.
-        if (k0 + kBK > p.N || (p.causal && qh0 < k0 + kBK - 1)) {
-          const int cmin = !key_ok ? 64 : (p.causal ? max(0, key - qh0) : 0);
-          bwd_probs<true, DROP>(sr, lse_addr, sl2, cmin, keep, pv2, pk);
-        } else {
-          bwd_probs<false, DROP>(sr, lse_addr, sl2, 0, keep, pv2, pk);
-        }
-        tmem_st32(tS, pk);
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(bar(C::B_PFULL));
-        // ---- dS = P (dP - D), 32 columns at a time (the workspace holds -D).
-        if (!mbar_wait(bar(C::B_DPFULL), t & 1, wc)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
+      if (!wait(bar(C::B_STFULL + s), (t / C::STAGES) & 1)) {
+        ok = false;
+        break;
+      }
+      if (!wait(bar(C::B_SFULL), t & 1)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      // ---- P for this warpgroup's 64 query columns.
+      uint32_t sr[2][32];
+      tmem_ld32(tS, sr[0]);
+      tmem_ld32(tS + 32, sr[1]);
+      tmem_ld_wait(sr[0]);
+      reg_fence32(sr[1]);
+      uint64_t pv2[32];  // P, column pairs
+      uint32_t pk[32];
+      const uint32_t lse_addr = st + C::ST_LSE + 4 * 64 * h;
+      // Tile-uniform test: a ragged key tile, or a causal tile that crosses the diagonal.
+      if (k0 + kBK > p.N || (p.causal && qh0 < k0 + kBK - 1)) {
+        const int cmin = !key_ok ? 64 : (p.causal ? max(0, key - qh0) : 0);
+        bwd_probs<true, DROP>(sr, lse_addr, sl2, cmin, keep, pv2, pk);
+      } else {
+        bwd_probs<false, DROP>(sr, lse_addr, sl2, 0, keep, pv2, pk);
+      }
+      tmem_st32(tS, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(bar(C::B_PFULL));
+      // ---- dS = P (dP - D), 32 columns at a time (the workspace holds -D).
+      if (!wait(bar(C::B_DPFULL), t & 1)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t dr[32];
-          tmem_ld32(tDP + 32 * half, dr);
-          tmem_ld_wait(dr);
+      for (int half = 0; half < 2; ++half) {
+        uint32_t dr[32];
+        tmem_ld32(tDP + 32 * half, dr);
+        tmem_ld_wait(dr);
 #pragma unroll
-          for (int c4 = 0; c4 < 8; ++c4) {
-            const float4 nd = lds_f4(st + C::ST_D + 4 * (64 * h + 32 * half + 4 * c4));
+        for (int c4 = 0; c4 < 8; ++c4) {
+          const float4 nd = lds_f4(st + C::ST_D + 4 * (64 * h + 32 * half + 4 * c4));
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int cp = 16 * half + 2 * c4 + u;  // column pair index
-              const int c = 4 * c4 + 2 * u;  // column of dr
-              const uint64_t nd2 = u == 0 ? f2pack(nd.x, nd.y) : f2pack(nd.z, nd.w);
-              uint64_t t2;
-              if (DROP) {
-                const float d0 = (keep[half] >> c) & 1 ? __uint_as_float(dr[c]) : 0.f;
-                const float d1 = (keep[half] >> (c + 1)) & 1 ? __uint_as_float(dr[c + 1]) : 0.f;
-                t2 = ffma2(f2pack(d0, d1), f2pack(p.drop.mul, p.drop.mul), nd2);
-              } else {
-                t2 = fadd2(f2pack(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])), nd2);
-              }
-              const uint64_t ds2 = fmul2(pv2[cp], t2);
-              float d0, d1;
-              f2unpack(ds2, d0, d1);
-              pk[cp] = pack_bf16(d0, d1);
+          for (int u = 0; u < 2; ++u) {
+            const int cp = 16 * half + 2 * c4 + u;  // column pair index
+            const int c = 4 * c4 + 2 * u;  // column of dr
+            const uint64_t nd2 = u == 0 ? f2pack(nd.x, nd.y) : f2pack(nd.z, nd.w);
+            uint64_t t2;
+            if (DROP) {
+              const float d0 = (keep[half] >> c) & 1 ? __uint_as_float(dr[c]) : 0.f;
+              const float d1 = (keep[half] >> (c + 1)) & 1 ? __uint_as_float(dr[c + 1]) : 0.f;
+              t2 = ffma2(f2pack(d0, d1), f2pack(p.drop.mul, p.drop.mul), nd2);
+            } else {
+              t2 = fadd2(f2pack(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])), nd2);
             }
+            const uint64_t ds2 = fmul2(pv2[cp], t2);
+            float d0, d1;
+            f2unpack(ds2, d0, d1);
+            pk[cp] = pack_bf16(d0, d1);
           }
         }
-        tmem_st32(tS + 32, pk);
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(bar(C::B_DSTMEM));
-        // dS^T rows into the dO slot (dV, its last reader, must be complete):
-        // block h holds query columns [64h, 64h+64); row kr is 128 bytes with
-        // the 16-byte chunk c stored at chunk position c ^ (kr & 7).
-        if (!mbar_wait(bar(C::B_DVDONE), t & 1, wc)) {
-          ok = false;
-          break;
-        }
-        const uint32_t dsrow = st + C::ST_DO + h * C::BLK + kr * 128;
+      }
+      tmem_st32(tS + 32, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(bar(C::B_DSTMEM));
+      // dS^T rows into the dO slot (dV, its last reader, must be complete):
+      // block h holds query columns [64h, 64h+64); row kr is 128 bytes with
+      // the 16-byte chunk c stored at chunk position c ^ (kr & 7).
+      if (!wait(bar(C::B_DVDONE), t & 1)) {
+        ok = false;
+        break;
+      }
+      const uint32_t dsrow = st + C::ST_DO + h * C::BLK + kr * 128;
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          sts_u4(dsrow + ((c ^ (kr & 7)) << 4), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-        fence_async_smem();
-        mbar_arrive(bar(C::B_DSSMEM));
-      } while (false);
-      // With dropout a wait that ran out ends its warp's work, not the lane's alone: the words
-      // are made by whole warps.  (One vote for the waits above: 750 us where none took 741, one in
-      // each wait 781.)
-      if (DROP) ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
+      for (int c = 0; c < 8; ++c)
+        sts_u4(dsrow + ((c ^ (kr & 7)) << 4), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+      fence_async_smem();
+      mbar_arrive(bar(C::B_DSSMEM));
       if (DROP && t + 1 < T) make_keep();
       // ---- dQ^T readback: 64 query columns of head-dim row dcol.
       if (!wait(bar(C::B_DQFULL), t & 1)) {
@@ -789,7 +786,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
     // head-dim columns [h*D/2, (h+1)*D/2).
     // (A key tile that no kept block reaches writes zero dK and dV.)
     const bool have = T > 0;
-    if (ok && (!have || mbar_wait(bar(C::B_KVDONE), (T - 1) & 1, wc))) {
+    if (ok && (!have || mbar_wait_warp(bar(C::B_KVDONE), (T - 1) & 1, wc))) {
       if (have) tc_fence_after();
       const size_t row = (size_t)bhk * p.N + key;
 #pragma unroll

@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int k0 = j * kBN;
       const float skj = skh[j];
       const float svj = svh[j];
-      if (!mbar_wait(bar(C::B_SFULL + t), j & 1, wc)) {
+      if (!mbar_wait_warp(bar(C::B_SFULL + t), j & 1, wc)) {
         ok = false;
         break;
       }
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (j > 0) {
         // P'_t V of the previous tile must be complete: it reads the P'_t
         // tile written below, and O_t may be rescaled.
-        if (!mbar_wait(bar(C::B_ODONE + t), (j - 1) & 1, wc)) {
+        if (!mbar_wait_warp(bar(C::B_ODONE + t), (j - 1) & 1, wc)) {
           ok = false;
           break;
         }
@@ -447,11 +447,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // Epilogue: O = max(sv) O' / (l - corr), LSE = (m - shift + log2 l) ln 2.
     // bf16 rows go out through this warp's quarter of the tile's P' buffer,
-    // free once the tile's last P' V has completed.  The staging needs the
-    // whole warp: a warp some of whose lanes gave up (a timed-out wait, already
-    // in the status word) writes nothing.
-    const bool ep = ok && mbar_wait(bar(C::B_ODONE + t), (n_kv - 1) & 1, wc);
-    if (__all_sync(0xffffffffu, ep)) {
+    // free once the tile's last P' V has completed.  A warp whose wait ran out
+    // (already in the status word) writes nothing.
+    const bool ep = ok && mbar_wait_warp(bar(C::B_ODONE + t), (n_kv - 1) & 1, wc);
+    if (ep) {
       tc_fence_after();
       const float lo = l - corr;
       const float inv_l = lo > 0.f ? svm / lo : 0.f;

@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool on = !masked || ((tlist[j] >> (15 - t)) & 1);  // this tile keeps the block
       uint32_t keep[4];
       if (DROP) keep_words(keep, qc, drop_head, k0 / 32, drop_key, p.drop);
-      if (!mbar_wait(bar(C::B_SFULL + t), j & 1, wc)) {
+      if (!mbar_wait_warp(bar(C::B_SFULL + t), j & 1, wc)) {
         ok = false;
         break;
       }
@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (j > 0) {
         // P_t V of the previous tile must be complete: it reads the P_t
         // columns written below, and O_t may be rescaled.
-        if (!mbar_wait(bar(C::B_ODONE + t), (j - 1) & 1, wc)) {
+        if (!mbar_wait_warp(bar(C::B_ODONE + t), (j - 1) & 1, wc)) {
           ok = false;
           break;
         }
@@ -465,12 +465,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // Epilogue: O / l and LSE (O = 0, LSE = -inf when no key was in range).
     const bool have = n_kv > 0;
-    const bool ep = ok && active && (!have || mbar_wait(bar(C::B_ODONE + t), (n_kv - 1) & 1, wc));
+    const bool ep = ok && active && (!have || mbar_wait_warp(bar(C::B_ODONE + t), (n_kv - 1) & 1, wc));
     // bf16 rows go out through this warp's quarter of its Q tile, free once
     // the tile's last P V -- and with it every product of the tile -- has
-    // completed.  The staging needs the whole warp: a warp some of whose lanes
-    // gave up (a timed-out wait, already in the status word) writes nothing.
-    if (__all_sync(0xffffffffu, ep)) {
+    // completed.  A warp whose wait ran out (already in the status word) writes
+    // nothing.
+    if (ep) {
       if (have) tc_fence_after();
       // O is divided by the row sum less the rounding of each tile's largest
       // P: when one key dominates a row, its bf16 rounding then cancels
