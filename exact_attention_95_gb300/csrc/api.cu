@@ -385,6 +385,7 @@ bool drop_params(float p, const void* rng, DropParams& out, int& T) {
   out.rng = static_cast<const unsigned long long*>(rng);
   for (int k = 0; k < 8; ++k) out.not_t[k] = (T >> k) & 1 ? 0u : 0xffffffffu;
   out.mul = 256.f / (float)(256 - T);
+  out.mostly_kept = T < 128;
   return true;
 }
 

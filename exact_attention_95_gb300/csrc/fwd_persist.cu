@@ -35,8 +35,9 @@
 // With dropout (DROP; dropout.cuh) a softmax warp makes its rows' keep words of a tile
 // before it waits for the tile's scores, sums the row as without, and clears
 // the dropped elements in P as it is packed; 1 / (1 - T / 256) goes into 1 / l.  (O is divided by
-// l less the rounding of each tile's largest P, also where that element was
-// dropped: half a bf16 step, as much as the correction saves elsewhere.)  Measured, 32
+// l less the rounding of each tile's largest P: right for rows that keep that element, off by up to half a
+// bf16 step in those that drop it.  It is done where more keep it, T < 128; elsewhere O is divided
+// by l, and rows that keep it have its rounding, those that drop it none.)  Measured, 32
 // heads of 4096 tokens twice, causal, d = 128: 250 us, 1100 TFLOPS; without dropout 190.  A step
 // of both tiles takes 4150 cycles instead of 2900: the words 1000 of them (80 wide
 // multiplies a row, 5.2 cycles of their pipe each, and what hangs on them), the
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int split = e[R_SPLIT];
       float* const o_out = p.out_f32 ? static_cast<float*>(p.O) + split * p.o_split_stride : nullptr;
       uint16_t* const o_out16 = p.out_f32 ? nullptr : static_cast<uint16_t*>(p.O);
-      const float lo = l - corr;
+      const float lo = DROP && !p.drop.mostly_kept ? l : l - corr;
       const float inv_l = lo > 0.f ? (DROP ? p.drop.mul : 1.f) / lo : 0.f;
       const int bh = e[R_BH];
       const bool bh_ok = dcheck(bh >= 0 && bh < p.heads && split >= 0 && split < p.n_splits, p.status);

@@ -474,7 +474,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (have) tc_fence_after();
       // O is divided by the row sum less the rounding of each tile's largest
       // P: when one key dominates a row, its bf16 rounding then cancels
-      // between O and the divisor.  LSE uses the exact sum.
+      // between O and the divisor.  LSE uses the exact sum.  (With dropout a row's
+      // keys are one tile: its largest P is 1 and has no rounding.)
       const float lo = l - corr;
       const float inv_l = lo > 0.f ? (DROP ? p.drop.mul : 1.f) / lo : 0.f;
       const bool split_ok = dcheck(split < p.n_splits, p.status);

@@ -13,6 +13,7 @@ struct DropParams {
   const unsigned long long* rng;  // seed, offset; in device memory
   uint32_t not_t[8];              // all ones where that bit of T = round(256 p) is clear
   float mul;                      // 1 / (1 - T / 256)
+  int mostly_kept;                // T < 128
 };
 
 struct FwdParams {
