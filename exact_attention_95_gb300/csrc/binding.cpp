@@ -20,6 +20,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <exception>
 
@@ -447,7 +448,8 @@ PyObject* bwd_dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!output(a[10], dQ, at::kBFloat16, Q->sizes(), s.dev) || !output(a[11], dK, at::kBFloat16, K->sizes(), s.dev) ||
         !output(a[12], dV, at::kBFloat16, K->sizes(), s.dev))
       Py_RETURN_NONE;
-    size_t bytes = g_bwd_workspace((int)s.B, (int)s.Hq, (int)s.Hkv, (int)s.N, (int)s.d, causal);
+    // (0 for sizes that the library refuses: with some workspace it says why.)
+    const size_t bytes = std::max<size_t>(g_bwd_workspace((int)s.B, (int)s.Hq, (int)s.Hkv, (int)s.N, (int)s.d, causal), 1);
     c10::DataPtr own;  // freed at the end of this call, for later work of the same stream
     void* ws = nullptr;
     if (a[13] == Py_None) {
