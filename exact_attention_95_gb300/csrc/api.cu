@@ -624,6 +624,7 @@ attn_status bwd_stages(unsigned stages, const void* Q, const void* K, const void
   if (drop) p.drop = *drop;
   p.q_splits = splits;
   p.parts = reinterpret_cast<float*>(ws + base_bytes);
+  p.parts_f4 = (workspace_bytes - base_bytes) / 16;
   p.scale = scale;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.causal = causal;

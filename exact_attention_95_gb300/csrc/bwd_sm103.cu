@@ -66,7 +66,7 @@
 namespace attn {
 namespace {
 
-constexpr int kBK = 128;  // keys per CTA
+constexpr int kBK = kBwdKeys;  // keys per CTA
 constexpr int kBQ = 128;  // query rows per inner tile
 constexpr int kMainThreads = 384;
 constexpr int kLaunchRegs = 168;  // per-thread registers of a 384-thread CTA
@@ -246,18 +246,6 @@ __device__ __forceinline__ int pairs_of(const BwdParams& p, int jt) {
 }
 __device__ __forceinline__ int pairs_of_part(const BwdParams& p, int pairs) { return (pairs + p.q_splits - 1) / p.q_splits; }
 
-// A part's fp32 rows of a key tile lie as [four columns][row]: a warp's 32 rows are written and
-// read 512 bytes at a time (row by row, 16 of every 512, a step of 256 CTAs took 20 us longer).
-// float4 of (which: 0 dV, 1 dK; kv head; key; columns 4 c ..) in part 0, and from part to part.
-template <int D>
-__device__ __forceinline__ size_t part_at(const BwdParams& p, int which, long long bhk, int key, int c) {
-  return (((size_t)which * p.B * p.Hkv + bhk) * p.Npad + key / kBK * kBK) * (D / 4) + c * kBK + key % kBK;
-}
-template <int D>
-__device__ __forceinline__ size_t part_stride(const BwdParams& p) {
-  return (size_t)2 * p.B * p.Hkv * p.Npad * (D / 4);
-}
-
 // dK, dV = bf16(sum of the parts' fp32 ones): 16 columns of a key a thread, neighbours have neighbouring keys.
 template <int D>
 __device__ __forceinline__ void dkv_rows(const BwdParams& p, int block, int blocks) {
@@ -276,7 +264,10 @@ __device__ __forceinline__ void dkv_rows(const BwdParams& p, int block, int bloc
     const int which = head >= (long long)p.B * p.Hkv;
     const long long bhk = head - which * (long long)p.B * p.Hkv;
     const int pairs = pairs_of(p, jt), each = pairs_of_part(p, pairs), n = (pairs + each - 1) / each;
-    const float4* src = reinterpret_cast<const float4*>(p.parts) + part_at<D>(p, which, bhk, key, 4 * piece);
+    const size_t at = part_at<D>(p, which, bhk, key, 4 * piece);
+    if (!dcheck(at + (n - 1) * stride + 3 * kBK < p.parts_f4 && bhk * p.N + key < (long long)p.B * p.Hkv * p.N, p.status))
+      continue;
+    const float4* src = reinterpret_cast<const float4*>(p.parts) + at;
     float4 sum[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) sum[c] = src[c * kBK];
@@ -807,9 +798,9 @@ __global__ void __launch_bounds__(kMainThreads, 1)
           }
           if (DROP && splits > 1) {
             // (A part without pairs is not read.)
-            if (have && key_ok && dcheck(split < splits && bhk < p.B * p.Hkv, p.status)) {
-              float4* f4 = reinterpret_cast<float4*>(p.parts) + split * part_stride<D>(p) +
-                           part_at<D>(p, which, bhk, key, col / 4);
+            const size_t at = split * part_stride<D>(p) + part_at<D>(p, which, bhk, key, col / 4);
+            if (have && key_ok && dcheck(at + 7 * kBK < p.parts_f4, p.status)) {
+              float4* f4 = reinterpret_cast<float4*>(p.parts) + at;
 #pragma unroll
               for (int i = 0; i < 8; ++i)
                 f4[i * kBK] = make_float4(__uint_as_float(o[4 * i]) * mul, __uint_as_float(o[4 * i + 1]) * mul,

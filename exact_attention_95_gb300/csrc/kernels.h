@@ -141,7 +141,20 @@ struct BwdParams {
   // where they are more than one their fp32 dV and dK [q_splits][2][B, Hkv, Npad / 128][d / 4][128][4].
   int q_splits;
   float* parts;
+  size_t parts_f4;  // float4 that there is room for (debug builds' checks)
 };
+constexpr int kBwdKeys = 128;  // keys of a tile
+// A part's fp32 rows of a key tile lie as [four columns][row]: a warp's 32 rows are written and
+// read 512 bytes at a time (row by row, 16 of every 512, a step of 256 CTAs took 20 us longer).
+// float4 of (which: 0 dV, 1 dK; kv head; key; columns 4 c ..) in part 0, and from part to part.
+template <int D>
+__host__ __device__ __forceinline__ size_t part_at(const BwdParams& p, int which, long long bhk, int key, int c) {
+  return (((size_t)which * p.B * p.Hkv + bhk) * p.Npad + key / kBwdKeys * kBwdKeys) * (D / 4) + c * kBwdKeys + key % kBwdKeys;
+}
+template <int D>
+__host__ __device__ __forceinline__ size_t part_stride(const BwdParams& p) {
+  return (size_t)2 * p.B * p.Hkv * p.Npad * (D / 4);
+}
 constexpr int kMaxMaskIters = 4096;  // (query head, query tile) pairs a masked backward CTA may list
 
 // Query rows are padded to a multiple of this in the backward workspace.
