@@ -74,19 +74,59 @@ struct Rows {
     return w <= token && (n[2] == 1 || stride[2] == token) && stride[0] % token == 0 ? w : 0;
   }
 };
+// Distances that rows of two sets have in common: `stride` times a number from lo to hi.
+struct Steps {
+  int64_t stride, lo, hi;
+};
+// Whether off plus one of each of the steps' distances is less than d away from 0; true also where that
+// takes more than `tries` tries to tell.  With strides that step over what lies below them, as those of a
+// packed array do, each step has two or three candidates.
+inline bool may_meet(int64_t off, const Steps* s, int count, int64_t d, int& tries) {
+  if (--tries < 0) return true;
+  if (count == 0) return off > -d && off < d;
+  int64_t low = 0, high = 0;  // of the steps behind this one
+  for (int i = 1; i < count; ++i) {
+    low += s[i].stride * s[i].lo;
+    high += s[i].stride * s[i].hi;
+  }
+  // off + stride * n + (low .. high) has to reach into (-d, d).
+  const int64_t from = -d + 1 - off - high, to = d - 1 - off - low, a = s[0].stride;
+  const int64_t first = from / a + (from % a > 0), last = to / a - (to % a < 0);
+  for (int64_t n = first > s[0].lo ? first : s[0].lo; n <= (last < s[0].hi ? last : s[0].hi); ++n)
+    if (may_meet(off + a * n, s + 1, count - 1, d, tries)) return true;
+  return false;
+}
 // Whether two sets of rows certainly share no element: their spans do not meet, or
 // both have their tokens' heads side by side in the same packed array (slices of
-// a projection), in parts of a token that do not meet.
+// a projection), in parts of a token that do not meet, or no distance between their rows is
+// less than a row.
 inline bool apart(const Rows& a, const Rows& b) {
   if (!overlap(a.span(), b.span())) return true;
-  const int64_t token = a.n[2] > 1 ? a.stride[2] : b.n[2] > 1 ? b.stride[2] : a.n[0] > 1 ? a.stride[0] : b.stride[0];
-  if (token <= 0 || a.size != b.size) return false;
-  const int64_t wa = a.token_width(token), wb = b.token_width(token);
-  if (!wa || !wb) return false;
+  if (a.size != b.size || a.d != b.d) return false;
   const int64_t bytes = (int64_t)(reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p));
   if (bytes % a.size) return false;
-  const int64_t off = ((bytes / a.size) % token + token) % token;  // of b's part behind a's, within a token
-  return off >= wa && off + wb <= token;
+  const int64_t token = a.n[2] > 1 ? a.stride[2] : b.n[2] > 1 ? b.stride[2] : a.n[0] > 1 ? a.stride[0] : b.stride[0];
+  if (token > 0) {
+    const int64_t wa = a.token_width(token), wb = b.token_width(token);
+    const int64_t off = ((bytes / a.size) % token + token) % token;  // of b's part behind a's, within a token
+    if (wa && wb && off >= wa && off + wb <= token) return true;
+  }
+  Steps s[6];
+  int count = 0;
+  for (int k = 0; k < 6; ++k) {
+    const Rows& r = k < 3 ? a : b;
+    const int64_t stride = r.stride[k % 3], most = r.n[k % 3] - 1;
+    if (most == 0 || stride == 0) continue;
+    int at = 0;
+    while (at < count && s[at].stride > stride) ++at;
+    if (at == count || s[at].stride != stride) {
+      for (int i = count++; i > at; --i) s[i] = s[i - 1];
+      s[at] = {stride, 0, 0};
+    }
+    (k < 3 ? s[at].lo : s[at].hi) += k < 3 ? -most : most;
+  }
+  int tries = 4096;
+  return !may_meet(bytes / a.size, s, count, a.d, tries);
 }
 
 }  // namespace attn

@@ -481,8 +481,10 @@ typedef struct {
  * memory: out of a packed projection into the attention's layout, for one.
  *   K and K_out may both be NULL (Hkv is then not read).
  *   Q_out may be Q and K_out may be K (same rows, same strides); an output may lie
- *   between other rows of one packed array [.., tokens, heads, d]; beyond that no output may
- *   overlap an array of the call (ATTN_ERR_INVALID_ARG), nor two rows of an output each other.
+ *   between other rows of one packed array, whatever its order ([tokens, heads, d], [tokens,
+ *   heads, 3, d], [heads, tokens, d], with or without batches); beyond that no output may
+ *   share an element with an array of the call (ATTN_ERR_INVALID_ARG; so are arrays whose
+ *   strides do not tell so in some thousand steps), nor two rows of an output with each other.
  *   positions [B, N] int32, positions_batch elements between batches (0: one
  *   [N] for all); NULL: 0 .. N - 1.  A row with a negative position has none and is
  *   copied as it is.
