@@ -649,7 +649,10 @@ def attn_rope_freqs(rot, base=10000.0, scaling="none", factor=1.0, original_len=
 
     scaling: "none"; for contexts `factor` times longer "linear" (positions divided),
     "base" (the base raised), or "parts" (pairs that turn at most `low` times over
-    original_len positions divided, those that turn `high` times left, a ramp between)."""
+    original_len positions divided, those that turn `high` times left, a ramp between).
+
+    Frequencies from elsewhere, w radians a position in float64 (below pi), are
+    (w / (2 * math.pi) * 2.0 ** 64).round().long()."""
     lib = load_library()
     if scaling not in _SCALINGS:
         raise ValueError(f"scaling must be one of {', '.join(_SCALINGS)}, got {scaling!r}")
@@ -869,7 +872,7 @@ def _check_rng(rng, device):
 
 def attn_fwd_dropout(Q, K, V, p, rng, scale=None, causal=False, out_dtype=None, O=None, LSE=None, stream=None):
     """attn_fwd (bf16) with elements of the softmax dropped with probability p, rounded to a
-    multiple of 1/256.
+    multiple of 1/256 (so nothing is dropped below 1/512; from 511/512 on p is refused).
 
     rng int64 [2] on the device: seed, and an offset (its low 32 bits count) that tells calls of
     one seed apart; read when the kernels run.  The mask follows from them and is
@@ -903,6 +906,8 @@ def attn_fwd_dropout(Q, K, V, p, rng, scale=None, causal=False, out_dtype=None, 
 
 
 def attn_bwd_dropout_workspace_size(B: int, Hq: int, Hkv: int, N: int, d: int, causal: bool = False) -> int:
+    """Bytes for attn_bwd_dropout.  They do not grow with N throughout: a workspace for several lengths has the
+    largest of their sizes."""
     return int(load_library().attn_bwd_dropout_workspace_size(B, Hq, Hkv, N, d, int(bool(causal))))
 
 

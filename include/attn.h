@@ -296,7 +296,10 @@ attn_status attn_bwd_dropout(const void* Q, const void* K, const void* V, const 
 
 /* Bytes of workspace attn_bwd_dropout needs on the current device: attn_bwd's, and where
  * there are fewer 128-key tiles (B * Hkv * ceil(N / 128)) than SMs, fp32 dK and dV of the parts
- * that a tile's work is cut into.  0 on bad sizes. */
+ * that a tile's work is cut into.  The number of parts falls as the tiles become more, so the size
+ * does not grow with N, B or Hkv throughout (32 heads on 8, d = 128, causal, 152 SMs: 67.6 MB for N = 2000,
+ * 40.5 MB for N = 2432): a workspace for several calls has the largest of their sizes, not that of the largest
+ * call.  0 on bad sizes. */
 size_t attn_bwd_dropout_workspace_size(int B, int Hq, int Hkv, int N, int d, int causal);
 
 /* Bytes of workspace attn_bwd needs: an fp32 dQ accumulator and two fp32
@@ -464,6 +467,8 @@ size_t attn_fwd_paged_workspace_size(int R, int T, int Hq, int Hkv, int d);
  *                     3.2 and 3.4; low 1, high 32 there).
  * factor is not read with ATTN_ROPE_NONE, the last three only with ATTN_ROPE_PARTS.
  *   freqs [rot / 2], rot even, 2 .. 1024; *amplitude: 1 but for ATTN_ROPE_PARTS.
+ * Any other frequencies below half a turn a position do as well: of w radians a position
+ * freqs[i] = round(w / (2 pi) * 2^64), in 64 bits.
  */
 typedef enum { ATTN_ROPE_NONE = 0, ATTN_ROPE_LINEAR = 1, ATTN_ROPE_BASE = 2, ATTN_ROPE_PARTS = 3 } attn_rope_scaling;
 attn_status attn_rope_freqs(uint64_t* freqs, double* amplitude, int rot, double base, attn_rope_scaling scaling,
