@@ -242,20 +242,36 @@ bool make_page_map(CUtensorMap* m, const void* base, long long planes, int page,
 
 namespace {
 
-// Diagnostic kernel: one thread waits on an mbarrier that is never completed.
+// Diagnostic kernel: each form of wait, a warp each, on an mbarrier that is never completed.
 __global__ void selftest_wait_kernel(int* status, unsigned long long limit_ns) {
   __shared__ __align__(8) uint64_t bar;
-  __shared__ int abort_flag;
+  // Of each form of wait: its abort flag, its status, the lanes that it gave up on.
+  __shared__ int abort_flag[4], result[4], lanes[4];
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&bar), 1);
-    abort_flag = 0;
     fence_mbar_init();
   }
+  const int form = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) abort_flag[form] = result[form] = lanes[form] = 0;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    WaitCtx wc{&abort_flag, status, limit_ns};
-    mbar_wait(smem_u32(&bar), 0, wc);
+  const WaitCtx wc{&abort_flag[form], &result[form], limit_ns};
+  bool got = true;
+  if (form == 0) {
+    if (lane == 0) got = mbar_wait(smem_u32(&bar), 0, wc);
+  } else if (form == 1) {
+    if (lane == 0) got = mbar_wait_drain(smem_u32(&bar), 0, wc);
+  } else if (form == 2) {
+    got = mbar_wait_warp(smem_u32(&bar), 0, wc);
+  } else {
+    got = mbar_wait_warp_short(smem_u32(&bar), 0, wc);
   }
+  if (!got) atomicAdd(&lanes[form], 1);
+  __syncthreads();
+  // (The drain sets no abort flag.)
+  bool all = true;
+  for (int k = 0; k < 4; ++k)
+    all = all && result[k] == kDevTimeout && lanes[k] == (k < 2 ? 1 : 32) && abort_flag[k] == (k == 1 ? 0 : 1);
+  if (threadIdx.x == 0 && all) atomicCAS(status, kDevOk, kDevTimeout);
 }
 
 }  // namespace
@@ -718,7 +734,7 @@ attn_status attn_selftest_wait_timeout(unsigned long long limit_ns, void* stream
   if (limit_ns == 0 || limit_ns > 1000000000ull) return ATTN_ERR_INVALID_ARG;
   int* status = status_ptr();
   if (!status) return ATTN_ERR_CUDA;
-  selftest_wait_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(status, limit_ns);
+  selftest_wait_kernel<<<1, 128, 0, static_cast<cudaStream_t>(stream)>>>(status, limit_ns);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

@@ -519,10 +519,10 @@ const char* attn_status_string(attn_status s);
  * since the last call, ATTN_OK otherwise (ATTN_ERR_CUDA if the read fails). */
 attn_status attn_last_device_status(void* stream);
 
-/* Diagnostic: launches one CTA that waits, with the library's bounded-wait
- * routine and a limit of `limit_ns` nanoseconds (at most 1e9), on an mbarrier
- * that nothing will ever complete, then returns.  A working timeout path makes
- * the following attn_last_device_status() report ATTN_ERR_TIMEOUT. */
+/* Diagnostic: launches one CTA that waits, with each form of the library's
+ * bounded wait side by side and a limit of `limit_ns` nanoseconds (at most 1e9), on an mbarrier
+ * that nothing will ever complete, then returns.  Working timeout paths (all of
+ * them) make the following attn_last_device_status() report ATTN_ERR_TIMEOUT. */
 attn_status attn_selftest_wait_timeout(unsigned long long limit_ns, void* stream);
 
 /* The same with the bounded wait of the paged cache's attention kernels. */
