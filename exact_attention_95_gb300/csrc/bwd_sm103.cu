@@ -45,14 +45,14 @@
 // with D_i = <dO_i, O_i> as before.  Lane l of a math warp makes the keep words of query
 // rows l and 32 + l of its warpgroup's 64 against the warp's 32 keys, and two
 // transposes of 32 x 32 bits give every key's thread its 64 bits.  dV gets the
-// factor in its epilogue.  Measured, 32 heads of 4096 tokens twice, causal, d = 128: 750 us
-// for all three kernels (916 TFLOPS), without dropout 663; of the difference the words and
-// their transposes are two thirds, the masking of P and dP the rest.
+// factor in its epilogue.  Measured, 32 heads of 4096 tokens twice, causal, d = 128: 728 us
+// for all three kernels (944 TFLOPS), without dropout 661: the words and
+// their transposes, and the masking of P and dP.
 //
 // Where there are fewer key tiles than SMs (few kv heads, short sequences), a tile's
 // (query head, query tile) pairs are cut into p.q_splits equal parts with a CTA
 // each, which write fp32 dK and dV of their own into the workspace; bwd_join, in place of
-// bwd_dq, adds them in the order of the parts (12 heads on 4, N = 777, twice: 35 us, in one
+// bwd_dq, adds them in the order of the parts (12 heads on 4, N = 777, twice: 34 us, in one
 // part 66; 16 heads on 1, N = 2000: 78 and 648).
 #include <algorithm>
 
@@ -913,7 +913,7 @@ size_t bwd_workspace_bytes(int B, int Hq, int N, int d) {
 // first) until the longest is done or, where they are more than the SMs, for the average
 // load of an SM and half a CTA more; and a part's sums are written and read again,
 // an eightieth of a step each.  Only where an unsplit grid leaves SMs idle.
-// Measured by the number of parts, us: 12 heads on 4, N = 777, twice, causal 1 66, 2 43.6, 3 35.0 (taken),
+// Measured by the number of parts, d = 128, us: 12 heads on 4, N = 777, twice, causal 1 66, 2 43.6, 3 35.0 (taken),
 // 4 37.9, 8 46.6; not causal 1 67, 2 43.7 (taken), 3 57, 5 50.6; 32 on 8, N = 1000, causal 1 96, 2 59.7,
 // 3 49.8 (taken), 4 50.7; 8 on 2, N = 4096, causal 1 331, 3 129, 4 103 (taken), 5 107; 4 heads, N = 4096,
 // causal 1 93, 2 65 (taken), 3 74; 16 heads, N = 256, four times 1 18 (taken), 2 30.

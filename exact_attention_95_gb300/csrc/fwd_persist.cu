@@ -38,10 +38,11 @@
 // l less the rounding of each tile's largest P: right for rows that keep that element, off by up to half a
 // bf16 step in those that drop it.  It is done where more keep it, T < 128; elsewhere O is divided
 // by l, and rows that keep it have its rounding, those that drop it none.)  Measured, 32
-// heads of 4096 tokens twice, causal, d = 128: 250 us, 1100 TFLOPS; without dropout 190.  A step
-// of both tiles takes 4150 cycles instead of 2900: the words 1000 of them (80 wide
+// heads of 4096 tokens twice, causal, d = 128: 250 us on the device, 251 a call among calls (1100 TFLOPS);
+// without dropout 184 to 188.  When this was built (without dropout 190) a step
+// of both tiles took 4150 cycles instead of 2900: the words 1000 of them (80 wide
 // multiplies a row, 5.2 cycles of their pipe each, and what hangs on them), the
-// masking 400; without the words it is 199 us, without the masking 223.  The words made elsewhere
+// masking 400; without the words it was 199 us, without the masking 223.  The words made elsewhere
 // -- behind the scores' read, the next tile's among or behind the exponentials, under the TMEM loads
 // and stores, by a fourth warpgroup through shared memory -- measured 249 to 294 us: the row's
 // chain S, P, P V is as long, or its warps have fewer issue slots.

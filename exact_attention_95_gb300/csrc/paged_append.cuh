@@ -62,7 +62,8 @@ __device__ __forceinline__ Run<D> run_of(const KvAppendParams& p, long long t, l
   return r;
 }
 
-// The end of a run: rows [0, off) at the new scale s where it is larger, and the scale.
+// The end of a run: rows [0, off) at the new scale s where it is larger, and the scale.  (By the run's
+// threads, 16 bytes each at a time: for a run of few threads a chain of up to 127 reads and writes.)
 template <int D>
 __device__ __forceinline__ void finish_run(const Run<D>& r, int id, int count, float old, float s) {
   if (r.n > 0 && r.off > 0 && s > old) {

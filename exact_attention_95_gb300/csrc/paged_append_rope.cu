@@ -19,7 +19,10 @@ namespace {
 // a warp for up to kWarpRun, else by the CTA, as in the append without
 // positions, all by one copy of the code.
 //
-// Measured, 8 kv and 32 query heads, d = 128: 64 requests of one token 4.4 us; 25157 tokens of nine
+// Measured, 8 kv and 32 query heads, d = 128: 64 requests of one token 4.4 us where no page's scale
+// grows, and with a page whose scale grows at its last row 17 us (64 tokens a page) or 30 (128), however many
+// they are: finish_run() takes the rows before the new one in turns of this run's eight threads, each a
+// trip to memory and back (without positions sixteen threads, 9 and 15 us of 2.7); 25157 tokens of nine
 // prompts 103 us, 5.5 TB/s, 82 % of the measured copy rate (the append alone 33 us, the
 // queries alone 65).  What holds it: the keys' angles (27 instructions an angle, 14 us) and the waits of
 // a run's chain (slots, rows, largest element, codes) with three CTAs of 80 registers an

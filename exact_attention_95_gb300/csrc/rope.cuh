@@ -17,9 +17,11 @@ namespace attn {
 // for every 32-bit position (a 32-bit float angle is off by 0.01 rad at 131072).
 // The nearest quarter turn is taken off in whole numbers; the rest, within
 // pi / 4, goes through Taylor's series up to x^9 and x^8 (cut off below 3e-8).
-// About 20 instructions.  Off by at most 2^-22: 2^-24 relative each from the
-// conversion and the constant, together 0.8 * 2^-23 of an angle of pi / 4, the
-// sums' roundings, and the rest of the series.
+// About 20 instructions.  Off by less than 3 * 2^-24, in units of 2^-24: the angle has the
+// product's cut at 2^-32 of a turn (0.03) and a rounding each of the conversion, the constant and their
+// product (3 x, which moves cos and sin by x sin x and x cos x, below 0.56, times 3: 1.67);
+// cos then its last sum's (0.5), z's (z / 2, 0.31), the inner terms' (0.07) and the rest of the series
+// (0.41), sin its last sum's (0.5), the inner terms' (0.33) and the rest (0.03).
 __device__ __forceinline__ void cos_sin(uint32_t pos, uint64_t freq, float& c, float& s) {
   const uint32_t t = __umulhi(pos, (uint32_t)freq) + pos * (uint32_t)(freq >> 32);  // of pos * freq, the upper half
   const uint32_t q = (t + 0x20000000u) >> 30;
@@ -84,10 +86,15 @@ constexpr int rope_tokens(int d) { return kRopeThreads / (d / 16); }
 // through them, a batch of heads' loads ahead of their use.  Measured (rope_kernel): 8192
 // tokens of 64 heads of 128, bf16, out of a packed projection 42.5 us, 6.3 TB/s, 94 % of the
 // measured copy rate; 64 tokens of 40 heads 2.4 us, a launch and two dependent
-// reads; 3003 tokens of 20 heads of 64 in fp32 7.5 to 8 us, which is mostly the start of a
-// grid of one round (30 MB).  The 16 elements are
+// reads.  The 16 elements are
 // two pieces of eight: i.. and rot / 2 + i.. where halves pair, 16 adjacent
-// ones otherwise, so both are 16-byte accesses (32 in fp32) and pairs never leave a thread.
+// ones otherwise, so accesses are of 16 bytes and pairs never leave a thread.  A warp's accesses lie side by
+// side only in bf16 where whole rows' halves pair; elsewhere each is 16 bytes of 32, in fp32 16 of 64
+// where 16 elements are adjacent.  L2 then has up to twice as many sectors to write for the same bytes,
+// DRAM no more than the bytes.  8192 tokens of 64 heads of 128: bf16 interleaved 44 us, 48 of 128
+// elements turned 43 (either way), fp32 85, interleaved 92.6 (87 % of the copy rate), 48 turned 90 to 92;
+// of 64: bf16 25 (79 to 82 %), fp32 45, interleaved 50.  3003 tokens of 20 heads of 64 in fp32 (30 MB), where half a
+// head turns 7.8 to 8.0 us, where all of it does in halves 6.6.
 template <class T, int D, bool INTER>
 __device__ __forceinline__ void rope_block(const RopeParams& p, int group, int h0, int heads) {
   constexpr int UNITS = D / 16;
